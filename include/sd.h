@@ -69,6 +69,10 @@ extern "C" {
                                    not written to input_ids */
 #define SD_ERR_DRAFT_COUNT 128  /* cu_drafts gives a request a draft count outside [0, K_max]:
                                    clamped (sd_verify_ragged) */
+#define SD_ERR_KV_SLOT 256      /* a slot beyond the cache: that token is not written */
+#define SD_ERR_KV_RANGE 512     /* a length, a prefix entry or a block-table entry of a cache read
+                                   is out of range: those tokens are left out (sd_kv_read writes
+                                   zeros for them) */
 
 /* input kinds for sd_verify */
 #define SD_F32_PROBS 0    /* fp32 probabilities, already at the sampling temperature */
@@ -439,6 +443,128 @@ SD_API int sd_verify_prepare_padded(
 SD_API int sd_hidden_gather(int capacity, int H, const int32_t* total_out, const int32_t* hidden_map,
                      const void* target_hidden, long ld_in, int n_in_rows, const void* h_shared,
                      void* out_hidden, long ld_out, int32_t* err, void* stream);
+
+/* ---- the paged 8-bit cache ----
+ *
+ * The slots, positions and block tables of the calls above index a paged KV cache; these calls
+ * write, read and attend to one. Conventions for all of them:
+ *   - A page is block_size tokens, a power of two from 8 to 128. K and V hold one e4m3 byte for
+ *     each value: value d of head h of slot t of page b is at
+ *     b*st_block + t*st_tok + h*st_head + d of k_cache and of v_cache (strides in elements; base
+ *     addresses 16-byte aligned, strides multiples of 16). D is a multiple of 16 from 16 to 128.
+ *   - k_scale and v_scale [num_blocks, Hkv] fp32 hold one scale for each page and head: the byte q
+ *     stands for e4m3(q) * scale. sd_kv_write makes powers of two, so that every product with a
+ *     scale is exact; reads take any positive scale. A scale of 0 means that the page holds zeros
+ *     (a cache may start as zeroed memory).
+ *   - block_table [B, max_blocks] as for sd_pdraft_expand: position p of request r is slot
+ *     p % block_size of page block_table[r][p / block_size].
+ */
+
+/*
+ * sd_kv_write -- quantise the K and V of n tokens into the pages that slot_mapping names.
+ *
+ * Token i goes to slot s = slot_mapping[i]: page s / block_size, offset s % block_size; a
+ * negative slot (PADDING_SLOT_ID: rejected and padding tokens) is skipped, one beyond the cache
+ * too, with SD_ERR_KV_SLOT. For each page that receives tokens, and each head of K and of V:
+ *   need  = the smallest power of two, 2^-100 at the least, with |x| <= 448 need for every finite
+ *           value x that the call writes to the page;
+ *   scale = max(old scale, need), the old scale counting as 0 when the call writes the page's
+ *           slot 0 (the page then starts afresh: pages fill in order, so what a rewound or reused
+ *           page held before is void);
+ *   the tokens written become e4m3(x / scale), to nearest even; infinities become +-448, NaN stays
+ *   NaN; when the scale grew, what the page's other slots hold is rounded again to the new scale:
+ *   e4m3(held * old / scale).
+ * The tokens of one page stand next to one another in slot_mapping, up to 31 negative entries in a
+ * row between them (the slots of a request's consecutive positions do); of tokens with the same slot the last is kept. Two stretches of the
+ * same page in one call race on its scale.
+ * Arguments: k, v: bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
+ *   strides multiples of 8; they may be slices of one projection); slot_mapping [n] int32;
+ *   num_blocks*block_size <= 2^31.
+ */
+SD_API int sd_kv_write(int n, int Hkv, int D, const void* k, long ld_k, long hs_k, const void* v,
+                       long ld_v, long hs_v, const int32_t* slot_mapping, void* k_cache,
+                       void* v_cache, long st_block, long st_tok, long st_head, float* k_scale,
+                       float* v_scale, int num_blocks, int block_size, int32_t* err,
+                       void* stream);
+
+/*
+ * sd_kv_read -- what the cache holds, as bf16 rows.
+ *
+ * Row i of k_out and v_out, cu_tokens[r] <= i < cu_tokens[r+1], is request r's token at position
+ * first_pos[r] + i - cu_tokens[r] (first_pos NULL: 0): e4m3(q) * scale rounded to bf16 (exact for
+ * power-of-two scales, unless it leaves bf16's range). Rows outside [cu_tokens[0], cu_tokens[B])
+ * are not written; a position that the table does not cover reads as 0 with SD_ERR_KV_RANGE.
+ * Arguments: n rows; cu_tokens [B+1], non-decreasing; k_out, v_out bf16, value d of head h of row
+ *   i at i*ld_out + h*hs_out + d (16-byte aligned, strides multiples of 8).
+ */
+SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const void* v_cache,
+                      long st_block, long st_tok, long st_head, const float* k_scale,
+                      const float* v_scale, int num_blocks, int block_size,
+                      const int32_t* block_table, int max_blocks, const int32_t* cu_tokens,
+                      const int32_t* first_pos, void* k_out, void* v_out, long ld_out,
+                      long hs_out, int32_t* err, void* stream);
+
+/*
+ * sd_kv_attend -- attention of each request's new tokens to its cached ones.
+ *
+ * Request r has the query tokens cu_q[r] .. cu_q[r+1]-1 of q (n_r of them: K+1 verify slots, a
+ * drafter batch's a_r + K slots, one token, a chunk of a prompt) and ctx_lens[r] tokens in the
+ * cache, its own new ones included (sd_kv_write before this call). Query token i of the request
+ * stands at position ctx_lens[r] - n_r + i and, when causal, sees the tokens up to its own
+ * position; else all ctx_lens[r]. Head h of Hq reads head h / (Hq / Hkv) of the cache.
+ *   S = sm_scale * q . k,  out = sum_j softmax(S)_j v_j,  lse = ln sum_j e^(S_j)
+ * q is taken exactly (its largest values to 2^-18), exponentials, sums and products are fp32,
+ * the weights of v have 8 significant bits (2^-18 of the row's largest at the least), out is
+ * rounded to bf16 once. A token that sees nothing gets out = 0 and lse = -inf. NaN in tokens that
+ * a query token does not see has no effect on it.
+ * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] raises
+ * SD_ERR_KV_RANGE; those tokens are left out. cu_q has B+1 non-decreasing entries in [0, n]
+ * (others are clamped, SD_ERR_KV_RANGE); tokens outside [cu_q[0], cu_q[B]) are not written.
+ * Arguments: q, out bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
+ *   strides multiples of 8); lse [n, Hq] fp32 or NULL; max_q: the most query tokens that a request
+ *   is expected to have, which only chooses the kernel (any value >= 1 is right); Hq a multiple of
+ *   Hkv; sm_scale positive and finite; workspace: at least sd_kv_attend_workspace_bytes(D) bytes of
+ *   device scratch, 16-byte aligned, its contents irrelevant before and after. Calls that may run
+ *   concurrently need separate workspaces.
+ */
+SD_API int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q, long ld_q,
+                        long hs_q, const void* k_cache, const void* v_cache, long st_block,
+                        long st_tok, long st_head, const float* k_scale, const float* v_scale,
+                        int num_blocks, int block_size, const int32_t* block_table,
+                        int max_blocks, const int32_t* ctx_lens, const int32_t* cu_q,
+                        float sm_scale, int causal, void* out, long ld_out, long hs_out,
+                        float* lse, void* workspace, size_t workspace_bytes, int32_t* err,
+                        void* stream);
+
+/* Scratch of sd_kv_attend, where the parts of a request that several CTAs share wait to be joined
+ * (it does not depend on the batch). */
+SD_API size_t sd_kv_attend_workspace_bytes(int D);
+
+/*
+ * sd_token_logprobs -- log probabilities of given tokens (a step's answer: sd_verify's
+ * out_tokens on its target rows), with each row's entropy and best alternatives.
+ *
+ * Row r*J + j of rows belongs to tokens[r][j] (J = K+1 for sd_verify's outputs). SD_F32_PROBS:
+ * p = the row. SD_BF16_LOGITS: p = softmax(l / T_r), T_r = temperature[r] (NULL, or 0: 1; a
+ * greedy request is reported at temperature 1).
+ *   logprob[r][j] = ln p(token)
+ *   entropy[r][j] = -sum p ln p
+ *   rank[r][j]    = 1 + the entries that come before the token, larger ones first, equal ones by
+ *                   lower index
+ *   top_ids, top_logprobs [r][j][0..n_top): the first n_top entries in that order.
+ * A row without a token (tokens -1, sd_verify's padding) is not read: logprob 0, entropy 0, rank 0,
+ * top_ids -1, top_logprobs -inf. A token outside [-1, V) raises SD_ERR_TOKEN_RANGE: logprob -inf and
+ * rank 0 for one >= V, a negative one counts as none.
+ * Arguments: B >= 0, J >= 1, 1 <= V <= SD_TOP_MAX_V; rows [B*J, V] of stride ld >= V;
+ *   0 <= n_top <= min(V, SD_TOP_MAX); entropy, rank may be NULL; top_ids and top_logprobs may be
+ *   NULL if n_top is 0.
+ */
+#define SD_TOP_MAX 32
+#define SD_TOP_MAX_V 33554432
+SD_API int sd_token_logprobs(int B, int J, int V, int dtype, const void* rows, long ld,
+                             const int32_t* tokens, const float* temperature, int n_top,
+                             float* logprob, float* entropy, int32_t* rank, int32_t* top_ids,
+                             float* top_logprobs, int32_t* err, void* stream);
 
 /* ---- diagnostics (test support; same conventions) ---- */
 

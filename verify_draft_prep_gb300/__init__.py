@@ -30,6 +30,11 @@ SD_ERR_ZERO_ROW = 16
 SD_ERR_TOTAL_RANGE = 32
 SD_ERR_WAIT = 64
 SD_ERR_DRAFT_COUNT = 128
+SD_ERR_KV_SLOT = 256
+SD_ERR_KV_RANGE = 512
+
+SD_TOP_MAX = 32
+SD_TOP_MAX_V = 33554432
 
 EXPORTED = ["sd_verify", "sd_verify_workspace_bytes", "sd_verify_kernels",
             "sd_verify_noalloc", "sd_draft_sample", "sd_pdraft_prepare_padded",
@@ -37,7 +42,8 @@ EXPORTED = ["sd_verify", "sd_verify_workspace_bytes", "sd_verify_kernels",
             "sd_race_E_approx_error", "sd_race_E_check", "sd_status_string", "sd_version",
             "sd_verify_prepare", "sd_verify_prepare_workspace_bytes", "sd_verify_prepare_kernels",
             "sd_verify_prepare_ragged", "sd_diag_verify_prepare_withheld",
-            "sd_verify_prepare_padded"]
+            "sd_verify_prepare_padded", "sd_kv_write", "sd_kv_read", "sd_kv_attend",
+            "sd_kv_attend_workspace_bytes", "sd_token_logprobs"]
 
 _lock = threading.Lock()
 _lib = None
@@ -119,6 +125,20 @@ def load():
         lib.sd_race_E_approx_error.restype = i32
         lib.sd_race_E_check.argtypes = [u32, u64, P, P]
         lib.sd_race_E_check.restype = i32
+        cache = [P, P, i64, i64, i64, P, P, i32, i32]
+        lib.sd_kv_write.argtypes = [i32, i32, i32, P, i64, i64, P, i64, i64, P] + cache + [P, P]
+        lib.sd_kv_write.restype = i32
+        lib.sd_kv_read.argtypes = [i32, i32, i32, i32] + cache + [P, i32, P, P, P, P, i64, i64,
+                                                                  P, P]
+        lib.sd_kv_read.restype = i32
+        lib.sd_kv_attend.argtypes = [i32, i32, i32, i32, i32, i32, P, i64, i64] + cache + [
+            P, i32, P, P, ctypes.c_float, i32, P, i64, i64, P, P, ctypes.c_size_t, P, P]
+        lib.sd_kv_attend.restype = i32
+        lib.sd_kv_attend_workspace_bytes.argtypes = [i32]
+        lib.sd_kv_attend_workspace_bytes.restype = ctypes.c_size_t
+        lib.sd_token_logprobs.argtypes = [i32, i32, i32, i32, P, i64, P, P, i32, P, P, P, P, P, P,
+                                          P]
+        lib.sd_token_logprobs.restype = i32
         lib.sd_status_string.argtypes = [i32]
         lib.sd_status_string.restype = ctypes.c_char_p
         lib.sd_version.argtypes = []
@@ -519,3 +539,182 @@ def sd_race_E_check(w_begin, count, counts, stream=None):
     took the double path) over [w_begin, w_begin + count)."""
     rc = load().sd_race_E_check(w_begin, count, _ptr(counts), _stream(counts, stream))
     _check(rc, "sd_race_E_check")
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale):
+    """The cache arguments of the C calls: pointers, strides and sizes of a cache in e4m3 (or its
+    bytes as uint8), [num_blocks, block_size, Hkv, D], with scales [num_blocks, Hkv] fp32."""
+    import torch
+
+    for t in (k_cache, v_cache):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or t.dim() != 4 or t.stride(3) != 1:
+            raise SDError("a cache is e4m3 (or uint8) [num_blocks, block_size, Hkv, D] with "
+                          "contiguous heads")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise SDError("k_cache and v_cache must have the same shape and strides")
+    nb, bs, Hkv, D = k_cache.shape
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or tuple(t.shape) != (nb, Hkv) or not t.is_contiguous():
+            raise SDError("scales must be contiguous float32 [num_blocks, Hkv]")
+    # a dimension of one has no stride of its own
+    strides = [t if n > 1 else 16 for n, t in zip((nb, bs, Hkv), k_cache.stride())]
+    return (_ptr(k_cache), _ptr(v_cache), *strides, _ptr(k_scale), _ptr(v_scale), nb, bs)
+
+
+def _head_rows(t, Hn, D, what):
+    """Strides of bf16 [n, heads, D] rows with contiguous heads."""
+    import torch
+
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (Hn, D) \
+            or (t.numel() and t.stride(2) != 1):
+        raise SDError(f"{what} must be bfloat16 [tokens, {Hn}, {D}] with contiguous heads")
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if Hn > 1 else 0)
+
+
+def _int32(t, shape, what):
+    import torch
+
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise SDError(f"{what} must be contiguous int32 {list(shape)}")
+
+
+def sd_kv_write(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None, stream=None):
+    """Quantise the K and V of n tokens into the pages that slot_mapping names (see include/sd.h).
+
+    k, v: [n, Hkv, D] bfloat16 (strided: they may be slices of one projection); slot_mapping: [n]
+    int32, negative where nothing is written; caches: [num_blocks, block_size, Hkv, D]
+    float8_e4m3fn; scales: [num_blocks, Hkv] float32 (zeroed before first use).
+    """
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    Hkv, D = k_cache.shape[2:]
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise SDError("k and v must hold the same tokens")
+    _int32(slot_mapping, (n,), "slot_mapping")
+    rc = load().sd_kv_write(n, Hkv, D, _ptr(k), *_head_rows(k, Hkv, D, "k"), _ptr(v),
+                            *_head_rows(v, Hkv, D, "v"), _ptr(slot_mapping), *cache, _ptr(err),
+                            _stream(k_cache, stream))
+    _check(rc, "sd_kv_write")
+
+
+def sd_kv_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_tokens, k_out, v_out,
+               first_pos=None, err=None, stream=None):
+    """Read tokens of every request back as bf16 rows (see include/sd.h).
+
+    block_table: [B, max_blocks] int32; cu_tokens: [B+1] int32, the rows of each request; k_out,
+    v_out: [n, Hkv, D] bfloat16 of the same strides; first_pos: [B] int32, the position of each
+    request's first row, or None for 0.
+    """
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    Hkv, D = k_cache.shape[2:]
+    B, mb = block_table.shape
+    _int32(block_table, (B, mb), "block_table")
+    _int32(cu_tokens, (B + 1,), "cu_tokens")
+    if first_pos is not None:
+        _int32(first_pos, (B,), "first_pos")
+    strides = _head_rows(k_out, Hkv, D, "k_out")
+    if v_out.shape != k_out.shape or _head_rows(v_out, Hkv, D, "v_out") != strides:
+        raise SDError("k_out and v_out must have the same shape and strides")
+    rc = load().sd_kv_read(B, k_out.shape[0], Hkv, D, *cache, _ptr(block_table), mb,
+                           _ptr(cu_tokens), _ptr(first_pos), _ptr(k_out), _ptr(v_out), *strides,
+                           _ptr(err), _stream(k_cache, stream))
+    _check(rc, "sd_kv_read")
+
+
+_attend_workspaces = {}
+
+
+def attend_workspace(device, D):
+    """Scratch of sd_kv_attend for this device, shared by calls that pass none (calls on
+    concurrent streams must pass their own)."""
+    import torch
+
+    need = max(load().sd_kv_attend_workspace_bytes(D), 16)
+    key = torch.device(device)
+    ws = _attend_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=key)
+        _attend_workspaces[key] = ws
+    return ws
+
+
+def sd_kv_attend_workspace_bytes(D):
+    """Bytes of scratch that sd_kv_attend needs for heads of D values."""
+    return load().sd_kv_attend_workspace_bytes(D)
+
+
+def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, cu_q, out, lse=None,
+                 max_q=None, sm_scale=None, causal=True, workspace_buf=None, err=None,
+                 stream=None):
+    """Attention of each request's new tokens to its cached ones (see include/sd.h).
+
+    q, out: [n, Hq, D] bfloat16; ctx_lens: [B] int32, tokens in the cache, the new ones included;
+    cu_q: [B+1] int32, the query tokens of each request; lse: [n, Hq] float32 or None; max_q: the
+    most query tokens of a request that is expected (None: n); sm_scale: None for D ** -0.5;
+    workspace_buf: uint8 device tensor of at least sd_kv_attend_workspace_bytes(D) bytes, or None
+    for this device's shared one.
+    """
+    import torch
+
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    Hkv, D = k_cache.shape[2:]
+    B, mb = block_table.shape
+    if q.dim() != 3:
+        raise SDError("q must be [tokens, Hq, D]")
+    n, Hq = q.shape[:2]
+    _int32(block_table, (B, mb), "block_table")
+    _int32(ctx_lens, (B,), "ctx_lens")
+    _int32(cu_q, (B + 1,), "cu_q")
+    sq, so = _head_rows(q, Hq, D, "q"), _head_rows(out, Hq, D, "out")
+    if out.shape[0] != n:
+        raise SDError("out must have q's shape")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, Hq)
+                            or not lse.is_contiguous()):
+        raise SDError("lse must be contiguous float32 [tokens, Hq]")
+    ws = workspace_buf if workspace_buf is not None else attend_workspace(k_cache.device, D)
+    rc = load().sd_kv_attend(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q), *sq,
+                             *cache, _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q),
+                             D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)),
+                             _ptr(out), *so, _ptr(lse), _ptr(ws), ws.numel(), _ptr(err),
+                             _stream(k_cache, stream))
+    _check(rc, "sd_kv_attend")
+
+
+def sd_token_logprobs(rows, tokens, logprob, entropy=None, rank=None, top_ids=None,
+                      top_logprobs=None, temperature=None, err=None, stream=None):
+    """Log probabilities of given tokens, with entropy, rank and alternatives (see include/sd.h).
+
+    rows: [B*J, V] float32 probabilities or bfloat16 logits; tokens: [B, J] int32, -1 for none (a
+    step's out_tokens); logprob, entropy: [B, J] float32; rank: [B, J] int32; top_ids,
+    top_logprobs: [B, J, n_top] int32 and float32; temperature: [B] float32 or None. Every output
+    but logprob may be None.
+    """
+    import torch
+
+    B, J = tokens.shape
+    V = rows.shape[1]
+    if rows.dtype == torch.float32:
+        dtype = SD_F32_PROBS
+    elif rows.dtype == torch.bfloat16:
+        dtype = SD_BF16_LOGITS
+    else:
+        raise SDError("rows must be float32 probabilities or bfloat16 logits")
+    if rows.shape[0] != B * J:
+        raise SDError("rows must hold B*J rows")
+    _int32(tokens, (B, J), "tokens")
+    n_top = 0 if top_ids is None else top_ids.shape[-1]
+    for t, dt, shape, what in ((logprob, torch.float32, (B, J), "logprob"),
+                               (entropy, torch.float32, (B, J), "entropy"),
+                               (rank, torch.int32, (B, J), "rank"),
+                               (top_ids, torch.int32, (B, J, n_top), "top_ids"),
+                               (top_logprobs, torch.float32, (B, J, n_top), "top_logprobs"),
+                               (temperature, torch.float32, (B,), "temperature")):
+        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise SDError(f"{what} must be contiguous {dt} {list(shape)}")
+    if n_top and top_logprobs is None:
+        raise SDError("top_ids comes with top_logprobs")
+    rc = load().sd_token_logprobs(B, J, V, dtype, _ptr(rows), _row_stride(rows), _ptr(tokens),
+                                  _ptr(temperature), n_top, _ptr(logprob), _ptr(entropy),
+                                  _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(err),
+                                  _stream(rows, stream))
+    _check(rc, "sd_token_logprobs")

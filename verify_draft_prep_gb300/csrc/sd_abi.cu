@@ -53,6 +53,19 @@ int sd_verify_prepare_padded_launch(int, int, int, int, const void*, long, const
                                     int, int32_t, int32_t*, int32_t*, int32_t*, int32_t*,
                                     uint8_t*, uint8_t*, int32_t*, int32_t*, int, const void*, long,
                                     int, const void*, void*, long, void*, int32_t*, cudaStream_t);
+int sd_kv_write_launch(int, int, int, const void*, long, long, const void*, long, long,
+                       const int32_t*, void*, void*, long, long, long, float*, float*, int, int,
+                       int32_t*, cudaStream_t);
+int sd_kv_read_launch(int, int, int, int, const void*, const void*, long, long, long,
+                      const float*, const float*, int, int, const int32_t*, int, const int32_t*,
+                      const int32_t*, void*, void*, long, long, int32_t*, cudaStream_t);
+size_t sd_kv_attend_workspace_launch(int);
+int sd_kv_attend_launch(int, int, int, int, int, int, const void*, long, long, const void*,
+                        const void*, long, long, long, const float*, const float*, int, int,
+                        const int32_t*, int, const int32_t*, const int32_t*, float, int, void*,
+                        long, long, float*, void*, int32_t*, cudaStream_t);
+int sd_logprobs_launch(int, int, int, int, const void*, long, const int32_t*, const float*, int,
+                       float*, float*, int32_t*, int32_t*, float*, int32_t*, cudaStream_t);
 }
 
 namespace {
@@ -571,6 +584,125 @@ int sd_verify_prepare_padded(int B, int K, int V, int dtype, const void* target,
       mask_token_id, input_ids, positions, slot_mapping, hidden_map, is_masked, rejected,
       scatter_map, new_token_idx, H, target_hidden, ld_in, n_in_rows, h_shared, out_hidden,
       ld_out, workspace, err, (cudaStream_t)stream);
+}
+
+namespace {
+
+// log2 of a page size that the cache kernels take (8 to 128, a power of two), or -1.
+int cache_log2_bs(int block_size) {
+  for (int i = 3; i <= 7; ++i)
+    if (block_size == 1 << i) return i;
+  return -1;
+}
+
+// What every call on the 8-bit cache checks of it.
+int check_cache(int Hkv, int D, long st_block, long st_tok, long st_head, int num_blocks,
+                int block_size) {
+  if (Hkv < 1 || D < 16 || D > 128 || D % 16) return SD_E_SHAPE;
+  const int l = cache_log2_bs(block_size);
+  if (l < 0 || num_blocks < 0 || ((long)num_blocks << l) > 2147483648L) return SD_E_SHAPE;
+  if (st_block < 1 || st_tok < 1 || st_head < 1) return SD_E_SHAPE;
+  if (st_block % 16 || st_tok % 16 || st_head % 16) return SD_E_ALIGN;
+  return SD_OK;
+}
+
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+}  // namespace
+
+int sd_kv_write(int n, int Hkv, int D, const void* k, long ld_k, long hs_k, const void* v,
+                long ld_v, long hs_v, const int32_t* slot_mapping, void* k_cache, void* v_cache,
+                long st_block, long st_tok, long st_head, float* k_scale, float* v_scale,
+                int num_blocks, int block_size, int32_t* err, void* stream) {
+  if (n < 0 || ld_k < 0 || ld_v < 0 || hs_k < 0 || hs_v < 0) return SD_E_SHAPE;
+  const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
+  if (rc != SD_OK) return rc;
+  if (n == 0) return SD_OK;
+  if (!k || !v || !slot_mapping) return SD_E_NULL;
+  if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)) return SD_E_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || ld_k % 8 ||
+      hs_k % 8 || ld_v % 8 || hs_v % 8)
+    return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_kv_write_launch(n, Hkv, D, k, ld_k, hs_k, v, ld_v, hs_v, slot_mapping, k_cache,
+                            v_cache, st_block, st_tok, st_head, k_scale, v_scale, num_blocks,
+                            cache_log2_bs(block_size), err, (cudaStream_t)stream);
+}
+
+int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const void* v_cache,
+               long st_block, long st_tok, long st_head, const float* k_scale,
+               const float* v_scale, int num_blocks, int block_size, const int32_t* block_table,
+               int max_blocks, const int32_t* cu_tokens, const int32_t* first_pos, void* k_out,
+               void* v_out, long ld_out, long hs_out, int32_t* err, void* stream) {
+  if (B < 0 || n < 0 || max_blocks < 0 || ld_out < 0 || hs_out < 0) return SD_E_SHAPE;
+  const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
+  if (rc != SD_OK) return rc;
+  if (B == 0 || n == 0) return SD_OK;
+  if (!cu_tokens || !k_out || !v_out || (max_blocks > 0 && !block_table)) return SD_E_NULL;
+  if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)) return SD_E_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
+      ld_out % 8 || hs_out % 8)
+    return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_kv_read_launch(B, n, Hkv, D, k_cache, v_cache, st_block, st_tok, st_head, k_scale,
+                           v_scale, num_blocks, cache_log2_bs(block_size), block_table, max_blocks,
+                           cu_tokens, first_pos, k_out, v_out, ld_out, hs_out, err,
+                           (cudaStream_t)stream);
+}
+
+size_t sd_kv_attend_workspace_bytes(int D) {
+  return D >= 16 && D <= 128 && D % 16 == 0 ? sd_kv_attend_workspace_launch(D) : 0;
+}
+
+int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q, long ld_q,
+                 long hs_q, const void* k_cache, const void* v_cache, long st_block, long st_tok,
+                 long st_head, const float* k_scale, const float* v_scale, int num_blocks,
+                 int block_size, const int32_t* block_table, int max_blocks,
+                 const int32_t* ctx_lens, const int32_t* cu_q, float sm_scale, int causal,
+                 void* out, long ld_out, long hs_out, float* lse, void* workspace,
+                 size_t workspace_bytes, int32_t* err, void* stream) {
+  if (B < 0 || n < 0 || max_q < 1 || max_blocks < 0 || Hq < 1 || ld_q < 0 || hs_q < 0 ||
+      ld_out < 0 || hs_out < 0)
+    return SD_E_SHAPE;
+  const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
+  if (rc != SD_OK) return rc;
+  if (Hq % Hkv || (long long)n * Hq > 2147483647LL) return SD_E_SHAPE;
+  if (!(sm_scale > 0.f && sm_scale <= 3.402823466e38f)) return SD_E_SHAPE;
+  if (B == 0 || n == 0) return SD_OK;
+  if (!q || !ctx_lens || !cu_q || !out || !workspace || (max_blocks > 0 && !block_table))
+    return SD_E_NULL;
+  if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)) return SD_E_NULL;
+  if (workspace_bytes < sd_kv_attend_workspace_bytes(D)) return SD_E_SHAPE;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(workspace) || ld_q % 8 || hs_q % 8 || ld_out % 8 || hs_out % 8)
+    return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_kv_attend_launch(B, n, max_q, Hq, Hkv, D, q, ld_q, hs_q, k_cache, v_cache, st_block,
+                             st_tok, st_head, k_scale, v_scale, num_blocks,
+                             cache_log2_bs(block_size), block_table, max_blocks, ctx_lens, cu_q,
+                             sm_scale, causal, out, ld_out, hs_out, lse, workspace, err,
+                             (cudaStream_t)stream);
+}
+
+int sd_token_logprobs(int B, int J, int V, int dtype, const void* rows, long ld,
+                      const int32_t* tokens, const float* temperature, int n_top, float* logprob,
+                      float* entropy, int32_t* rank, int32_t* top_ids, float* top_logprobs,
+                      int32_t* err, void* stream) {
+  if (dtype != SD_F32_PROBS && dtype != SD_BF16_LOGITS) return SD_E_DTYPE;
+  if (B < 0 || J < 1 || V < 1 || V > SD_TOP_MAX_V || ld < V) return SD_E_SHAPE;
+  if (n_top < 0 || n_top > SD_TOP_MAX || n_top > V) return SD_E_SHAPE;
+  // rows of up to 8 CTAs each
+  if ((long long)B * J * 8 > 2147483647LL) return SD_E_SHAPE;
+  if (B == 0) return SD_OK;
+  if (!rows || !tokens || !logprob || (n_top > 0 && (!top_ids || !top_logprobs))) return SD_E_NULL;
+  if ((uintptr_t)rows % (dtype == SD_F32_PROBS ? 4 : 2)) return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_logprobs_launch(B, J, V, dtype, rows, ld, tokens, temperature, n_top, logprob, entropy,
+                            rank, top_ids, top_logprobs, err, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,44 @@
+// sd_kv.cuh -- the paged 8-bit cache as its kernels see it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sd_common.cuh"
+
+namespace sdk {
+
+// Element [page][slot][head][d] of K and V at page * st_block + slot * st_tok + head * st_head + d
+// (64-bit: a long cache passes 2^32 elements); scales [num_blocks][Hkv].
+struct KvCache {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  long st_block, st_tok, st_head;
+  int num_blocks, log2_bs, Hkv, D;
+};
+
+constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100, the smallest scale a page is given
+
+// Two e4m3 values as two fp32 (exact).
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// Two fp32 to e4m3 (lo in the low byte): to nearest even, beyond +-448 (infinities too) to +-448,
+// NaN to NaN.
+__device__ __forceinline__ uint16_t f32_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+}  // namespace sdk
