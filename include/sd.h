@@ -523,7 +523,7 @@ SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const v
  * Arguments: q, out bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
  *   strides multiples of 8); lse [n, Hq] fp32 or NULL; max_q: the most query tokens that a request
  *   is expected to have, which only chooses the kernel (any value >= 1 is right); Hq a multiple of
- *   Hkv; sm_scale positive and finite; workspace: at least sd_kv_attend_workspace_bytes(D) bytes of
+ *   Hkv; num_blocks >= 1; sm_scale positive and finite; workspace: at least sd_kv_attend_workspace_bytes(D) bytes of
  *   device scratch, 16-byte aligned, its contents irrelevant before and after. Calls that may run
  *   concurrently need separate workspaces.
  */

@@ -668,12 +668,12 @@ int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q,
     return SD_E_SHAPE;
   const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
   if (rc != SD_OK) return rc;
-  if (Hq % Hkv || (long long)n * Hq > 2147483647LL) return SD_E_SHAPE;
+  if (Hq % Hkv || (long long)n * Hq > 2147483647LL || num_blocks < 1) return SD_E_SHAPE;
   if (!(sm_scale > 0.f && sm_scale <= 3.402823466e38f)) return SD_E_SHAPE;
   if (B == 0 || n == 0) return SD_OK;
   if (!q || !ctx_lens || !cu_q || !out || !workspace || (max_blocks > 0 && !block_table))
     return SD_E_NULL;
-  if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)) return SD_E_NULL;
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return SD_E_NULL;
   if (workspace_bytes < sd_kv_attend_workspace_bytes(D)) return SD_E_SHAPE;
   if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(workspace) || ld_q % 8 || hs_q % 8 || ld_out % 8 || hs_out % 8)
