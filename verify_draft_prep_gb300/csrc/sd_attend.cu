@@ -11,7 +11,7 @@
 // that), and so is each weight P = P1 + P2 (P at most 448 there, too). Two e4m3 products take the
 // time of one bf16 product, and K and V cost half the shared memory and no instructions. A page's
 // scales enter as numbers per 8 columns of S: with y = log2(e) S + log2(v_scale),
-//   P = 2^(y - M + 8),  O = sum P v_byte,  L = sum P / v_scale,
+//   P = 2^(y - M + kShift),  O = sum P v_byte,  L = sum P / v_scale,
 // M the running maximum of y, so that one exponential serves both sums.
 //
 // A unit is one request's 128 (or 256) rows of one KV head; a row is a query token and one of the
@@ -36,11 +36,17 @@ constexpr int kScaleSlots = 16;            // tiles of scales in flight
 // A page whose V scale is 0 holds zeros: its tokens weigh in L only. They are given a scale below
 // that of any page with values, so that those keep P's full precision.
 constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
+// P = 2^(y - M + kShift) is at most 448 while M is no more than kSlack behind the row's maximum. A
+// larger shift keeps more of the small weights, a smaller one has the accumulator rescaled less
+// often: weights lose bits below 2^-14 of the row's largest, and end at 2^-18 of it.
+constexpr float kShift = 8.f, kSlack = 0.75f;
+constexpr float kTiny = 1.17549435e-38f;  // -inf times it is -inf, S times it is nothing
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
 
 struct AttendParams {
   KvCache c;
-  int B, n, Hq, G, max_blocks, causal, min_share;
+  int B, n, Hq, G, max_blocks, causal, min_share, out_32;  // out_32: every 16 values of out 32-byte aligned
+  unsigned long long g_magic;  // ceil(2^64 / G); 0 for G = 1
   const uint16_t* q;
   long ld_q, hs_q;
   const int32_t* table;
@@ -61,18 +67,20 @@ struct JoinDesc {
   int pad[3];
 };
 
-template <int DP, int NS>
+// R: how often a unit's rows stand in the 128 lanes (each copy takes 1/R of a tile's columns).
+// NS: Q tiles of a unit (1: both streams share it, 2: one each).
+template <int DP, int NS, int R>
 struct AttLayout {
-  // NS: Q tiles of a unit (1: the streams share one, 2: one each)
-  static constexpr int kRows = NS * kTile;
+  static constexpr int kRows = NS * kTile / R;      // of a unit
   static constexpr int kQBytes = kTile * DP;        // one term of one Q tile
   static constexpr int kTileBytes = kTile * DP;     // K or V of one tile
-  static constexpr int kStages = DP == 64 ? 8 : (NS == 1 ? 5 : 4);
-  static constexpr int kQ = 0;
-  static constexpr int kK = kQ + NS * 2 * kQBytes;
+  static constexpr int kStages = DP == 64 ? 8 : (R > 1 ? 3 : 4);
+  static constexpr int kQ = 0;                      // two buffers (NS = 1), or two tiles
+  static constexpr int kK = kQ + 2 * 2 * kQBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kScales = kV + kStages * kTileBytes;
-  static constexpr int kMisc = kScales + kScaleSlots * 16 * 16;
+  static constexpr int kJoin = kScales + kScaleSlots * 16 * 16;  // [8 warps][32 rows][33] floats
+  static constexpr int kMisc = kJoin + (R > 1 ? 8 * 32 * 33 * 4 : 0);
   static constexpr long kSlotFloats = (long)kRows * DP + kRows;
 };
 
@@ -91,6 +99,12 @@ struct AttMisc {
   uint32_t tmem;
   int gave_up;
 };
+
+// row / G and row % G, exactly for every 32-bit row.
+__device__ __forceinline__ int2 token_head(const AttendParams& P, int row) {
+  const int t = P.g_magic ? (int)__umul64hi((unsigned long long)row, P.g_magic) : row;
+  return make_int2(t, row - t * P.G);
+}
 
 struct Request {
   int tok0, n_q, rows, len, off;
@@ -118,7 +132,7 @@ __device__ __forceinline__ bool request_bad(const AttendParams& P, int r) {
 // Tokens that a row sees.
 __device__ __forceinline__ int seen_by(const AttendParams& P, const Request& q, int row) {
   if (!P.causal) return q.len;
-  const long t = (long)q.off + row / P.G + 1;
+  const long t = (long)q.off + token_head(P, row).x + 1;
   return (int)max(0L, min((long)q.len, t));
 }
 // Tiles that rows up to `row` need; a row that sees nothing has one, in which all is masked.
@@ -130,46 +144,59 @@ __device__ __forceinline__ int tiles_for(const AttendParams& P, const Request& q
 struct Segment {
   Request q;
   int r, h, row0, rows, a, b, n;
-  int cnt[2];  // tiles of each stream
+  int cnt[2];       // tiles of each stream
+  long long first;  // the unit's first tile on the line
 };
 
-template <int NS>
+// Every unit takes kUnitCost places on the line before its tiles, for what it costs beside them (its
+// queries, its result), so that CTAs with many short units get fewer tiles.
+constexpr int kUnitCost = 4;
+
+template <int NS, int ROWS>
 struct Schedule {
-  long long g, end;
-  int r, qt, h, tile;
+  long long g, end;  // this CTA's part of the line
+  int r, qt, h, off; // the unit at g, and how far into its places g lies
 
   __device__ __forceinline__ bool next(const AttendParams& P, Segment& s) {
-    if (g >= end) return false;
-    s.q = request_of(P, r);
-    while (s.q.rows == 0) s.q = request_of(P, ++r);  // the line ends before the requests do
-    s.r = r;
-    s.h = h;
-    s.row0 = qt * NS * kTile;
-    s.rows = min(s.q.rows - s.row0, NS * kTile);
-    s.n = tiles_for(P, s.q, s.row0 + s.rows - 1);
-    s.a = tile;
-    s.b = (int)min((long long)s.n, tile + (end - g));
-    if (NS == 1) {
-      s.cnt[0] = (s.b - s.a + 1) / 2;
-      s.cnt[1] = (s.b - s.a) / 2;
-    } else {
-      const int n0 = s.rows > kTile ? tiles_for(P, s.q, s.row0 + kTile - 1) : s.n;
-      s.cnt[0] = max(0, min(s.b, n0) - s.a);
-      s.cnt[1] = s.rows > kTile ? s.b - s.a : 0;
-    }
-    g += s.b - s.a;
-    tile = s.b;
-    if (s.b == s.n) {
-      tile = 0;
-      if (++h == P.c.Hkv) {
-        h = 0;
-        if ((++qt) * NS * kTile >= s.q.rows) {
-          qt = 0;
-          ++r;
+    while (g < end) {
+      s.q = request_of(P, r);
+      if (s.q.rows == 0) {  // the line ends before the requests do
+        ++r;
+        continue;
+      }
+      s.r = r;
+      s.h = h;
+      s.row0 = qt * ROWS;
+      s.rows = min(s.q.rows - s.row0, ROWS);
+      s.n = tiles_for(P, s.q, s.row0 + s.rows - 1);
+      s.first = g - off + kUnitCost;
+      const int take = (int)min((long long)(s.n + kUnitCost - off), end - g);
+      s.a = max(0, off - kUnitCost);
+      s.b = max(0, off + take - kUnitCost);
+      g += take;
+      off += take;
+      if (off == s.n + kUnitCost) {
+        off = 0;
+        if (++h == P.c.Hkv) {
+          h = 0;
+          if ((++qt) * ROWS >= s.q.rows) {
+            qt = 0;
+            ++r;
+          }
         }
       }
+      if (s.b <= s.a) continue;
+      if (NS == 1) {
+        s.cnt[0] = (s.b - s.a + 1) / 2;
+        s.cnt[1] = (s.b - s.a) / 2;
+      } else {
+        const int n0 = s.rows > kTile ? tiles_for(P, s.q, s.row0 + kTile - 1) : s.n;
+        s.cnt[0] = max(0, min(s.b, n0) - s.a);
+        s.cnt[1] = s.rows > kTile ? s.b - s.a : 0;
+      }
+      return true;
     }
-    return true;
+    return false;
   }
 };
 
@@ -179,11 +206,160 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-template <int DP, int NS>
+// Q rows [first, first + count) of a unit, one 8-value part a thread, as two e4m3 terms into the
+// swizzled operand at q (and q + kQBytes), R copies of them, with the rows' scales. `rows` valid.
+template <int DP, int R, int THREADS>
+__device__ __forceinline__ void load_q(const AttendParams& P, const Segment& s, int row0, int rows,
+                                       unsigned char* q, float* row_scale, int t) {
+  constexpr int kLanes = DP / 8, kPerPass = THREADS / kLanes;
+  constexpr int kAhead = 4;  // loads in flight, while the code of one row stays small
+  const int c8 = t % kLanes;
+  const int padded = (rows + 31) & ~31;
+  auto fetch = [&](int r) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < rows && c8 * 8 < P.c.D) {
+      const int row = row0 + r;
+      const int2 th = token_head(P, row);
+      const long tok = s.q.tok0 + th.x;
+      const int hq = s.h * P.G + th.y;
+      v = __ldg(reinterpret_cast<const uint4*>(P.q + tok * P.ld_q + hq * P.hs_q + c8 * 8));
+    }
+    return v;
+  };
+  uint4 q4[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) q4[i] = fetch(i * kPerPass + t / kLanes);
+#pragma unroll 2
+  for (int rb = 0; rb < padded; rb += kPerPass) {
+    const int r = rb + t / kLanes;
+    const uint4 v = q4[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i) q4[i] = q4[i + 1];
+    q4[kAhead - 1] = fetch(r + kAhead * kPerPass);
+    {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t mg = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mg = __vmaxu2(mg, w[k] & 0x7fff7fffu);
+      mg = max(mg & 0xffffu, mg >> 16);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) mg = max(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+      // 2^up brings the largest to [224, 448]; a row with an infinity or a NaN becomes NaN, as its
+      // softmax is
+      int up = 135 - (int)(mg >> 7) - ((mg & 0x7fu) > 0x60u ? 1 : 0);
+      up = mg == 0 ? 0 : min(up, 64);
+      const bool bad = mg >= 0x7f80u;
+      const float mul = bad ? nanf("") : __uint_as_float((uint32_t)(up + 127) << 23);
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float f[4], h[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f[u] = (u & 1 ? bf16_hi(w[2 * k + (u >> 1)]) : bf16_lo(w[2 * k + (u >> 1)])) * mul;
+          h[u] = __uint_as_float(__float_as_uint(f[u]) & 0xfff00000u);
+        }
+        hi[k] = f32_to_e4m3x4(h[0], h[1], h[2], h[3]);
+        lo[k] = f32_to_e4m3x4(f[0] - h[0], f[1] - h[1], f[2] - h[2], f[3] - h[3]);
+      }
+      // 16-byte chunks of a row are swizzled by the row within its 8-row (or 4-pair) atom; the
+      // copies lie whole atoms apart
+      const int sw = DP == 128 ? r & 7 : (r >> 1) & 3;
+      unsigned char* at = q + r * DP + (((c8 >> 1) ^ sw) << 4) + (c8 & 1) * 8;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        *reinterpret_cast<uint2*>(at + k * (kTile / R) * DP) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(at + k * (kTile / R) * DP + kTile * DP) =
+            make_uint2(lo[0], lo[1]);
+      }
+      if (c8 == 0) row_scale[r] = P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
+    }
+  }
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+  return d;
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 32 bytes: a whole sector, so that rows far apart are written without partial ones.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// The largest y of 32 columns.
+__device__ __forceinline__ float row_max(const uint32_t (&v)[32], const float4* sc, float rs) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __uint_as_float(v[g * 8 + i]);
+    const float t = max3f(max3f(b[0], b[1], b[2]), max3f(b[3], b[4], b[5]), fmaxf(b[6], b[7]));
+    mx = fmaxf(mx, fmaf(t, fmaxf(sc[g].x * rs, kTiny), sc[g].y));
+  }
+  return mx;
+}
+
+// P = P1 + P2 of 32 columns, and their part of L. Returned as 8 words of P1, then 8 of P2. A
+// masked column is -inf (and its factor is never 0).
+__device__ __forceinline__ float weights(const uint32_t (&v)[32], const float4* sc, float rs,
+                                         float shift, uint32_t (&o)[16]) {
+  float part = 0.f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float4 f = sc[g];
+    const float k = fmaxf(f.x * rs, kTiny), a = f.y + shift;
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 h[2], l[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = g * 8 + 4 * i + 2 * u;
+        const float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                              make_float2(k, k), make_float2(a, a));
+        const float2 p = make_float2(ex2f(x.x), ex2f(x.y));
+        sum = add2(sum, p);
+        // the leading 4 significant bits, and the rest
+        h[u] = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xfff00000u),
+                           __uint_as_float(__float_as_uint(p.y) & 0xfff00000u));
+        l[u] = fma2(h[u], make_float2(-1.f, -1.f), p);
+      }
+      o[g * 2 + i] = f32_to_e4m3x4(h[0].x, h[0].y, h[1].x, h[1].y);
+      o[8 + g * 2 + i] = f32_to_e4m3x4(l[0].x, l[0].y, l[1].x, l[1].y);
+    }
+    part = fmaf(sum.x + sum.y, f.z, part);
+  }
+  return part;
+}
+
+template <int DP, int NS, int R>
 __global__ void __launch_bounds__(kAttThreads, 1)
 attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
-  using L = AttLayout<DP, NS>;
+  using L = AttLayout<DP, NS, R>;
   constexpr int S = L::kStages;
   extern __shared__ unsigned char s_raw[];
   unsigned char* smem = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
@@ -205,8 +381,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       mbar_init(smem_u32(&m.s_full[i]), 1);
       mbar_init(smem_u32(&m.p_full[i]), 4);
       mbar_init(smem_u32(&m.o_done[i]), 1);
-      mbar_init(smem_u32(&m.q_full[i]), NS == 1 ? 8 : 4);
-      mbar_init(smem_u32(&m.q_empty[i]), 1);
+      mbar_init(smem_u32(&m.q_full[i]), NS == 1 ? 1 : 4);
+      mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(smem_u32(&m.sc_full[i]), 1);
@@ -225,7 +401,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   for (int r = r0; r < r1; ++r) {
     const Request q = request_of(P, r);
     for (int row = 0; row < q.rows; row += L::kRows)
-      mine += tiles_for(P, q, min(q.rows, row + L::kRows) - 1);
+      mine += tiles_for(P, q, min(q.rows, row + L::kRows) - 1) + kUnitCost;
     if (blockIdx.x == 0) bad |= request_bad(P, r);
   }
   if (bad) raise_err(P.err, SD_ERR_KV_RANGE);
@@ -252,11 +428,11 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       const Request q = request_of(P, r);
       bool found = false;
       for (int row = 0; row < q.rows; row += L::kRows) {
-        const int n = tiles_for(P, q, min(q.rows, row + L::kRows) - 1);
+        const int n = tiles_for(P, q, min(q.rows, row + L::kRows) - 1) + kUnitCost;
         if (g0 < at + (long long)n * P.c.Hkv) {
           m.start_item[0] = r;
           m.start_item[1] = row / L::kRows;
-          m.start_item[2] = (int)(g0 - at);  // head * n + tile
+          m.start_item[2] = (int)(g0 - at);  // head * n + place
           m.start[0] = n;
           found = true;
           break;
@@ -273,16 +449,16 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   JoinDesc* desc = reinterpret_cast<JoinDesc*>(P.ws) + blockIdx.x;
   float* slots = reinterpret_cast<float*>(P.ws + kMaxCtas * sizeof(JoinDesc));
 
-  Schedule<NS> sched;
+  Schedule<NS, L::kRows> sched;
   sched.g = g0;
   sched.end = g1;
-  sched.r = sched.qt = sched.h = sched.tile = 0;
+  sched.r = sched.qt = sched.h = sched.off = 0;
   if (g0 < g1) {
     const int n = (int)m.start[0];
     sched.r = m.start_item[0];
     sched.qt = m.start_item[1];
     sched.h = m.start_item[2] / n;
-    sched.tile = m.start_item[2] % n;
+    sched.off = m.start_item[2] % n;
   }
   Segment s;
   const int log2_bs = P.c.log2_bs, bs = 1 << log2_bs;
@@ -336,96 +512,124 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       }
     }
   } else if (warp == 1) {
-    // ---- products: one thread ----
-    if (lane == 0) {
-      const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + DP};
-      constexpr uint32_t qk_desc = mma_desc(kTile, false), pv_desc = mma_desc(DP, true);
-      int it = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-      bool ok = true;
-      auto qk = [&](int st_i, int x, int qi) {  // S[x] = Q[qi] K
-        const uint64_t k = smem_desc<DP>(base + L::kK + st_i * L::kTileBytes);
+    // ---- products: the warp waits, one elected lane issues ----
+    constexpr uint32_t hi = desc_hi<DP>();
+    constexpr uint32_t qk_idesc = mma_desc(kTile, false), pv_idesc = mma_desc(DP, true);
+    const bool lead = elect_one();
+    const uint32_t q_lo = desc_lo<DP>(base + L::kQ), k_lo = desc_lo<DP>(base + L::kK),
+                   v_lo = desc_lo<DP>(base + L::kV);
+    int st = 0, nq[2] = {0, 0};
+    uint32_t ph = 0;       // parity of the ring's current round
+    uint32_t pp[2] = {0, 0};
+    bool ok = true;
+    auto qk = [&](int k_st, int x, int qi) {  // S[x] = Q[qi] K
+      const uint32_t d = tmem + x * 128, a = q_lo + qi * (2 * L::kQBytes / 16),
+                     k = k_lo + k_st * (L::kTileBytes / 16);
 #pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const uint64_t a = smem_desc<DP>(base + L::kQ + (qi * 2 + term) * L::kQBytes);
+      for (int term = 0; term < 2; ++term)
 #pragma unroll
-          for (int kk = 0; kk < DP / 32; ++kk)
-            mma_ss(tS[x], a + kk * 2, k + kk * 2, qk_desc, term + kk > 0);
-        }
-      };
-      auto pv = [&](int st_i, int x, bool add) {  // O[x] += P V
-        const uint64_t v = smem_desc<DP>(base + L::kV + st_i * L::kTileBytes);
+        for (int kk = 0; kk < DP / 32; ++kk)
+          mma_ss<hi, qk_idesc>(d, a + term * (L::kQBytes / 16) + kk * 2, k + kk * 2,
+                               term + kk > 0);
+    };
+    auto pv = [&](int v_st, int x, bool add) {  // O[x] += P V
+      const uint32_t d = tmem + 256 + x * DP, a = tmem + x * 128,
+                     v = v_lo + v_st * (L::kTileBytes / 16);
 #pragma unroll
-        for (int kk = 0; kk < kTile / 32; ++kk)
+      for (int kk = 0; kk < kTile / 32; ++kk)
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
-            mma_ts(tO[x], tS[x] + kk * 16 + term * 8, v + kk * (32 * DP / 16), pv_desc,
-                   add || kk + term > 0);
-      };
-      while (ok && sched.next(P, s)) {
-        const int T = s.b - s.a;
-        if (NS == 1) {
-          ok = mbar_wait(smem_u32(&m.q_full[0]), nq[0] & 1, gave_up);
-          ++nq[0];
-          auto do_qk = [&](int j) {
-            const int st = (it + j) % S;
-            if (!mbar_wait(smem_u32(&m.k_full[st]), ((it + j) / S) & 1, gave_up)) return false;
-            tc_fence_after();
-            qk(st, j & 1, 0);
-            mma_commit(smem_u32(&m.k_empty[st]));
-            if (j == T - 1) mma_commit(smem_u32(&m.q_empty[0]));
-            mma_commit(smem_u32(&m.s_full[j & 1]));
-            return true;
-          };
-          ok = ok && do_qk(0) && (T < 2 || do_qk(1));
-          for (int j = 0; ok && j < T; ++j) {
-            const int x = j & 1, st = (it + j) % S;
-            ok = mbar_wait(smem_u32(&m.p_full[x]), np[x] & 1, gave_up) &&
-                 mbar_wait(smem_u32(&m.v_full[st]), ((it + j) / S) & 1, gave_up);
-            if (!ok) break;
-            ++np[x];
-            tc_fence_after();
-            pv(st, x, j >= 2);
-            mma_commit(smem_u32(&m.v_empty[st]));
-            mma_commit(smem_u32(&m.o_done[x]));
-            if (j + 2 < T) ok = do_qk(j + 2);
-          }
-        } else {
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (s.cnt[x] > 0) {
-              ok = mbar_wait(smem_u32(&m.q_full[x]), nq[x] & 1, gave_up);
-              ++nq[x];
-            }
-          }
-          auto do_qk = [&](int j, int x) {
-            const int st = (it + j) % S;
-            if (!mbar_wait(smem_u32(&m.k_full[st]), ((it + j) / S) & 1, gave_up)) return false;
-            tc_fence_after();
-            qk(st, x, x);
-            if (j == s.cnt[x] - 1) mma_commit(smem_u32(&m.q_empty[x]));
+        for (int term = 0; term < 2; ++term)
+          mma_ts<hi, pv_idesc>(d, a + kk * 16 + term * 8, v + kk * (32 * DP / 16),
+                               add || kk + term > 0);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait_warp(smem_u32(bar), parity, gave_up);
+      return ok;
+    };
+    while (ok && sched.next(P, s)) {
+      const int T = s.b - s.a;
+      if (NS == 1) {
+        const int qb = nq[0] & 1;  // units alternate between two buffers
+        if (!wait(&m.q_full[qb], (nq[0] >> 1) & 1)) break;
+        ++nq[0];
+        // QK runs two tiles ahead of PV: (kst, kph) is its place in the ring
+        int kst = st;
+        uint32_t kph = ph;
+        auto do_qk = [&](int j, int x) {
+          if (!wait(&m.k_full[kst], kph)) return;
+          tc_fence_after();
+          if (lead) {
+            qk(kst, x, qb);
             mma_commit(smem_u32(&m.s_full[x]));
-            return true;
-          };
-          for (int x = 0; x < 2; ++x)
-            if (ok && s.cnt[x] > 0) ok = do_qk(0, x);
-          if (ok) mma_commit(smem_u32(&m.k_empty[it % S]));
-          for (int j = 0; ok && j < T; ++j) {
-            const int st = (it + j) % S;
-            for (int x = 0; ok && x < 2; ++x) {
-              if (j >= s.cnt[x]) continue;
-              ok = mbar_wait(smem_u32(&m.p_full[x]), np[x] & 1, gave_up) &&
-                   mbar_wait(smem_u32(&m.v_full[st]), ((it + j) / S) & 1, gave_up);
-              if (!ok) break;
-              ++np[x];
-              tc_fence_after();
+            mma_commit(smem_u32(&m.k_empty[kst]));
+            if (j == T - 1) mma_commit(smem_u32(&m.q_empty[qb]));
+          }
+          if (++kst == S) {
+            kst = 0;
+            kph ^= 1;
+          }
+        };
+        do_qk(0, 0);
+        if (T > 1) do_qk(1, 1);
+        for (int j0 = 0; ok && j0 < T; j0 += 2) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int j = j0 + x;
+            if (j >= T) break;
+            wait(&m.p_full[x], pp[x]);
+            if (!wait(&m.v_full[st], ph)) break;
+            pp[x] ^= 1;
+            tc_fence_after();
+            if (lead) {
+              pv(st, x, j0 > 0);
+              mma_commit(smem_u32(&m.v_empty[st]));
+              mma_commit(smem_u32(&m.o_done[x]));
+            }
+            if (++st == S) {
+              st = 0;
+              ph ^= 1;
+            }
+            if (j + 2 < T) do_qk(j + 2, x);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (s.cnt[x] > 0) wait(&m.q_full[x], nq[x]++ & 1);
+        auto do_qk = [&](int j, int x, int kst, uint32_t kph) {
+          if (!wait(&m.k_full[kst], kph)) return;
+          tc_fence_after();
+          if (lead) {
+            qk(kst, x, x);
+            mma_commit(smem_u32(&m.s_full[x]));
+            if (j == s.cnt[x] - 1) mma_commit(smem_u32(&m.q_empty[x]));
+          }
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (s.cnt[x] > 0) do_qk(0, x, st, ph);
+        if (ok && lead) mma_commit(smem_u32(&m.k_empty[st]));
+        for (int j = 0; ok && j < T; ++j) {
+          const int nst = st + 1 == S ? 0 : st + 1;
+          const uint32_t nph = ph ^ (nst == 0 ? 1u : 0u);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j >= s.cnt[x]) continue;
+            wait(&m.p_full[x], pp[x]);
+            if (!wait(&m.v_full[st], ph)) break;
+            pp[x] ^= 1;
+            tc_fence_after();
+            if (lead) {
               pv(st, x, j > 0);
               if (x == 1 || j >= s.cnt[1]) mma_commit(smem_u32(&m.v_empty[st]));
               mma_commit(smem_u32(&m.o_done[x]));
-              if (j + 1 < s.cnt[x]) ok = do_qk(j + 1, x);
             }
-            if (ok && j + 1 < T) mma_commit(smem_u32(&m.k_empty[(it + j + 1) % S]));
+            if (j + 1 < s.cnt[x]) do_qk(j + 1, x, nst, nph);
           }
+          if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
+          st = nst;
+          ph = nph;
         }
-        it += T;
       }
     }
     __syncwarp();
@@ -476,10 +680,32 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         }
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // ---- Q of the next unit, while this one is computed ----
+    if (NS == 1) {
+      int nq = 0;
+      bool ok = true;
+      while (ok && sched.next(P, s)) {
+        const int qb = nq & 1;
+        ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((nq >> 1) & 1) ^ 1, gave_up);
+        if (!ok) break;
+        load_q<DP, R, 32>(P, s, s.row0, s.rows, smem + L::kQ + qb * 2 * L::kQBytes,
+                             m.row_scale + qb * kTile, lane);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&m.q_full[qb]));
+        ++nq;
+      }
+    }
+  }
+  if (warp >= 4) {
     // ---- softmax: stream x, one row a thread ----
+    constexpr int NC = 4 / R;                             // 32-column chunks of a thread
     const int x = (warp - 4) >> 2, wt = tid - 128 - x * 128;  // thread of its stream
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // this warp's quarter of the lanes
+    const int quarter = warp & 3;                             // of the lanes
+    const int copy = quarter / NC;                            // which columns: chunks copy*NC..
+    const int wr = (quarter % NC) * 32 + lane;                // row of this thread in its tile
+    const uint32_t lanes = (uint32_t)quarter << 21;
     const uint32_t tS = tmem + x * 128 + lanes;
     const uint32_t tO[2] = {tmem + 256 + lanes, tmem + 256 + DP + lanes};
     int it = 0, nq = 0, done[2] = {0, 0}, unit = 0;
@@ -492,77 +718,32 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     while (sched.next(P, s)) {
       const int T = s.b - s.a;
       const int buf = unit & 1;
-      // 1. Q: the rows' two terms into shared memory, their scales
-      if (NS == 1 || s.cnt[x] > 0) {
-        ok = ok && mbar_wait_warp(smem_u32(&m.q_empty[NS == 1 ? 0 : x]), (nq & 1) ^ 1, gave_up);
+      const int row_base = NS == 1 ? 0 : x * kTile;       // of this stream in the unit
+      const int my_rows = NS == 1 ? s.rows : min(kTile, s.rows - row_base);
+      float rs = 0.f;
+      // 1. Q (with two Q tiles, loaded here), and this row's scale
+      if (NS == 1) {
+        ok = ok && mbar_wait_warp(smem_u32(&m.q_full[unit & 1]), (unit >> 1) & 1, gave_up);
+        rs = m.row_scale[(unit & 1) * kTile + wr];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&m.q_empty[unit & 1]));
+      } else if (s.cnt[x] > 0) {
+        ok = ok && mbar_wait_warp(smem_u32(&m.q_empty[x]), (nq & 1) ^ 1, gave_up);
         ++nq;
-        constexpr int kLanes = DP / 8;  // of a row, 8 values each
-        constexpr int kThreads = NS == 1 ? 256 : 128;
-        const int t = NS == 1 ? tid - 128 : wt;
-        const int c8 = t % kLanes;
-        const int qi = NS == 1 ? 0 : x;
-        const int rows = ok ? min(kTile, s.rows - qi * kTile) : 0;
-        for (int r = t / kLanes; r < ((rows + 31) & ~31); r += kThreads / kLanes) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r < rows && c8 * 8 < P.c.D) {
-            const int row = s.row0 + qi * kTile + r;
-            const long tok = s.q.tok0 + row / P.G;
-            const int hq = s.h * P.G + row % P.G;
-            v = __ldg(reinterpret_cast<const uint4*>(P.q + tok * P.ld_q + hq * P.hs_q + c8 * 8));
-          }
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          float f[8], mag = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo(w[i]);
-            f[2 * i + 1] = bf16_hi(w[i]);
-            mag = fmaxf(mag, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-          }
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1)
-            mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, o));
-          // 2^up brings mag to [224, 448]; an infinity stays one and ends as NaN
-          const uint32_t mb = __float_as_uint(mag);
-          int up = 135 - (int)(mb >> 23) - ((mb & 0x7fffffu) > 0x600000u ? 1 : 0);
-          up = mag == 0.f || !(mag < INFINITY) ? 0 : min(up, 120);
-          const float mul = __uint_as_float((uint32_t)(up + 127) << 23);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint16_t h2[2], l2[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float a = f[4 * i + 2 * k] * mul, b = f[4 * i + 2 * k + 1] * mul;
-              if (!(fabsf(a) < INFINITY)) a = nanf("");
-              if (!(fabsf(b) < INFINITY)) b = nanf("");
-              h2[k] = f32_to_e4m3x2(a, b);
-              const float2 r2 = e4m3x2_to_f32(h2[k]);
-              l2[k] = f32_to_e4m3x2(a - r2.x, b - r2.y);
-            }
-            hi[i] = h2[0] | (uint32_t)h2[1] << 16;
-            lo[i] = l2[0] | (uint32_t)l2[1] << 16;
-          }
-          // 16-byte chunks of a row are swizzled by the row within its 8-row (or 4-pair) atom
-          const int sw = DP == 128 ? r & 7 : (r >> 1) & 3;
-          unsigned char* at = smem + L::kQ + qi * 2 * L::kQBytes + r * DP +
-                              (((c8 >> 1) ^ sw) << 4) + (c8 & 1) * 8;
-          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(at + L::kQBytes) = make_uint2(lo[0], lo[1]);
-          if (c8 == 0)
-            m.row_scale[qi * kTile + r] = P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
-        }
+        if (ok)
+          load_q<DP, 1, 128>(P, s, s.row0 + row_base, my_rows,
+                                smem + L::kQ + x * 2 * L::kQBytes, m.row_scale + row_base, wt);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&m.q_full[NS == 1 ? 0 : x]));
-        named_bar(NS == 1 ? 1 : 2 + x, kThreads);  // every row's scale is there
+        if (lane == 0) mbar_arrive(smem_u32(&m.q_full[x]));
+        named_bar(2 + x, 128);  // every row's scale is there
+        rs = m.row_scale[row_base + wr];
       }
-      const int my_rows = NS == 1 ? s.rows : min(kTile, s.rows - x * kTile);  // of this stream
-      const int row = s.row0 + (NS == 1 ? 0 : x * kTile) + wt;
-      const bool warp_live = (warp & 3) * 32 < my_rows;
-      const bool live = wt < my_rows;
+      const int row = s.row0 + row_base + wr;
+      const bool warp_live = (quarter % NC) * 32 < my_rows;
+      const bool live = wr < my_rows;
       const int lim = seen_by(P, s.q, min(row, s.row0 + s.rows - 1));
-      const int min_lim = seen_by(P, s.q, s.row0 + (NS == 1 ? 0 : x * kTile));
-      const float rs = m.row_scale[(NS == 1 ? 0 : x * kTile) + wt];
+      const int min_lim = seen_by(P, s.q, s.row0 + row_base);
       float M = -INFINITY, Lsum = 0.f;
 
       // 2. tiles
@@ -616,86 +797,70 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         if (!ok) break;
         tc_fence_after();
         if (warp_live) {
-          const float4* sc = scales + slot * 16;
-          const int edge = lim - t0;  // columns from here on are masked
-          float mx = -INFINITY;
+          const float4* sc = scales + slot * 16 + copy * NC * 4;
+          const int edge = lim - t0 - copy * NC * 32;  // columns from here on are masked
+          const uint32_t tC = tS + copy * NC * 32;
+          if (masked) {  // rare: the masked columns of S become -inf where they lie
+#pragma unroll 1
+            for (int c = 0; c < NC; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tC + c * 32, v);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tS + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float4 f = sc[c * 4 + g];
-              float b = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float a = __uint_as_float(v[g * 8 + i]);
-                b = fmaxf(b, masked && c * 32 + g * 8 + i >= edge ? -INFINITY : a);
-              }
-              // a column group without a token: 0 times its zeros, and -inf
-              const float y = fmaf(b, f.x * rs, f.y);
-              mx = fmaxf(mx, y);
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= edge) v[i] = 0xff800000u;
+              tmem_st32(tC + c * 32, v);
             }
+            tmem_wait_st();
           }
-          // P stays within e4m3 while M is at most 0.75 behind
-          const bool grow = mx > M + 0.75f;
+          // 32 columns at a time, twice: the code of one pass stays small enough for the
+          // instruction cache that eight warps share
+          uint32_t v[32];
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c) {
+            tmem_ld32(tC + c * 32, v);
+            tmem_wait_ld();
+            mx = fmaxf(mx, row_max(v, sc + c * 4, rs));
+          }
+          const bool grow = mx > M + kSlack;
           if (__any_sync(0xffffffffu, grow)) {
             const float Mn = fmaxf(M, mx);
-            if (done[x] > 0 && j >= (NS == 1 ? 2 : 1)) {
+            if (j >= (NS == 1 ? 2 : 1)) {
               const float fac = M == -INFINITY ? 0.f : ex2f(M - Mn);
               ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
               if (!ok) break;
               tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < DP / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(tO[x] + c * 32, v);
+#pragma unroll 1
+              for (int c = 0; c < DP; c += 16) {
+                uint32_t w[16];
+                tmem_ld16(tO[x] + c, w);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  v[i] = __float_as_uint(__uint_as_float(v[i]) * fac);
-                tmem_st32(tO[x] + c * 32, v);
+                for (int i = 0; i < 16; ++i)
+                  w[i] = __float_as_uint(__uint_as_float(w[i]) * fac);
+                tmem_st16(tO[x] + c, w);
               }
               Lsum *= fac;
             }
             M = Mn;
           }
-          const float shift = 8.f - (M == -INFINITY ? 0.f : M);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], o[16];
-            tmem_ld32(tS + c * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float4 f = sc[c * 4 + g];
-              const float k = f.x * rs, add = f.y + shift;
-              float sum = 0.f;
-              uint16_t p1[4], p2[4];
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                float p[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  const float a = __uint_as_float(v[g * 8 + i + u]);
-                  p[u] = ex2f(fmaf(a, k, add));
-                  if (masked && c * 32 + g * 8 + i + u >= edge) p[u] = 0.f;
-                  sum += p[u];
-                }
-                // the leading 4 significant bits, and the rest
-                const float a1 = __uint_as_float(__float_as_uint(p[0]) & 0xfff00000u);
-                const float b1 = __uint_as_float(__float_as_uint(p[1]) & 0xfff00000u);
-                p1[i >> 1] = f32_to_e4m3x2(a1, b1);
-                p2[i >> 1] = f32_to_e4m3x2(p[0] - a1, p[1] - b1);
-              }
-              Lsum = fmaf(sum, f.z, Lsum);
-              o[g * 2] = p1[0] | (uint32_t)p1[1] << 16;
-              o[g * 2 + 1] = p1[2] | (uint32_t)p1[3] << 16;
-              o[8 + g * 2] = p2[0] | (uint32_t)p2[1] << 16;
-              o[8 + g * 2 + 1] = p2[2] | (uint32_t)p2[3] << 16;
+          const float shift = kShift - (M == -INFINITY ? 0.f : M);
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c) {
+            uint32_t o[16];
+            if (NC > 1) {
+              tmem_ld32(tC + c * 32, v);
+              tmem_wait_ld();
             }
-            tmem_st16(tS + c * 16, o);
+            Lsum += weights(v, sc + c * 4, rs, shift, o);
+            tmem_st16(tS + (copy * NC + c) * 16, o);
+          }
+          if (R > 1) {  // the other copies' columns count as zero here
+            const uint32_t none[16] = {};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (c / NC != copy) tmem_st16(tS + c * 16, none);
           }
           tmem_wait_st();
         }
@@ -725,81 +890,158 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       const bool has_nan = m.nan_any[buf] != 0;
       if (tid - 128 < 128) m.nan_first[buf ^ 1][tid - 128] = 0x7fffffff;
       if (tid == 128) m.nan_any[buf ^ 1] = 0;
-      float wa = 1.f, wb = 0.f, Mt = M, Lt = Lsum;
-      if (NS == 1) {
-        const float2 a = m.ml[0][wt], b = m.ml[1][wt];
-        if (cnt_b > 0) {
-          Mt = fmaxf(a.x, b.x);
-          wa = a.x == Mt ? 1.f : ex2f(a.x - Mt);
-          wb = b.x == Mt ? 1.f : ex2f(b.x - Mt);
-          Lt = a.y * wa + b.y * wb;
-        } else {
-          Mt = a.x;
-          Lt = a.y;
-        }
-      }
-      const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
-      const float lse2 = Lt == 0.f ? -INFINITY : Mt - 8.f + log2f(Lt);
-      wa *= inv;
-      wb *= inv;
-      const int unit_row = (NS == 1 ? 0 : x * kTile) + wt;
-      const long tok = s.q.tok0 + row / P.G;
-      const int hq = s.h * P.G + row % P.G;
       float* slot = slots + (2L * blockIdx.x + (s.a > 0 ? 0 : 1)) * L::kSlotFloats;
-      const bool mine_any = NS == 1 || s.cnt[x] > 0;
-      if (ok && warp_live && my_rows > 0) {
-        constexpr int kCols = NS == 1 ? DP / 2 : DP;  // this thread's share of the row
-        const int c0 = NS == 1 ? x * kCols : 0;
-        if (mine_any) {
+      const int* nan_first = m.nan_first[buf];
+      if (R > 1) {
+        // 2R partial rows: every warp leaves 32 columns of its own, weighed by their common
+        // maximum, then the threads add them up in the warps' order
+        float* join = reinterpret_cast<float*>(smem + L::kJoin);
+        constexpr int parts = 2 * R;  // a stream without a tile counts with weight 0
+        float Mt = -INFINITY, Lt = 0.f;
+        float2 ml[parts];
 #pragma unroll
-          for (int c = 0; c < kCols; c += 32) {
-            uint32_t u[32], w[32];
-            tmem_ld32(tO[NS == 1 ? 0 : x] + c0 + c, u);
-            if (NS == 1 && cnt_b > 0) tmem_ld32(tO[1] + c0 + c, w);
+        for (int i = 0; i < parts; ++i) {
+          ml[i] = m.ml[i / R][(i % R) * (kTile / R) + wr];
+          Mt = fmaxf(Mt, ml[i].x);
+        }
+#pragma unroll
+        for (int i = 0; i < parts; ++i)
+          Lt += ml[i].y * (ml[i].x == Mt ? 1.f : ex2f(ml[i].x - Mt));
+        const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
+        const float lse2 = Lt == 0.f ? -INFINITY : Mt - kShift + log2f(Lt);
+        const float wm = (M == Mt ? 1.f : ex2f(M - Mt)) * inv;
+        const bool used = x == 0 || cnt_b > 0;
+        if (ok && x == 0 && copy == 0 && live) {
+          if (split) slot[(long)L::kRows * DP + wr] = lse2;
+          else if (P.lse) {
+            const int2 th = token_head(P, row);
+            P.lse[(long)(s.q.tok0 + th.x) * P.Hq + s.h * P.G + th.y] = lse2 * kLn2F;
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+          if (ok && warp_live) {
+            uint32_t u[32];
+            tmem_ld32(tO[x] + c, u);
             tmem_wait_ld();
-            if (!live) continue;
-            float o[32];
+            float* mine = join + ((warp - 4) * 32 + lane) * 33;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              o[i] = __uint_as_float(u[i]) * wa;
-              if (NS == 1 && cnt_b > 0) o[i] = fmaf(__uint_as_float(w[i]), wb, o[i]);
+            for (int i = 0; i < 32; ++i) mine[i] = used ? __uint_as_float(u[i]) * wm : 0.f;
+          }
+          named_bar(1, 256);
+          // 4 columns a thread, 32 rows a pass
+          const int cc = ((tid - 128) & 7) * 4;
+          for (int r = (tid - 128) >> 3; ok && r < s.rows; r += 32) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < parts; ++i) {
+              const int w = (i / R) * 4 + (i % R) * NC + (r >> 5);
+              const float* from = join + (w * 32 + (r & 31)) * 33 + cc;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[k] += from[k];
             }
+            const int rr = s.row0 + r;
             if (has_nan) {
-              for (int i = 0; i < 32; ++i)
-                if (m.nan_first[buf][c0 + c + i] < lim) o[i] = nanf("");
+              const int l = seen_by(P, s.q, rr);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (nan_first[c + cc + k] < l) o[k] = nanf("");
             }
             if (split) {
-              float4* p = reinterpret_cast<float4*>(slot + (long)unit_row * DP + c0 + c);
+              *reinterpret_cast<float4*>(slot + (long)r * DP + c + cc) =
+                  make_float4(o[0], o[1], o[2], o[3]);
+            } else if (c + cc < P.c.D) {
+              const __nv_bfloat162 a = __floats2bfloat162_rn(o[0], o[1]);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(o[2], o[3]);
+              const int2 th = token_head(P, rr);
+              *reinterpret_cast<uint2*>(P.out + (long)(s.q.tok0 + th.x) * P.ld_out +
+                                        (long)(s.h * P.G + th.y) * P.hs_out + c + cc) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                             *reinterpret_cast<const uint32_t*>(&b));
+            }
+          }
+          if (c + 32 < DP) named_bar(1, 256);
+        }
+      } else {
+        float wa = 1.f, wb = 0.f, Mt = M, Lt = Lsum;
+        if (NS == 1) {
+          const float2 a = m.ml[0][wt], b = m.ml[1][wt];
+          Mt = a.x;
+          Lt = a.y;
+          if (cnt_b > 0) {
+            Mt = fmaxf(a.x, b.x);
+            wa = a.x == Mt ? 1.f : ex2f(a.x - Mt);
+            wb = b.x == Mt ? 1.f : ex2f(b.x - Mt);
+            Lt = a.y * wa + b.y * wb;
+          }
+        }
+        const float inv = Lt == 0.f ? 0.f : 1.f / Lt;
+        const float lse2 = Lt == 0.f ? -INFINITY : Mt - kShift + log2f(Lt);
+        wa *= inv;
+        wb *= inv;
+        const int unit_row = row_base + wt;
+        const int2 th = token_head(P, row);
+        const long tok = s.q.tok0 + th.x;
+        const int hq = s.h * P.G + th.y;
+        const bool mine_any = NS == 1 || s.cnt[x] > 0;
+        if (ok && warp_live && my_rows > 0) {
+          constexpr int kCols = NS == 1 ? DP / 2 : DP;  // this thread's share of the row
+          const int c0 = NS == 1 ? x * kCols : 0;
+          if (mine_any) {
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+              uint32_t u[32], w[32];
+              tmem_ld32(tO[NS == 1 ? 0 : x] + c0 + c, u);
+              if (NS == 1 && cnt_b > 0) tmem_ld32(tO[1] + c0 + c, w);
+              tmem_wait_ld();
+              if (!live) continue;
+              float o[32];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                p[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
-              uint16_t* p = P.out + tok * P.ld_out + hq * P.hs_out + c0 + c;
+              for (int i = 0; i < 32; ++i) {
+                o[i] = __uint_as_float(u[i]) * wa;
+                if (NS == 1 && cnt_b > 0) o[i] = fmaf(__uint_as_float(w[i]), wb, o[i]);
+              }
+              if (has_nan) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (c0 + c + i * 8 < P.c.D) {
-                  uint32_t b[4];
+                for (int i = 0; i < 32; ++i)
+                  if (nan_first[c0 + c + i] < lim) o[i] = nanf("");
+              }
+              if (split) {
+                float* p = slot + (long)unit_row * DP + c0 + c;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 h2 =
-                        __floats2bfloat162_rn(o[i * 8 + 2 * k], o[i * 8 + 2 * k + 1]);
-                    b[k] = *reinterpret_cast<const uint32_t*>(&h2);
+                for (int i = 0; i < 4; ++i)
+                  store32(p + i * 8, reinterpret_cast<const uint32_t*>(o + i * 8));
+              } else {
+                uint16_t* p = P.out + tok * P.ld_out + hq * P.hs_out + c0 + c;
+                uint32_t b[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                  b[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (c0 + c + i * 16 >= P.c.D) break;  // D is a multiple of 16
+                  if (P.out_32) {
+                    store32(p + i * 16, b + i * 8);
+                  } else {
+                    uint4* q4 = reinterpret_cast<uint4*>(p + i * 16);
+                    q4[0] = make_uint4(b[i * 8], b[i * 8 + 1], b[i * 8 + 2], b[i * 8 + 3]);
+                    q4[1] = make_uint4(b[i * 8 + 4], b[i * 8 + 5], b[i * 8 + 6], b[i * 8 + 7]);
                   }
-                  *reinterpret_cast<uint4*>(p + i * 8) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
               }
             }
           }
-        }
-        if (live && (NS == 2 || x == 0)) {
-          if (split) slot[(long)L::kRows * DP + unit_row] = mine_any ? lse2 : -INFINITY;
-          else if (P.lse) P.lse[tok * P.Hq + hq] = lse2 * kLn2F;
+          if (live && (NS == 2 || x == 0)) {
+            if (split) slot[(long)L::kRows * DP + unit_row] = mine_any ? lse2 : -INFINITY;
+            else if (P.lse) P.lse[tok * P.Hq + hq] = lse2 * kLn2F;
+          }
         }
       }
       if (s.a == 0 && s.b < s.n) {  // begun here, ended by a later CTA
         continues = true;
-        const long long first = sched.g - (s.b - s.a);  // the unit's place on the line
-        jd.pieces = (int)((first + s.n - 1) / share - blockIdx.x + 1);
+        jd.pieces = (int)((s.first + s.n - 1) / share - blockIdx.x + 1);
         jd.tok0 = s.q.tok0;
         jd.head = s.h;
         jd.row0 = s.row0;
@@ -831,9 +1073,9 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
 }
 
 // Joins the parts of a unit that several CTAs shared: one warp a row, parts in their order.
-template <int DP, int NS>
+template <int DP, int NS, int R>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams P) {
-  using L = AttLayout<DP, NS>;
+  using L = AttLayout<DP, NS, R>;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinDesc d = reinterpret_cast<const JoinDesc*>(P.ws)[blockIdx.x];
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -873,9 +1115,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams P) 
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(w, v[i], acc[i]);
   }
-  const int row = d.row0 + r;
-  const long tok = d.tok0 + row / P.G;
-  const int hq = d.head * P.G + row % P.G;
+  const int2 th = token_head(P, d.row0 + r);
+  const long tok = d.tok0 + th.x;
+  const int hq = d.head * P.G + th.y;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint16_t* out = P.out + tok * P.ld_out + hq * P.hs_out + lane * V;
   if (lane * V < P.c.D) {
@@ -940,17 +1182,17 @@ static int sm_count() {
   return count[dev];
 }
 
-template <int DP, int NS>
+template <int DP, int NS, int R>
 static int launch_attend(const AttendParams& P, const CUtensorMap& km, const CUtensorMap& vm,
                          int ctas, bool join, cudaStream_t stream) {
-  using L = AttLayout<DP, NS>;
+  using L = AttLayout<DP, NS, R>;
   constexpr int smem = L::kMisc + (int)sizeof(AttMisc) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   static bool set[64];  // per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
   if (!set[dev]) {
-    if (cudaFuncSetAttribute(attend_kernel<DP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attend_kernel<DP, NS, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return SD_E_LAUNCH;
     set[dev] = true;
@@ -960,7 +1202,7 @@ static int launch_attend(const AttendParams& P, const CUtensorMap& km, const CUt
   cfg.blockDim = dim3(kAttThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  if (cudaLaunchKernelEx(&cfg, attend_kernel<DP, NS>, P, km, vm) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, attend_kernel<DP, NS, R>, P, km, vm) != cudaSuccess)
     return SD_E_LAUNCH;
   if (!join) return SD_OK;
   cudaLaunchAttribute attr[1];
@@ -972,14 +1214,15 @@ static int launch_attend(const AttendParams& P, const CUtensorMap& km, const CUt
   jc.stream = stream;
   jc.attrs = attr;
   jc.numAttrs = 1;
-  return cudaLaunchKernelEx(&jc, attend_join_kernel<DP, NS>, P) == cudaSuccess ? SD_OK
+  return cudaLaunchKernelEx(&jc, attend_join_kernel<DP, NS, R>, P) == cudaSuccess ? SD_OK
                                                                                : SD_E_LAUNCH;
 }
 
 }  // namespace sdk
 
 extern "C" size_t sd_kv_attend_workspace_launch(int D) {
-  const long slot = D <= 64 ? sdk::AttLayout<64, 2>::kSlotFloats : sdk::AttLayout<128, 2>::kSlotFloats;
+  const long slot = D <= 64 ? sdk::AttLayout<64, 2, 1>::kSlotFloats
+                            : sdk::AttLayout<128, 2, 1>::kSlotFloats;
   return sdk::kMaxCtas * sizeof(sdk::JoinDesc) + (size_t)2 * sdk::kMaxCtas * slot * sizeof(float);
 }
 
@@ -1006,14 +1249,16 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   P.table = table;
   P.ctx = ctx;
   P.cu = cu;
+  P.g_magic = P.G > 1 ? ~0ull / (unsigned)P.G + 1 : 0;
   P.scale = sm_scale * sdk::kLog2eF;
   P.out = (uint16_t*)out;
   P.ld_out = ld_out;
   P.hs_out = hs_out;
   P.lse = lse;
+  P.out_32 = (uintptr_t)out % 32 == 0 && ld_out % 16 == 0 && hs_out % 16 == 0;
   P.ws = (unsigned char*)workspace;
   P.err = err;
-  P.min_share = 4;
+  P.min_share = sdk::kUnitCost + 4;
   const int sms = sdk::sm_count();
   if (sms < 1) return SD_E_DEVICE;
   const int ctas = sms < sdk::kMaxCtas ? sms : sdk::kMaxCtas;
@@ -1023,10 +1268,17 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
     return SD_E_SHAPE;
   // units of one tile are never shared
   const bool join = ((long)max_blocks << log2_bs) > sdk::kTile;
-  const bool many = (long)max_q * P.G > sdk::kTile;
-  if (DP == 64)
-    return many ? sdk::launch_attend<64, 2>(P, km, vm, ctas, join, stream)
-                : sdk::launch_attend<64, 1>(P, km, vm, ctas, join, stream);
-  return many ? sdk::launch_attend<128, 2>(P, km, vm, ctas, join, stream)
-              : sdk::launch_attend<128, 1>(P, km, vm, ctas, join, stream);
+  // The expected rows of a request choose the unit: 32 or 64 rows stand in the lanes four times or
+  // twice, so that all softmax warps share a tile's columns.
+  const long rows = (long)max_q * P.G;
+  if (DP == 64) {
+    if (rows <= 32) return sdk::launch_attend<64, 1, 4>(P, km, vm, ctas, join, stream);
+    if (rows <= 64) return sdk::launch_attend<64, 1, 2>(P, km, vm, ctas, join, stream);
+    if (rows <= 128) return sdk::launch_attend<64, 1, 1>(P, km, vm, ctas, join, stream);
+    return sdk::launch_attend<64, 2, 1>(P, km, vm, ctas, join, stream);
+  }
+  if (rows <= 32) return sdk::launch_attend<128, 1, 4>(P, km, vm, ctas, join, stream);
+  if (rows <= 64) return sdk::launch_attend<128, 1, 2>(P, km, vm, ctas, join, stream);
+  if (rows <= 128) return sdk::launch_attend<128, 1, 1>(P, km, vm, ctas, join, stream);
+  return sdk::launch_attend<128, 2, 1>(P, km, vm, ctas, join, stream);
 }

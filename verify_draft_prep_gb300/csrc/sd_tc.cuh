@@ -37,7 +37,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // Waits for the phase of this parity to end, for a second of the GPU clock at most or until
 // another thread of the CTA has given up (*gave_up). False: the wait did not end.
 constexpr long long kWaitClocks = 2000000000LL;
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
                                             volatile int* gave_up) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity)) {
@@ -114,6 +114,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
       : "r"(a)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
@@ -140,12 +150,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
 // one after another. It serves an operand whose rows run along the summed index's partner (K-major,
 // as Q and K) and one whose rows run along the summed index (MN-major, as V): in both the stride
 // between 8-row groups is 8 W and the other stride is never taken, because a row is one atom wide.
+// The high word is a constant; the low one moves with the address, 16 bytes a step.
 template <int W>
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  constexpr uint64_t layout = W == 128 ? 2 : 4;
-  constexpr uint64_t stride = (8 * W) >> 4;
-  return (uint64_t)((addr & 0x3ffff) >> 4) | stride << 16 | stride << 32 | (uint64_t)1 << 46 |
-         layout << 61;
+__host__ __device__ constexpr uint32_t desc_hi() {
+  return (uint32_t)((8 * W) >> 4) | 1u << 14 | (W == 128 ? 2u : 4u) << 29;
+}
+template <int W>
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
+  return (addr & 0x3ffff) >> 4 | (uint32_t)((8 * W) >> 4) << 16;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(one));
+  return one != 0;
 }
 
 // M = 128, fp32 accumulator, both operands e4m3; b_mn: B's rows run along the summed index.
@@ -153,20 +172,22 @@ __host__ __device__ constexpr uint32_t mma_desc(int N, bool b_mn) {
   return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+template <uint32_t HI, uint32_t IDESC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n .reg .b32 i;\n setp.ne.b32 p, %3, 0;\n"
+      " mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+      " mov.b32 i, %5;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, i, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "n"(HI), "n"(IDESC)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool add) {
+template <uint32_t HI, uint32_t IDESC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 y;\n .reg .b32 i;\n setp.ne.b32 p, %3, 0;\n"
+      " mov.b64 y, {%2, %4};\n mov.b32 i, %5;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, i, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "n"(HI), "n"(IDESC)
       : "memory");
 }
 // Arrives on bar when every product issued so far by this thread is done.
