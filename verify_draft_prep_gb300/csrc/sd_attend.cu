@@ -72,6 +72,11 @@ struct JoinDesc {
 template <int DP, int NS, int R>
 struct AttLayout {
   static constexpr int kRows = NS * kTile / R;      // of a unit
+  // Tensor memory, 512 columns: S of both streams, O of both; with heads of 64 there is room for P
+  // beside S, so that the next S is formed while this one's P is; else P takes S's place.
+  static constexpr bool kOwnP = DP == 64;
+  static constexpr int kTmS = 0, kTmO = 256, kTmP = kOwnP ? 256 + 2 * DP : 0;
+  static constexpr int kTmPStep = kOwnP ? 64 : 128;
   static constexpr int kQBytes = kTile * DP;        // one term of one Q tile
   static constexpr int kTileBytes = kTile * DP;     // K or V of one tile
   static constexpr int kStages = DP == 64 ? 8 : (R > 1 ? 3 : 4);
@@ -86,7 +91,7 @@ struct AttLayout {
 
 struct AttMisc {
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
-  uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2];
+  uint64_t s_full[2], s_read[2], p_full[2], o_done[2], q_full[2], q_empty[2];
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
   int sc_zero[kScaleSlots];   // bit e: entry e's V scale is zero
   float row_scale[2 * kTile];
@@ -301,6 +306,13 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
+// This warp has its columns of S in registers.
+__device__ __forceinline__ void stream_read(uint64_t& bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&bar));
+}
+
 // 32 bytes: a whole sector, so that rows far apart are written without partial ones.
 __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
@@ -380,6 +392,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&m.s_full[i]), 1);
       mbar_init(smem_u32(&m.p_full[i]), 4);
+      mbar_init(smem_u32(&m.s_read[i]), 4);
       mbar_init(smem_u32(&m.o_done[i]), 1);
       mbar_init(smem_u32(&m.q_full[i]), NS == 1 ? 1 : 4);
       mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
@@ -520,7 +533,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                    v_lo = desc_lo<DP>(base + L::kV);
     int st = 0, nq[2] = {0, 0};
     uint32_t ph = 0;       // parity of the ring's current round
-    uint32_t pp[2] = {0, 0};
+    uint32_t pp[2] = {0, 0}, sp[2] = {0, 0};
     bool ok = true;
     auto qk = [&](int k_st, int x, int qi) {  // S[x] = Q[qi] K
       const uint32_t d = tmem + x * 128, a = q_lo + qi * (2 * L::kQBytes / 16),
@@ -533,7 +546,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                                term + kk > 0);
     };
     auto pv = [&](int v_st, int x, bool add) {  // O[x] += P V
-      const uint32_t d = tmem + 256 + x * DP, a = tmem + x * 128,
+      const uint32_t d = tmem + L::kTmO + x * DP, a = tmem + L::kTmP + x * L::kTmPStep,
                      v = v_lo + v_st * (L::kTileBytes / 16);
 #pragma unroll
       for (int kk = 0; kk < kTile / 32; ++kk)
@@ -571,25 +584,37 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         };
         do_qk(0, 0);
         if (T > 1) do_qk(1, 1);
-        for (int j0 = 0; ok && j0 < T; j0 += 2) {
+        auto do_pv = [&](int j, int x) {
+          wait(&m.p_full[x], pp[x]);
+          if (!wait(&m.v_full[st], ph)) return;
+          pp[x] ^= 1;
+          tc_fence_after();
+          if (lead) {
+            pv(st, x, j >= 2);
+            mma_commit(smem_u32(&m.v_empty[st]));
+            mma_commit(smem_u32(&m.o_done[x]));
+          }
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        };
+        for (int j0 = 0; ok && j0 <= T; j0 += 2) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int j = j0 + x;
-            if (j >= T) break;
-            wait(&m.p_full[x], pp[x]);
-            if (!wait(&m.v_full[st], ph)) break;
-            pp[x] ^= 1;
-            tc_fence_after();
-            if (lead) {
-              pv(st, x, j0 > 0);
-              mma_commit(smem_u32(&m.v_empty[st]));
-              mma_commit(smem_u32(&m.o_done[x]));
+            if (!ok || j > T) break;
+            if (L::kOwnP) {
+              // the next S of this stream as soon as the last one is read, then the other
+              // stream's PV
+              if (j < T) wait(&m.s_read[x], sp[x]);
+              sp[x] ^= j < T ? 1 : 0;
+              if (j + 2 < T) do_qk(j + 2, x);
+              if (j > 0) do_pv(j - 1, x ^ 1);
+            } else if (j < T) {
+              do_pv(j, x);
+              if (j + 2 < T) do_qk(j + 2, x);
             }
-            if (++st == S) {
-              st = 0;
-              ph ^= 1;
-            }
-            if (j + 2 < T) do_qk(j + 2, x);
           }
         }
       } else {
@@ -609,27 +634,52 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         for (int x = 0; x < 2; ++x)
           if (s.cnt[x] > 0) do_qk(0, x, st, ph);
         if (ok && lead) mma_commit(smem_u32(&m.k_empty[st]));
+        int pst = st;  // the tile before
+        uint32_t pph = ph;
+        auto do_pv = [&](int j, int x, int v_st, uint32_t v_ph, bool last) {
+          wait(&m.p_full[x], pp[x]);
+          if (!wait(&m.v_full[v_st], v_ph)) return;
+          pp[x] ^= 1;
+          tc_fence_after();
+          if (lead) {
+            pv(v_st, x, j > 0);
+            if (last) mma_commit(smem_u32(&m.v_empty[v_st]));
+            mma_commit(smem_u32(&m.o_done[x]));
+          }
+        };
         for (int j = 0; ok && j < T; ++j) {
           const int nst = st + 1 == S ? 0 : st + 1;
           const uint32_t nph = ph ^ (nst == 0 ? 1u : 0u);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j >= s.cnt[x]) continue;
-            wait(&m.p_full[x], pp[x]);
-            if (!wait(&m.v_full[st], ph)) break;
-            pp[x] ^= 1;
-            tc_fence_after();
-            if (lead) {
-              pv(st, x, j > 0);
-              if (x == 1 || j >= s.cnt[1]) mma_commit(smem_u32(&m.v_empty[st]));
-              mma_commit(smem_u32(&m.o_done[x]));
+          if (L::kOwnP) {
+            // each stream's next S as soon as its last one is read, the other's PV between
+            if (j < s.cnt[0]) {
+              wait(&m.s_read[0], sp[0]);
+              sp[0] ^= 1;
+              if (j + 1 < s.cnt[0]) do_qk(j + 1, 0, nst, nph);
             }
-            if (j + 1 < s.cnt[x]) do_qk(j + 1, x, nst, nph);
+            if (j > 0 && j - 1 < s.cnt[1]) do_pv(j - 1, 1, pst, pph, true);
+            if (j < s.cnt[1]) {
+              wait(&m.s_read[1], sp[1]);
+              sp[1] ^= 1;
+              if (j + 1 < s.cnt[1]) do_qk(j + 1, 1, nst, nph);
+            }
+            if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
+            if (j < s.cnt[0]) do_pv(j, 0, st, ph, j >= s.cnt[1]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (j >= s.cnt[x]) continue;
+              do_pv(j, x, st, ph, x == 1 || j >= s.cnt[1]);
+              if (j + 1 < s.cnt[x]) do_qk(j + 1, x, nst, nph);
+            }
+            if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
           }
-          if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
+          pst = st;
+          pph = ph;
           st = nst;
           ph = nph;
         }
+        if (L::kOwnP && ok && T - 1 < s.cnt[1]) do_pv(T - 1, 1, pst, pph, true);
       }
     }
     __syncwarp();
@@ -707,7 +757,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     const int wr = (quarter % NC) * 32 + lane;                // row of this thread in its tile
     const uint32_t lanes = (uint32_t)quarter << 21;
     const uint32_t tS = tmem + x * 128 + lanes;
-    const uint32_t tO[2] = {tmem + 256 + lanes, tmem + 256 + DP + lanes};
+    const uint32_t tP = tmem + L::kTmP + x * L::kTmPStep + lanes;
+    const uint32_t tO[2] = {tmem + L::kTmO + lanes, tmem + L::kTmO + DP + lanes};
     int it = 0, nq = 0, done[2] = {0, 0}, unit = 0;
     bool ok = true;
     bool continues = false;
@@ -813,15 +864,24 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             }
             tmem_wait_st();
           }
-          // 32 columns at a time, twice: the code of one pass stays small enough for the
-          // instruction cache that eight warps share
-          uint32_t v[32];
+          // 32 columns at a time, the next ones on their way, twice: the code of one pass stays
+          // small enough for the instruction cache that eight warps share
+          uint32_t v[32], w[32];
           float mx = -INFINITY;
+          tmem_ld32(tC, v);
+          tmem_wait_ld();
+          if (NC == 1) {
+            mx = row_max(v, sc, rs);
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            tmem_ld32(tC + c * 32, v);
-            tmem_wait_ld();
-            mx = fmaxf(mx, row_max(v, sc + c * 4, rs));
+            for (int c = 0; c < NC; c += 2) {
+              tmem_ld32(tC + (c + 1) * 32, w);
+              mx = fmaxf(mx, row_max(v, sc + c * 4, rs));
+              tmem_wait_ld();
+              tmem_ld32(tC + (c + 2 < NC ? c + 2 : 0) * 32, v);
+              mx = fmaxf(mx, row_max(w, sc + c * 4 + 4, rs));
+              tmem_wait_ld();
+            }
           }
           const bool grow = mx > M + kSlack;
           if (__any_sync(0xffffffffu, grow)) {
@@ -845,24 +905,44 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             }
             M = Mn;
           }
+          if (L::kOwnP && j >= (NS == 1 ? 2 : 1)) {  // the last P has been used
+            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
+            if (!ok) break;
+          }
           const float shift = kShift - (M == -INFINITY ? 0.f : M);
+          uint32_t o[16];
+          if (NC == 1) {
+            if (L::kOwnP) stream_read(m.s_read[x], lane);
+            Lsum += weights(v, sc, rs, shift, o);
+            tmem_st16(tP + copy * 16, o);
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            uint32_t o[16];
-            if (NC > 1) {
-              tmem_ld32(tC + c * 32, v);
+            for (int c = 0; c < NC; c += 2) {
+              tmem_ld32(tC + (c + 1) * 32, w);
+              Lsum += weights(v, sc + c * 4, rs, shift, o);
               tmem_wait_ld();
+              tmem_st16(tP + (copy * NC + c) * 16, o);
+              if (c + 2 < NC) tmem_ld32(tC + (c + 2) * 32, v);
+              else if (L::kOwnP) stream_read(m.s_read[x], lane);
+              Lsum += weights(w, sc + c * 4 + 4, rs, shift, o);
+              tmem_wait_ld();
+              tmem_st16(tP + (copy * NC + c + 1) * 16, o);
             }
-            Lsum += weights(v, sc + c * 4, rs, shift, o);
-            tmem_st16(tS + (copy * NC + c) * 16, o);
           }
           if (R > 1) {  // the other copies' columns count as zero here
             const uint32_t none[16] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (c / NC != copy) tmem_st16(tS + c * 16, none);
+              if (c / NC != copy) tmem_st16(tP + c * 16, none);
           }
           tmem_wait_st();
+        } else if (L::kOwnP) {
+          // a warp without rows keeps pace with the others: its arrivals belong to this tile
+          stream_read(m.s_read[x], lane);
+          if (j >= (NS == 1 ? 2 : 1)) {
+            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
+            if (!ok) break;
+          }
         }
         tc_fence_before();
         __syncwarp();

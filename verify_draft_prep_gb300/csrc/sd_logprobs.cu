@@ -6,17 +6,18 @@
 // tree's. Probability rows need no Z: log p = ln p_x, H = -sum p ln p.
 //
 // A warp takes 256 neighbouring entries (a group) at a time. The group's maximum, one warp
-// reduction, serves twice: as the running maximum of the softmax (it is the same in every lane, so
-// a rescale is a branch of the whole warp) and, kept in shared memory, to find the best n entries:
-// they lie in the n groups that come first by (maximum, lowest index), because each of those
-// holds an entry that beats everything of any later group. Only these n groups are read again.
+// reduction, is kept in shared memory to find the best n entries: they lie in the n groups that
+// come first by (maximum, lowest index), because each of those holds an entry that beats everything
+// of any later group. Only these n groups are read again. Entries are compared and bounded two at
+// a time as they are stored; only the exponential and the sums take single fp32 values.
 // Bound by memory: the row once.
 
 #include "sd_common.cuh"
 
 namespace sdk {
 
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32, kGroup = 256;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kGroup = 256;
+constexpr int kCandidates = 512;
 constexpr int kLpMaxCluster = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -119,10 +120,10 @@ __device__ __forceinline__ float p_log2_p(float p) {
 }
 
 struct Sums {
-  float m, z, s;  // logits: max of l, sum 2^t, sum t 2^t with t = (l - m) c; probabilities: s only
+  float m, z, s;  // logits: a reference l, sum 2^t, sum t 2^t with t = (l - m) c; probabilities: s
 };
 
-// Joins sums over different maxima; c = log2(e) / T.
+// Joins sums over different references; c = log2(e) / T.
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
   Sums r;
   r.m = fmaxf(a.m, b.m);
@@ -140,13 +141,103 @@ struct LpShared {
   Sums sums[kLpMaxCluster];     // rank 0's, written by every CTA of the cluster
   int rank[kLpMaxCluster];
   uint64_t best[kLpMaxCluster][SD_TOP_MAX];
+  uint64_t cand[kCandidates];
+  uint64_t round[2][kLpWarps];
   int first[SD_TOP_MAX];        // the groups that hold this CTA's best entries
   int count;
   uint64_t floor;               // no entry below it is among the best
 };
 
+__device__ __forceinline__ uint64_t warp_max64(uint64_t q) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(q >> 32));
+  const uint32_t lo =
+      __reduce_max_sync(0xffffffffu, (uint32_t)(q >> 32) == hi ? (uint32_t)q : 0u);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// Sums, group maximum and rank of one lane's 8 entries; `edge`: the group holds the token or ends
+// the row, so that its entries are looked at one by one.
+struct Lane {
+  Sums a;
+  float better;
+};
+
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
+__device__ __forceinline__ float take(Lane& s, const Raw<DT>& raw, float c, float xt, int g0,
+                                      int token, int V, int lane) {
+  float gm;
+  const bool edge = (token >= g0 && token < g0 + kGroup) || g0 + kGroup > V;
+  if (DT == SD_BF16_LOGITS) {
+    // -inf becomes a finite number far below (2^t is 0 and t 2^t, too); NaN stays
+    const __nv_bfloat162 low = __float2bfloat162_rn(-1e30f);
+    __nv_bfloat162 w[4] = {*reinterpret_cast<const __nv_bfloat162*>(&raw.a.x),
+                           *reinterpret_cast<const __nv_bfloat162*>(&raw.a.y),
+                           *reinterpret_cast<const __nv_bfloat162*>(&raw.a.z),
+                           *reinterpret_cast<const __nv_bfloat162*>(&raw.a.w)};
+    const __nv_bfloat162 m2 = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    gm = fmaxf(__low2float(m2), __high2float(m2));
+    if (!edge) {
+      // entries before the token count from equality on, those behind it from above it on
+      const __nv_bfloat162 x2 = __float2bfloat162_rn(xt);
+      __nv_bfloat162 n2;
+      if (g0 < token)
+        n2 = __hadd2(__hadd2(__hge2(w[0], x2), __hge2(w[1], x2)),
+                     __hadd2(__hge2(w[2], x2), __hge2(w[3], x2)));
+      else
+        n2 = __hadd2(__hadd2(__hgt2(w[0], x2), __hgt2(w[1], x2)),
+                     __hadd2(__hgt2(w[2], x2), __hgt2(w[3], x2)));
+      s.better += __low2float(n2) + __high2float(n2);
+    }
+    // the reference moves only when it is some way behind (the sums have room, and a logarithm
+    // near 0 still comes from numbers near 0)
+    if (!((gm - s.a.m) * c <= 8.f) && gm > -INFINITY) {
+      const float d = s.a.m == -INFINITY ? 0.f : fmaxf((s.a.m - gm) * c, -1e4f);
+      const float f = ex2(d);
+      s.a.s = (s.a.s + d * s.a.z) * f;
+      s.a.z *= f;
+      s.a.m = gm;
+    }
+    const float m = s.a.m == -INFINITY ? 0.f : s.a.m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 x = __hmax2_nan(w[i], low);
+      const float2 f = __bfloat1622float2(x);
+      const float t0 = (f.x - m) * c, t1 = (f.y - m) * c;
+      const float p0 = ex2(t0), p1 = ex2(t1);
+      s.a.z += p0 + p1;
+      s.a.s = fmaf(t0, p0, s.a.s);
+      s.a.s = fmaf(t1, p1, s.a.s);
+    }
+  } else {
+    float v[8];
+    unpack<DT>(raw, v);
+    gm = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
+               fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    if (!edge) {
+      int n = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n += g0 < token ? v[e] >= xt : v[e] > xt;
+      s.better += (float)n;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s.a.s += p_log2_p(v[e]);
+  }
+  if (edge) {
+    float v[8];
+    unpack<DT>(raw, v);
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = g0 + entry<DT>(lane, e);
+      n += (v[e] > xt || (v[e] == xt && i < token)) && i < V;
+    }
+    s.better += (float)n;
+  }
+  return gm;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P) {
   extern __shared__ __align__(16) unsigned char s_dyn[];
   __shared__ LpShared sm;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -175,6 +266,19 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
   const int esize = DT == SD_BF16_LOGITS ? 2 : 4;
   const void* x = (const unsigned char*)P.x + (long)row * P.ld * esize;
   const bool vec = (uintptr_t)x % 16 == 0;
+  const int begin = part * P.span;
+  const int end = min(P.V, begin + P.span);
+  const int groups = begin < end ? (end - begin + kGroup - 1) / kGroup : 0;
+  uint32_t* gmax = reinterpret_cast<uint32_t*>(s_dyn);  // [span / kGroup], as order_of()
+
+  // 1. One pass: sums, rank, group maxima. Each warp takes U groups in flight.
+  constexpr int U = DT == SD_BF16_LOGITS ? 4 : 2;
+  Raw<DT> raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int gi = warp * U + u;
+    if (gi < groups) raw[u] = load_group<DT>(x, begin + gi * kGroup, P.V, vec, lane);
+  }
   const bool in_range = token < P.V;
   float xt = INFINITY;
   if (in_range)
@@ -184,77 +288,42 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
   if (!(T > 0.f)) T = 1.f;  // a greedy request's rows are reported at temperature 1
   const float inv_T = 1.f / T;
   const float c = kLog2e * inv_T;
-
-  const int begin = part * P.span;
-  const int end = min(P.V, begin + P.span);
-  const int groups = begin < end ? (end - begin + kGroup - 1) / kGroup : 0;
-  float* gmax = reinterpret_cast<float*>(s_dyn);  // [span / kGroup]
-  uint64_t* cand = reinterpret_cast<uint64_t*>(s_dyn + ((P.span / kGroup * 4 + 15) & ~15));
-
-  // 1. One pass: sums, rank, group maxima.
-  Sums a{-INFINITY, 0.f, 0.f};
-  int better = 0;
-  constexpr int U = DT == SD_BF16_LOGITS ? 4 : 2;  // groups in flight: 64 bytes a lane
-  for (int g = warp; g < groups; g += kLpWarps * U) {
-    Raw<DT> raw[U];
+  Lane s{{-INFINITY, 0.f, 0.f}, 0.f};
+  int rank_part = 0;
+  for (int g = warp * U; g < groups; g += kLpWarps * U) {
+    Raw<DT> now[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) now[u] = raw[u];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int gi = g + u * kLpWarps;
+      const int gi = g + kLpWarps * U + u;
       if (gi < groups) raw[u] = load_group<DT>(x, begin + gi * kGroup, P.V, vec, lane);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int gi = g + u * kLpWarps;
+      const int gi = g + u;
       if (gi >= groups) break;
-      const int g0 = begin + gi * kGroup;
-      float v[8];
-      unpack<DT>(raw[u], v);
-      float gm = v[0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) gm = fmaxf(gm, v[e]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-      if (lane == 0) gmax[gi] = gm;
-      if (DT == SD_BF16_LOGITS) {
-        if (gm > a.m) {
-          const float d = a.m == -INFINITY ? 0.f : fmaxf((a.m - gm) * c, -1e4f);
-          const float f = ex2(d);
-          a.s = (a.s + d * a.z) * f;
-          a.z *= f;
-          a.m = gm;
-        }
-        if (a.m != -INFINITY) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float t = fmaxf((v[e] - a.m) * c, -1e4f);  // -inf: 2^t is 0, and t 2^t too
-            const float p = v[e] == v[e] ? ex2(t) : nanf("");
-            a.z += p;
-            a.s = fmaf(t, p, a.s);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a.s += p_log2_p(v[e]);
-      }
-      // how many come before the token: larger ones, and equal ones of a lower index
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = g0 + entry<DT>(lane, e);
-        better += (v[e] > xt || (v[e] == xt && i < token)) && i < P.V;
+      const float gm = take<DT>(s, now[u], c, xt, begin + gi * kGroup, token, P.V, lane);
+      if (P.n_top > 0) {
+        const uint32_t o = __reduce_max_sync(0xffffffffu, order_of(gm));
+        if (lane == 0) gmax[gi] = o;
       }
     }
+    rank_part += (int)s.better;
+    s.better = 0.f;
   }
+  Sums a = s.a;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     Sums b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.z, o),
            __shfl_xor_sync(0xffffffffu, a.s, o)};
     if (DT == SD_BF16_LOGITS) a = join(a, b, c);
     else a.s += b.s;
-    better += __shfl_xor_sync(0xffffffffu, better, o);
   }
+  rank_part = __reduce_add_sync(0xffffffffu, rank_part);
   if (lane == 0) {
     sm.warp_sums[warp] = a;
-    sm.warp_rank[warp] = better;
+    sm.warp_rank[warp] = rank_part;
   }
   if (tid == 0) sm.count = 0;
   if (C > 1) cluster.barrier_wait();
@@ -268,66 +337,105 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     Sums b = lane < kLpWarps ? sm.warp_sums[lane] : Sums{-INFINITY, 0.f, 0.f};
     int r = lane < kLpWarps ? sm.warp_rank[lane] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = kLpWarps / 2; o > 0; o >>= 1) {
       Sums d{__shfl_xor_sync(0xffffffffu, b.m, o), __shfl_xor_sync(0xffffffffu, b.z, o),
              __shfl_xor_sync(0xffffffffu, b.s, o)};
       if (DT == SD_BF16_LOGITS) b = join(b, d, c);
       else b.s += d.s;
-      r += __shfl_xor_sync(0xffffffffu, r, o);
     }
+    r = __reduce_add_sync(0xffffffffu, r);
     if (lane == 0) {
       root->sums[part] = b;
       root->rank[part] = r;
     }
-  } else if (warp == 1 && n > 0) {
-    uint64_t mine = 0;  // this lane's best group that is not taken yet
-    for (int g = lane; g < groups; g += 32) mine = max(mine, key_of(gmax[g], g) );
-    uint64_t last = 0;
-    for (int k = 0; k < ng; ++k) {
-      uint64_t b = mine;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
-      const int g = (int)~(uint32_t)b;
+  } else if (warp == 1 && groups > n) {
+    // lane i watches over groups i, i + 32, ...: key (maximum, lower index first)
+    uint64_t mine = 0;
+    for (int g = lane; g < groups; g += 32) mine = max(mine, (uint64_t)gmax[g] << 32 | (uint32_t)~g);
+    uint64_t best = 0;
+    for (int k = 0; k < n; ++k) {
+      best = warp_max64(mine);
+      const int g = (int)~(uint32_t)best;
       if (lane == 0) sm.first[k] = g;
-      last = b;
-      if (mine == b) {  // the next one of this lane
-        mine = 0;
-        for (int i = lane; i < groups; i += 32) {
-          const uint64_t q = key_of(gmax[i], i);
-          if (q < b) mine = max(mine, q);
-        }
+      // the watcher's next one, looked up by the whole warp
+      uint64_t next = 0;
+      for (int i = (g & 31) + 32 * lane; i < groups; i += 1024) {
+        const uint64_t q = (uint64_t)gmax[i] << 32 | (uint32_t)~i;
+        if (q < best) next = max(next, q);
       }
+      next = warp_max64(next);
+      if (lane == (g & 31)) mine = next;
     }
-    // with n groups, n entries reach the last one's maximum
-    if (lane == 0) sm.floor = ng == n ? (last >> 32) << 32 : 0;
+    if (lane == 0) sm.floor = (best >> 32) << 32;  // n entries reach the last group's maximum
+  } else if (warp == 1) {  // every group
+    if (lane < ng) sm.first[lane] = lane;
+    if (lane == 0) sm.floor = 0;
   }
   __syncthreads();
 
-  // 3. The entries of those groups that may be among the best.
+  // 3. Their best entries: those that reach the floor are few, but for ties.
   if (n > 0) {
     const uint64_t floor = sm.floor;
-    for (int k = warp; k < ng; k += kLpWarps) {
-      const int g0 = begin + sm.first[k] * kGroup;
-      const Raw<DT> raw = load_group<DT>(x, g0, P.V, vec, lane);
-      float v[8];
-      unpack<DT>(raw, v);
+    bool many = floor == 0;
+    if (!many) {
+      for (int k = warp; k < ng; k += kLpWarps) {
+        const int g0 = begin + sm.first[k] * kGroup;
+        const Raw<DT> r = load_group<DT>(x, g0, P.V, vec, lane);
+        float v[8];
+        unpack<DT>(r, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = g0 + entry<DT>(lane, e);
-        const uint64_t q = key_of(v[e], i);
-        if (i < P.V && q >= floor) cand[atomicAdd(&sm.count, 1)] = q;
+        for (int e = 0; e < 8; ++e) {
+          const int i = g0 + entry<DT>(lane, e);
+          const uint64_t q = key_of(v[e], i);
+          if (i < P.V && q >= floor) {
+            const int at = atomicAdd(&sm.count, 1);
+            if (at < kCandidates) sm.cand[at] = q;
+          }
+        }
+      }
+      __syncthreads();
+      const int m = sm.count;
+      many = m > kCandidates;
+      // their order by counting, which does not depend on the order that they were found in
+      for (int k = tid; !many && k < max(m, n); k += kLpThreads) {
+        if (k >= m) {
+          root->best[part][k] = 0;
+          continue;
+        }
+        const uint64_t q = sm.cand[k];
+        int before = 0;
+        for (int i = 0; i < m; ++i) before += sm.cand[i] > q;
+        if (before < n) root->best[part][before] = q;
       }
     }
-    __syncthreads();
-    // their order by counting, which does not depend on the order that they were found in
-    const int m = sm.count;
-    for (int k = tid; k < m; k += kLpThreads) {
-      const uint64_t q = cand[k];
-      int before = 0;
-      for (int i = 0; i < m; ++i) before += cand[i] > q;
-      if (before < n) root->best[part][before] = q;
+    if (many) {
+      // few groups, or many equal entries: n rounds, each thread with its best one not yet taken
+      const int items = ng * kGroup;
+      auto best_below = [&](uint64_t limit) {
+        uint64_t b = 0;
+        for (int k = tid; k < items; k += kLpThreads) {
+          const int i = begin + sm.first[k / kGroup] * kGroup + k % kGroup;
+          if (i >= P.V) continue;
+          const float v = DT == SD_BF16_LOGITS
+                              ? __uint_as_float((uint32_t)__ldg((const uint16_t*)x + i) << 16)
+                              : __ldg((const float*)x + i);
+          const uint64_t q = key_of(v, i);
+          if (q < limit) b = max(b, q);
+        }
+        return b;
+      };
+      uint64_t mine = best_below(~0ull);
+      for (int k = 0; k < n; ++k) {
+        const uint64_t w = warp_max64(mine);
+        if (lane == 0) sm.round[k & 1][warp] = w;
+        __syncthreads();
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kLpWarps; ++i) best = max(best, sm.round[k & 1][i]);
+        if (tid == 0) root->best[part][k] = best;
+        if (best && mine == best) mine = best_below(best);
+      }
     }
-    for (int k = m + tid; k < n; k += kLpThreads) root->best[part][k] = 0;
   }
   if (C > 1) cluster.sync();
   else __syncthreads();
@@ -352,7 +460,13 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LpParams P) {
     if (P.rank) P.rank[row] = in_range ? rank + 1 : 0;
     if (!in_range) raise_err(P.err, SD_ERR_TOKEN_RANGE);
   }
-  if (n > 0) {
+  if (C == 1) {  // already in order
+    if (tid < n) {
+      const uint64_t q = sm.best[0][tid];
+      P.top_ids[(long)row * n + tid] = (int32_t)~(uint32_t)q;
+      P.top_lp[(long)row * n + tid] = lp(value_of((uint32_t)(q >> 32)));
+    }
+  } else if (n > 0) {
     for (int k = tid; k < C * n; k += kLpThreads) {
       const uint64_t q = sm.best[k / n][k % n];
       int before = 0;
@@ -387,15 +501,14 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   P.top_ids = top_ids;
   P.top_lp = top_lp;
   P.err = err;
-  // Few rows: a cluster of CTAs shares one, until the rows fill two CTAs on every SM or a CTA has
-  // less than 8 groups for each warp pair.
+  // Few rows: a cluster of CTAs shares one, until the rows fill four CTAs on every SM or a CTA has
+  // less than two groups for each warp.
   int C = 1;
-  while (C < sdk::kLpMaxCluster && (long)P.rows * C < 2 * 152 && V / (2 * C) >= 4096) C *= 2;
+  while (C < sdk::kLpMaxCluster && (long)P.rows * C < 4 * 152 && V / (2 * C) >= 4096) C *= 2;
   while (C < sdk::kLpMaxCluster && V / C > SD_TOP_MAX_V / sdk::kLpMaxCluster) C *= 2;
   const long span = ((long)V + C - 1) / C;
   P.span = (int)((span + sdk::kGroup - 1) / sdk::kGroup * sdk::kGroup);
-  const size_t smem = (((size_t)P.span / sdk::kGroup * 4 + 15) & ~(size_t)15) +
-                      (size_t)n_top * sdk::kGroup * 8;
+  const size_t smem = (size_t)P.span / sdk::kGroup * 4;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
@@ -410,7 +523,7 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   cfg.numAttrs = 1;
   auto kernel = dtype == SD_BF16_LOGITS ? sdk::logprob_kernel<SD_BF16_LOGITS>
                                         : sdk::logprob_kernel<SD_F32_PROBS>;
-  if (smem > 32 * 1024 &&
+  if (smem > 16 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess)
     return SD_E_LAUNCH;
