@@ -5,7 +5,7 @@
 // H = -sum p ln p = ln Z - (sum e^(y - m) (y - m)) / Z. Sums are fp32, each thread's own and then a
 // tree's. Probability rows need no Z: log p = ln p_x, H = -sum p ln p.
 //
-// A warp takes 256 neighbouring entries (a group) at a time. The group's maximum, one warp
+// A warp takes 256 or more neighbouring entries (a group) at a time. The group's maximum, one warp
 // reduction, is kept in shared memory to find the best n entries: they lie in the n groups that
 // come first by (maximum, lowest index), because each of those holds an entry that beats everything
 // of any later group. Only these n groups are read again. Entries are compared and bounded two at
@@ -16,7 +16,8 @@
 
 namespace sdk {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32, kGroup = 256;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kVec = 256;  // entries that a warp loads at once, 8 a lane; a group is U of them
 constexpr int kCandidates = 512;
 constexpr int kLpMaxCluster = 8;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -78,7 +79,7 @@ template <int DT>
 __device__ __forceinline__ Raw<DT> load_group(const void* row, int g0, int V, bool vec, int lane) {
   Raw<DT> r;
   r.b = make_uint4(0, 0, 0, 0);
-  if (vec && g0 + kGroup <= V) {
+  if (vec && g0 + kVec <= V) {
     if (DT == SD_BF16_LOGITS) {
       r.a = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)row + g0) + lane);
     } else {
@@ -119,20 +120,40 @@ __device__ __forceinline__ float p_log2_p(float p) {
   return p * (p > 0.5f ? log2f(p) : __log2f(p));
 }
 
+// Logits: a reference r, z = sum 2^t and s = sum t 2^t with t = c l - r, c = log2(e) / T;
+// probabilities: s = sum p log2 p.
 struct Sums {
-  float m, z, s;  // logits: a reference l, sum 2^t, sum t 2^t with t = (l - m) c; probabilities: s
+  float r, z, s;
 };
 
-// Joins sums over different references; c = log2(e) / T.
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = a.m == r.m ? 0.f : fmaxf((a.m - r.m) * c, -1e4f);
-  const float db = b.m == r.m ? 0.f : fmaxf((b.m - r.m) * c, -1e4f);
+// Joins sums over different references.
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+  Sums q;
+  q.r = fmaxf(a.r, b.r);
+  const float da = a.r == q.r ? 0.f : fmaxf(a.r - q.r, -1e4f);
+  const float db = b.r == q.r ? 0.f : fmaxf(b.r - q.r, -1e4f);
   const float fa = ex2(da), fb = ex2(db);
-  r.z = a.z * fa + b.z * fb;
-  r.s = (a.s + da * a.z) * fa + (b.s + db * b.z) * fb;
-  return r;
+  q.z = a.z * fa + b.z * fb;
+  q.s = (a.s + da * a.z) * fa + (b.s + db * b.z) * fb;
+  return q;
+}
+
+__device__ __forceinline__ float2 lp_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 lp_add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+  return d;
 }
 
 struct LpShared {
@@ -155,89 +176,117 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t q) {
   return (uint64_t)hi << 32 | lo;
 }
 
-// Sums, group maximum and rank of one lane's 8 entries; `edge`: the group holds the token or ends
-// the row, so that its entries are looked at one by one.
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+// A lane's running sums, in pairs, and how many entries come before the token.
 struct Lane {
-  Sums a;
-  float better;
+  float r;
+  float2 z, s;
+  int better;
 };
 
-template <int DT>
-__device__ __forceinline__ float take(Lane& s, const Raw<DT>& raw, float c, float xt, int g0,
+// Takes in a group of U vectors a lane (entries g0 .. g0 + 256 U - 1); returns the lane's largest.
+template <int DT, int U>
+__device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], float c, float xt, int g0,
                                       int token, int V, int lane) {
   float gm;
-  const bool edge = (token >= g0 && token < g0 + kGroup) || g0 + kGroup > V;
+  // a group that holds the token or ends the row is looked at entry by entry for the rank
+  const bool edge = (token >= g0 && token < g0 + U * kVec) || g0 + U * kVec > V;
   if (DT == SD_BF16_LOGITS) {
-    // -inf becomes a finite number far below (2^t is 0 and t 2^t, too); NaN stays
-    const __nv_bfloat162 low = __float2bfloat162_rn(-1e30f);
-    __nv_bfloat162 w[4] = {*reinterpret_cast<const __nv_bfloat162*>(&raw.a.x),
-                           *reinterpret_cast<const __nv_bfloat162*>(&raw.a.y),
-                           *reinterpret_cast<const __nv_bfloat162*>(&raw.a.z),
-                           *reinterpret_cast<const __nv_bfloat162*>(&raw.a.w)};
-    const __nv_bfloat162 m2 = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    __nv_bfloat162 m2 = as_bf162(raw[0].a.x);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const __nv_bfloat162 h = __hmax2(__hmax2(as_bf162(raw[u].a.x), as_bf162(raw[u].a.y)),
+                                       __hmax2(as_bf162(raw[u].a.z), as_bf162(raw[u].a.w)));
+      m2 = u == 0 ? h : __hmax2(m2, h);
+    }
     gm = fmaxf(__low2float(m2), __high2float(m2));
     if (!edge) {
       // entries before the token count from equality on, those behind it from above it on
       const __nv_bfloat162 x2 = __float2bfloat162_rn(xt);
-      __nv_bfloat162 n2;
-      if (g0 < token)
-        n2 = __hadd2(__hadd2(__hge2(w[0], x2), __hge2(w[1], x2)),
-                     __hadd2(__hge2(w[2], x2), __hge2(w[3], x2)));
-      else
-        n2 = __hadd2(__hadd2(__hgt2(w[0], x2), __hgt2(w[1], x2)),
-                     __hadd2(__hgt2(w[2], x2), __hgt2(w[3], x2)));
-      s.better += __low2float(n2) + __high2float(n2);
+      __nv_bfloat162 n2 = __float2bfloat162_rn(0.f);
+      if (g0 < token) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          n2 = __hadd2(n2, __hadd2(__hadd2(__hge2(as_bf162(raw[u].a.x), x2),
+                                           __hge2(as_bf162(raw[u].a.y), x2)),
+                                   __hadd2(__hge2(as_bf162(raw[u].a.z), x2),
+                                           __hge2(as_bf162(raw[u].a.w), x2))));
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          n2 = __hadd2(n2, __hadd2(__hadd2(__hgt2(as_bf162(raw[u].a.x), x2),
+                                           __hgt2(as_bf162(raw[u].a.y), x2)),
+                                   __hadd2(__hgt2(as_bf162(raw[u].a.z), x2),
+                                           __hgt2(as_bf162(raw[u].a.w), x2))));
+      }
+      q.better += (int)(__low2float(n2) + __high2float(n2));
     }
     // the reference moves only when it is some way behind (the sums have room, and a logarithm
     // near 0 still comes from numbers near 0)
-    if (!((gm - s.a.m) * c <= 8.f) && gm > -INFINITY) {
-      const float d = s.a.m == -INFINITY ? 0.f : fmaxf((s.a.m - gm) * c, -1e4f);
+    const float y = gm * c;
+    if (!(y - q.r <= 8.f) && gm > -INFINITY) {
+      const float d = q.r == -INFINITY ? 0.f : fmaxf(q.r - y, -1e4f);
       const float f = ex2(d);
-      s.a.s = (s.a.s + d * s.a.z) * f;
-      s.a.z *= f;
-      s.a.m = gm;
+      q.s = make_float2((q.s.x + d * q.z.x) * f, (q.s.y + d * q.z.y) * f);
+      q.z = make_float2(q.z.x * f, q.z.y * f);
+      q.r = y;
     }
-    const float m = s.a.m == -INFINITY ? 0.f : s.a.m;
+    const float nr = q.r == -INFINITY ? 0.f : -q.r;
+    // -inf becomes a finite number far below (2^t is 0 and t 2^t, too); NaN stays
+    const __nv_bfloat162 low = __float2bfloat162_rn(-1e30f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 x = __hmax2_nan(w[i], low);
-      const float2 f = __bfloat1622float2(x);
-      const float t0 = (f.x - m) * c, t1 = (f.y - m) * c;
-      const float p0 = ex2(t0), p1 = ex2(t1);
-      s.a.z += p0 + p1;
-      s.a.s = fmaf(t0, p0, s.a.s);
-      s.a.s = fmaf(t1, p1, s.a.s);
+    for (int u = 0; u < U; ++u) {
+      const uint32_t w[4] = {raw[u].a.x, raw[u].a.y, raw[u].a.z, raw[u].a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(__hmax2_nan(as_bf162(w[i]), low));
+        const float2 t = lp_fma2(f, make_float2(c, c), make_float2(nr, nr));
+        const float2 p = make_float2(ex2(t.x), ex2(t.y));
+        q.z = lp_add2(q.z, p);
+        q.s = lp_fma2(t, p, q.s);
+      }
     }
   } else {
-    float v[8];
-    unpack<DT>(raw, v);
-    gm = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
-               fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-    if (!edge) {
-      int n = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n += g0 < token ? v[e] >= xt : v[e] > xt;
-      s.better += (float)n;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s.a.s += p_log2_p(v[e]);
-  }
-  if (edge) {
-    float v[8];
-    unpack<DT>(raw, v);
+    gm = -INFINITY;
     int n = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = g0 + entry<DT>(lane, e);
-      n += (v[e] > xt || (v[e] == xt && i < token)) && i < V;
+    for (int u = 0; u < U; ++u) {
+      float v[8];
+      unpack<DT>(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        gm = fmaxf(gm, v[e]);
+        n += g0 < token ? v[e] >= xt : v[e] > xt;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2)
+        q.s = lp_add2(q.s, make_float2(p_log2_p(v[e]), p_log2_p(v[e + 1])));
     }
-    s.better += (float)n;
+    if (!edge) q.better += n;
+  }
+  if (edge) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float v[8];
+      unpack<DT>(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = g0 + u * kVec + entry<DT>(lane, e);
+        n += (v[e] > xt || (v[e] == xt && i < token)) && i < V;
+      }
+    }
+    q.better += n;
   }
   return gm;
 }
 
-template <int DT>
+template <int DT, int U>
 __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P) {
+  constexpr int kGroup = U * kVec;
   extern __shared__ __align__(16) unsigned char s_dyn[];
   __shared__ LpShared sm;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -271,14 +320,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P
   const int groups = begin < end ? (end - begin + kGroup - 1) / kGroup : 0;
   uint32_t* gmax = reinterpret_cast<uint32_t*>(s_dyn);  // [span / kGroup], as order_of()
 
-  // 1. One pass: sums, rank, group maxima. Each warp takes U groups in flight.
-  constexpr int U = DT == SD_BF16_LOGITS ? 4 : 2;
+  // 1. One pass: sums, rank, group maxima; the next group on its way while one is taken in.
   Raw<DT> raw[U];
+  auto fetch = [&](int g) {
+    if (g < groups) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int gi = warp * U + u;
-    if (gi < groups) raw[u] = load_group<DT>(x, begin + gi * kGroup, P.V, vec, lane);
-  }
+      for (int u = 0; u < U; ++u)
+        raw[u] = load_group<DT>(x, begin + g * kGroup + u * kVec, P.V, vec, lane);
+    }
+  };
+  fetch(warp);
   const bool in_range = token < P.V;
   float xt = INFINITY;
   if (in_range)
@@ -286,41 +337,28 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P
                               : ((const float*)x)[token];
   float T = DT == SD_BF16_LOGITS && P.temperature ? P.temperature[row / P.J] : 1.f;
   if (!(T > 0.f)) T = 1.f;  // a greedy request's rows are reported at temperature 1
-  const float inv_T = 1.f / T;
-  const float c = kLog2e * inv_T;
-  Lane s{{-INFINITY, 0.f, 0.f}, 0.f};
-  int rank_part = 0;
-  for (int g = warp * U; g < groups; g += kLpWarps * U) {
+  const float c = kLog2e / T;
+  Lane q{-INFINITY, make_float2(0.f, 0.f), make_float2(0.f, 0.f), 0};
+  for (int g = warp; g < groups; g += kLpWarps) {
     Raw<DT> now[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) now[u] = raw[u];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int gi = g + kLpWarps * U + u;
-      if (gi < groups) raw[u] = load_group<DT>(x, begin + gi * kGroup, P.V, vec, lane);
+    fetch(g + kLpWarps);
+    const float gm = take<DT, U>(q, now, c, xt, begin + g * kGroup, token, P.V, lane);
+    if (P.n_top > 0) {
+      const uint32_t o = __reduce_max_sync(0xffffffffu, order_of(gm));
+      if (lane == 0) gmax[g] = o;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int gi = g + u;
-      if (gi >= groups) break;
-      const float gm = take<DT>(s, now[u], c, xt, begin + gi * kGroup, token, P.V, lane);
-      if (P.n_top > 0) {
-        const uint32_t o = __reduce_max_sync(0xffffffffu, order_of(gm));
-        if (lane == 0) gmax[gi] = o;
-      }
-    }
-    rank_part += (int)s.better;
-    s.better = 0.f;
   }
-  Sums a = s.a;
+  Sums a{q.r, q.z.x + q.z.y, q.s.x + q.s.y};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Sums b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.z, o),
+    Sums b{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.z, o),
            __shfl_xor_sync(0xffffffffu, a.s, o)};
-    if (DT == SD_BF16_LOGITS) a = join(a, b, c);
+    if (DT == SD_BF16_LOGITS) a = join(a, b);
     else a.s += b.s;
   }
-  rank_part = __reduce_add_sync(0xffffffffu, rank_part);
+  const int rank_part = __reduce_add_sync(0xffffffffu, q.better);
   if (lane == 0) {
     sm.warp_sums[warp] = a;
     sm.warp_rank[warp] = rank_part;
@@ -338,9 +376,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P
     int r = lane < kLpWarps ? sm.warp_rank[lane] : 0;
 #pragma unroll
     for (int o = kLpWarps / 2; o > 0; o >>= 1) {
-      Sums d{__shfl_xor_sync(0xffffffffu, b.m, o), __shfl_xor_sync(0xffffffffu, b.z, o),
+      Sums d{__shfl_xor_sync(0xffffffffu, b.r, o), __shfl_xor_sync(0xffffffffu, b.z, o),
              __shfl_xor_sync(0xffffffffu, b.s, o)};
-      if (DT == SD_BF16_LOGITS) b = join(b, d, c);
+      if (DT == SD_BF16_LOGITS) b = join(b, d);
       else b.s += d.s;
     }
     r = __reduce_add_sync(0xffffffffu, r);
@@ -378,18 +416,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P
     const uint64_t floor = sm.floor;
     bool many = floor == 0;
     if (!many) {
-      for (int k = warp; k < ng; k += kLpWarps) {
-        const int g0 = begin + sm.first[k] * kGroup;
+      const float least = value_of((uint32_t)(floor >> 32));
+      for (int k = warp; k < ng * U; k += kLpWarps) {
+        const int g0 = begin + sm.first[k / U] * kGroup + (k % U) * kVec;
         const Raw<DT> r = load_group<DT>(x, g0, P.V, vec, lane);
         float v[8];
         unpack<DT>(r, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int i = g0 + entry<DT>(lane, e);
-          const uint64_t q = key_of(v[e], i);
-          if (i < P.V && q >= floor) {
+          if (v[e] >= least && i < P.V) {
             const int at = atomicAdd(&sm.count, 1);
-            if (at < kCandidates) sm.cand[at] = q;
+            if (at < kCandidates) sm.cand[at] = key_of(v[e], i);
           }
         }
       }
@@ -445,18 +483,18 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P
   Sums t = sm.sums[0];
   int rank = sm.rank[0];
   for (int i = 1; i < C; ++i) {
-    if (DT == SD_BF16_LOGITS) t = join(t, sm.sums[i], c);
+    if (DT == SD_BF16_LOGITS) t = join(t, sm.sums[i]);
     else t.s += sm.sums[i].s;
     rank += sm.rank[i];
   }
-  const float ln_z = DT == SD_BF16_LOGITS ? logf(t.z) : 0.f;
+  const float log2_z = DT == SD_BF16_LOGITS ? log2f(t.z) : 0.f;
   auto lp = [&](float v) {
-    return DT == SD_BF16_LOGITS ? (v - t.m) * inv_T - ln_z : logf(v);
+    return DT == SD_BF16_LOGITS ? (fmaf(v, c, -t.r) - log2_z) * kLn2 : logf(v);
   };
   if (tid == 0) {
     P.logprob[row] = in_range ? lp(xt) : -INFINITY;
     if (P.entropy)
-      P.entropy[row] = DT == SD_BF16_LOGITS ? ln_z - t.s * kLn2 / t.z : 0.f - t.s * kLn2;
+      P.entropy[row] = DT == SD_BF16_LOGITS ? (log2_z - t.s / t.z) * kLn2 : 0.f - t.s * kLn2;
     if (P.rank) P.rank[row] = in_range ? rank + 1 : 0;
     if (!in_range) raise_err(P.err, SD_ERR_TOKEN_RANGE);
   }
@@ -502,13 +540,18 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   P.top_lp = top_lp;
   P.err = err;
   // Few rows: a cluster of CTAs shares one, until the rows fill four CTAs on every SM or a CTA has
-  // less than two groups for each warp.
+  // less than two vectors for each warp.
   int C = 1;
   while (C < sdk::kLpMaxCluster && (long)P.rows * C < 4 * 152 && V / (2 * C) >= 4096) C *= 2;
   while (C < sdk::kLpMaxCluster && V / C > SD_TOP_MAX_V / sdk::kLpMaxCluster) C *= 2;
+  // Groups of one vector while there are few of them, so that the best n groups are few entries
+  // (and n of them at all); else of several, which saves most of a group's own work.
+  const int wide = dtype == SD_BF16_LOGITS ? 4 : 2;
+  const int U = V / C >= 65536 ? wide : 1;
+  const int group = U * sdk::kVec;
   const long span = ((long)V + C - 1) / C;
-  P.span = (int)((span + sdk::kGroup - 1) / sdk::kGroup * sdk::kGroup);
-  const size_t smem = (size_t)P.span / sdk::kGroup * 4;
+  P.span = (int)((span + group - 1) / group * group);
+  const size_t smem = (size_t)P.span / group * 4;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
@@ -521,8 +564,11 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = dtype == SD_BF16_LOGITS ? sdk::logprob_kernel<SD_BF16_LOGITS>
-                                        : sdk::logprob_kernel<SD_F32_PROBS>;
+  auto kernel = dtype == SD_BF16_LOGITS
+                    ? (U > 1 ? sdk::logprob_kernel<SD_BF16_LOGITS, 4>
+                             : sdk::logprob_kernel<SD_BF16_LOGITS, 1>)
+                    : (U > 1 ? sdk::logprob_kernel<SD_F32_PROBS, 2>
+                             : sdk::logprob_kernel<SD_F32_PROBS, 1>);
   if (smem > 16 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess)
