@@ -541,40 +541,68 @@ def sd_race_E_check(w_begin, count, counts, stream=None):
     _check(rc, "sd_race_E_check")
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported once (these calls run every few microseconds)."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _quick():
+    """The library, without the lock once it is loaded."""
+    return _lib if _lib is not None else load()
+
+
+def _raw_stream(t, stream):
+    """The given stream, or the current one of the tensor's device. (As a bare handle, where torch
+    gives one: building its stream object takes longer than the rest of a call's checks.)"""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    raw = getattr(_t()._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not t.is_cuda:
+        return _t().cuda.current_stream(_device(t)).cuda_stream
+    return raw(t.get_device())
+
+
 def _cache_args(k_cache, v_cache, k_scale, v_scale):
     """The cache arguments of the C calls: pointers, strides and sizes of a cache in e4m3 (or its
     bytes as uint8), [num_blocks, block_size, Hkv, D], with scales [num_blocks, Hkv] fp32."""
-    import torch
-
-    for t in (k_cache, v_cache):
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or t.dim() != 4 or t.stride(3) != 1:
-            raise SDError("a cache is e4m3 (or uint8) [num_blocks, block_size, Hkv, D] with "
-                          "contiguous heads")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    torch = _t()
+    shape, st = k_cache.shape, k_cache.stride()
+    kinds = (torch.float8_e4m3fn, torch.uint8)
+    if len(shape) != 4 or st[3] != 1 or k_cache.dtype not in kinds or v_cache.dtype not in kinds:
+        raise SDError("a cache is e4m3 (or uint8) [num_blocks, block_size, Hkv, D] with "
+                      "contiguous heads")
+    if v_cache.shape != shape or v_cache.stride() != st:
         raise SDError("k_cache and v_cache must have the same shape and strides")
-    nb, bs, Hkv, D = k_cache.shape
+    nb, bs, Hkv, _ = shape
     for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or tuple(t.shape) != (nb, Hkv) or not t.is_contiguous():
+        if t.dtype != torch.float32 or t.shape != (nb, Hkv) or not t.is_contiguous():
             raise SDError("scales must be contiguous float32 [num_blocks, Hkv]")
     # a dimension of one has no stride of its own
-    strides = [t if n > 1 else 16 for n, t in zip((nb, bs, Hkv), k_cache.stride())]
-    return (_ptr(k_cache), _ptr(v_cache), *strides, _ptr(k_scale), _ptr(v_scale), nb, bs)
+    return (_ptr(k_cache), _ptr(v_cache), st[0] if nb > 1 else 16, st[1] if bs > 1 else 16,
+            st[2] if Hkv > 1 else 16, _ptr(k_scale), _ptr(v_scale), nb, bs)
 
 
 def _head_rows(t, Hn, D, what):
     """Strides of bf16 [n, heads, D] rows with contiguous heads."""
-    import torch
-
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (Hn, D) \
-            or (t.numel() and t.stride(2) != 1):
+    shape = t.shape
+    if t.dtype != _t().bfloat16 or len(shape) != 3 or shape[1] != Hn or shape[2] != D:
         raise SDError(f"{what} must be bfloat16 [tokens, {Hn}, {D}] with contiguous heads")
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if Hn > 1 else 0)
+    st = t.stride()
+    if st[2] != 1 and shape[0]:
+        raise SDError(f"{what} must be bfloat16 [tokens, {Hn}, {D}] with contiguous heads")
+    return (st[0] if shape[0] > 1 else 0), (st[1] if Hn > 1 else 0)
 
 
 def _int32(t, shape, what):
-    import torch
-
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != _t().int32 or t.shape != shape or not t.is_contiguous():
         raise SDError(f"{what} must be contiguous int32 {list(shape)}")
 
 
@@ -591,9 +619,9 @@ def sd_kv_write(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None
     if v.shape[0] != n:
         raise SDError("k and v must hold the same tokens")
     _int32(slot_mapping, (n,), "slot_mapping")
-    rc = load().sd_kv_write(n, Hkv, D, _ptr(k), *_head_rows(k, Hkv, D, "k"), _ptr(v),
+    rc = _quick().sd_kv_write(n, Hkv, D, _ptr(k), *_head_rows(k, Hkv, D, "k"), _ptr(v),
                             *_head_rows(v, Hkv, D, "v"), _ptr(slot_mapping), *cache, _ptr(err),
-                            _stream(k_cache, stream))
+                            _raw_stream(k_cache, stream))
     _check(rc, "sd_kv_write")
 
 
@@ -615,9 +643,9 @@ def sd_kv_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_tokens, k_out
     strides = _head_rows(k_out, Hkv, D, "k_out")
     if v_out.shape != k_out.shape or _head_rows(v_out, Hkv, D, "v_out") != strides:
         raise SDError("k_out and v_out must have the same shape and strides")
-    rc = load().sd_kv_read(B, k_out.shape[0], Hkv, D, *cache, _ptr(block_table), mb,
+    rc = _quick().sd_kv_read(B, k_out.shape[0], Hkv, D, *cache, _ptr(block_table), mb,
                            _ptr(cu_tokens), _ptr(first_pos), _ptr(k_out), _ptr(v_out), *strides,
-                           _ptr(err), _stream(k_cache, stream))
+                           _ptr(err), _raw_stream(k_cache, stream))
     _check(rc, "sd_kv_read")
 
 
@@ -629,7 +657,7 @@ def attend_workspace(device, D):
     concurrent streams must pass their own)."""
     import torch
 
-    need = max(load().sd_kv_attend_workspace_bytes(D), 16)
+    need = max(_quick().sd_kv_attend_workspace_bytes(D), 16)
     key = torch.device(device)
     ws = _attend_workspaces.get(key)
     if ws is None or ws.numel() < need:
@@ -640,7 +668,7 @@ def attend_workspace(device, D):
 
 def sd_kv_attend_workspace_bytes(D):
     """Bytes of scratch that sd_kv_attend needs for heads of D values."""
-    return load().sd_kv_attend_workspace_bytes(D)
+    return _quick().sd_kv_attend_workspace_bytes(D)
 
 
 def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, cu_q, out, lse=None,
@@ -654,8 +682,6 @@ def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, c
     workspace_buf: uint8 device tensor of at least sd_kv_attend_workspace_bytes(D) bytes, or None
     for this device's shared one.
     """
-    import torch
-
     cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     Hkv, D = k_cache.shape[2:]
     B, mb = block_table.shape
@@ -668,15 +694,15 @@ def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, c
     sq, so = _head_rows(q, Hq, D, "q"), _head_rows(out, Hq, D, "out")
     if out.shape[0] != n:
         raise SDError("out must have q's shape")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, Hq)
+    if lse is not None and (lse.dtype != _t().float32 or lse.shape != (n, Hq)
                             or not lse.is_contiguous()):
         raise SDError("lse must be contiguous float32 [tokens, Hq]")
     ws = workspace_buf if workspace_buf is not None else attend_workspace(k_cache.device, D)
-    rc = load().sd_kv_attend(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q), *sq,
+    rc = _quick().sd_kv_attend(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q), *sq,
                              *cache, _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q),
                              D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)),
                              _ptr(out), *so, _ptr(lse), _ptr(ws), ws.numel(), _ptr(err),
-                             _stream(k_cache, stream))
+                             _raw_stream(k_cache, stream))
     _check(rc, "sd_kv_attend")
 
 
@@ -689,8 +715,7 @@ def sd_token_logprobs(rows, tokens, logprob, entropy=None, rank=None, top_ids=No
     top_logprobs: [B, J, n_top] int32 and float32; temperature: [B] float32 or None. Every output
     but logprob may be None.
     """
-    import torch
-
+    torch = _t()
     B, J = tokens.shape
     V = rows.shape[1]
     if rows.dtype == torch.float32:
@@ -709,12 +734,12 @@ def sd_token_logprobs(rows, tokens, logprob, entropy=None, rank=None, top_ids=No
                                (top_ids, torch.int32, (B, J, n_top), "top_ids"),
                                (top_logprobs, torch.float32, (B, J, n_top), "top_logprobs"),
                                (temperature, torch.float32, (B,), "temperature")):
-        if t is not None and (t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous()):
+        if t is not None and (t.dtype != dt or t.shape != shape or not t.is_contiguous()):
             raise SDError(f"{what} must be contiguous {dt} {list(shape)}")
     if n_top and top_logprobs is None:
         raise SDError("top_ids comes with top_logprobs")
-    rc = load().sd_token_logprobs(B, J, V, dtype, _ptr(rows), _row_stride(rows), _ptr(tokens),
+    rc = _quick().sd_token_logprobs(B, J, V, dtype, _ptr(rows), _row_stride(rows), _ptr(tokens),
                                   _ptr(temperature), n_top, _ptr(logprob), _ptr(entropy),
                                   _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(err),
-                                  _stream(rows, stream))
+                                  _raw_stream(rows, stream))
     _check(rc, "sd_token_logprobs")

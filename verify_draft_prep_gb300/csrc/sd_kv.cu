@@ -40,20 +40,30 @@ __device__ __forceinline__ float pow2_scale(float a) {
   return k <= -100 ? kMinScale : __uint_as_float((uint32_t)(k + 127) << 23);
 }
 
-// Largest finite magnitude of two bf16, as two 16-bit patterns.
-__device__ __forceinline__ uint32_t finite_mag2(uint32_t w) {
-  const uint32_t a = w & 0x7fff7fffu;
-  return a & __vcmpltu2(a, 0x7f807f80u);
+// The largest finite of 8 bf16 magnitudes, as a 16-bit pattern (infinities and NaN count as 0).
+__device__ __forceinline__ uint32_t finite_max(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+    m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+  }
+  return m;
 }
 
-__device__ __forceinline__ uint16_t quant2(uint32_t w, float s, float inv) {
-  const float a = bf16_lo(w), b = bf16_hi(w);
-  // 1/s is exact for a power of two; any other scale (one the caller wrote) divides
-  return inv > 0.f ? f32_to_e4m3x2(a * inv, b * inv)
-                   : f32_to_e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s));
+// 8 bf16 times r (exact: r a power of two), or over s where r is 0, as e4m3 to nearest even.
+__device__ __forceinline__ uint2 quant8(const uint4& v, float r, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = r > 0.f ? f32_to_e4m3x2(bf16_lo(w[i]) * r, bf16_hi(w[i]) * r)
+                   : f32_to_e4m3x2(__fdiv_rn(bf16_lo(w[i]), s), __fdiv_rn(bf16_hi(w[i]), s));
+  return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
 
-__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const KvWriteParams P) {
+__global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWriteParams P) {
   extern __shared__ int32_t s_map[];  // [runs of this CTA][block_size]: the token of each slot
   __shared__ int32_t s_lead[32];
   __shared__ int s_runs;
@@ -68,10 +78,11 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const KvWritePa
     bool lead = false, bad = false;
     if (lane < P.chunk && i0 + lane < P.n) {
       const int s = P.slots[i0 + lane];
+      int prev = i0 + lane > 0 ? P.slots[i0 + lane - 1] : -1;
       bad = s >= limit;
       if (s >= 0 && !bad) {
-        int prev = -1;  // the last slot before this one, over up to 31 negative ones
-        for (int j = i0 + lane - 1; j >= 0 && j >= i0 + lane - 32 && prev < 0; --j)
+        // the last slot before this one, over up to 31 negative ones
+        for (int j = i0 + lane - 2; j >= 0 && j >= i0 + lane - 32 && prev < 0; --j)
           prev = P.slots[j];
         lead = prev < 0 || (prev >> P.log2_bs) != (s >> P.log2_bs);
       }
@@ -109,7 +120,7 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const KvWritePa
   const int teams = (kWriteThreads / 32) / team_warps;
   const int team = warp / team_warps, sub = warp % team_warps;
   const int row_lanes = P.D / 8;                // lanes that hold one token's head, 8 values each
-  const int rows = 32 / row_lanes;              // tokens that a warp holds in one register set
+  const int rows = 32 / row_lanes;              // tokens of one of its 8 register sets, 2 or more
   const int my_row = lane / row_lanes, col = lane % row_lanes;
   const int slots = bs < 16 ? bs : 16;          // slots of the page that this warp holds
   const int pairs = 2 * P.Hkv;
@@ -125,28 +136,32 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const KvWritePa
     uint8_t* base = P.cache[kv] + page * P.st_block + h * P.st_head + col * 8;
 
     uint4 x[8];
-    uint32_t mag = 0;
+    uint32_t mag = 0, have = 0;  // have: the sets of which this lane holds a token of the call
 #pragma unroll
     for (int it = 0; it < 8; ++it) {
       const int j = it * rows + my_row;
       x[it] = make_uint4(0, 0, 0, 0);
       if (active && my_row < rows && j < slots) {
         const int t = map[sub * 16 + j];
+        if (t >= 0) have |= 1u << it;
         if (t >= 0)
           x[it] = __ldcs(reinterpret_cast<const uint4*>(P.x[kv] + t * P.ld[kv] + h * P.hs[kv] +
                                                         col * 8));
       }
     }
-    // rows of 16 and 24 values: more than 8 sets would be needed for 16 tokens only if a warp held
-    // fewer than two tokens, and D <= 128 leaves it two at the least
     float s_old = active ? *sp : 0.f;
 #pragma unroll
     for (int it = 0; it < 8; ++it) {
-      mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(finite_mag2(x[it].x), finite_mag2(x[it].y)),
-                                   __vmaxu2(finite_mag2(x[it].z), finite_mag2(x[it].w))));
+      mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x[it].x & 0x7fff7fffu, x[it].y & 0x7fff7fffu),
+                                   __vmaxu2(x[it].z & 0x7fff7fffu, x[it].w & 0x7fff7fffu)));
     }
-    mag = max(mag & 0xffffu, mag >> 16);
-    mag = __reduce_max_sync(0xffffffffu, mag);
+    mag = __reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16));
+    if (mag >= 0x7f80u) {  // an infinity or a NaN: rare, and it does not enter the scale
+      mag = 0;
+#pragma unroll
+      for (int it = 0; it < 8; ++it) mag = max(mag, finite_max(x[it]));
+      mag = __reduce_max_sync(0xffffffffu, mag);
+    }
     if (team_warps > 1) {
       __syncthreads();  // the last round's magnitudes are read, and every scale of this round
       if (lane == 0) s_mag[warp] = mag;
@@ -163,18 +178,25 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const KvWritePa
     const float inv = (__float_as_uint(s) & 0x7fffffu) == 0 && r >= 1.17549435e-38f ? r : 0.f;
     const bool again = !fresh && s != s_old;
     const float ratio = __fdiv_rn(s_old, s);
+    if (inv > 0.f) {
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int j = it * rows + my_row;
-      if (my_row >= rows || j >= slots) continue;
-      const int off = sub * 16 + j;
-      uint2* dst = reinterpret_cast<uint2*>(base + off * P.st_tok);
-      if (map[off] >= 0) {
-        uint2 o;
-        o.x = quant2(x[it].x, s, inv) | (uint32_t)quant2(x[it].y, s, inv) << 16;
-        o.y = quant2(x[it].z, s, inv) | (uint32_t)quant2(x[it].w, s, inv) << 16;
-        *dst = o;
-      } else if (again) {  // what the page held, at its new scale
+      for (int it = 0; it < 8; ++it)
+        if ((have >> it) & 1)
+          *reinterpret_cast<uint2*>(base + (sub * 16 + it * rows + my_row) * P.st_tok) =
+              quant8(x[it], inv, s);
+    } else {
+#pragma unroll
+      for (int it = 0; it < 8; ++it)
+        if ((have >> it) & 1)
+          *reinterpret_cast<uint2*>(base + (sub * 16 + it * rows + my_row) * P.st_tok) =
+              quant8(x[it], 0.f, s);
+    }
+    if (again) {  // what the page held in its other slots, at its new scale
+#pragma unroll 1
+      for (int it = 0; it < 8; ++it) {
+        if (my_row >= rows || it * rows + my_row >= slots || (have >> it) & 1) continue;
+        uint2* dst =
+            reinterpret_cast<uint2*>(base + (sub * 16 + it * rows + my_row) * P.st_tok);
         const uint2 q = *dst;
         uint32_t o[2];
 #pragma unroll
@@ -248,6 +270,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadParam
   }
   __syncthreads();
   const int parts = c.D / 16, per_row = c.Hkv * parts;
+#pragma unroll 4
   for (int u = tid; u < kReadRows * per_row; u += kReadThreads) {
     const int row = u / per_row, e = u % per_row, h = e / parts, d = (e % parts) * 16;
     const int page = s_page[row];
