@@ -18,7 +18,7 @@
 // Hq / Hkv heads that share the KV head. All units' tiles of 128 tokens form one line, which the
 // CTAs (one per SM) divide evenly, whatever the lengths of the requests: a unit that several CTAs
 // share leaves its parts in the workspace and attend_join_kernel joins them in a fixed order.
-// Within a CTA: warp 0 loads pages (TMA), warp 1 issues the products, warp 2 fetches scales, two
+// Within a CTA: warps 0 and 2 load pages (TMA) and their scales, warp 1 issues the products, two
 // groups of four warps turn S into P, one row a thread. The groups are two streams that keep
 // the tensor cores busy in turn: with few rows they take alternate tiles of the same rows (and
 // the accumulators are joined at the unit's end), with many they take 128 rows each of the same
@@ -39,7 +39,7 @@ constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
 // P = 2^(y - M + kShift) is at most 448 while M is no more than kSlack behind the row's maximum. A
 // larger shift keeps more of the small weights, a smaller one has the accumulator rescaled less
 // often: weights lose bits below 2^-14 of the row's largest, and end at 2^-18 of it.
-constexpr float kShift = 8.f, kSlack = 0.75f;
+constexpr float kShift = 7.f, kSlack = 1.75f;
 constexpr float kTiny = 1.17549435e-38f;  // -inf times it is -inf, S times it is nothing
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
 
@@ -73,8 +73,9 @@ template <int DP, int NS, int R>
 struct AttLayout {
   static constexpr int kRows = NS * kTile / R;      // of a unit
   // Tensor memory, 512 columns: S of both streams, O of both; with heads of 64 there is room for P
-  // beside S, so that the next S is formed while this one's P is; else P takes S's place.
-  static constexpr bool kOwnP = DP == 64;
+  // beside S, so that the next S is formed while this one's P is, which pays where a thread takes
+  // S into registers at once (R > 1); else P takes S's place.
+  static constexpr bool kOwnP = DP == 64 && R > 1;
   static constexpr int kTmS = 0, kTmO = 256, kTmP = kOwnP ? 256 + 2 * DP : 0;
   static constexpr int kTmPStep = kOwnP ? 64 : 128;
   static constexpr int kQBytes = kTile * DP;        // one term of one Q tile
@@ -149,7 +150,7 @@ __device__ __forceinline__ int tiles_for(const AttendParams& P, const Request& q
 struct Segment {
   Request q;
   int r, h, row0, rows, a, b, n;
-  int cnt[2];       // tiles of each stream
+  int cnt0, cnt1;   // tiles of each stream
   long long first;  // the unit's first tile on the line
 };
 
@@ -192,12 +193,12 @@ struct Schedule {
       }
       if (s.b <= s.a) continue;
       if (NS == 1) {
-        s.cnt[0] = (s.b - s.a + 1) / 2;
-        s.cnt[1] = (s.b - s.a) / 2;
+        s.cnt0 = (s.b - s.a + 1) / 2;
+        s.cnt1 = (s.b - s.a) / 2;
       } else {
         const int n0 = s.rows > kTile ? tiles_for(P, s.q, s.row0 + kTile - 1) : s.n;
-        s.cnt[0] = max(0, min(s.b, n0) - s.a);
-        s.cnt[1] = s.rows > kTile ? s.b - s.a : 0;
+        s.cnt0 = max(0, min(s.b, n0) - s.a);
+        s.cnt1 = s.rows > kTile ? s.b - s.a : 0;
       }
       return true;
     }
@@ -398,7 +399,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(smem_u32(&m.sc_full[i]), 1);
+      mbar_init(smem_u32(&m.sc_full[i]), 2);
       mbar_init(smem_u32(&m.sc_empty[i]), NS == 1 ? 4 : 8);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -476,52 +477,91 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   Segment s;
   const int log2_bs = P.c.log2_bs, bs = 1 << log2_bs;
 
-  if (warp == 0) {
-    // ---- loads: lane p of a tile's pages issues that page ----
-    const int pages = kTile >> log2_bs;              // of a tile, 1 to 16
+  if (warp == 0 || warp == 2) {
+    // ---- loads: K by one warp and V by another, each with its scales. Lane p of a tile's pages
+    // issues that page; entries and scales are fetched one and two batches of tiles ahead ----
+    const bool is_v = warp == 2;
+    const CUtensorMap* map = is_v ? &v_map : &k_map;
+    const float* page_scale = is_v ? P.c.v_scale : P.c.k_scale;
+    uint64_t* full = is_v ? m.v_full : m.k_full;
+    uint64_t* empty = is_v ? m.v_empty : m.k_empty;
+    const int pages = kTile >> log2_bs;                 // of a tile, 1 to 16
     const int batch = 32 / pages < 8 ? 32 / pages : 8;  // tiles whose entries a warp reads at once
     const int my_tile = lane / pages, my_page = lane % pages;
-    const uint32_t box = (uint32_t)bs * DP;
-    int it = 0;
+    const int span = bs >> 3;                           // scale entries of a page
+    const uint32_t dst = base + (is_v ? L::kV : L::kK) + my_page * (uint32_t)(bs * DP);
+    int st = 0, slot = 0;
+    uint32_t ph = 1, sc_ph = 1;
     bool ok = true;
     while (ok && sched.next(P, s)) {
       const int32_t* table = P.table + (long)s.r * P.max_blocks;
       const int last_page = (s.q.len + bs - 1) >> log2_bs;
-      auto entry = [&](int t0) {
+      auto entry = [&](int t0) {  // this lane's page; -1: none
         const int pg = ((t0 + my_tile) << (7 - log2_bs)) + my_page;
         int e = -1;
         if (my_tile < batch && t0 + my_tile < s.b && pg < last_page) {
           e = __ldg(table + pg);
           if (e < 0 || e >= P.c.num_blocks) {
             e = -1;
-            raise_err(P.err, SD_ERR_KV_RANGE);
+            if (!is_v) raise_err(P.err, SD_ERR_KV_RANGE);
           }
         }
-        return e < 0 ? P.c.num_blocks : e;  // beyond the tensor: the copy fills in zeros
+        return e;
       };
-      int cur = entry(s.a);
+      auto scale_of = [&](int e) {
+        return e < 0 ? -1.f : fmaxf(__ldg(page_scale + (long)e * P.c.Hkv + s.h), 0.f);
+      };
+      int cur = entry(s.a), nxt = entry(s.a + batch);
+      float sc = scale_of(cur);
       for (int t0 = s.a; ok && t0 < s.b; t0 += batch) {
-        const int nxt = t0 + batch < s.b ? entry(t0 + batch) : 0;
-        for (int j = 0; j < batch && t0 + j < s.b; ++j, ++it) {
-          const int st = it % S;
-          const uint32_t par = ((it / S) & 1) ^ 1;
-          const uint32_t kf = smem_u32(&m.k_full[st]), vf = smem_u32(&m.v_full[st]);
-          ok = mbar_wait_warp(smem_u32(&m.k_empty[st]), par, gave_up);
+        const int far = entry(t0 + 2 * batch);
+        const float sc_nxt = scale_of(nxt);
+        for (int j = 0; j < batch && t0 + j < s.b; ++j) {
+          const uint32_t bar = smem_u32(full + st);
+          ok = mbar_wait_warp(smem_u32(empty + st), ph, gave_up);
           if (!ok) break;
-          if (lane == 0) mbar_expect_tx(kf, L::kTileBytes);
+          if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
           __syncwarp();
-          if (my_tile == j && my_tile < batch)
-            tma_load_4d(base + L::kK + st * L::kTileBytes + my_page * box, &k_map, 0, s.h, 0, cur,
-                        kf);
-          ok = mbar_wait_warp(smem_u32(&m.v_empty[st]), par, gave_up);
+          const bool mine = my_tile == j && my_tile < batch;
+          // a page that there is not: beyond the tensor, where the copy fills in zeros
+          if (mine)
+            tma_load_4d(dst + st * L::kTileBytes, map, 0, s.h, 0,
+                        cur < 0 ? P.c.num_blocks : cur, bar);
+          ok = mbar_wait_warp(smem_u32(&m.sc_empty[slot]), sc_ph, gave_up);
           if (!ok) break;
-          if (lane == 0) mbar_expect_tx(vf, L::kTileBytes);
+          if (is_v) {
+            const bool z = sc == 0.f;
+            const uint32_t zero = __reduce_or_sync(
+                0xffffffffu, mine && z ? ((1u << span) - 1) << (my_page * span) : 0u);
+            if (mine) {
+              const float v = fmaxf(sc, kMinScale);
+              const float2 f = sc < 0.f ? make_float2(-INFINITY, 1.f)
+                               : z      ? make_float2(kZeroLog2, kZeroInv)
+                                        : make_float2(__log2f(v), __fdividef(1.f, v));
+              for (int i = 0; i < span; ++i) {
+                scales[slot * 16 + my_page * span + i].y = f.x;
+                scales[slot * 16 + my_page * span + i].z = f.y;
+              }
+            }
+            if (lane == 0) m.sc_zero[slot] = (int)zero;
+          } else if (mine) {
+            for (int i = 0; i < span; ++i)
+              scales[slot * 16 + my_page * span + i].x = fmaxf(sc, 0.f);
+          }
           __syncwarp();
-          if (my_tile == j && my_tile < batch)
-            tma_load_4d(base + L::kV + st * L::kTileBytes + my_page * box, &v_map, 0, s.h, 0, cur,
-                        vf);
+          if (lane == 0) mbar_arrive(smem_u32(&m.sc_full[slot]));
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (++slot == kScaleSlots) {
+            slot = 0;
+            sc_ph ^= 1;
+          }
         }
         cur = nxt;
+        nxt = far;
+        sc = sc_nxt;
       }
     }
   } else if (warp == 1) {
@@ -620,22 +660,20 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       } else {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (s.cnt[x] > 0) wait(&m.q_full[x], nq[x]++ & 1);
+          if ((x ? s.cnt1 : s.cnt0) > 0) wait(&m.q_full[x], nq[x]++ & 1);
         auto do_qk = [&](int j, int x, int kst, uint32_t kph) {
           if (!wait(&m.k_full[kst], kph)) return;
           tc_fence_after();
           if (lead) {
             qk(kst, x, x);
             mma_commit(smem_u32(&m.s_full[x]));
-            if (j == s.cnt[x] - 1) mma_commit(smem_u32(&m.q_empty[x]));
+            if (j == (x ? s.cnt1 : s.cnt0) - 1) mma_commit(smem_u32(&m.q_empty[x]));
           }
         };
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (s.cnt[x] > 0) do_qk(0, x, st, ph);
+          if ((x ? s.cnt1 : s.cnt0) > 0) do_qk(0, x, st, ph);
         if (ok && lead) mma_commit(smem_u32(&m.k_empty[st]));
-        int pst = st;  // the tile before
-        uint32_t pph = ph;
         auto do_pv = [&](int j, int x, int v_st, uint32_t v_ph, bool last) {
           wait(&m.p_full[x], pp[x]);
           if (!wait(&m.v_full[v_st], v_ph)) return;
@@ -650,86 +688,19 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         for (int j = 0; ok && j < T; ++j) {
           const int nst = st + 1 == S ? 0 : st + 1;
           const uint32_t nph = ph ^ (nst == 0 ? 1u : 0u);
-          if (L::kOwnP) {
-            // each stream's next S as soon as its last one is read, the other's PV between
-            if (j < s.cnt[0]) {
-              wait(&m.s_read[0], sp[0]);
-              sp[0] ^= 1;
-              if (j + 1 < s.cnt[0]) do_qk(j + 1, 0, nst, nph);
-            }
-            if (j > 0 && j - 1 < s.cnt[1]) do_pv(j - 1, 1, pst, pph, true);
-            if (j < s.cnt[1]) {
-              wait(&m.s_read[1], sp[1]);
-              sp[1] ^= 1;
-              if (j + 1 < s.cnt[1]) do_qk(j + 1, 1, nst, nph);
-            }
-            if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
-            if (j < s.cnt[0]) do_pv(j, 0, st, ph, j >= s.cnt[1]);
-          } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (j >= s.cnt[x]) continue;
-              do_pv(j, x, st, ph, x == 1 || j >= s.cnt[1]);
-              if (j + 1 < s.cnt[x]) do_qk(j + 1, x, nst, nph);
-            }
-            if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
+          for (int x = 0; x < 2; ++x) {
+            if (j >= (x ? s.cnt1 : s.cnt0)) continue;
+            do_pv(j, x, st, ph, x == 1 || j >= s.cnt1);
+            if (j + 1 < (x ? s.cnt1 : s.cnt0)) do_qk(j + 1, x, nst, nph);
           }
-          pst = st;
-          pph = ph;
+          if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
           st = nst;
           ph = nph;
         }
-        if (L::kOwnP && ok && T - 1 < s.cnt[1]) do_pv(T - 1, 1, pst, pph, true);
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ---- scales: 16 entries a tile, one for 8 tokens; 8 tiles at a time ----
-    const int e = lane & 15, half = lane >> 4;
-    int it = 0;
-    bool ok = true;
-    while (ok && sched.next(P, s)) {
-      const int32_t* table = P.table + (long)s.r * P.max_blocks;
-      for (int t0 = s.a; ok && t0 < s.b; t0 += 8) {
-        float ks[4], vs[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long tok = (long)(t0 + 2 * i + half) * kTile + e * 8;
-          ks[i] = 0.f;
-          vs[i] = -1.f;  // nothing here
-          if (t0 + 2 * i + half < s.b && tok < s.q.len) {
-            const int page = __ldg(table + (tok >> log2_bs));
-            if (page >= 0 && page < P.c.num_blocks) {
-              const long at = (long)page * P.c.Hkv + s.h;
-              ks[i] = __ldg(P.c.k_scale + at);
-              vs[i] = fmaxf(__ldg(P.c.v_scale + at), 0.f);
-              if (vs[i] > 0.f) vs[i] = fmaxf(vs[i], kMinScale);
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (t0 + 2 * i + k >= s.b || !ok) break;
-            const int slot = it % kScaleSlots;
-            ok = mbar_wait_warp(smem_u32(&m.sc_empty[slot]), ((it / kScaleSlots) & 1) ^ 1, gave_up);
-            if (!ok) break;
-            const uint32_t zero = __ballot_sync(0xffffffffu, half == k && vs[i] == 0.f);
-            if (half == k) {
-              const bool none = vs[i] < 0.f, z = vs[i] == 0.f;
-              scales[slot * 16 + e] =
-                  make_float4(ks[i], none ? -INFINITY : z ? kZeroLog2 : log2f(vs[i]),
-                              none ? 1.f : z ? kZeroInv : __fdiv_rn(1.f, vs[i]), 0.f);
-            }
-            if (lane == 0) m.sc_zero[slot] = (int)(k ? zero >> 16 : zero & 0xffffu);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&m.sc_full[slot]));
-            ++it;
-          }
-        }
-      }
-    }
   } else if (warp == 3) {
     // ---- Q of the next unit, while this one is computed ----
     if (NS == 1) {
@@ -758,8 +729,9 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     const uint32_t lanes = (uint32_t)quarter << 21;
     const uint32_t tS = tmem + x * 128 + lanes;
     const uint32_t tP = tmem + L::kTmP + x * L::kTmPStep + lanes;
-    const uint32_t tO[2] = {tmem + L::kTmO + lanes, tmem + L::kTmO + DP + lanes};
-    int it = 0, nq = 0, done[2] = {0, 0}, unit = 0;
+    const uint32_t tO0 = tmem + L::kTmO + lanes, tO = tO0 + x * DP;  // the first's, this stream's
+    int it = 0, nq = 0, unit = 0;
+    int done = 0, done_other = 0;  // tiles of this stream and of the other one so far
     bool ok = true;
     bool continues = false;
     JoinDesc jd;
@@ -768,6 +740,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     // nothing is computed any more).
     while (sched.next(P, s)) {
       const int T = s.b - s.a;
+      const int cnt_x = x ? s.cnt1 : s.cnt0;
       const int buf = unit & 1;
       const int row_base = NS == 1 ? 0 : x * kTile;       // of this stream in the unit
       const int my_rows = NS == 1 ? s.rows : min(kTile, s.rows - row_base);
@@ -778,7 +751,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         rs = m.row_scale[(unit & 1) * kTile + wr];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&m.q_empty[unit & 1]));
-      } else if (s.cnt[x] > 0) {
+      } else if (cnt_x > 0) {
         ok = ok && mbar_wait_warp(smem_u32(&m.q_empty[x]), (nq & 1) ^ 1, gave_up);
         ++nq;
         if (ok)
@@ -802,7 +775,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         const int slot = (it + j) % kScaleSlots;
         ok = mbar_wait_warp(smem_u32(&m.sc_full[slot]), ((it + j) / kScaleSlots) & 1, gave_up);
         if (!ok) break;
-        if (NS == 2 && j >= s.cnt[x]) {  // the other stream's alone
+        if (NS == 2 && j >= cnt_x) {  // the other stream's alone
           if (lane == 0) mbar_arrive(smem_u32(&m.sc_empty[slot]));
           continue;
         }
@@ -844,7 +817,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           }
           fence_async_shared();
         }
-        ok = mbar_wait_warp(smem_u32(&m.s_full[x]), done[x] & 1, gave_up);
+        ok = mbar_wait_warp(smem_u32(&m.s_full[x]), done & 1, gave_up);
         if (!ok) break;
         tc_fence_after();
         if (warp_live) {
@@ -864,14 +837,18 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             }
             tmem_wait_st();
           }
-          // 32 columns at a time, the next ones on their way, twice: the code of one pass stays
-          // small enough for the instruction cache that eight warps share
+          // Up to 64 columns of S stay in registers; of 128, 32 at a time are read, twice, the next
+          // ones on their way. (The code of one pass stays small for the instruction cache, which
+          // eight warps share.)
           uint32_t v[32], w[32];
           float mx = -INFINITY;
           tmem_ld32(tC, v);
+          if (NC == 2) tmem_ld32(tC + 32, w);
           tmem_wait_ld();
-          if (NC == 1) {
+          if (NC <= 2) {
+            if (L::kOwnP) stream_read(m.s_read[x], lane);
             mx = row_max(v, sc, rs);
+            if (NC == 2) mx = fmaxf(mx, row_max(w, sc + 4, rs));
           } else {
 #pragma unroll 1
             for (int c = 0; c < NC; c += 2) {
@@ -888,45 +865,51 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             const float Mn = fmaxf(M, mx);
             if (j >= (NS == 1 ? 2 : 1)) {
               const float fac = M == -INFINITY ? 0.f : ex2f(M - Mn);
-              ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
+              ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < DP; c += 16) {
-                uint32_t w[16];
-                tmem_ld16(tO[x] + c, w);
+              for (int c = 0; c < DP; c += 32) {
+                uint32_t u[2][16];
+                tmem_ld16(tO + c, u[0]);
+                tmem_ld16(tO + c + 16, u[1]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  w[i] = __float_as_uint(__uint_as_float(w[i]) * fac);
-                tmem_st16(tO[x] + c, w);
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    u[k][i] = __float_as_uint(__uint_as_float(u[k][i]) * fac);
+                  tmem_st16(tO + c + k * 16, u[k]);
+                }
               }
               Lsum *= fac;
             }
             M = Mn;
           }
           if (L::kOwnP && j >= (NS == 1 ? 2 : 1)) {  // the last P has been used
-            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
+            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
             if (!ok) break;
           }
           const float shift = kShift - (M == -INFINITY ? 0.f : M);
           uint32_t o[16];
-          if (NC == 1) {
-            if (L::kOwnP) stream_read(m.s_read[x], lane);
+          if (NC <= 2) {
             Lsum += weights(v, sc, rs, shift, o);
-            tmem_st16(tP + copy * 16, o);
+            tmem_st16(tP + copy * NC * 16, o);
+            if (NC == 2) {
+              Lsum += weights(w, sc + 4, rs, shift, o);
+              tmem_st16(tP + (copy * NC + 1) * 16, o);
+            }
           } else {
 #pragma unroll 1
             for (int c = 0; c < NC; c += 2) {
               tmem_ld32(tC + (c + 1) * 32, w);
               Lsum += weights(v, sc + c * 4, rs, shift, o);
               tmem_wait_ld();
-              tmem_st16(tP + (copy * NC + c) * 16, o);
+              tmem_st16(tP + c * 16, o);
               if (c + 2 < NC) tmem_ld32(tC + (c + 2) * 32, v);
-              else if (L::kOwnP) stream_read(m.s_read[x], lane);
               Lsum += weights(w, sc + c * 4 + 4, rs, shift, o);
               tmem_wait_ld();
-              tmem_st16(tP + (copy * NC + c + 1) * 16, o);
+              tmem_st16(tP + (c + 1) * 16, o);
             }
           }
           if (R > 1) {  // the other copies' columns count as zero here
@@ -940,7 +923,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           // a warp without rows keeps pace with the others: its arrivals belong to this tile
           stream_read(m.s_read[x], lane);
           if (j >= (NS == 1 ? 2 : 1)) {
-            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
+            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
             if (!ok) break;
           }
         }
@@ -950,20 +933,23 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           mbar_arrive(smem_u32(&m.sc_empty[slot]));
           mbar_arrive(smem_u32(&m.p_full[x]));
         }
-        ++done[x];
+        ++done;
       }
-      if (NS == 1) done[x ^ 1] += s.cnt[x ^ 1];
+      if (NS == 1) done_other += x ? s.cnt0 : s.cnt1;
 
       // 3. the unit's (or this part's) result
       const bool split = s.a > 0 || s.b < s.n;
-      const int cnt_b = NS == 1 ? s.cnt[1] : 0;
+      const int cnt_b = NS == 1 ? s.cnt1 : 0;
       if (NS == 1) {
-        ok = ok && mbar_wait_warp(smem_u32(&m.o_done[0]), (done[0] - 1) & 1, gave_up);
-        if (cnt_b > 0)
-          ok = ok && mbar_wait_warp(smem_u32(&m.o_done[1]), (done[1] - 1) & 1, gave_up);
+        // (a stream's count goes on from unit to unit; one without a tile here has no phase to wait
+        // for)
+        if (x == 0 || cnt_b > 0)
+          ok = ok && mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
+        if (x == 1 || cnt_b > 0)
+          ok = ok && mbar_wait_warp(smem_u32(&m.o_done[x ^ 1]), (done_other - 1) & 1, gave_up);
         m.ml[x][wt] = make_float2(M, Lsum);
-      } else if (s.cnt[x] > 0) {
-        ok = ok && mbar_wait_warp(smem_u32(&m.o_done[x]), (done[x] - 1) & 1, gave_up);
+      } else if (cnt_x > 0) {
+        ok = ok && mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
       }
       tc_fence_after();
       named_bar(1, 256);
@@ -1002,7 +988,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         for (int c = 0; c < DP; c += 32) {
           if (ok && warp_live) {
             uint32_t u[32];
-            tmem_ld32(tO[x] + c, u);
+            tmem_ld32(tO + c, u);
             tmem_wait_ld();
             float* mine = join + ((warp - 4) * 32 + lane) * 33;
 #pragma unroll
@@ -1063,7 +1049,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         const int2 th = token_head(P, row);
         const long tok = s.q.tok0 + th.x;
         const int hq = s.h * P.G + th.y;
-        const bool mine_any = NS == 1 || s.cnt[x] > 0;
+        const bool mine_any = NS == 1 || cnt_x > 0;
         if (ok && warp_live && my_rows > 0) {
           constexpr int kCols = NS == 1 ? DP / 2 : DP;  // this thread's share of the row
           const int c0 = NS == 1 ? x * kCols : 0;
@@ -1071,8 +1057,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
 #pragma unroll 1
             for (int c = 0; c < kCols; c += 32) {
               uint32_t u[32], w[32];
-              tmem_ld32(tO[NS == 1 ? 0 : x] + c0 + c, u);
-              if (NS == 1 && cnt_b > 0) tmem_ld32(tO[1] + c0 + c, w);
+              tmem_ld32((NS == 1 ? tO0 : tO) + c0 + c, u);
+              if (NS == 1 && cnt_b > 0) tmem_ld32(tO0 + DP + c0 + c, w);
               tmem_wait_ld();
               if (!live) continue;
               float o[32];
