@@ -18,8 +18,8 @@
 // Hq / Hkv heads that share the KV head. All units' tiles of 128 tokens form one line, which the
 // CTAs (one per SM) divide evenly, whatever the lengths of the requests: a unit that several CTAs
 // share leaves its parts in the workspace and attend_join_kernel joins them in a fixed order.
-// Within a CTA: warps 0 and 2 load pages (TMA) and their scales, warp 1 issues the products, two
-// groups of four warps turn S into P, one row a thread. The groups are two streams that keep
+// Within a CTA: warps 0 and 2 load pages (TMA), warp 1 issues the products, warp 3 fetches the
+// scales and the next unit's queries, two groups of four warps turn S into P, one row a thread. The groups are two streams that keep
 // the tensor cores busy in turn: with few rows they take alternate tiles of the same rows (and
 // the accumulators are joined at the unit's end), with many they take 128 rows each of the same
 // tiles, which halves the traffic of K and V.
@@ -80,18 +80,20 @@ struct AttLayout {
   static constexpr int kTmPStep = kOwnP ? 64 : 128;
   static constexpr int kQBytes = kTile * DP;        // one term of one Q tile
   static constexpr int kTileBytes = kTile * DP;     // K or V of one tile
-  static constexpr int kStages = DP == 64 ? 8 : (R > 1 ? 3 : 4);
+  // Tiles in flight. V's stay longer (until P is formed and used) than K's.
+  static constexpr int kKStages = DP == 64 ? 6 : (NS == 1 ? 3 : 4);
+  static constexpr int kVStages = DP == 64 ? 10 : (NS == 1 ? 5 : 4);
   static constexpr int kQ = 0;                      // two buffers (NS = 1), or two tiles
   static constexpr int kK = kQ + 2 * 2 * kQBytes;
-  static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kScales = kV + kStages * kTileBytes;
-  static constexpr int kJoin = kScales + kScaleSlots * 16 * 16;  // [8 warps][32 rows][33] floats
-  static constexpr int kMisc = kJoin + (R > 1 ? 8 * 32 * 33 * 4 : 0);
+  static constexpr int kV = kK + kKStages * kTileBytes;
+  static constexpr int kScales = kV + kVStages * kTileBytes;
+  static constexpr int kJoin = kScales + kScaleSlots * 16 * 16;  // [8 warps][32 rows][17] floats
+  static constexpr int kMisc = kJoin + (R > 1 ? 8 * 32 * 17 * 4 : 0);
   static constexpr long kSlotFloats = (long)kRows * DP + kRows;
 };
 
 struct AttMisc {
-  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t k_full[10], k_empty[10], v_full[10], v_empty[10];
   uint64_t s_full[2], s_read[2], p_full[2], o_done[2], q_full[2], q_empty[2];
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
   int sc_zero[kScaleSlots];   // bit e: entry e's V scale is zero
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
               const __grid_constant__ CUtensorMap v_map) {
   using L = AttLayout<DP, NS, R>;
-  constexpr int S = L::kStages;
+  constexpr int SK = L::kKStages, SV = L::kVStages;
   extern __shared__ unsigned char s_raw[];
   unsigned char* smem = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
   AttMisc& m = *reinterpret_cast<AttMisc*>(smem + L::kMisc);
@@ -384,7 +386,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
 
   // ---- setup: barriers, tensor memory, this CTA's share of the line of tiles ----
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < 10; ++i) {
       mbar_init(smem_u32(&m.k_full[i]), 1);
       mbar_init(smem_u32(&m.k_empty[i]), 1);
       mbar_init(smem_u32(&m.v_full[i]), 1);
@@ -399,7 +401,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(smem_u32(&m.sc_full[i]), 2);
+      mbar_init(smem_u32(&m.sc_full[i]), 1);
       mbar_init(smem_u32(&m.sc_empty[i]), NS == 1 ? 4 : 8);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -478,90 +480,54 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   const int log2_bs = P.c.log2_bs, bs = 1 << log2_bs;
 
   if (warp == 0 || warp == 2) {
-    // ---- loads: K by one warp and V by another, each with its scales. Lane p of a tile's pages
-    // issues that page; entries and scales are fetched one and two batches of tiles ahead ----
+    // ---- loads: K by one warp and V by another (a warp takes about 75 cycles to issue a page, 8
+    // pages of 16 tokens a tile). Lane p of a tile's pages issues that page; table entries are
+    // fetched two batches of tiles ahead and looked at only when they are used ----
     const bool is_v = warp == 2;
     const CUtensorMap* map = is_v ? &v_map : &k_map;
-    const float* page_scale = is_v ? P.c.v_scale : P.c.k_scale;
     uint64_t* full = is_v ? m.v_full : m.k_full;
     uint64_t* empty = is_v ? m.v_empty : m.k_empty;
+    const int stages = is_v ? SV : SK;
     const int pages = kTile >> log2_bs;                 // of a tile, 1 to 16
     const int batch = 32 / pages < 8 ? 32 / pages : 8;  // tiles whose entries a warp reads at once
-    const int my_tile = lane / pages, my_page = lane % pages;
-    const int span = bs >> 3;                           // scale entries of a page
+    const int my_tile = lane / pages < batch ? lane / pages : -1, my_page = lane % pages;
     const uint32_t dst = base + (is_v ? L::kV : L::kK) + my_page * (uint32_t)(bs * DP);
-    int st = 0, slot = 0;
-    uint32_t ph = 1, sc_ph = 1;
+    int st = 0;
+    uint32_t ph = 1;
     bool ok = true;
     while (ok && sched.next(P, s)) {
       const int32_t* table = P.table + (long)s.r * P.max_blocks;
       const int last_page = (s.q.len + bs - 1) >> log2_bs;
-      auto entry = [&](int t0) {  // this lane's page; -1: none
+      auto entry = [&](int t0) {  // this lane's page of the batch from t0 on; -1: past the context
         const int pg = ((t0 + my_tile) << (7 - log2_bs)) + my_page;
-        int e = -1;
-        if (my_tile < batch && t0 + my_tile < s.b && pg < last_page) {
-          e = __ldg(table + pg);
-          if (e < 0 || e >= P.c.num_blocks) {
-            e = -1;
-            if (!is_v) raise_err(P.err, SD_ERR_KV_RANGE);
-          }
-        }
-        return e;
-      };
-      auto scale_of = [&](int e) {
-        return e < 0 ? -1.f : fmaxf(__ldg(page_scale + (long)e * P.c.Hkv + s.h), 0.f);
+        return my_tile >= 0 && t0 + my_tile < s.b && pg < last_page ? __ldg(table + pg)
+                                                                    : P.c.num_blocks;
       };
       int cur = entry(s.a), nxt = entry(s.a + batch);
-      float sc = scale_of(cur);
       for (int t0 = s.a; ok && t0 < s.b; t0 += batch) {
         const int far = entry(t0 + 2 * batch);
-        const float sc_nxt = scale_of(nxt);
+        // a page that there is not: beyond the tensor, where the copy fills in zeros
+        if ((unsigned)cur >= (unsigned)P.c.num_blocks) {
+          if (!is_v && my_tile >= 0 && t0 + my_tile < s.b &&
+              ((t0 + my_tile) << (7 - log2_bs)) + my_page < last_page)
+            raise_err(P.err, SD_ERR_KV_RANGE);
+          cur = P.c.num_blocks;
+        }
         for (int j = 0; j < batch && t0 + j < s.b; ++j) {
           const uint32_t bar = smem_u32(full + st);
           ok = mbar_wait_warp(smem_u32(empty + st), ph, gave_up);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
           __syncwarp();
-          const bool mine = my_tile == j && my_tile < batch;
-          // a page that there is not: beyond the tensor, where the copy fills in zeros
-          if (mine)
-            tma_load_4d(dst + st * L::kTileBytes, map, 0, s.h, 0,
-                        cur < 0 ? P.c.num_blocks : cur, bar);
-          ok = mbar_wait_warp(smem_u32(&m.sc_empty[slot]), sc_ph, gave_up);
-          if (!ok) break;
-          if (is_v) {
-            const bool z = sc == 0.f;
-            const uint32_t zero = __reduce_or_sync(
-                0xffffffffu, mine && z ? ((1u << span) - 1) << (my_page * span) : 0u);
-            if (mine) {
-              const float v = fmaxf(sc, kMinScale);
-              const float2 f = sc < 0.f ? make_float2(-INFINITY, 1.f)
-                               : z      ? make_float2(kZeroLog2, kZeroInv)
-                                        : make_float2(__log2f(v), __fdividef(1.f, v));
-              for (int i = 0; i < span; ++i) {
-                scales[slot * 16 + my_page * span + i].y = f.x;
-                scales[slot * 16 + my_page * span + i].z = f.y;
-              }
-            }
-            if (lane == 0) m.sc_zero[slot] = (int)zero;
-          } else if (mine) {
-            for (int i = 0; i < span; ++i)
-              scales[slot * 16 + my_page * span + i].x = fmaxf(sc, 0.f);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&m.sc_full[slot]));
-          if (++st == S) {
+          if (my_tile == j)
+            tma_load_4d(dst + st * L::kTileBytes, map, 0, s.h, 0, cur, bar);
+          if (++st == stages) {
             st = 0;
             ph ^= 1;
-          }
-          if (++slot == kScaleSlots) {
-            slot = 0;
-            sc_ph ^= 1;
           }
         }
         cur = nxt;
         nxt = far;
-        sc = sc_nxt;
       }
     }
   } else if (warp == 1) {
@@ -571,8 +537,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     const bool lead = elect_one();
     const uint32_t q_lo = desc_lo<DP>(base + L::kQ), k_lo = desc_lo<DP>(base + L::kK),
                    v_lo = desc_lo<DP>(base + L::kV);
-    int st = 0, nq[2] = {0, 0};
-    uint32_t ph = 0;       // parity of the ring's current round
+    int kst = 0, vst = 0, nq[2] = {0, 0};  // the next unit's first tile in the rings
+    uint32_t kph = 0, vph = 0;             // and the parity of its round
     uint32_t pp[2] = {0, 0}, sp[2] = {0, 0};
     bool ok = true;
     auto qk = [&](int k_st, int x, int qi) {  // S[x] = Q[qi] K
@@ -605,63 +571,111 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         const int qb = nq[0] & 1;  // units alternate between two buffers
         if (!wait(&m.q_full[qb], (nq[0] >> 1) & 1)) break;
         ++nq[0];
-        // QK runs two tiles ahead of PV: (kst, kph) is its place in the ring
-        int kst = st;
-        uint32_t kph = ph;
-        auto do_qk = [&](int j, int x) {
-          if (!wait(&m.k_full[kst], kph)) return;
-          tc_fence_after();
-          if (lead) {
-            qk(kst, x, qb);
-            mma_commit(smem_u32(&m.s_full[x]));
-            mma_commit(smem_u32(&m.k_empty[kst]));
-            if (j == T - 1) mma_commit(smem_u32(&m.q_empty[qb]));
+        // Each stream has its own place in the rings. Whatever is ready is issued: a stream's PV
+        // once its P is there, its next QK once S is free (read, or with P in its place: used).
+        int kj[2] = {0, 1}, vj[2] = {0, 1}, ks[2], vs[2];
+        uint32_t kp[2], vp[2];
+        bool s_free[2] = {true, true};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ks[x] = kst + x;
+          kp[x] = kph;
+          if (ks[x] >= SK) {
+            ks[x] -= SK;
+            kp[x] ^= 1;
           }
-          if (++kst == S) {
-            kst = 0;
-            kph ^= 1;
+          vs[x] = vst + x;
+          vp[x] = vph;
+          if (vs[x] >= SV) {
+            vs[x] -= SV;
+            vp[x] ^= 1;
           }
-        };
-        do_qk(0, 0);
-        if (T > 1) do_qk(1, 1);
-        auto do_pv = [&](int j, int x) {
-          wait(&m.p_full[x], pp[x]);
-          if (!wait(&m.v_full[st], ph)) return;
-          pp[x] ^= 1;
-          tc_fence_after();
-          if (lead) {
-            pv(st, x, j >= 2);
-            mma_commit(smem_u32(&m.v_empty[st]));
-            mma_commit(smem_u32(&m.o_done[x]));
-          }
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
-        };
-        for (int j0 = 0; ok && j0 <= T; j0 += 2) {
+        }
+        long long idle = 0;  // the clock when nothing was ready first
+        while (vj[0] < T || vj[1] < T) {
+          bool did = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int j = j0 + x;
-            if (!ok || j > T) break;
-            if (L::kOwnP) {
-              // the next S of this stream as soon as the last one is read, then the other
-              // stream's PV
-              if (j < T) wait(&m.s_read[x], sp[x]);
-              sp[x] ^= j < T ? 1 : 0;
-              if (j + 2 < T) do_qk(j + 2, x);
-              if (j > 0) do_pv(j - 1, x ^ 1);
-            } else if (j < T) {
-              do_pv(j, x);
-              if (j + 2 < T) do_qk(j + 2, x);
+            if (vj[x] < T && mbar_test_warp(smem_u32(&m.p_full[x]), pp[x])) {
+              if (!wait(&m.v_full[vs[x]], vp[x])) break;
+              pp[x] ^= 1;
+              tc_fence_after();
+              if (lead) {
+                pv(vs[x], x, vj[x] >= 2);
+                mma_commit(smem_u32(&m.o_done[x]));
+                mma_commit(smem_u32(&m.v_empty[vs[x]]));
+              }
+              if (!L::kOwnP) s_free[x] = true;
+              vj[x] += 2;
+              vs[x] += 2;
+              if (vs[x] >= SV) {
+                vs[x] -= SV;
+                vp[x] ^= 1;
+              }
+              did = true;
+            }
+            if (L::kOwnP && !s_free[x] && mbar_test_warp(smem_u32(&m.s_read[x]), sp[x])) {
+              sp[x] ^= 1;
+              s_free[x] = true;
+            }
+            if (s_free[x] && kj[x] < T && mbar_test_warp(smem_u32(&m.k_full[ks[x]]), kp[x])) {
+              tc_fence_after();
+              if (lead) {
+                qk(ks[x], x, qb);
+                mma_commit(smem_u32(&m.s_full[x]));
+                mma_commit(smem_u32(&m.k_empty[ks[x]]));
+                if (kj[x] + 2 >= T && kj[x ^ 1] >= T) mma_commit(smem_u32(&m.q_empty[qb]));
+              }
+              s_free[x] = false;
+              kj[x] += 2;
+              ks[x] += 2;
+              if (ks[x] >= SK) {
+                ks[x] -= SK;
+                kp[x] ^= 1;
+              }
+              did = true;
             }
           }
+          if (!ok) break;
+          if (did) {
+            idle = 0;
+          } else {
+            const long long now = clock64();
+            if (idle == 0) idle = now;
+            // (lane 0's clock decides for the warp)
+            if (__shfl_sync(0xffffffffu, (int)(now - idle > kWaitClocks || *gave_up), 0)) {
+              *gave_up = 1;
+              ok = false;
+              break;
+            }
+          }
+        }
+        if (L::kOwnP) {
+          // the last S of each stream has been read, too (its P was formed from it)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (ok && x < T && !s_free[x]) {
+              wait(&m.s_read[x], sp[x]);
+              sp[x] ^= 1;
+            }
+        }
+        kst += T % SK;
+        kph ^= (T / SK) & 1;
+        if (kst >= SK) {
+          kst -= SK;
+          kph ^= 1;
+        }
+        vst += T % SV;
+        vph ^= (T / SV) & 1;
+        if (vst >= SV) {
+          vst -= SV;
+          vph ^= 1;
         }
       } else {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if ((x ? s.cnt1 : s.cnt0) > 0) wait(&m.q_full[x], nq[x]++ & 1);
-        auto do_qk = [&](int j, int x, int kst, uint32_t kph) {
+        auto do_qk = [&](int j, int x) {
           if (!wait(&m.k_full[kst], kph)) return;
           tc_fence_after();
           if (lead) {
@@ -670,52 +684,98 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             if (j == (x ? s.cnt1 : s.cnt0) - 1) mma_commit(smem_u32(&m.q_empty[x]));
           }
         };
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if ((x ? s.cnt1 : s.cnt0) > 0) do_qk(0, x, st, ph);
-        if (ok && lead) mma_commit(smem_u32(&m.k_empty[st]));
-        auto do_pv = [&](int j, int x, int v_st, uint32_t v_ph, bool last) {
-          wait(&m.p_full[x], pp[x]);
-          if (!wait(&m.v_full[v_st], v_ph)) return;
-          pp[x] ^= 1;
-          tc_fence_after();
-          if (lead) {
-            pv(v_st, x, j > 0);
-            if (last) mma_commit(smem_u32(&m.v_empty[v_st]));
-            mma_commit(smem_u32(&m.o_done[x]));
+        auto k_done = [&] {
+          if (ok && lead) mma_commit(smem_u32(&m.k_empty[kst]));
+          if (++kst == SK) {
+            kst = 0;
+            kph ^= 1;
           }
         };
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if ((x ? s.cnt1 : s.cnt0) > 0) do_qk(0, x);
+        k_done();
         for (int j = 0; ok && j < T; ++j) {
-          const int nst = st + 1 == S ? 0 : st + 1;
-          const uint32_t nph = ph ^ (nst == 0 ? 1u : 0u);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (j >= (x ? s.cnt1 : s.cnt0)) continue;
-            do_pv(j, x, st, ph, x == 1 || j >= s.cnt1);
-            if (j + 1 < (x ? s.cnt1 : s.cnt0)) do_qk(j + 1, x, nst, nph);
+            const int cnt = x ? s.cnt1 : s.cnt0;
+            if (j >= cnt) continue;
+            wait(&m.p_full[x], pp[x]);
+            if (!wait(&m.v_full[vst], vph)) break;
+            pp[x] ^= 1;
+            tc_fence_after();
+            if (lead) {
+              pv(vst, x, j > 0);
+              if (x == 1 || j >= s.cnt1) mma_commit(smem_u32(&m.v_empty[vst]));
+              mma_commit(smem_u32(&m.o_done[x]));
+            }
+            if (j + 1 < cnt) do_qk(j + 1, x);
           }
-          if (ok && lead && j + 1 < T) mma_commit(smem_u32(&m.k_empty[nst]));
-          st = nst;
-          ph = nph;
+          if (j + 1 < T) k_done();
+          if (++vst == SV) {
+            vst = 0;
+            vph ^= 1;
+          }
         }
       }
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ---- Q of the next unit, while this one is computed ----
-    if (NS == 1) {
-      int nq = 0;
-      bool ok = true;
-      while (ok && sched.next(P, s)) {
+    // ---- Q of the next unit while this one is computed, and the scales: 16 entries a tile, one
+    // for 8 tokens, two tiles at a time; table entries two passes and scales one pass ahead ----
+    const int e = lane & 15, half = lane >> 4;
+    int nq = 0, slot = 0;
+    uint32_t sc_ph = 1;
+    bool ok = true;
+    while (ok && sched.next(P, s)) {
+      const int32_t* table = P.table + (long)s.r * P.max_blocks;
+      auto entry = [&](int t0) {
+        const long tok = (long)(t0 + half) * kTile + e * 8;
+        return t0 + half < s.b && tok < s.q.len ? __ldg(table + (tok >> log2_bs)) : -1;
+      };
+      auto scales_of = [&](int page) {  // (K's, V's; -1: no page)
+        if ((unsigned)page >= (unsigned)P.c.num_blocks) return make_float2(0.f, -1.f);
+        const long at = (long)page * P.c.Hkv + s.h;
+        return make_float2(__ldg(P.c.k_scale + at), __ldg(P.c.v_scale + at));
+      };
+      int nxt = entry(s.a + 2);
+      float2 sc = scales_of(entry(s.a));
+      if (NS == 1) {
         const int qb = nq & 1;
         ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((nq >> 1) & 1) ^ 1, gave_up);
         if (!ok) break;
         load_q<DP, R, 32>(P, s, s.row0, s.rows, smem + L::kQ + qb * 2 * L::kQBytes,
-                             m.row_scale + qb * kTile, lane);
+                          m.row_scale + qb * kTile, lane);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&m.q_full[qb]));
         ++nq;
+      }
+      for (int t0 = s.a; ok && t0 < s.b; t0 += 2) {
+        const int far = entry(t0 + 4);
+        const float2 sc_nxt = scales_of(nxt);
+        const bool none = sc.y == -1.f, zero = !none && !(sc.y > 0.f) && sc.y == sc.y;
+        const float v = fmaxf(sc.y, kMinScale);  // (a NaN stays out of here)
+        const float4 f = make_float4(
+            sc.x, none ? -INFINITY : zero ? kZeroLog2 : sc.y != sc.y ? sc.y : __log2f(v),
+            none ? 1.f : zero ? kZeroInv : __fdividef(1.f, v), 0.f);
+        const uint32_t zeros = __ballot_sync(0xffffffffu, zero);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (t0 + k >= s.b) break;
+          ok = mbar_wait_warp(smem_u32(&m.sc_empty[slot]), sc_ph, gave_up);
+          if (!ok) break;
+          if (half == k) scales[slot * 16 + e] = f;
+          if (lane == 0) m.sc_zero[slot] = (int)(k ? zeros >> 16 : zeros & 0xffffu);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&m.sc_full[slot]));
+          if (++slot == kScaleSlots) {
+            slot = 0;
+            sc_ph ^= 1;
+          }
+        }
+        nxt = far;
+        sc = sc_nxt;
       }
     }
   }
@@ -785,8 +845,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         if (masked || zero) {
           // V's rows that no row of this call sees become 0, and NaN among the others too (they
           // are noted, for the rows that see them): 0 times NaN is no 0
-          const int st = (it + j) % S;
-          ok = mbar_wait_warp(smem_u32(&m.v_full[st]), ((it + j) / S) & 1, gave_up);
+          const int st = (it + j) % SV;
+          ok = mbar_wait_warp(smem_u32(&m.v_full[st]), ((it + j) / SV) & 1, gave_up);
           if (!ok) break;
           unsigned char* vr = smem + L::kV + st * L::kTileBytes + wt * DP;
           const bool gone = t0 + wt >= s.q.len || ((zero >> (wt >> 3)) & 1);
@@ -959,7 +1019,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       float* slot = slots + (2L * blockIdx.x + (s.a > 0 ? 0 : 1)) * L::kSlotFloats;
       const int* nan_first = m.nan_first[buf];
       if (R > 1) {
-        // 2R partial rows: every warp leaves 32 columns of its own, weighed by their common
+        // 2R partial rows: every warp leaves 16 columns of its own, weighed by their common
         // maximum, then the threads add them up in the warps' order
         float* join = reinterpret_cast<float*>(smem + L::kJoin);
         constexpr int parts = 2 * R;  // a stream without a tile counts with weight 0
@@ -985,24 +1045,25 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           }
         }
 #pragma unroll 1
-        for (int c = 0; c < DP; c += 32) {
+        for (int c = 0; c < DP; c += 16) {
           if (ok && warp_live) {
-            uint32_t u[32];
-            tmem_ld32(tO + c, u);
+            uint32_t u[16];
+            tmem_ld16(tO + c, u);
             tmem_wait_ld();
-            float* mine = join + ((warp - 4) * 32 + lane) * 33;
+            float* mine = join + ((warp - 4) * 32 + lane) * 17;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mine[i] = used ? __uint_as_float(u[i]) * wm : 0.f;
+            for (int i = 0; i < 16; ++i) mine[i] = used ? __uint_as_float(u[i]) * wm : 0.f;
           }
           named_bar(1, 256);
-          // 4 columns a thread, 32 rows a pass
-          const int cc = ((tid - 128) & 7) * 4;
-          for (int r = (tid - 128) >> 3; ok && r < s.rows; r += 32) {
+          // 4 columns a thread, 64 rows a pass
+          const int cc = ((tid - 128) & 3) * 4;
+          const int r = (tid - 128) >> 2;
+          if (ok && r < s.rows) {
             float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < parts; ++i) {
               const int w = (i / R) * 4 + (i % R) * NC + (r >> 5);
-              const float* from = join + (w * 32 + (r & 31)) * 33 + cc;
+              const float* from = join + (w * 32 + (r & 31)) * 17 + cc;
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[k] += from[k];
             }
@@ -1026,7 +1087,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                              *reinterpret_cast<const uint32_t*>(&b));
             }
           }
-          if (c + 32 < DP) named_bar(1, 256);
+          if (c + 16 < DP) named_bar(1, 256);
         }
       } else {
         float wa = 1.f, wb = 0.f, Mt = M, Lt = Lsum;

@@ -34,6 +34,19 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase of this parity has ended, without waiting; one answer for the whole warp.
+__device__ __forceinline__ bool mbar_test_warp(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
 // Waits for the phase of this parity to end, for a second of the GPU clock at most or until
 // another thread of the CTA has given up (*gave_up). False: the wait did not end.
 constexpr long long kWaitClocks = 2000000000LL;
