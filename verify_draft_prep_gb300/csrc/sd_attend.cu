@@ -72,19 +72,18 @@ struct JoinDesc {
 template <int DP, int NS, int R>
 struct AttLayout {
   static constexpr int kRows = NS * kTile / R;      // of a unit
-  // Tensor memory, 512 columns: S of both streams, O of both; with heads of 64 there is room for P
-  // beside S, so that the next S is formed while this one's P is, which pays where a thread takes
-  // S into registers at once (R > 1); else P takes S's place.
-  static constexpr bool kOwnP = DP == 64 && R > 1;
-  static constexpr int kTmS = 0, kTmO = 256, kTmP = kOwnP ? 256 + 2 * DP : 0;
-  static constexpr int kTmPStep = kOwnP ? 64 : 128;
+  // Tensor memory, 512 columns: S of both streams (P takes its place), O of both, and with heads of
+  // 64 also Q, a copy for each stream: a product that takes Q from there reads half as much shared
+  // memory, which the softmax, the barriers and the loads need, too.
+  static constexpr bool kQTm = DP == 64;
+  static constexpr int kTmO = 256, kTmQ = 256 + 2 * DP;
   static constexpr int kQBytes = kTile * DP;        // one term of one Q tile
   static constexpr int kTileBytes = kTile * DP;     // K or V of one tile
   // Tiles in flight. V's stay longer (until P is formed and used) than K's.
-  static constexpr int kKStages = DP == 64 ? 6 : (NS == 1 ? 3 : 4);
-  static constexpr int kVStages = DP == 64 ? 10 : (NS == 1 ? 5 : 4);
+  static constexpr int kKStages = DP == 64 ? 8 : (NS == 1 ? 3 : 4);
+  static constexpr int kVStages = DP == 64 ? 12 : (NS == 1 ? 5 : 4);
   static constexpr int kQ = 0;                      // two buffers (NS = 1), or two tiles
-  static constexpr int kK = kQ + 2 * 2 * kQBytes;
+  static constexpr int kK = kQ + (kQTm ? 0 : 2 * 2 * kQBytes);
   static constexpr int kV = kK + kKStages * kTileBytes;
   static constexpr int kScales = kV + kVStages * kTileBytes;
   static constexpr int kJoin = kScales + kScaleSlots * 16 * 16;  // [8 warps][32 rows][17] floats
@@ -93,8 +92,8 @@ struct AttLayout {
 };
 
 struct AttMisc {
-  uint64_t k_full[10], k_empty[10], v_full[10], v_empty[10];
-  uint64_t s_full[2], s_read[2], p_full[2], o_done[2], q_full[2], q_empty[2];
+  uint64_t k_full[12], k_empty[12], v_full[12], v_empty[12];
+  uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2];
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
   int sc_zero[kScaleSlots];   // bit e: entry e's V scale is zero
   float row_scale[2 * kTile];
@@ -214,6 +213,30 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// 2^up that brings a row's largest magnitude (a bf16 pattern) to [224, 448]; a row with an infinity
+// or a NaN becomes NaN, as its softmax is.
+__device__ __forceinline__ float q_factor(uint32_t mg, int& up) {
+  up = 135 - (int)(mg >> 7) - ((mg & 0x7fu) > 0x60u ? 1 : 0);
+  up = mg == 0 ? 0 : min(up, 64);
+  return mg >= 0x7f80u ? nanf("") : __uint_as_float((uint32_t)(up + 127) << 23);
+}
+
+// 8 bf16 times mul as two e4m3 terms: the leading 4 significant bits, and the rest.
+__device__ __forceinline__ void split8(const uint4& v, float mul, uint32_t* hi, uint32_t* lo) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float f[4], h[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f[u] = (u & 1 ? bf16_hi(w[2 * k + (u >> 1)]) : bf16_lo(w[2 * k + (u >> 1)])) * mul;
+      h[u] = __uint_as_float(__float_as_uint(f[u]) & 0xfff00000u);
+    }
+    hi[k] = f32_to_e4m3x4(h[0], h[1], h[2], h[3]);
+    lo[k] = f32_to_e4m3x4(f[0] - h[0], f[1] - h[1], f[2] - h[2], f[3] - h[3]);
+  }
+}
+
 // Q rows [first, first + count) of a unit, one 8-value part a thread, as two e4m3 terms into the
 // swizzled operand at q (and q + kQBytes), R copies of them, with the rows' scales. `rows` valid.
 template <int DP, int R, int THREADS>
@@ -245,31 +268,15 @@ __device__ __forceinline__ void load_q(const AttendParams& P, const Segment& s, 
     for (int i = 0; i + 1 < kAhead; ++i) q4[i] = q4[i + 1];
     q4[kAhead - 1] = fetch(r + kAhead * kPerPass);
     {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t mg = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mg = __vmaxu2(mg, w[k] & 0x7fff7fffu);
+      uint32_t mg = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
       mg = max(mg & 0xffffu, mg >> 16);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) mg = max(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-      // 2^up brings the largest to [224, 448]; a row with an infinity or a NaN becomes NaN, as its
-      // softmax is
-      int up = 135 - (int)(mg >> 7) - ((mg & 0x7fu) > 0x60u ? 1 : 0);
-      up = mg == 0 ? 0 : min(up, 64);
-      const bool bad = mg >= 0x7f80u;
-      const float mul = bad ? nanf("") : __uint_as_float((uint32_t)(up + 127) << 23);
+      int up;
+      const float mul = q_factor(mg, up);
       uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float f[4], h[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          f[u] = (u & 1 ? bf16_hi(w[2 * k + (u >> 1)]) : bf16_lo(w[2 * k + (u >> 1)])) * mul;
-          h[u] = __uint_as_float(__float_as_uint(f[u]) & 0xfff00000u);
-        }
-        hi[k] = f32_to_e4m3x4(h[0], h[1], h[2], h[3]);
-        lo[k] = f32_to_e4m3x4(f[0] - h[0], f[1] - h[1], f[2] - h[2], f[3] - h[3]);
-      }
+      split8(v, mul, hi, lo);
       // 16-byte chunks of a row are swizzled by the row within its 8-row (or 4-pair) atom; the
       // copies lie whole atoms apart
       const int sw = DP == 128 ? r & 7 : (r >> 1) & 3;
@@ -283,6 +290,37 @@ __device__ __forceinline__ void load_q(const AttendParams& P, const Segment& s, 
       if (c8 == 0) row_scale[r] = P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
     }
   }
+}
+
+// One row of Q (up to 64 values), by the thread of its lane, as two e4m3 terms into tensor memory:
+// 16 columns each, 4 values a column. Returns the row's scale.
+__device__ __forceinline__ float q_to_tmem(const AttendParams& P, const Segment& s, int row,
+                                           bool live, uint32_t dst) {
+  uint4 v[8];
+  const int2 th = token_head(P, row);
+  const uint16_t* q = P.q + (long)(s.q.tok0 + th.x) * P.ld_q + (long)(s.h * P.G + th.y) * P.hs_q;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = live && i * 8 < P.c.D ? __ldg(reinterpret_cast<const uint4*>(q) + i)
+                                 : make_uint4(0, 0, 0, 0);
+  uint32_t mg = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    mg = __vmaxu2(mg, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                               __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+  mg = max(mg & 0xffffu, mg >> 16);
+  int up;
+  const float mul = q_factor(mg, up);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t o[16];  // 8 words of the first term, 8 of the second
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split8(v[half * 4 + i], mul, o + 2 * i, o + 8 + 2 * i);
+    tmem_st8(dst + half * 8, o);
+    tmem_st8(dst + 16 + half * 8, o + 8);
+  }
+  tmem_wait_st();
+  return P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -307,13 +345,6 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// This warp has its columns of S in registers.
-__device__ __forceinline__ void stream_read(uint64_t& bar, int lane) {
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&bar));
 }
 
 // 32 bytes: a whole sector, so that rows far apart are written without partial ones.
@@ -386,7 +417,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
 
   // ---- setup: barriers, tensor memory, this CTA's share of the line of tiles ----
   if (tid == 0) {
-    for (int i = 0; i < 10; ++i) {
+    for (int i = 0; i < 12; ++i) {
       mbar_init(smem_u32(&m.k_full[i]), 1);
       mbar_init(smem_u32(&m.k_empty[i]), 1);
       mbar_init(smem_u32(&m.v_full[i]), 1);
@@ -395,9 +426,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&m.s_full[i]), 1);
       mbar_init(smem_u32(&m.p_full[i]), 4);
-      mbar_init(smem_u32(&m.s_read[i]), 4);
       mbar_init(smem_u32(&m.o_done[i]), 1);
-      mbar_init(smem_u32(&m.q_full[i]), NS == 1 ? 1 : 4);
+      mbar_init(smem_u32(&m.q_full[i]), NS == 1 && !L::kQTm ? 1 : 4);
       mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
@@ -539,9 +569,19 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                    v_lo = desc_lo<DP>(base + L::kV);
     int kst = 0, vst = 0, nq[2] = {0, 0};  // the next unit's first tile in the rings
     uint32_t kph = 0, vph = 0;             // and the parity of its round
-    uint32_t pp[2] = {0, 0}, sp[2] = {0, 0};
+    uint32_t pp[2] = {0, 0};
     bool ok = true;
     auto qk = [&](int k_st, int x, int qi) {  // S[x] = Q[qi] K
+      if (L::kQTm) {
+        const uint32_t d = tmem + x * 128, a = tmem + L::kTmQ + x * 32,
+                       k = k_lo + k_st * (L::kTileBytes / 16);
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int kk = 0; kk < DP / 32; ++kk)
+            mma_ts<hi, qk_idesc>(d, a + term * 16 + kk * 8, k + kk * 2, term + kk > 0);
+        return;
+      }
       const uint32_t d = tmem + x * 128, a = q_lo + qi * (2 * L::kQBytes / 16),
                      k = k_lo + k_st * (L::kTileBytes / 16);
 #pragma unroll
@@ -552,7 +592,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                                term + kk > 0);
     };
     auto pv = [&](int v_st, int x, bool add) {  // O[x] += P V
-      const uint32_t d = tmem + L::kTmO + x * DP, a = tmem + L::kTmP + x * L::kTmPStep,
+      const uint32_t d = tmem + L::kTmO + x * DP, a = tmem + x * 128,
                      v = v_lo + v_st * (L::kTileBytes / 16);
 #pragma unroll
       for (int kk = 0; kk < kTile / 32; ++kk)
@@ -569,10 +609,13 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       const int T = s.b - s.a;
       if (NS == 1) {
         const int qb = nq[0] & 1;  // units alternate between two buffers
-        if (!wait(&m.q_full[qb], (nq[0] >> 1) & 1)) break;
-        ++nq[0];
+        bool q_there[2] = {!L::kQTm, !L::kQTm};
+        if (!L::kQTm) {
+          if (!wait(&m.q_full[qb], (nq[0] >> 1) & 1)) break;
+          ++nq[0];
+        }
         // Each stream has its own place in the rings. Whatever is ready is issued: a stream's PV
-        // once its P is there, its next QK once S is free (read, or with P in its place: used).
+        // once its P is there, its next QK once P, in the place of S, is used.
         int kj[2] = {0, 1}, vj[2] = {0, 1}, ks[2], vs[2];
         uint32_t kp[2], vp[2];
         bool s_free[2] = {true, true};
@@ -605,7 +648,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                 mma_commit(smem_u32(&m.o_done[x]));
                 mma_commit(smem_u32(&m.v_empty[vs[x]]));
               }
-              if (!L::kOwnP) s_free[x] = true;
+              s_free[x] = true;
               vj[x] += 2;
               vs[x] += 2;
               if (vs[x] >= SV) {
@@ -614,17 +657,20 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
               }
               did = true;
             }
-            if (L::kOwnP && !s_free[x] && mbar_test_warp(smem_u32(&m.s_read[x]), sp[x])) {
-              sp[x] ^= 1;
-              s_free[x] = true;
+            if (L::kQTm && !q_there[x] && kj[x] < T &&
+                mbar_test_warp(smem_u32(&m.q_full[x]), nq[x] & 1)) {
+              ++nq[x];
+              q_there[x] = true;
             }
-            if (s_free[x] && kj[x] < T && mbar_test_warp(smem_u32(&m.k_full[ks[x]]), kp[x])) {
+            if (q_there[x] && s_free[x] && kj[x] < T &&
+                mbar_test_warp(smem_u32(&m.k_full[ks[x]]), kp[x])) {
               tc_fence_after();
               if (lead) {
                 qk(ks[x], x, qb);
                 mma_commit(smem_u32(&m.s_full[x]));
                 mma_commit(smem_u32(&m.k_empty[ks[x]]));
-                if (kj[x] + 2 >= T && kj[x ^ 1] >= T) mma_commit(smem_u32(&m.q_empty[qb]));
+                if (!L::kQTm && kj[x] + 2 >= T && kj[x ^ 1] >= T)
+                  mma_commit(smem_u32(&m.q_empty[qb]));
               }
               s_free[x] = false;
               kj[x] += 2;
@@ -650,15 +696,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             }
           }
         }
-        if (L::kOwnP) {
-          // the last S of each stream has been read, too (its P was formed from it)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (ok && x < T && !s_free[x]) {
-              wait(&m.s_read[x], sp[x]);
-              sp[x] ^= 1;
-            }
-        }
         kst += T % SK;
         kph ^= (T / SK) & 1;
         if (kst >= SK) {
@@ -681,7 +718,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           if (lead) {
             qk(kst, x, x);
             mma_commit(smem_u32(&m.s_full[x]));
-            if (j == (x ? s.cnt1 : s.cnt0) - 1) mma_commit(smem_u32(&m.q_empty[x]));
+            if (!L::kQTm && j == (x ? s.cnt1 : s.cnt0) - 1)
+              mma_commit(smem_u32(&m.q_empty[x]));
           }
         };
         auto k_done = [&] {
@@ -740,7 +778,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       };
       int nxt = entry(s.a + 2);
       float2 sc = scales_of(entry(s.a));
-      if (NS == 1) {
+      if (NS == 1 && !L::kQTm) {
         const int qb = nq & 1;
         ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((nq >> 1) & 1) ^ 1, gave_up);
         if (!ok) break;
@@ -788,7 +826,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     const int wr = (quarter % NC) * 32 + lane;                // row of this thread in its tile
     const uint32_t lanes = (uint32_t)quarter << 21;
     const uint32_t tS = tmem + x * 128 + lanes;
-    const uint32_t tP = tmem + L::kTmP + x * L::kTmPStep + lanes;
     const uint32_t tO0 = tmem + L::kTmO + lanes, tO = tO0 + x * DP;  // the first's, this stream's
     int it = 0, nq = 0, unit = 0;
     int done = 0, done_other = 0;  // tiles of this stream and of the other one so far
@@ -805,8 +842,18 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       const int row_base = NS == 1 ? 0 : x * kTile;       // of this stream in the unit
       const int my_rows = NS == 1 ? s.rows : min(kTile, s.rows - row_base);
       float rs = 0.f;
-      // 1. Q (with two Q tiles, loaded here), and this row's scale
-      if (NS == 1) {
+      const int row = s.row0 + row_base + wr;
+      const bool warp_live = (quarter % NC) * 32 < my_rows;
+      const bool live = wr < my_rows;
+      // 1. Q (but for one Q tile in shared memory, loaded here), and this row's scale
+      if (L::kQTm) {
+        if (cnt_x > 0) {  // (every product of this stream's last unit is done)
+          if (ok && warp_live) rs = q_to_tmem(P, s, row, live, tmem + L::kTmQ + x * 32 + lanes);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&m.q_full[x]));
+        }
+      } else if (NS == 1) {
         ok = ok && mbar_wait_warp(smem_u32(&m.q_full[unit & 1]), (unit >> 1) & 1, gave_up);
         rs = m.row_scale[(unit & 1) * kTile + wr];
         __syncwarp();
@@ -816,16 +863,13 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         ++nq;
         if (ok)
           load_q<DP, 1, 128>(P, s, s.row0 + row_base, my_rows,
-                                smem + L::kQ + x * 2 * L::kQBytes, m.row_scale + row_base, wt);
+                             smem + L::kQ + x * 2 * L::kQBytes, m.row_scale + row_base, wt);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&m.q_full[x]));
         named_bar(2 + x, 128);  // every row's scale is there
         rs = m.row_scale[row_base + wr];
       }
-      const int row = s.row0 + row_base + wr;
-      const bool warp_live = (quarter % NC) * 32 < my_rows;
-      const bool live = wr < my_rows;
       const int lim = seen_by(P, s.q, min(row, s.row0 + s.rows - 1));
       const int min_lim = seen_by(P, s.q, s.row0 + row_base);
       float M = -INFINITY, Lsum = 0.f;
@@ -906,7 +950,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           if (NC == 2) tmem_ld32(tC + 32, w);
           tmem_wait_ld();
           if (NC <= 2) {
-            if (L::kOwnP) stream_read(m.s_read[x], lane);
             mx = row_max(v, sc, rs);
             if (NC == 2) mx = fmaxf(mx, row_max(w, sc + 4, rs));
           } else {
@@ -946,18 +989,14 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             }
             M = Mn;
           }
-          if (L::kOwnP && j >= (NS == 1 ? 2 : 1)) {  // the last P has been used
-            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
-            if (!ok) break;
-          }
           const float shift = kShift - (M == -INFINITY ? 0.f : M);
           uint32_t o[16];
           if (NC <= 2) {
             Lsum += weights(v, sc, rs, shift, o);
-            tmem_st16(tP + copy * NC * 16, o);
+            tmem_st16(tS + copy * NC * 16, o);
             if (NC == 2) {
               Lsum += weights(w, sc + 4, rs, shift, o);
-              tmem_st16(tP + (copy * NC + 1) * 16, o);
+              tmem_st16(tS + (copy * NC + 1) * 16, o);
             }
           } else {
 #pragma unroll 1
@@ -965,27 +1004,20 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
               tmem_ld32(tC + (c + 1) * 32, w);
               Lsum += weights(v, sc + c * 4, rs, shift, o);
               tmem_wait_ld();
-              tmem_st16(tP + c * 16, o);
+              tmem_st16(tS + c * 16, o);
               if (c + 2 < NC) tmem_ld32(tC + (c + 2) * 32, v);
               Lsum += weights(w, sc + c * 4 + 4, rs, shift, o);
               tmem_wait_ld();
-              tmem_st16(tP + (c + 1) * 16, o);
+              tmem_st16(tS + (c + 1) * 16, o);
             }
           }
           if (R > 1) {  // the other copies' columns count as zero here
             const uint32_t none[16] = {};
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (c / NC != copy) tmem_st16(tP + c * 16, none);
+              if (c / NC != copy) tmem_st16(tS + c * 16, none);
           }
           tmem_wait_st();
-        } else if (L::kOwnP) {
-          // a warp without rows keeps pace with the others: its arrivals belong to this tile
-          stream_read(m.s_read[x], lane);
-          if (j >= (NS == 1 ? 2 : 1)) {
-            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
-            if (!ok) break;
-          }
         }
         tc_fence_before();
         __syncwarp();
