@@ -157,7 +157,7 @@ struct Segment {
 
 // Every unit takes kUnitCost places on the line before its tiles, for what it costs beside them (its
 // queries, its result), so that CTAs with many short units get fewer tiles.
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 8;
 
 template <int NS, int ROWS>
 struct Schedule {
@@ -320,6 +320,37 @@ __device__ __forceinline__ float q_to_tmem(const AttendParams& P, const Segment&
     tmem_st8(dst + 16 + half * 8, o + 8);
   }
   tmem_wait_st();
+  return P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
+// One row of Q (up to 128 values) by a thread of its own, into the swizzled operand in shared memory
+// (lane: the row there). Returns the row's scale.
+__device__ __forceinline__ float q_to_smem(const AttendParams& P, const Segment& s, int row,
+                                           bool live, int lane, unsigned char* q_smem) {
+  uint4 v[16];
+  const int2 th = token_head(P, row);
+  const uint16_t* q = P.q + (long)(s.q.tok0 + th.x) * P.ld_q + (long)(s.h * P.G + th.y) * P.hs_q;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    v[i] = live && i * 8 < P.c.D ? __ldg(reinterpret_cast<const uint4*>(q) + i)
+                                 : make_uint4(0, 0, 0, 0);
+  uint32_t mg = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    mg = __vmaxu2(mg, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                               __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+  mg = max(mg & 0xffffu, mg >> 16);
+  int up;
+  const float mul = q_factor(mg, up);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t hi[4], lo[4];
+    split8(v[2 * i], mul, hi, lo);
+    split8(v[2 * i + 1], mul, hi + 2, lo + 2);
+    unsigned char* at = q_smem + lane * 128 + ((i ^ (lane & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + kTile * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
   return P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
 }
 
@@ -861,14 +892,11 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       } else if (cnt_x > 0) {
         ok = ok && mbar_wait_warp(smem_u32(&m.q_empty[x]), (nq & 1) ^ 1, gave_up);
         ++nq;
-        if (ok)
-          load_q<DP, 1, 128>(P, s, s.row0 + row_base, my_rows,
-                             smem + L::kQ + x * 2 * L::kQBytes, m.row_scale + row_base, wt);
+        if (ok && warp_live)
+          rs = q_to_smem(P, s, row, live, wt, smem + L::kQ + x * 2 * L::kQBytes);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&m.q_full[x]));
-        named_bar(2 + x, 128);  // every row's scale is there
-        rs = m.row_scale[row_base + wr];
       }
       const int lim = seen_by(P, s.q, min(row, s.row0 + s.rows - 1));
       const int min_lim = seen_by(P, s.q, s.row0 + row_base);
