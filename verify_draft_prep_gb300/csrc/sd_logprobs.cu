@@ -16,7 +16,7 @@
 
 namespace sdk {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpThreads = 128, kLpWarps = kLpThreads / 32;
 constexpr int kVec = 256;  // entries that a warp loads at once, 8 a lane; a group is U of them
 constexpr int kCandidates = 512;
 constexpr int kLpMaxCluster = 8;
@@ -203,7 +203,7 @@ __device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], float c,
       m2 = u == 0 ? h : __hmax2(m2, h);
     }
     gm = fmaxf(__low2float(m2), __high2float(m2));
-    if (!edge) {
+    if (!edge && !(gm < xt)) {
       // entries before the token count from equality on, those behind it from above it on
       const __nv_bfloat162 x2 = __float2bfloat162_rn(xt);
       __nv_bfloat162 n2 = __float2bfloat162_rn(0.f);
@@ -285,7 +285,7 @@ __device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], float c,
 }
 
 template <int DT, int U>
-__global__ void __launch_bounds__(kLpThreads, 4) logprob_kernel(const LpParams P) {
+__global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P) {
   constexpr int kGroup = U * kVec;
   extern __shared__ __align__(16) unsigned char s_dyn[];
   __shared__ LpShared sm;
@@ -539,10 +539,10 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   P.top_ids = top_ids;
   P.top_lp = top_lp;
   P.err = err;
-  // Few rows: a cluster of CTAs shares one, until the rows fill four CTAs on every SM or a CTA has
+  // Few rows: a cluster of CTAs shares one, until the rows fill eight CTAs on every SM or a CTA has
   // less than two vectors for each warp.
   int C = 1;
-  while (C < sdk::kLpMaxCluster && (long)P.rows * C < 4 * 152 && V / (2 * C) >= 4096) C *= 2;
+  while (C < sdk::kLpMaxCluster && (long)P.rows * C < 8 * 152 && V / (2 * C) >= 4096) C *= 2;
   while (C < sdk::kLpMaxCluster && V / C > SD_TOP_MAX_V / sdk::kLpMaxCluster) C *= 2;
   // Groups of one vector while there are few of them, so that the best n groups are few entries
   // (and n of them at all); else of several, which saves most of a group's own work.
