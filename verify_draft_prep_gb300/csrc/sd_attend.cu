@@ -86,8 +86,9 @@ struct AttLayout {
   static constexpr int kK = kQ + (kQTm ? 0 : 2 * 2 * kQBytes);
   static constexpr int kV = kK + kKStages * kTileBytes;
   static constexpr int kScales = kV + kVStages * kTileBytes;
-  static constexpr int kJoin = kScales + kScaleSlots * 16 * 16;  // [8 warps][32 rows][17] floats
-  static constexpr int kMisc = kJoin + (R > 1 ? 8 * 32 * 17 * 4 : 0);
+  static constexpr int kJoinCols = DP == 64 ? 32 : 16;           // joined at a time
+  static constexpr int kJoin = kScales + kScaleSlots * 16 * 16;  // [8 warps][32 rows][those + 1]
+  static constexpr int kMisc = kJoin + (R > 1 ? 8 * 32 * (kJoinCols + 1) * 4 : 0);
   static constexpr long kSlotFloats = (long)kRows * DP + kRows;
 };
 
@@ -447,30 +448,30 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   volatile int* gave_up = &m.gave_up;
 
   // ---- setup: barriers, tensor memory, this CTA's share of the line of tiles ----
-  if (tid == 0) {
-    for (int i = 0; i < 12; ++i) {
-      mbar_init(smem_u32(&m.k_full[i]), 1);
-      mbar_init(smem_u32(&m.k_empty[i]), 1);
-      mbar_init(smem_u32(&m.v_full[i]), 1);
-      mbar_init(smem_u32(&m.v_empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&m.s_full[i]), 1);
-      mbar_init(smem_u32(&m.p_full[i]), 4);
-      mbar_init(smem_u32(&m.o_done[i]), 1);
-      mbar_init(smem_u32(&m.q_full[i]), NS == 1 && !L::kQTm ? 1 : 4);
-      mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(smem_u32(&m.sc_full[i]), 1);
-      mbar_init(smem_u32(&m.sc_empty[i]), NS == 1 ? 4 : 8);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (tid < 12) {
+    mbar_init(smem_u32(&m.k_full[tid]), 1);
+    mbar_init(smem_u32(&m.k_empty[tid]), 1);
+    mbar_init(smem_u32(&m.v_full[tid]), 1);
+    mbar_init(smem_u32(&m.v_empty[tid]), 1);
+  } else if (tid < 14) {
+    const int i = tid - 12;
+    mbar_init(smem_u32(&m.s_full[i]), 1);
+    mbar_init(smem_u32(&m.p_full[i]), 4);
+    mbar_init(smem_u32(&m.o_done[i]), 1);
+    mbar_init(smem_u32(&m.q_full[i]), NS == 1 && !L::kQTm ? 1 : 4);
+    mbar_init(smem_u32(&m.q_empty[i]), NS == 1 ? 9 : 1);
+    m.nan_any[i] = 0;
     m.gave_up = 0;
-    m.nan_any[0] = m.nan_any[1] = 0;
+  } else if (tid >= 32 && tid < 32 + kScaleSlots) {
+    const int i = tid - 32;
+    mbar_init(smem_u32(&m.sc_full[i]), 1);
+    mbar_init(smem_u32(&m.sc_empty[i]), NS == 1 ? 4 : 8);
   }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (tid < 256) m.nan_first[tid >> 7][tid & 127] = 0x7fffffff;
-  if (warp == 1) tmem_alloc(smem_u32(&m.tmem), 512);
+  if (warp == 2) tmem_alloc(smem_u32(&m.tmem), 512);
+  // What comes before this call on its stream may still be running up to here.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = (P.B + kAttThreads - 1) / kAttThreads;
   const int r0 = min(P.B, tid * per), r1 = min(P.B, r0 + per);
   long long mine = 0;
@@ -1079,7 +1080,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       float* slot = slots + (2L * blockIdx.x + (s.a > 0 ? 0 : 1)) * L::kSlotFloats;
       const int* nan_first = m.nan_first[buf];
       if (R > 1) {
-        // 2R partial rows: every warp leaves 16 columns of its own, weighed by their common
+        // 2R partial rows: every warp leaves some columns of its own, weighed by their common
         // maximum, then the threads add them up in the warps' order
         float* join = reinterpret_cast<float*>(smem + L::kJoin);
         constexpr int parts = 2 * R;  // a stream without a tile counts with weight 0
@@ -1104,26 +1105,30 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             P.lse[(long)(s.q.tok0 + th.x) * P.Hq + s.h * P.G + th.y] = lse2 * kLn2F;
           }
         }
+        constexpr int kJC = L::kJoinCols;
 #pragma unroll 1
-        for (int c = 0; c < DP; c += 16) {
+        for (int c = 0; c < DP; c += kJC) {
           if (ok && warp_live) {
-            uint32_t u[16];
-            tmem_ld16(tO + c, u);
-            tmem_wait_ld();
-            float* mine = join + ((warp - 4) * 32 + lane) * 17;
+            float* mine = join + ((warp - 4) * 32 + lane) * (kJC + 1);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mine[i] = used ? __uint_as_float(u[i]) * wm : 0.f;
+            for (int k = 0; k < kJC; k += 16) {
+              uint32_t u[16];
+              tmem_ld16(tO + c + k, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                mine[k + i] = used ? __uint_as_float(u[i]) * wm : 0.f;
+            }
           }
           named_bar(1, 256);
-          // 4 columns a thread, 64 rows a pass
-          const int cc = ((tid - 128) & 3) * 4;
-          const int r = (tid - 128) >> 2;
-          if (ok && r < s.rows) {
+          // 4 columns a thread
+          const int cc = ((tid - 128) % (kJC / 4)) * 4;
+          for (int r = (tid - 128) / (kJC / 4); ok && r < s.rows; r += 1024 / kJC) {
             float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < parts; ++i) {
               const int w = (i / R) * 4 + (i % R) * NC + (r >> 5);
-              const float* from = join + (w * 32 + (r & 31)) * 17 + cc;
+              const float* from = join + (w * 32 + (r & 31)) * (kJC + 1) + cc;
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[k] += from[k];
             }
@@ -1147,7 +1152,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
                              *reinterpret_cast<const uint32_t*>(&b));
             }
           }
-          if (c + 16 < DP) named_bar(1, 256);
+          if (c + kJC < DP) named_bar(1, 256);
         }
       } else {
         float wa = 1.f, wb = 0.f, Mt = M, Lt = Lsum;
@@ -1255,7 +1260,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     __syncthreads();
   }
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem, 512);
+  if (warp == 2) tmem_free(tmem, 512);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -1264,6 +1269,7 @@ template <int DP, int NS, int R>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams P) {
   using L = AttLayout<DP, NS, R>;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const JoinDesc d = reinterpret_cast<const JoinDesc*>(P.ws)[blockIdx.x];
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (d.pieces == 0 || r >= d.rows) return;
@@ -1389,12 +1395,14 @@ static int launch_attend(const AttendParams& P, const CUtensorMap& km, const CUt
   cfg.blockDim = dim3(kAttThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  if (cudaLaunchKernelEx(&cfg, attend_kernel<DP, NS, R>, P, km, vm) != cudaSuccess)
-    return SD_E_LAUNCH;
-  if (!join) return SD_OK;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attend_kernel<DP, NS, R>, P, km, vm) != cudaSuccess)
+    return SD_E_LAUNCH;
+  if (!join) return SD_OK;
   cudaLaunchConfig_t jc = {};
   jc.gridDim = dim3((unsigned)ctas, (unsigned)(L::kRows / 8), 1);
   jc.blockDim = dim3(256, 1, 1);
