@@ -474,9 +474,9 @@ SD_API int sd_hidden_gather(int capacity, int H, const int32_t* total_out, const
  *   the tokens written become e4m3(x / scale), to nearest even; infinities become +-448, NaN stays
  *   NaN; when the scale grew, what the page's other slots hold is rounded again to the new scale:
  *   e4m3(held * old / scale).
- * The tokens of one page stand next to one another in slot_mapping, up to 31 negative entries in a
- * row between them (the slots of a request's consecutive positions do); of tokens with the same slot the last is kept. Two stretches of the
- * same page in one call race on its scale.
+ * The tokens of one page stand next to one another in slot_mapping, up to 31 skipped entries in a
+ * row between them (the slots of a request's consecutive positions do); of tokens with the same
+ * slot the last is kept. Two stretches of the same page in one call race on its scale.
  * Arguments: k, v: bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
  *   strides multiples of 8; they may be slices of one projection); slot_mapping [n] int32;
  *   num_blocks*block_size <= 2^31.

@@ -42,9 +42,12 @@ class Case:
         torch.cuda.synchronize()
         return int(err)
 
-    def check(self, causal=True, hide=None):
+    def check(self, causal=True, hide=None, only=None):
         at = 0
         for r, n in enumerate(self.n_q):
+            if only is not None and r not in only:
+                at += n
+                continue
             T = self.ctx[r]
             k = kvref.held(self.cache[0], self.cache[2], self.table[r], T)
             v = kvref.held(self.cache[1], self.cache[3], self.table[r], T)
@@ -343,3 +346,18 @@ def test_write_then_attend_matches_attention_on_what_was_written():
     c.check()
     got = kvref.held(c.cache[0], c.cache[2], c.table[0], 100)[-4:]
     assert float((got - k[:4].double()).norm() / k[:4].double().norm()) < 0.04
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 32, 8), (64, 64, 8)])
+def test_a_large_cache_seen_for_the_first_time(D, Hq, Hkv):
+    """Pages all over gigabytes of memory that the GPU has not touched lately arrive late and in
+    any order: every stage of K and V is waited for in its own phase, whichever stream runs
+    ahead. Every kernel of this head size, units of a part of a request and of whole ones, rows that
+    do not fill a warp."""
+    g = torch.Generator().manual_seed(8)
+    B, n = 96, 28 if D == 128 else 14
+    ctx = [int(x) for x in torch.randint(n, 16000, (B,), generator=g)]
+    c = Case([n] * B, ctx, Hq, Hkv, D, 16, seed=8)
+    for rows in (32, 64, 128, 256):
+        assert c.run(max_q=max(1, rows * Hkv // Hq)) == 0
+        c.check(only=(0, 31, 64, 95))

@@ -243,3 +243,18 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("gap", [[2 ** 31 - 1], [-1, 1 << 20, -7], [1 << 20] * 31])
+def test_a_page_around_slots_beyond_the_cache(gap):
+    """Skipped entries inside a page's tokens, of either kind, leave them one stretch."""
+    g = gen(12)
+    bs, H, D = 16, 2, 64
+    nb, table = kvref.make_table([40], bs, g, DEV)
+    cache = list(kvref.make_cache(nb, bs, H, D, g, DEV))
+    pos = [(0, i) for i in range(16, 30)]
+    slots = slots_of(table, bs, pos)
+    slots = torch.cat([slots[:6], torch.tensor(gap, dtype=torch.int32, device=DEV), slots[6:]])
+    k = 100 * torch.randn(slots.numel(), H, D, generator=g, device=DEV)
+    check_write(k.bfloat16(), (k / 3).bfloat16(), slots, cache,
+                sd.SD_ERR_KV_SLOT if max(gap) > 0 else 0)

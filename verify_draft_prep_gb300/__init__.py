@@ -652,16 +652,15 @@ def sd_kv_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_tokens, k_out
 _attend_workspaces = {}
 
 
-def attend_workspace(device, D):
+def attend_workspace(device):
     """Scratch of sd_kv_attend for this device, shared by calls that pass none (calls on
     concurrent streams must pass their own)."""
     import torch
 
-    need = max(_quick().sd_kv_attend_workspace_bytes(D), 16)
     key = torch.device(device)
     ws = _attend_workspaces.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=key)
+    if ws is None:  # for the largest heads: it is never replaced, a captured graph may hold it
+        ws = torch.empty(_quick().sd_kv_attend_workspace_bytes(128), dtype=torch.uint8, device=key)
         _attend_workspaces[key] = ws
     return ws
 
@@ -697,7 +696,7 @@ def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, c
     if lse is not None and (lse.dtype != _t().float32 or lse.shape != (n, Hq)
                             or not lse.is_contiguous()):
         raise SDError("lse must be contiguous float32 [tokens, Hq]")
-    ws = workspace_buf if workspace_buf is not None else attend_workspace(k_cache.device, D)
+    ws = workspace_buf if workspace_buf is not None else attend_workspace(k_cache.device)
     rc = _quick().sd_kv_attend(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q), *sq,
                              *cache, _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q),
                              D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)),

@@ -12,7 +12,7 @@ namespace sdk {
 
 // ---------------------------------------------------------------------------------------------
 // Write. A run is the tokens of one page in one call (they stand next to one another in the slot
-// mapping, up to 31 negative entries between them). A page of up to 16 tokens of one head of K or V is one warp's work, so that the page
+// mapping, up to 31 entries that are not written between them). A page of up to 16 tokens of one head of K or V is one warp's work, so that the page
 // stays in registers between the largest magnitude and the quantisation: every value is read
 // once. Larger pages take a team of warps, 16 tokens each, that meet over the magnitude. Per
 // element 2 bytes are read and 1 is written; the kernel is bound by memory for prompts and by the
@@ -72,18 +72,19 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
   const int bs = 1 << P.log2_bs;
   const int i0 = blockIdx.x * P.chunk;
   const long limit = (long)P.num_blocks << P.log2_bs;
+  auto written = [&](int s) { return s < limit ? s : -1; };  // a slot, or -1
 
   // 1. The runs that begin in this CTA's tokens.
   if (warp == 0) {
     bool lead = false, bad = false;
     if (lane < P.chunk && i0 + lane < P.n) {
       const int s = P.slots[i0 + lane];
-      int prev = i0 + lane > 0 ? P.slots[i0 + lane - 1] : -1;
+      int prev = i0 + lane > 0 ? written(P.slots[i0 + lane - 1]) : -1;
       bad = s >= limit;
       if (s >= 0 && !bad) {
-        // the last slot before this one, over up to 31 negative ones
+        // the last slot before this one, over up to 31 that are not written
         for (int j = i0 + lane - 2; j >= 0 && j >= i0 + lane - 32 && prev < 0; --j)
-          prev = P.slots[j];
+          prev = written(P.slots[j]);
         lead = prev < 0 || (prev >> P.log2_bs) != (s >> P.log2_bs);
       }
     }
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
     const int first = s_lead[r];
     const int page = P.slots[first] >> P.log2_bs;
     for (int i = first; i < P.n;) {
-      const int s = i + lane < P.n ? P.slots[i + lane] : -1;
+      const int s = i + lane < P.n ? written(P.slots[i + lane]) : -1;
       const bool here = s >= 0 && (s >> P.log2_bs) == page;
       const uint32_t other = __ballot_sync(0xffffffffu, s >= 0 && !here);
       const int len = other ? __ffs(other) - 1 : 32;
