@@ -185,3 +185,36 @@ def test_optional_outputs_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(lp, want)
+
+
+@pytest.mark.parametrize("V,rows_n", [(1000, 3), (8192, 5), (32000, 5), (32000, 1300), (201088, 3),
+                                      (201088, 1300)])
+@pytest.mark.parametrize("n_top", [1, 20, 32])
+def test_rows_of_few_entries(V, rows_n, n_top):
+    """Rows cut to their largest entries, as sampling leaves them: fewer than n_top positive
+    probabilities, and logits of -inf everywhere else."""
+    g = gen(V + n_top)
+    for kind in ("probs", "logits"):
+        x = 2 * torch.randn(rows_n, V, generator=g, device=DEV)
+        keep = torch.randint(1, 40, (rows_n, 1), generator=g, device=DEV)
+        kth = x.sort(-1, descending=True).values.gather(1, keep)
+        x = torch.where(x >= kth, x, torch.full_like(x, -math.inf))
+        rows = torch.softmax(x, -1) if kind == "probs" else x.bfloat16()
+        check(rows, rows.argmax(-1).to(torch.int32)[:, None], n_top)
+
+
+@pytest.mark.parametrize("V", [8192, 32000, 201088])
+@pytest.mark.parametrize("kind", ["probs", "logits"])
+def test_best_entries_in_one_place(V, kind):
+    """The largest entries all where one thread reads, in one block, or in order along the row."""
+    g = gen(V)
+    x = torch.randn(6, V, generator=g, device=DEV)
+    i = torch.arange(V, device=DEV)
+    x[0] += 20.0 * ((i % 256) < 8)          # a lane of every warp
+    x[1] += 20.0 * ((i % 1024) < 4)
+    x[2] += 20.0 * ((i >= 1000) & (i < 1700))
+    x[3] = 8.0 * i / V
+    x[4] = -8.0 * i / V
+    x[5] += 20.0 * ((i % 4096) >= 4088)
+    rows = torch.softmax(x, -1) if kind == "probs" else x.bfloat16()
+    check(rows, torch.full((6, 1), 1001, dtype=torch.int32, device=DEV), 32)

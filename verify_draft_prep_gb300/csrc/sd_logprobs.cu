@@ -5,12 +5,18 @@
 // H = -sum p ln p = ln Z - (sum e^(y - m) (y - m)) / Z. Sums are fp32, each thread's own and then a
 // tree's. Probability rows need no Z: log p = ln p_x, H = -sum p ln p.
 //
-// A warp takes 256 or more neighbouring entries (a group) at a time. The group's maximum, one warp
+// A warp takes 256 or 1024 neighbouring entries (a group) at a time. The group's maximum, one warp
 // reduction, is kept in shared memory to find the best n entries: they lie in the n groups that
 // come first by (maximum, lowest index), because each of those holds an entry that beats everything
-// of any later group. Only these n groups are read again. Entries are compared and bounded two at
-// a time as they are stored; only the exponential and the sums take single fp32 values.
-// Bound by memory: the row once.
+// of any later group. Only these n groups are read again (from L2). Entries are compared and
+// bounded two at a time as they are stored; only the exponential and the sums take single fp32
+// values.
+//
+// Bound by memory on paper, the row once: 9216 rows of 201088 logits with 20 alternatives, 2.04 GB
+// of rows with a token, take 400 us, 75% of the copy rate. The rest goes to instructions: at 16 a clock
+// and SM the exponentials alone take 220 us. CTAs of 128 threads, eight on an SM, so that one
+// row's tail (the selection, some 3 us) overlaps seven others' loads (434 instead of 396 us with 256
+// threads, four on an SM). 5 rows of 1024 probabilities with 5 alternatives: 4.5 us in a graph.
 
 #include "sd_common.cuh"
 
@@ -162,11 +168,11 @@ struct LpShared {
   Sums sums[kLpMaxCluster];     // rank 0's, written by every CTA of the cluster
   int rank[kLpMaxCluster];
   uint64_t best[kLpMaxCluster][SD_TOP_MAX];
-  uint64_t cand[kCandidates];
+  alignas(16) uint64_t cand[kCandidates];  // (before them the threads' maxima, as order_of())
   uint64_t round[2][kLpWarps];
   int first[SD_TOP_MAX];        // the groups that hold this CTA's best entries
   int count;
-  uint64_t floor;               // no entry below it is among the best
+  uint32_t floor;               // as order_of(): no entry below it is among the best
 };
 
 __device__ __forceinline__ uint64_t warp_max64(uint64_t q) {
@@ -284,6 +290,84 @@ __device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], float c,
   return gm;
 }
 
+// More entries reach the floor than there is room for: those above it, and the first of those at it.
+// Their number, 0 if those above it are too many as well. Out of line, so that it does not weigh on
+// the pass over the row (9216 rows of 201088 logits: 407 us with it inside, 404 without).
+template <int DT, int U>
+__device__ __noinline__ int of_many(LpShared& sm, const void* x, int begin, int V, bool vec, int ng,
+                                    int n) {
+  constexpr int kGroup = U * kVec;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t floor = sm.floor;
+  const float least = value_of(floor), bound = value_of(floor + 1);
+  __syncthreads();
+  if (threadIdx.x == 0) sm.count = 0;
+  __syncthreads();
+  for (int k = warp; k < ng * U; k += kLpWarps) {
+    const int g0 = begin + sm.first[k / U] * kGroup + (k % U) * kVec;
+    const Raw<DT> r = load_group<DT>(x, g0, V, vec, lane);
+    float v[8];
+    unpack<DT>(r, v);
+    int full = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = g0 + entry<DT>(lane, e);
+      if (v[e] >= bound && i < V) {
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kCandidates) sm.cand[at] = key_of(v[e], i);
+        else full = 1;
+      }
+    }
+    if (full) break;
+  }
+  __syncthreads();
+  const int m = sm.count;
+  if (m > kCandidates) return 0;
+  if (m >= n) return m;
+  __syncthreads();
+  if (warp == 0) {  // the groups in the order of their indices
+    const int f = lane < ng ? sm.first[lane] : 0x7fffffff;
+    int place = 0;
+    for (int i = 0; i < ng; ++i) place += __shfl_sync(0xffffffffu, f, i) < f;
+    if (lane < ng) sm.first[place] = f;
+    __syncwarp();
+    int to = m;
+    for (int k = 0; to < n && k < ng * U; ++k) {
+      const int g0 = begin + sm.first[k / U] * kGroup + (k % U) * kVec;
+      const Raw<DT> r = load_group<DT>(x, g0, V, vec, lane);
+      float v[8];
+      unpack<DT>(r, v);
+      constexpr int kRun = DT == SD_BF16_LOGITS ? 8 : 4;  // a lane's neighbouring entries
+#pragma unroll
+      for (int e0 = 0; e0 < 8; e0 += kRun) {
+        int mine = 0;
+#pragma unroll
+        for (int e = e0; e < e0 + kRun; ++e)
+          mine += v[e] == least && g0 + entry<DT>(lane, e) < V;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        int at = to + upto - mine;
+#pragma unroll
+        for (int e = e0; e < e0 + kRun; ++e) {
+          const int i = g0 + entry<DT>(lane, e);
+          if (v[e] == least && i < V) {
+            if (at < n) sm.cand[at] = key_of(v[e], i);
+            ++at;
+          }
+        }
+        to += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+    if (lane == 0) sm.count = min(to, n);
+  }
+  __syncthreads();
+  return sm.count;
+}
+
 template <int DT, int U>
 __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P) {
   constexpr int kGroup = U * kVec;
@@ -339,12 +423,14 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P
   if (!(T > 0.f)) T = 1.f;  // a greedy request's rows are reported at temperature 1
   const float c = kLog2e / T;
   Lane q{-INFINITY, make_float2(0.f, 0.f), make_float2(0.f, 0.f), 0};
+  float tm = nanf("");  // the largest entry of this thread
   for (int g = warp; g < groups; g += kLpWarps) {
     Raw<DT> now[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) now[u] = raw[u];
     fetch(g + kLpWarps);
     const float gm = take<DT, U>(q, now, c, xt, begin + g * kGroup, token, P.V, lane);
+    if (U == 1) tm = fmaxf(tm, gm);
     if (P.n_top > 0) {
       const uint32_t o = __reduce_max_sync(0xffffffffu, order_of(gm));
       if (lane == 0) gmax[g] = o;
@@ -363,6 +449,8 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P
     sm.warp_sums[warp] = a;
     sm.warp_rank[warp] = rank_part;
   }
+  uint32_t* thread_max = reinterpret_cast<uint32_t*>(sm.cand);
+  if (U == 1) thread_max[tid] = order_of(tm);
   if (tid == 0) sm.count = 0;
   if (C > 1) cluster.barrier_wait();
   __syncthreads();
@@ -404,50 +492,67 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P
       next = warp_max64(next);
       if (lane == (g & 31)) mine = next;
     }
-    if (lane == 0) sm.floor = (best >> 32) << 32;  // n entries reach the last group's maximum
-  } else if (warp == 1) {  // every group
-    if (lane < ng) sm.first[lane] = lane;
-    if (lane == 0) sm.floor = 0;
+    if (lane == 0) sm.floor = (uint32_t)(best >> 32);  // n entries reach the last group's maximum
+  }
+  if (U == 1 && n > 0 && groups <= n) {
+    // Every group. The threads hold 128 disjoint parts of the entries: n entries reach the n-th
+    // largest of their maxima. (With groups of several vectors a CTA has 57 groups at the least.)
+    if (tid < ng) sm.first[tid] = tid;
+    const uint32_t mine = thread_max[tid];
+    int before = 0;
+#pragma unroll 8
+    for (int i = 0; i < kLpThreads; i += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(thread_max + i);
+      const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) before += w[k] > mine || (w[k] == mine && i + k < tid);
+    }
+    if (before == n - 1) sm.floor = mine;
   }
   __syncthreads();
 
-  // 3. Their best entries: those that reach the floor are few, but for ties.
+  // 3. Their entries that reach the floor: few, but for ties (a row that is 0 or -inf but for a
+  // few). Then those above the floor, and the first of those at it.
   if (n > 0) {
-    const uint64_t floor = sm.floor;
+    const uint32_t floor = sm.floor;
     bool many = floor == 0;
+    int m = 0;
     if (!many) {
-      const float least = value_of((uint32_t)(floor >> 32));
+      const float least = value_of(floor);
       for (int k = warp; k < ng * U; k += kLpWarps) {
         const int g0 = begin + sm.first[k / U] * kGroup + (k % U) * kVec;
         const Raw<DT> r = load_group<DT>(x, g0, P.V, vec, lane);
         float v[8];
         unpack<DT>(r, v);
+        int full = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int i = g0 + entry<DT>(lane, e);
           if (v[e] >= least && i < P.V) {
             const int at = atomicAdd(&sm.count, 1);
             if (at < kCandidates) sm.cand[at] = key_of(v[e], i);
+            else full = 1;
           }
         }
+        if (full) break;  // (rows cut to 9 entries 525 us without, full ones 404 us instead of 401)
       }
       __syncthreads();
-      const int m = sm.count;
-      many = m > kCandidates;
+      m = sm.count;
+      if (m > kCandidates)
+        m = of_many<DT, U>(sm, x, begin, P.V, vec, ng, n);
+      many = m < n;  // (what lies past the row's end was among the maxima)
+    }
+    if (!many) {
       // their order by counting, which does not depend on the order that they were found in
-      for (int k = tid; !many && k < max(m, n); k += kLpThreads) {
-        if (k >= m) {
-          root->best[part][k] = 0;
-          continue;
-        }
+      for (int k = tid; k < m; k += kLpThreads) {
         const uint64_t q = sm.cand[k];
         int before = 0;
         for (int i = 0; i < m; ++i) before += sm.cand[i] > q;
         if (before < n) root->best[part][before] = q;
       }
-    }
-    if (many) {
-      // few groups, or many equal entries: n rounds, each thread with its best one not yet taken
+    } else {
+      // fewer than n numbers here, or hundreds above the floor: n rounds, each thread with its best
+      // one not yet taken
       const int items = ng * kGroup;
       auto best_below = [&](uint64_t limit) {
         uint64_t b = 0;
@@ -540,14 +645,21 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   P.top_lp = top_lp;
   P.err = err;
   // Few rows: a cluster of CTAs shares one, until the rows fill eight CTAs on every SM or a CTA has
-  // less than two vectors for each warp.
+  // few entries left, while there is a free SM for each fewer. Measured in us, 20 alternatives, 1, 2,
+  // 4 or 8 CTAs: 5 rows of 1024 logits 5.7, 7.0, 7.8, 10.6; of 8192 12.6, 9.2, 8.3, 10.0; of 32000
+  // 18.2, 16.0, 15.0, 12.2; of 201088 43, 32, 24, 21. 192 rows of 32000: 19.1, 17.4, 18.0, 21.2.
+  // 768 rows of 201088: 82, 71, 80, 109. 2304 rows of 131072: 104, 122, 158, 232.
   int C = 1;
-  while (C < sdk::kLpMaxCluster && (long)P.rows * C < 8 * 152 && V / (2 * C) >= 4096) C *= 2;
+  while (C < sdk::kLpMaxCluster && (long)P.rows * C < 8 * 152 &&
+         V / (2 * C) >= ((long)P.rows * 2 * C <= 152 ? 2048 : 4096))
+    C *= 2;
   while (C < sdk::kLpMaxCluster && V / C > SD_TOP_MAX_V / sdk::kLpMaxCluster) C *= 2;
-  // Groups of one vector while there are few of them, so that the best n groups are few entries
-  // (and n of them at all); else of several, which saves most of a group's own work.
-  const int wide = dtype == SD_BF16_LOGITS ? 4 : 2;
-  const int U = V / C >= 65536 ? wide : 1;
+  // Groups of one vector while there are few of them, so that the best n groups are few entries;
+  // of logits else of four, which saves most of a group's own work. One against four vectors: 5
+  // rows of 201088 in CTAs of 25136 logits 21 to 26 us, 192 rows in CTAs of 50272 33.5 to 35.1, 2304
+  // rows of 131072 in CTAs of 65536 141 to 122, of 131072 152 to 104. Probabilities, which bring half
+  // as many entries with each byte, gain nothing (2304 rows of 131072: 222 to 222 us with two).
+  const int U = dtype == SD_BF16_LOGITS && V / C >= 65536 ? 4 : 1;
   const int group = U * sdk::kVec;
   const long span = ((long)V + C - 1) / C;
   P.span = (int)((span + group - 1) / group * group);
@@ -564,11 +676,9 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = dtype == SD_BF16_LOGITS
-                    ? (U > 1 ? sdk::logprob_kernel<SD_BF16_LOGITS, 4>
-                             : sdk::logprob_kernel<SD_BF16_LOGITS, 1>)
-                    : (U > 1 ? sdk::logprob_kernel<SD_F32_PROBS, 2>
-                             : sdk::logprob_kernel<SD_F32_PROBS, 1>);
+  auto kernel = U > 1                     ? sdk::logprob_kernel<SD_BF16_LOGITS, 4>
+                : dtype == SD_BF16_LOGITS ? sdk::logprob_kernel<SD_BF16_LOGITS, 1>
+                                          : sdk::logprob_kernel<SD_F32_PROBS, 1>;
   if (smem > 16 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess)
