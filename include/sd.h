@@ -23,7 +23,9 @@
  *     zeroes; may be NULL). The kernel then takes the documented fallback. No kernel traps or
  *     asserts. One kernel waits on a value written by another CTA of the same launch: the
  *     single launch of sd_verify_prepare (see there), whose wait is bounded by time (20 ms on
- *     the GPU clock) and ends with SD_ERR_WAIT, never with a hang.
+ *     the GPU clock) and ends with SD_ERR_WAIT, never with a hang. The warps of a CTA of
+ *     sd_kv_attend wait for one another and for its loads, each time about a second at most;
+ *     SD_ERR_WAIT there too means that the call's output is incomplete.
  *
  * Notation: B requests, K drafts per request (1 <= K <= SD_K_MAX), V vocabulary entries,
  * H hidden size. Target rows p_0..p_K of request r are rows r*(K+1)+j of `target`; draft rows
@@ -66,7 +68,8 @@ extern "C" {
 #define SD_ERR_TOTAL_RANGE 32   /* total_out outside [0, capacity]: clamped */
 #define SD_ERR_WAIT 64          /* sd_verify_prepare: a request's first drafter slot was not
                                    published within the bounded wait (20 ms); its final token is
-                                   not written to input_ids */
+                                   not written to input_ids. sd_kv_attend: a wait inside the
+                                   kernel ran out, outputs are incomplete */
 #define SD_ERR_DRAFT_COUNT 128  /* cu_drafts gives a request a draft count outside [0, K_max]:
                                    clamped (sd_verify_ragged) */
 #define SD_ERR_KV_SLOT 256      /* a slot beyond the cache: that token is not written */
@@ -513,19 +516,21 @@ SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const v
  * stands at position ctx_lens[r] - n_r + i and, when causal, sees the tokens up to its own
  * position; else all ctx_lens[r]. Head h of Hq reads head h / (Hq / Hkv) of the cache.
  *   S = sm_scale * q . k,  out = sum_j softmax(S)_j v_j,  lse = ln sum_j e^(S_j)
- * q is taken exactly (its largest values to 2^-18), exponentials, sums and products are fp32,
- * the weights of v have 8 significant bits (2^-18 of the row's largest at the least), out is
- * rounded to bf16 once. A token that sees nothing gets out = 0 and lse = -inf. NaN in tokens that
- * a query token does not see has no effect on it.
+ * q is taken exactly but for what lies below 2^-17 of its largest magnitude; exponentials, sums and
+ * products are fp32; the weights of v have 8 significant bits, and steps of 2^-16 of the row's
+ * largest at the finest; out is rounded to bf16 once. The V scales of the pages that one token sees
+ * lie within 2^80 of one another (a scale of 0 may be among them). A token that sees nothing gets
+ * out = 0 and lse = -inf. NaN in tokens that a query token does not see has no effect on it. The
+ * same call gives the same bits: parts of a request are joined in a fixed order.
  * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] raises
  * SD_ERR_KV_RANGE; those tokens are left out. cu_q has B+1 non-decreasing entries in [0, n]
  * (others are clamped, SD_ERR_KV_RANGE); tokens outside [cu_q[0], cu_q[B]) are not written.
  * Arguments: q, out bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
  *   strides multiples of 8); lse [n, Hq] fp32 or NULL; max_q: the most query tokens that a request
  *   is expected to have, which only chooses the kernel (any value >= 1 is right); Hq a multiple of
- *   Hkv; num_blocks >= 1; sm_scale positive and finite; workspace: at least sd_kv_attend_workspace_bytes(D) bytes of
- *   device scratch, 16-byte aligned, its contents irrelevant before and after. Calls that may run
- *   concurrently need separate workspaces.
+ *   Hkv; num_blocks >= 1; sm_scale positive and finite; workspace: at least
+ *   sd_kv_attend_workspace_bytes(D) bytes of device scratch, 16-byte aligned, its contents
+ *   irrelevant before and after. Calls that may run concurrently need separate workspaces.
  */
 SD_API int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q, long ld_q,
                         long hs_q, const void* k_cache, const void* v_cache, long st_block,

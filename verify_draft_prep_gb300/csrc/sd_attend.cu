@@ -7,7 +7,7 @@
 //
 // The cache's bytes go to the tensor cores as they are, without being converted: an e4m3 value has
 // 4 significant bits and bf16 has 8, so q is split into two e4m3 terms, q = q1 + q2 (after a power
-// of two per row brings its largest magnitude to [224, 448]; exact but for values below 2^-17 of
+// of two per row brings its largest magnitude to [224, 448]; exact but for what lies below 2^-17 of
 // that), and so is each weight P = P1 + P2 (P at most 448 there, too). Two e4m3 products take the
 // time of one bf16 product, and K and V cost half the shared memory and no instructions. A page's
 // scales enter as numbers per 8 columns of S: with y = log2(e) S + log2(v_scale),
@@ -19,10 +19,20 @@
 // CTAs (one per SM) divide evenly, whatever the lengths of the requests: a unit that several CTAs
 // share leaves its parts in the workspace and attend_join_kernel joins them in a fixed order.
 // Within a CTA: warps 0 and 2 load pages (TMA), warp 1 issues the products, warp 3 fetches the
-// scales and the next unit's queries, two groups of four warps turn S into P, one row a thread. The groups are two streams that keep
-// the tensor cores busy in turn: with few rows they take alternate tiles of the same rows (and
-// the accumulators are joined at the unit's end), with many they take 128 rows each of the same
-// tiles, which halves the traffic of K and V.
+// scales and the next unit's queries, two groups of four warps turn S into P, one row a thread. The
+// groups are two streams that keep the tensor cores busy in turn: with few rows they take alternate
+// tiles of the same rows (and the accumulators are joined at the unit's end), with many they take
+// 128 rows each of the same tiles, which halves the traffic of K and V.
+//
+// What bounds it (measured, 8 heads of K and V, pages of 16): 256 requests of 8 slots, 32 heads of
+// 128, 1000 to 16000 tokens: 800 to 860 us with the clocks of the box, memory (79 to 84% of the copy
+// rate). 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 122 us against 40 of memory, 128
+// drafter rows of 8 to 16 slots 400 us against 109: the softmax, 270 to 330 cycles for 32 columns of
+// 32 rows in each of an SM's four schedulers, while a tile of 48 rows costs as much as one of 64. A
+// prompt of 8192 tokens, 32 heads of 128: 588 us, 47% of the bf16 rate, softmax again. One token at
+// 32000, 32 heads of 128: 31 us in a graph against 9.7 of memory: 14 tiles a CTA do not hide the
+// setup, the first pages' latency and the join of 19 parts. (Softmax beside a product that takes both
+// operands from shared memory is 2.3 times slower; that is why heads of 64 keep Q in tensor memory.)
 
 #include "sd_kv.cuh"
 #include "sd_tc.cuh"
@@ -37,8 +47,9 @@ constexpr int kScaleSlots = 16;            // tiles of scales in flight
 // that of any page with values, so that those keep P's full precision.
 constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
 // P = 2^(y - M + kShift) is at most 448 while M is no more than kSlack behind the row's maximum. A
-// larger shift keeps more of the small weights, a smaller one has the accumulator rescaled less
-// often: weights lose bits below 2^-14 of the row's largest, and end at 2^-18 of it.
+// larger shift keeps more of the small weights, a larger slack has the accumulator rescaled less
+// often, and the two share e4m3's range (2^(7 + 1.75) < 448). P has 8 bits, steps of 2^-9 at the
+// finest: 2^-16 of 2^7, the row's largest weight when M is its maximum.
 constexpr float kShift = 7.f, kSlack = 1.75f;
 constexpr float kTiny = 1.17549435e-38f;  // -inf times it is -inf, S times it is nothing
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
@@ -79,7 +90,7 @@ struct AttLayout {
   static constexpr int kTmO = 256, kTmQ = 256 + 2 * DP;
   static constexpr int kQBytes = kTile * DP;        // one term of one Q tile
   static constexpr int kTileBytes = kTile * DP;     // K or V of one tile
-  // Tiles in flight. V's stay longer (until P is formed and used) than K's.
+  // Tiles in flight, as many as fit. V's stay longer (until P is formed and used) than K's.
   static constexpr int kKStages = DP == 64 ? 8 : (NS == 1 ? 3 : 4);
   static constexpr int kVStages = DP == 64 ? 12 : (NS == 1 ? 5 : 4);
   static constexpr int kQ = 0;                      // two buffers (NS = 1), or two tiles
@@ -158,7 +169,9 @@ struct Segment {
 };
 
 // Every unit takes kUnitCost places on the line before its tiles, for what it costs beside them (its
-// queries, its result), so that CTAs with many short units get fewer tiles.
+// queries, its result), so that CTAs with many short units get fewer tiles. With 2, 4, 8 and 16: one
+// token at 32000 37.2, 35.2, 34.5, 36.9 us; 64 requests 146, 131, 120, 129; 256 requests 854, 833, 808,
+// 830; drafter batch 441, 392, 395, 444; prompt 832, 612, 589, 636.
 constexpr int kUnitCost = 8;
 
 template <int NS, int ROWS>
@@ -1472,6 +1485,8 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   P.out_32 = (uintptr_t)out % 32 == 0 && ld_out % 16 == 0 && hs_out % 16 == 0;
   P.ws = (unsigned char*)workspace;
   P.err = err;
+  // A CTA's least share: a unit's cost and 4 tiles. With 1, 4 and 16 tiles one token at 500 tokens
+  // takes 16.2, 14.7, 21.5 us, at 1000 19.8, 19.1, 27.5, at 4000 20.9, 23.1, 30.8.
   P.min_share = sdk::kUnitCost + 4;
   const int sms = sdk::sm_count();
   if (sms < 1) return SD_E_DEVICE;
@@ -1483,7 +1498,11 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   // units of one tile are never shared
   const bool join = ((long)max_blocks << log2_bs) > sdk::kTile;
   // The expected rows of a request choose the unit: 32 or 64 rows stand in the lanes four times or
-  // twice, so that all softmax warps share a tile's columns.
+  // twice, so that all softmax warps share a tile's columns; more than 128 make two Q tiles. Measured
+  // in us with units of 32, 64, 128 and 256 rows: heads of 64, 64 requests of 32 rows 100, 105, 141,
+  // 195; 48 rows 186, 119, 158, 202; 96 rows 264, 209, 157, 204; 192 rows 568, 341, 327, 278. Heads of
+  // 128, 256 requests of 32 rows 863, 876, 1127, 1689; 56 rows 1667, 954, 1202, 1652; 112 rows 3627,
+  // 1958, 1395, 1740; 64 requests of 240 rows 1715, 1035, 802, 553.
   const long rows = (long)max_q * P.G;
   if (DP == 64) {
     if (rows <= 32) return sdk::launch_attend<64, 1, 4>(P, km, vm, ctas, join, stream);
