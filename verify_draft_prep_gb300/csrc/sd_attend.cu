@@ -112,8 +112,8 @@ struct AttMisc {
   float2 ml[2][kTile];        // (M, L) of both streams
   int nan_first[2][128];      // first token with a NaN in dimension d of V, of a masked tile
   int nan_any[2];
-  long long start[2];         // of the schedule
-  int start_item[3];
+  int start_item[4];          // of the schedule
+  long long g0, share;
   long long warp_sum[kAttThreads / 32];
   uint32_t tmem;
   int gave_up;
@@ -174,6 +174,12 @@ struct Segment {
 // 830; drafter batch 441, 392, 395, 444; prompt 832, 612, 589, 636.
 constexpr int kUnitCost = 8;
 
+// The order of the line: heads outermost (requests, then their Q tiles inside), or, with two Q tiles,
+// innermost. Outermost against innermost: 64 requests 117 to 122 us, drafter batch 385 to 400, 256
+// requests 838 to 840, prompt (two Q tiles) 612 to 590.
+template <int NS>
+constexpr bool kHeadsInside = NS == 2;
+
 template <int NS, int ROWS>
 struct Schedule {
   long long g, end;  // this CTA's part of the line
@@ -181,8 +187,12 @@ struct Schedule {
 
   __device__ __forceinline__ bool next(const AttendParams& P, Segment& s) {
     while (g < end) {
+      if (!kHeadsInside<NS> && r == P.B) {
+        r = 0;
+        ++h;
+      }
       s.q = request_of(P, r);
-      if (s.q.rows == 0) {  // the line ends before the requests do
+      if (s.q.rows == 0) {
         ++r;
         continue;
       }
@@ -199,8 +209,8 @@ struct Schedule {
       off += take;
       if (off == s.n + kUnitCost) {
         off = 0;
-        if (++h == P.c.Hkv) {
-          h = 0;
+        if (!kHeadsInside<NS> || ++h == P.c.Hkv) {
+          if (kHeadsInside<NS>) h = 0;
           if ((++qt) * ROWS >= s.q.rows) {
             qt = 0;
             ++r;
@@ -498,7 +508,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     if (blockIdx.x == 0) bad |= request_bad(P, r);
   }
   if (bad) raise_err(P.err, SD_ERR_KV_RANGE);
-  mine *= P.c.Hkv;
   long long before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -507,30 +516,46 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   }
   if (lane == 31) m.warp_sum[warp] = before;
   __syncthreads();
-  long long total = 0;
+  long long line = 0;  // of one head
   before -= mine;
   for (int w = 0; w < kAttThreads / 32; ++w) {
     if (w < warp) before += m.warp_sum[w];
-    total += m.warp_sum[w];
+    line += m.warp_sum[w];
   }
-  const long long share = max((long long)P.min_share, (total + gridDim.x - 1) / gridDim.x);
-  const long long g0 = min(total, blockIdx.x * share), g1 = min(total, g0 + share);
-  if (mine > 0 && before <= g0 && g0 < before + mine) {
+  // Heads outermost: their lines lie one behind another. Where the CTAs divide evenly among them, each
+  // head's line is divided for itself: the CTAs at the same place of theirs then read the heads of
+  // the same pages at about the same time.
+  const int inside = kHeadsInside<NS> ? P.c.Hkv : 1, outside = P.c.Hkv / inside;
+  mine *= inside;
+  before *= inside;
+  line *= inside;
+  const int parts = gridDim.x % outside == 0 ? outside : 1, per_part = gridDim.x / parts;
+  const long long part = line * (outside / parts);
+  const long long share = max((long long)P.min_share, (part + per_part - 1) / per_part);
+  const long long p0 = blockIdx.x / per_part * part;
+  const long long g0 = p0 + min(part, blockIdx.x % per_part * share), g1 = min(p0 + part, g0 + share);
+  if (tid == 0) {
+    m.g0 = g0;
+    m.share = share;
+  }
+  const int head0 = line > 0 ? (int)(g0 / line) : 0;
+  const long long in_line = g0 - head0 * line;
+  if (mine > 0 && g0 < g1 && before <= in_line && in_line < before + mine) {
     long long at = before;
     for (int r = r0; r < r1; ++r) {
       const Request q = request_of(P, r);
       bool found = false;
       for (int row = 0; row < q.rows; row += L::kRows) {
         const int n = tiles_for(P, q, min(q.rows, row + L::kRows) - 1) + kUnitCost;
-        if (g0 < at + (long long)n * P.c.Hkv) {
+        if (in_line < at + (long long)n * inside) {
           m.start_item[0] = r;
           m.start_item[1] = row / L::kRows;
-          m.start_item[2] = (int)(g0 - at);  // head * n + place
-          m.start[0] = n;
+          m.start_item[2] = (int)(in_line - at) / n;
+          m.start_item[3] = (int)(in_line - at) % n;
           found = true;
           break;
         }
-        at += (long long)n * P.c.Hkv;
+        at += (long long)n * inside;
       }
       if (found) break;
     }
@@ -547,11 +572,10 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   sched.end = g1;
   sched.r = sched.qt = sched.h = sched.off = 0;
   if (g0 < g1) {
-    const int n = (int)m.start[0];
     sched.r = m.start_item[0];
     sched.qt = m.start_item[1];
-    sched.h = m.start_item[2] / n;
-    sched.off = m.start_item[2] % n;
+    sched.h = head0 + m.start_item[2];
+    sched.off = m.start_item[3];
   }
   Segment s;
   const int log2_bs = P.c.log2_bs, bs = 1 << log2_bs;
@@ -1265,7 +1289,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       }
       if (s.a == 0 && s.b < s.n) {  // begun here, ended by a later CTA
         continues = true;
-        jd.pieces = (int)((s.first + s.n - 1) / share - blockIdx.x + 1);
+        // (the last tile's place over the share, counted from this CTA's)
+        jd.pieces = (int)((s.first + s.n - 1 - m.g0) / m.share + 1);
         jd.tok0 = s.q.tok0;
         jd.head = s.h;
         jd.row0 = s.row0;

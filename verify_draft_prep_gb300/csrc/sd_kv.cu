@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
 // Read back. Output row i is token i - cu[r] + first[r] of request r. A CTA takes 16 rows: their
 // pages are looked up once into shared memory (a binary search over the prefix), then every
 // thread moves 16 values at a time (16 bytes in, 32 out), four of them on their way. Bound by
-// memory, 1 byte read and 2 written for each value: 278000 tokens of 8 heads of 64 take 147 us, 97% of
+// memory, 1 byte read and 2 written for each value: 316000 tokens of 8 heads of 64 take 147 us, 97% of
 // the copy rate; one request of 32000 tokens of 8 heads of 128 36 us, 79%.
 // ---------------------------------------------------------------------------------------------
 struct KvReadParams {
