@@ -25,12 +25,12 @@
 // 128 rows each of the same tiles, which halves the traffic of K and V.
 //
 // What bounds it (measured, 8 heads of K and V, pages of 16): 256 requests of 8 slots, 32 heads of
-// 128, 1000 to 16000 tokens: 800 to 860 us with the clocks of the box, memory (79 to 84% of the copy
-// rate). 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 122 us against 40 of memory, 128
-// drafter rows of 8 to 16 slots 400 us against 109: the softmax, 270 to 330 cycles for 32 columns of
-// 32 rows in each of an SM's four schedulers, while a tile of 48 rows costs as much as one of 64. A
-// prompt of 8192 tokens, 32 heads of 128: 588 us, 47% of the bf16 rate, softmax again. One token at
-// 32000, 32 heads of 128: 31 us in a graph against 9.7 of memory: 14 tiles a CTA do not hide the
+// 128, 1000 to 16000 tokens: 840 to 860 us, memory (79 to 81% of the copy rate). 64 requests of 6
+// slots, 64 heads of 64, 512 to 8192 tokens: 117 us against 40 of memory, 128 drafter requests of 8 to
+// 16 slots 374 us against 109: the softmax, 270 to 330 cycles for 32 columns of 32 rows in each of an
+// SM's four schedulers, while a tile of 48 rows costs as much as one of 64. A prompt of 8192 tokens,
+// 32 heads of 128: 578 us, 48% of the bf16 rate, softmax again. One token at 32000, 32 heads of 128:
+// 31 us in a graph against 9.7 of memory: 14 tiles a CTA do not hide the
 // setup, the first pages' latency and the join of 19 parts. (Softmax beside a product that takes both
 // operands from shared memory is 2.3 times slower; that is why heads of 64 keep Q in tensor memory.)
 
@@ -169,10 +169,10 @@ struct Segment {
 };
 
 // Every unit takes kUnitCost places on the line before its tiles, for what it costs beside them (its
-// queries, its result), so that CTAs with many short units get fewer tiles. With 2, 4, 8 and 16: one
-// token at 32000 37.2, 35.2, 34.5, 36.9 us; 64 requests 146, 131, 120, 129; 256 requests 854, 833, 808,
-// 830; drafter batch 441, 392, 395, 444; prompt 832, 612, 589, 636.
-constexpr int kUnitCost = 8;
+// queries, its result), so that CTAs with many short units get fewer tiles. With 2, 4, 6, 8 and 16:
+// 64 requests 122, 120, 117, 117, 125 us; 256 requests 863, 861, 854, 853, 861; drafter batch 387, 373,
+// 374, 384, 429; prompt 833, 607, 578, 588, 631; one token 34 everywhere but 36 with 16.
+constexpr int kUnitCost = 6;
 
 // The order of the line: heads outermost (requests, then their Q tiles inside), or, with two Q tiles,
 // innermost. Outermost against innermost: 64 requests 117 to 122 us, drafter batch 385 to 400, 256
@@ -1524,10 +1524,10 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   const bool join = ((long)max_blocks << log2_bs) > sdk::kTile;
   // The expected rows of a request choose the unit: 32 or 64 rows stand in the lanes four times or
   // twice, so that all softmax warps share a tile's columns; more than 128 make two Q tiles. Measured
-  // in us with units of 32, 64, 128 and 256 rows: heads of 64, 64 requests of 32 rows 100, 105, 141,
-  // 195; 48 rows 186, 119, 158, 202; 96 rows 264, 209, 157, 204; 192 rows 568, 341, 327, 278. Heads of
-  // 128, 256 requests of 32 rows 863, 876, 1127, 1689; 56 rows 1667, 954, 1202, 1652; 112 rows 3627,
-  // 1958, 1395, 1740; 64 requests of 240 rows 1715, 1035, 802, 553.
+  // in us with units of 32, 64, 128 and 256 rows: heads of 64, 64 requests of 32 rows 95, 102, 131,
+  // 193; 48 rows 182, 113, 150, 200; 96 rows 262, 201, 152, 203; 192 rows 563, 338, 315, 279. Heads of
+  // 128, 256 requests of 32 rows 852, 860, 1087, 1691; 56 rows 1640, 910, 1161, 1659; 112 rows 3613,
+  // 1894, 1337, 1744; 64 requests of 240 rows 1693, 942, 697, 553.
   const long rows = (long)max_q * P.G;
   if (DP == 64) {
     if (rows <= 32) return sdk::launch_attend<64, 1, 4>(P, km, vm, ctas, join, stream);
