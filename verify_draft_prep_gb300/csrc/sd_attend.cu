@@ -24,16 +24,19 @@
 // tiles of the same rows (and the accumulators are joined at the unit's end), with many they take
 // 128 rows each of the same tiles, which halves the traffic of K and V.
 //
-// What bounds it (measured, 8 heads of K and V, pages of 16): 256 requests of 8 slots, 32 heads of
-// 128, 1000 to 16000 tokens: 830 to 860 us, memory (79 to 82% of the copy rate), and 910 to 960 once
-// the power limit lowers the clocks after some tenths of a second. 64 requests of 6
-// slots, 64 heads of 64, 512 to 8192 tokens: 117 us against 40 of memory, 128 drafter requests of 8 to
-// 16 slots 374 us against 109: the softmax, 270 to 330 cycles for 32 columns of 32 rows in each of an
-// SM's four schedulers, while a tile of 48 rows costs as much as one of 64. A prompt of 8192 tokens,
-// 32 heads of 128: 578 us, 48% of the bf16 rate, softmax again. One token at 32000, 32 heads of 128:
-// 31 us in a graph against 9.7 of memory: 14 tiles a CTA do not hide the
-// setup, the first pages' latency and the join of 19 parts. (Softmax beside a product that takes both
-// operands from shared memory is 2.3 times slower; that is why heads of 64 keep Q in tensor memory.)
+// What bounds it (measured, 8 heads of K and V, pages of 16):
+//   - 256 requests of 8 slots, 32 heads of 128, 1000 to 16000 tokens: 830 to 860 us, memory (79 to
+//     82% of the copy rate), and 910 to 960 once the power limit lowers the clocks after some tenths
+//     of a second.
+//   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 117 us against 40 of memory, 128
+//     drafter requests of 8 to 16 slots 374 us against 109: the softmax, 270 to 330 cycles for 32
+//     columns of 32 rows in each of an SM's four schedulers, while a tile of 48 rows costs as much as
+//     one of 64.
+//   - A prompt of 8192 tokens, 32 heads of 128: 578 us, 48% of the bf16 rate, softmax again.
+//   - One token at 32000, 32 heads of 128: 31 us in a graph against 9.7 of memory: 14 tiles a CTA do
+//     not hide the setup, the first pages' latency and the join of 19 parts.
+// Softmax beside a product that takes both operands from shared memory is 2.3 times slower; that is
+// why heads of 64 keep Q in tensor memory.
 
 #include "sd_kv.cuh"
 #include "sd_tc.cuh"
