@@ -519,7 +519,7 @@ SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const v
  * q is taken exactly but for what lies below 2^-17 of its largest magnitude; exponentials, sums and
  * products are fp32; the weights of v have 8 significant bits, and steps of 2^-16 of the row's
  * largest at the finest; out is rounded to bf16 once. The V scales of the pages that one token sees
- * lie within 2^80 of one another (a scale of 0 may be among them). A token that sees nothing gets
+ * lie within 2^80 of one another (a scale of 0 counts as 2^-60). A token that sees nothing gets
  * out = 0 and lse = -inf. NaN in tokens that a query token does not see has no effect on it. The
  * same call gives the same bits: parts of a request are joined in a fixed order.
  * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] raises

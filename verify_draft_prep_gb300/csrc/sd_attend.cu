@@ -47,8 +47,8 @@ constexpr int kTile = 128;                 // tokens of a tile, rows of a stream
 constexpr int kAttThreads = 384;
 constexpr int kMaxCtas = 160;
 constexpr int kScaleSlots = 16;            // tiles of scales in flight
-// A page whose V scale is 0 holds zeros: its tokens weigh in L only. They are given a scale below
-// that of any page with values, so that those keep P's full precision.
+// A page whose V scale is 0 holds zeros: its tokens weigh in L only. They are given a scale far below
+// that of pages with values of any ordinary size, so that those keep P's full precision.
 constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
 // P = 2^(y - M + kShift) is at most 448 while M is no more than kSlack behind the row's maximum. A
 // larger shift keeps more of the small weights, a larger slack has the accumulator rescaled less
