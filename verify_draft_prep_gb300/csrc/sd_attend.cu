@@ -8,11 +8,11 @@
 // The cache's bytes go to the tensor cores as they are, without being converted: an e4m3 value has
 // 4 significant bits and bf16 has 8, so q is split into two e4m3 terms, q = q1 + q2 (after a power
 // of two per row brings its largest magnitude to [224, 448]; exact but for what lies below 2^-17 of
-// that), and so is each weight P = P1 + P2 (P at most 448 there, too). Two e4m3 products take the
+// that), and each weight into an e5m2 and an e4m3 term, P = P1 + P2. Two 8-bit products take the
 // time of one bf16 product, and K and V cost half the shared memory and no instructions. A page's
 // scales enter as numbers per 8 columns of S: with y = log2(e) S + log2(v_scale),
 //   P = 2^(y - M + kShift),  O = sum P v_byte,  L = sum P / v_scale,
-// M the running maximum of y, so that one exponential serves both sums.
+// M a reference that keeps near the tiles' largest y, so that one exponential serves both sums.
 //
 // A unit is one request's 128 (or 256) rows of one KV head; a row is a query token and one of the
 // Hq / Hkv heads that share the KV head. All units' tiles of 128 tokens form one line, which the
@@ -50,11 +50,19 @@ constexpr int kScaleSlots = 16;            // tiles of scales in flight
 // A page whose V scale is 0 holds zeros: its tokens weigh in L only. They are given a scale far below
 // that of pages with values of any ordinary size, so that those keep P's full precision.
 constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
-// P = 2^(y - M + kShift) is at most 448 while M is no more than kSlack behind the row's maximum. A
-// larger shift keeps more of the small weights, a larger slack has the accumulator rescaled less
-// often, and the two share e4m3's range (2^(7 + 1.75) < 448). P has 8 bits, steps of 2^-9 at the
-// finest: 2^-16 of 2^7, the row's largest weight when M is its maximum.
-constexpr float kShift = 7.f, kSlack = 1.75f;
+// P = 2^(y - M + kShift), M the row's reference, as P1 + P2: P1 is P to 3 significant bits (e5m2),
+// P2 the rest, at most 2^-3 of P's binade, to 4 (e4m3). Below 2^12 P2 stays within e4m3's 448. P has 8
+// significant bits down to 2^-2, where P2 reaches e4m3's finest step of 2^-9, and fewer below, 3 down to
+// 2^-14. A long context can hold thousands of weights far below one dominant token's, which together
+// are the answer where that token's V is small. So M follows the tiles both ways: up where a tile's
+// largest y passes M + kSlack, down where it lies below M - kFall, and every tile's largest P is
+// between 2^(kShift - kFall) = 2^-2 and 2^(kShift + kSlack) < 2^12. A window narrower than that has the
+// accumulator rescaled more often. M falls to kAbove above the tile's largest y, so that the next
+// tiles find room on either side, and kDeepest at most below the largest M so far, so that the
+// accumulator (up to 2^21 a token at the largest M) stays within fp32; nor beyond kMaxL for L, which a
+// small V scale enlarges.
+constexpr float kShift = 10.f, kSlack = 1.9f, kFall = 12.f, kAbove = 2.f, kDeepest = 60.f;
+constexpr float kMaxL = 1e30f;
 constexpr float kTiny = 1.17549435e-38f;  // -inf times it is -inf, S times it is nothing
 constexpr float kLog2eF = 1.4426950408889634f, kLn2F = 0.6931471805599453f;
 
@@ -113,7 +121,7 @@ struct AttMisc {
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
   int sc_zero[kScaleSlots];   // bit e: entry e's V scale is zero
   float row_scale[2 * kTile];
-  float2 ml[2][kTile];        // (M, L) of both streams
+  float2 ml[2][kTile];        // (M, L) of both streams; before a unit's end (the largest M so far, -)
   int nan_first[2][128];      // first token with a NaN in dimension d of V, of a masked tile
   int nan_any[2];
   int start_item[4];          // of the schedule
@@ -449,12 +457,13 @@ __device__ __forceinline__ float weights(const uint32_t (&v)[32], const float4* 
                               make_float2(k, k), make_float2(a, a));
         const float2 p = make_float2(ex2f(x.x), ex2f(x.y));
         sum = add2(sum, p);
-        // the leading 4 significant bits, and the rest
-        h[u] = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xfff00000u),
-                           __uint_as_float(__float_as_uint(p.y) & 0xfff00000u));
+        // to 3 significant bits, and the rest: the last bit of 2^21 p + p is worth a quarter of p's
+        // binade, of which 2^21 p is a multiple
+        const float2 up = fma2(p, make_float2(2097152.f, 2097152.f), p);
+        h[u] = fma2(p, make_float2(-2097152.f, -2097152.f), up);
         l[u] = fma2(h[u], make_float2(-1.f, -1.f), p);
       }
-      o[g * 2 + i] = f32_to_e4m3x4(h[0].x, h[0].y, h[1].x, h[1].y);
+      o[g * 2 + i] = f32_to_e5m2x4(h[0].x, h[0].y, h[1].x, h[1].y);
       o[8 + g * 2 + i] = f32_to_e4m3x4(l[0].x, l[0].y, l[1].x, l[1].y);
     }
     part = fmaf(sum.x + sum.y, f.z, part);
@@ -638,7 +647,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
   } else if (warp == 1) {
     // ---- products: the warp waits, one elected lane issues ----
     constexpr uint32_t hi = desc_hi<DP>();
-    constexpr uint32_t qk_idesc = mma_desc(kTile, false), pv_idesc = mma_desc(DP, true);
+    constexpr uint32_t qk_idesc = mma_desc(kTile, false, false);
+    constexpr uint32_t pv_idesc[2] = {mma_desc(DP, true, true), mma_desc(DP, true, false)};
     const bool lead = elect_one();
     const uint32_t q_lo = desc_lo<DP>(base + L::kQ), k_lo = desc_lo<DP>(base + L::kK),
                    v_lo = desc_lo<DP>(base + L::kV);
@@ -670,11 +680,10 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       const uint32_t d = tmem + L::kTmO + x * DP, a = tmem + x * 128,
                      v = v_lo + v_st * (L::kTileBytes / 16);
 #pragma unroll
-      for (int kk = 0; kk < kTile / 32; ++kk)
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-          mma_ts<hi, pv_idesc>(d, a + kk * 16 + term * 8, v + kk * (32 * DP / 16),
-                               add || kk + term > 0);
+      for (int kk = 0; kk < kTile / 32; ++kk) {
+        mma_ts<hi, pv_idesc[0]>(d, a + kk * 16, v + kk * (32 * DP / 16), add || kk > 0);
+        mma_ts<hi, pv_idesc[1]>(d, a + kk * 16 + 8, v + kk * (32 * DP / 16), true);
+      }
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && mbar_wait_warp(smem_u32(bar), parity, gave_up);
@@ -910,6 +919,10 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     // comes after that stream's product with it, has to be there. Else it was this stream's own.
     // (Waiting for S first everywhere: a prompt of 8192 tokens 602 instead of 588 us.)
     constexpr bool kSFirst = NS == 1 && SV % 2 == 1;
+    // The accumulator is rescaled before P is formed (heads of 64), or after, when S's registers are
+    // free and 64 columns go at a time. Before against after: 64 requests 120 to 123 us, drafter batch
+    // 408 to 413, prompt 663 to 639.
+    constexpr bool kLate = DP == 128;
     int it = 0, nq = 0, unit = 0;
     int done = 0;  // tiles of this stream so far
     bool ok = true;
@@ -953,6 +966,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
       const int lim = seen_by(P, s.q, min(row, s.row0 + s.rows - 1));
       const int min_lim = seen_by(P, s.q, s.row0 + row_base);
       float M = -INFINITY, Lsum = 0.f;
+      m.ml[x][wt].x = -INFINITY;  // (every reader of the last unit's has passed its barrier)
 
       // 2. tiles
       for (int j = NS == 1 ? x : 0; ok && j < T; j += NS == 1 ? 2 : 1) {
@@ -1051,32 +1065,42 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
               tmem_wait_ld();
             }
           }
-          const bool grow = mx > M + kSlack;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float Mn = fmaxf(M, mx);
-            if (j >= (NS == 1 ? 2 : 1)) {
-              const float fac = M == -INFINITY ? 0.f : ex2f(M - Mn);
-              ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < DP; c += 32) {
-                uint32_t u[2][16];
-                tmem_ld16(tO + c, u[0]);
-                tmem_ld16(tO + c + 16, u[1]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    u[k][i] = __float_as_uint(__uint_as_float(u[k][i]) * fac);
-                  tmem_st16(tO + c + k * 16, u[k]);
-                }
-              }
-              Lsum *= fac;
-            }
+          const bool fall = mx < M - kFall && mx > -INFINITY;
+          const bool moved = __any_sync(0xffffffffu, mx > M + kSlack || fall);
+          float fac = 1.f;
+          if (moved) {
+            const float top = m.ml[x][wt].x;
+            float Mn = fall ? fmaxf(mx + kAbove, top - kDeepest) : fmaxf(M, mx);
+            if (fall && !(Lsum * ex2f(M - Mn) < kMaxL)) Mn = M;
+            m.ml[x][wt].x = fmaxf(top, Mn);
+            fac = M == -INFINITY ? 0.f : ex2f(M - Mn);
+            Lsum *= fac;
             M = Mn;
           }
+          // The accumulator's old sums in the new reference's units.
+          auto rescale = [&] {
+            if (!moved || j < (NS == 1 ? 2 : 1)) return;
+            ok = mbar_wait_warp(smem_u32(&m.o_done[x]), (done - 1) & 1, gave_up);
+            if (!ok) return;
+            tc_fence_after();
+            constexpr int kStep = kLate ? 2 : 1;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32 * kStep) {
+              uint32_t u[kStep][32];
+#pragma unroll
+              for (int k = 0; k < kStep; ++k) tmem_ld32(tO + c + k * 32, u[k]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < kStep; ++k) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  u[k][i] = __float_as_uint(__uint_as_float(u[k][i]) * fac);
+                tmem_st32(tO + c + k * 32, u[k]);
+              }
+            }
+          };
+          if (!kLate) rescale();
+          if (!ok) break;
           const float shift = kShift - (M == -INFINITY ? 0.f : M);
           uint32_t o[16];
           if (NC <= 2) {
@@ -1099,6 +1123,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
               tmem_st16(tS + (c + 1) * 16, o);
             }
           }
+          if (kLate) rescale();
+          if (!ok) break;
           if (R > 1) {  // the other copies' columns count as zero here
             const uint32_t none[16] = {};
 #pragma unroll

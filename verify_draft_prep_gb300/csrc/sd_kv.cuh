@@ -50,6 +50,15 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x4(float v0, float v1, float v2, 
   return r;
 }
 
+// Four fp32 of 3 significant bits to e5m2, exactly from 2^-14 to 57344, NaN to NaN.
+__device__ __forceinline__ uint32_t f32_to_e5m2x4(float v0, float v1, float v2, float v3) {
+  uint32_t r;
+  asm("cvt.rs.satfinite.e5m2x4.f32 %0, {%1, %2, %3, %4}, %5;"
+      : "=r"(r)
+      : "f"(v3), "f"(v2), "f"(v1), "f"(v0), "r"(0x80018001u));
+  return r;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 

@@ -187,9 +187,9 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// M = 128, fp32 accumulator, both operands e4m3; b_mn: B's rows run along the summed index.
-__host__ __device__ constexpr uint32_t mma_desc(int N, bool b_mn) {
-  return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
+// M = 128, fp32 accumulator, B e4m3, A e4m3 or e5m2; b_mn: B's rows run along the summed index.
+__host__ __device__ constexpr uint32_t mma_desc(int N, bool b_mn, bool a_e5m2) {
+  return 1u << 4 | (a_e5m2 ? 1u << 7 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
 
 template <uint32_t HI, uint32_t IDESC>
