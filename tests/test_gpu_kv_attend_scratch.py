@@ -1,0 +1,50 @@
+"""The scratch of sd_kv_attend: where it may begin, and who may use it at the same time."""
+
+import pytest
+import torch
+
+import kvref
+import verify_draft_prep_gb300 as sd
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+class Call:
+    """Requests of uneven lengths, of which several CTAs share some."""
+
+    def __init__(self, n_q, ctx, Hq, Hkv, D, seed):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        nb, self.table = kvref.make_table(ctx, 16, g, DEV)
+        self.cache = kvref.make_cache(nb, 16, Hkv, D, g, DEV)
+        n = sum(n_q)
+        self.q = torch.randn(n, Hq, D, generator=g, device=DEV).bfloat16()
+        self.cu = kvref.prefix(n_q, DEV)
+        self.lens = torch.tensor(ctx, dtype=torch.int32, device=DEV)
+        self.max_q = max(n_q)
+
+    def __call__(self, out=None, **kw):
+        out = torch.zeros_like(self.q) if out is None else out
+        sd.sd_kv_attend(self.q, *self.cache, self.table, self.lens, self.cu, out, max_q=self.max_q,
+                        **kw)
+        return out
+
+
+# units of 32, 64, 128 and 256 rows
+FORMS = [(4, 8), (8, 8), (15, 8), (40, 8)]
+
+
+@pytest.mark.parametrize("n,G", FORMS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_scratch_at_any_multiple_of_16(n, G, D):
+    c = Call([n, n, n], [9000, 200, 4000], 2 * G, 2, D, seed=n + D)
+    need = sd.sd_kv_attend_workspace_bytes(D)
+    room = torch.empty(need + 64, dtype=torch.uint8, device=DEV)
+    want = c()
+    for at in (0, 16, 32, 48):
+        guard = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device=DEV)
+        room.copy_(guard)
+        assert torch.equal(c(workspace_buf=room[at:at + need]), want)
+        assert torch.equal(room[:at], guard[:at])
+        assert torch.equal(room[at + need:], guard[at + need:])

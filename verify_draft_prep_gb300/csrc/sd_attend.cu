@@ -416,7 +416,8 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
-// 32 bytes: a whole sector, so that rows far apart are written without partial ones.
+// 32 bytes: a whole sector, so that rows far apart are written without partial ones. p is a multiple
+// of 32.
 __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -1505,7 +1506,9 @@ static int launch_attend(const AttendParams& P, const CUtensorMap& km, const CUt
 extern "C" size_t sd_kv_attend_workspace_launch(int D) {
   const long slot = D <= 64 ? sdk::AttLayout<64, 2, 1>::kSlotFloats
                             : sdk::AttLayout<128, 2, 1>::kSlotFloats;
-  return sdk::kMaxCtas * sizeof(sdk::JoinDesc) + (size_t)2 * sdk::kMaxCtas * slot * sizeof(float);
+  // (16 bytes to begin at a multiple of 32)
+  return 16 + sdk::kMaxCtas * sizeof(sdk::JoinDesc) +
+         (size_t)2 * sdk::kMaxCtas * slot * sizeof(float);
 }
 
 extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q,
@@ -1538,7 +1541,9 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   P.hs_out = hs_out;
   P.lse = lse;
   P.out_32 = (uintptr_t)out % 32 == 0 && ld_out % 16 == 0 && hs_out % 16 == 0;
-  P.ws = (unsigned char*)workspace;
+  // store32 needs every part of a row at a multiple of 32; the caller's scratch is at one of 16
+  static_assert(sizeof(sdk::JoinDesc) % 32 == 0, "the parts begin at a multiple of 32");
+  P.ws = (unsigned char*)(((uintptr_t)workspace + 31) / 32 * 32);
   P.err = err;
   // A CTA's least share: a unit's cost and 4 tiles. With 1, 4 and 16 tiles one token at 500 tokens
   // takes 16.2, 14.7, 21.5 us, at 1000 19.8, 19.1, 27.5, at 4000 20.9, 23.1, 30.8.
