@@ -454,7 +454,8 @@ SD_API int sd_hidden_gather(int capacity, int H, const int32_t* total_out, const
  *   - A page is block_size tokens, a power of two from 8 to 128. K and V hold one e4m3 byte for
  *     each value: value d of head h of slot t of page b is at
  *     b*st_block + t*st_tok + h*st_head + d of k_cache and of v_cache (strides in elements; base
- *     addresses 16-byte aligned, strides multiples of 16). D is a multiple of 16 from 16 to 128.
+ *     addresses 16-byte aligned, strides multiples of 16). D is a multiple of 16 from 16 to 128,
+ *     Hkv at most 2^22.
  *   - k_scale and v_scale [num_blocks, Hkv] fp32 hold one scale for each page and head: the byte q
  *     stands for e4m3(q) * scale. sd_kv_write makes powers of two, so that every product with a
  *     scale is exact; reads take any positive scale. A scale of 0 means that the page holds zeros
@@ -482,7 +483,7 @@ SD_API int sd_hidden_gather(int capacity, int H, const int32_t* total_out, const
  * slot the last is kept. Two stretches of the same page in one call race on its scale.
  * Arguments: k, v: bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
  *   strides multiples of 8; they may be slices of one projection); slot_mapping [n] int32;
- *   num_blocks*block_size <= 2^31.
+ *   num_blocks*block_size <= 2^31; n <= 2^31 - 1024.
  */
 SD_API int sd_kv_write(int n, int Hkv, int D, const void* k, long ld_k, long hs_k, const void* v,
                        long ld_v, long hs_v, const int32_t* slot_mapping, void* k_cache,
@@ -497,8 +498,8 @@ SD_API int sd_kv_write(int n, int Hkv, int D, const void* k, long ld_k, long hs_
  * first_pos[r] + i - cu_tokens[r] (first_pos NULL: 0): e4m3(q) * scale rounded to bf16 (exact for
  * power-of-two scales, unless it leaves bf16's range). Rows outside [cu_tokens[0], cu_tokens[B])
  * are not written; a position that the table does not cover reads as 0 with SD_ERR_KV_RANGE.
- * Arguments: n rows; cu_tokens [B+1], non-decreasing; k_out, v_out bf16, value d of head h of row
- *   i at i*ld_out + h*hs_out + d (16-byte aligned, strides multiples of 8).
+ * Arguments: n rows, n <= 2^31 - 1024; cu_tokens [B+1], non-decreasing; k_out, v_out bf16, value d
+ *   of head h of row i at i*ld_out + h*hs_out + d (16-byte aligned, strides multiples of 8).
  */
 SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const void* v_cache,
                       long st_block, long st_tok, long st_head, const float* k_scale,
@@ -524,14 +525,14 @@ SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const v
  * token, too. The V scales of the pages that one token sees lie within 2^80 of one another (a scale of
  * 0 counts as 2^-60). A token that sees nothing gets out = 0 and lse = -inf. NaN in tokens that a query token does not see has no effect on it. The
  * same call gives the same bits: parts of a request are joined in a fixed order.
- * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] raises
- * SD_ERR_KV_RANGE; those tokens are left out. cu_q has B+1 non-decreasing entries in [0, n]
- * (others are clamped, SD_ERR_KV_RANGE); tokens outside [cu_q[0], cu_q[B]) are not written.
+ * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] (or beyond
+ * 2^31 - 256) raises SD_ERR_KV_RANGE; those tokens are left out. cu_q has B+1 non-decreasing entries
+ * in [0, n] (others are clamped, SD_ERR_KV_RANGE); tokens outside [cu_q[0], cu_q[B]) are not written.
  * Arguments: q, out bf16, value d of head h of token i at i*ld + h*hs + d (16-byte aligned,
  *   strides multiples of 8); lse [n, Hq] fp32 or NULL; max_q: the most query tokens that a request
  *   is expected to have, which only chooses the kernel (any value >= 1 is right); Hq a multiple of
- *   Hkv; num_blocks >= 1; sm_scale positive and finite; workspace: at least
- *   sd_kv_attend_workspace_bytes(D) bytes of device scratch, 16-byte aligned, its contents
+ *   Hkv; n*Hq and B <= 2^31 - 1024; num_blocks >= 1; sm_scale positive and finite; workspace: at
+ *   least sd_kv_attend_workspace_bytes(D) bytes of device scratch, 16-byte aligned, its contents
  *   irrelevant before and after. Calls that may run concurrently need separate workspaces.
  */
 SD_API int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q, long ld_q,

@@ -16,3 +16,46 @@ def test_attend_scratch_has_room_to_be_aligned(lib, D):
     """The parts are written 32 bytes at a time and take a whole number of them; a caller's scratch
     begins at any multiple of 16, so there are 16 bytes more than the parts take."""
     assert lib.sd_kv_attend_workspace_bytes(D) % 32 == 16
+
+
+P = 256  # a well aligned dummy address; no call below gets as far as using it
+END = 2 ** 31 - 1
+CACHE = [P, P, 2048, 128, 64, P, P, 4, 16]  # k, v, strides, scales, num_blocks, block_size
+
+
+def write(lib, n):
+    return lib.sd_kv_write(n, 2, 64, P, 128, 64, P, 128, 64, P, *CACHE, None, None)
+
+
+def read(lib, n):
+    return lib.sd_kv_read(2, n, 2, 64, *CACHE, P, 4, P, None, P, P, 128, 64, None, None)
+
+
+def attend(lib, B, n, Hq, Hkv):
+    return lib.sd_kv_attend(B, n, 8, Hq, Hkv, 64, P, 256, 64, *CACHE, P, 4, P, P, 0.125, 1, P, 256,
+                            64, None, P, 1 << 40, None, None)
+
+
+@pytest.mark.parametrize("below", [0, 1, 15, 255, 1022])
+def test_counts_near_the_end_of_int_are_refused(lib, below):
+    """The kernels step over tokens and rows in int: within a step of its end they would wrap around
+    and, over rows, never end."""
+    n = END - below
+    assert write(lib, n) == -2
+    assert read(lib, n) == -2
+    assert attend(lib, 2, n, 1, 1) == -2
+    assert attend(lib, n, 3, 4, 2) == -2
+
+
+def test_rows_of_shared_heads_count_too(lib):
+    assert attend(lib, 2, END // 16, 16, 1) == -2
+    assert attend(lib, 2, END // 48, 48, 2) == -2
+
+
+def test_heads_that_one_token_cannot_have_are_refused(lib):
+    """A CTA counts a token's heads times its tokens in int."""
+    for Hkv in (END, 1 << 30, (1 << 22) + 1):
+        assert lib.sd_kv_write(3, Hkv, 64, P, 128, 64, P, 128, 64, P, *CACHE, None, None) == -2
+        assert lib.sd_kv_read(2, 3, Hkv, 64, *CACHE, P, 4, P, None, P, P, 128, 64, None, None) == -2
+        assert lib.sd_kv_attend(2, 3, 8, Hkv, Hkv, 64, P, 256, 64, *CACHE, P, 4, P, P, 0.125, 1, P,
+                                256, 64, None, P, 1 << 40, None, None) == -2

@@ -598,7 +598,7 @@ int cache_log2_bs(int block_size) {
 // What every call on the 8-bit cache checks of it.
 int check_cache(int Hkv, int D, long st_block, long st_tok, long st_head, int num_blocks,
                 int block_size) {
-  if (Hkv < 1 || D < 16 || D > 128 || D % 16) return SD_E_SHAPE;
+  if (Hkv < 1 || Hkv > 1 << 22 || D < 16 || D > 128 || D % 16) return SD_E_SHAPE;
   const int l = cache_log2_bs(block_size);
   if (l < 0 || num_blocks < 0 || ((long)num_blocks << l) > 2147483648L) return SD_E_SHAPE;
   if (st_block < 1 || st_tok < 1 || st_head < 1) return SD_E_SHAPE;
@@ -608,13 +608,17 @@ int check_cache(int Hkv, int D, long st_block, long st_tok, long st_head, int nu
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
+// The kernels step over tokens, rows and requests in int, some hundreds at a time: their numbers stay
+// this far below 2^31.
+constexpr long long kMostCounted = 2147483647LL - 1023;
+
 }  // namespace
 
 int sd_kv_write(int n, int Hkv, int D, const void* k, long ld_k, long hs_k, const void* v,
                 long ld_v, long hs_v, const int32_t* slot_mapping, void* k_cache, void* v_cache,
                 long st_block, long st_tok, long st_head, float* k_scale, float* v_scale,
                 int num_blocks, int block_size, int32_t* err, void* stream) {
-  if (n < 0 || ld_k < 0 || ld_v < 0 || hs_k < 0 || hs_v < 0) return SD_E_SHAPE;
+  if (n < 0 || n > kMostCounted || ld_k < 0 || ld_v < 0 || hs_k < 0 || hs_v < 0) return SD_E_SHAPE;
   const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
   if (rc != SD_OK) return rc;
   if (n == 0) return SD_OK;
@@ -635,7 +639,8 @@ int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const void* v_
                const float* v_scale, int num_blocks, int block_size, const int32_t* block_table,
                int max_blocks, const int32_t* cu_tokens, const int32_t* first_pos, void* k_out,
                void* v_out, long ld_out, long hs_out, int32_t* err, void* stream) {
-  if (B < 0 || n < 0 || max_blocks < 0 || ld_out < 0 || hs_out < 0) return SD_E_SHAPE;
+  if (B < 0 || n < 0 || n > kMostCounted || max_blocks < 0 || ld_out < 0 || hs_out < 0)
+    return SD_E_SHAPE;
   const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
   if (rc != SD_OK) return rc;
   if (B == 0 || n == 0) return SD_OK;
@@ -668,7 +673,8 @@ int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q,
     return SD_E_SHAPE;
   const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
   if (rc != SD_OK) return rc;
-  if (Hq % Hkv || (long long)n * Hq > 2147483647LL || num_blocks < 1) return SD_E_SHAPE;
+  if (Hq % Hkv || (long long)n * Hq > kMostCounted || B > kMostCounted || num_blocks < 1)
+    return SD_E_SHAPE;
   if (!(sm_scale > 0.f && sm_scale <= 3.402823466e38f)) return SD_E_SHAPE;
   if (B == 0 || n == 0) return SD_OK;
   if (!q || !ctx_lens || !cu_q || !out || !workspace || (max_blocks > 0 && !block_table))

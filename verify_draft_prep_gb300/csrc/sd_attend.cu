@@ -141,6 +141,11 @@ struct Request {
   int tok0, n_q, rows, len, off;
 };
 
+// Tokens that a request's table covers; positions of a tile's end stay within int.
+__device__ __forceinline__ long covered(const AttendParams& P) {
+  return min((long)P.max_blocks << P.c.log2_bs, 2147483648L - 2 * kTile);
+}
+
 __device__ __forceinline__ Request request_of(const AttendParams& P, int r) {
   Request q;
   // (plain loads: a read-only one may be moved up before the wait for the work before this kernel)
@@ -150,15 +155,14 @@ __device__ __forceinline__ Request request_of(const AttendParams& P, int r) {
   q.n_q = hi - lo;
   q.rows = q.n_q * P.G;
   const int ctx = P.ctx[r];
-  const long cover = (long)P.max_blocks << P.c.log2_bs;
-  q.len = ctx < 0 ? 0 : (int)min((long)ctx, cover);
+  q.len = ctx < 0 ? 0 : (int)min((long)ctx, covered(P));
   q.off = (int)max((long)ctx - q.n_q, -2147483647L);
   return q;
 }
 
 __device__ __forceinline__ bool request_bad(const AttendParams& P, int r) {
   const int a = P.cu[r], b = P.cu[r + 1], ctx = P.ctx[r];
-  return a < 0 || b < a || b > P.n || ctx < 0 || ctx > ((long)P.max_blocks << P.c.log2_bs);
+  return a < 0 || b < a || b > P.n || ctx < 0 || ctx > covered(P);
 }
 
 // Tokens that a row sees.

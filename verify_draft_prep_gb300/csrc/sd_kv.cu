@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadParam
     if (i < P.n && i >= P.cu[0] && i < P.cu[P.B]) {
       int lo = 0, hi = P.B;  // the last r with cu[r] <= i
       while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);
         if (P.cu[mid] <= i) lo = mid;
         else hi = mid;
       }
