@@ -553,8 +553,8 @@ SD_API size_t sd_kv_attend_workspace_bytes(int D);
  * out_tokens on its target rows), with each row's entropy and best alternatives.
  *
  * Row r*J + j of rows belongs to tokens[r][j] (J = K+1 for sd_verify's outputs). SD_F32_PROBS:
- * p = the row. SD_BF16_LOGITS: p = softmax(l / T_r), T_r = temperature[r] (NULL, or 0: 1; a
- * greedy request is reported at temperature 1).
+ * p = the row. SD_BF16_LOGITS: p = softmax(l / T_r), T_r = temperature[r], taken within 2^-100 and
+ * 2^100 (NULL, or 0: 1; a greedy request is reported at temperature 1).
  *   logprob[r][j] = ln p(token)
  *   entropy[r][j] = -sum p ln p
  *   rank[r][j]    = 1 + the entries that come before the token, larger ones first, equal ones by

@@ -126,18 +126,34 @@ __device__ __forceinline__ float p_log2_p(float p) {
   return p * (p > 0.5f ? log2f(p) : __log2f(p));
 }
 
-// Logits: a reference r, z = sum 2^t and s = sum t 2^t with t = c l - r, c = log2(e) / T;
-// probabilities: s = sum p log2 p.
+// Logits: a reference logit ref, z = sum 2^t and s = sum t 2^t with t = c l - r, c = log2(e) / T and
+// r = ref c rounded once; probabilities: s = sum p log2 p.
 struct Sums {
-  float r, z, s;
+  float ref, z, s;
 };
 
-// Joins sums over different references.
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+// The temperature of a row: c = log2(e) / T, and what of its logits is taken with it as it stands.
+// Where |ref| c passes 2^26, bf16 logits that differ from ref do so by 2^18 units or more, products can
+// overflow and r's rounding is no small part of a binade: a row with a logit from `to` on, or without
+// one above `from`, is taken by extreme_sums. `low`, 2^27 units below 0, stands for what is below it: 2^t
+// is 0 there under any reference, and t 2^t too because t stays finite (-inf would make it NaN).
+struct Heat {
+  float c, from, to;
+  __nv_bfloat162 low;
+};
+__device__ __forceinline__ Heat heat_of(float c) {
+  const float most = 67108864.f / c;
+  return Heat{c, -most, most, __float2bfloat162_rn(-2.f * most)};
+}
+
+// Joins sums over different references (-inf: none yet, +inf: one beyond Heat::to).
+__device__ __forceinline__ float shift_of(float from, float to, float c) {
+  return from == to ? 0.f : fmaxf(__fmul_rn(from, c) - __fmul_rn(to, c), -1e4f);
+}
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
   Sums q;
-  q.r = fmaxf(a.r, b.r);
-  const float da = a.r == q.r ? 0.f : fmaxf(a.r - q.r, -1e4f);
-  const float db = b.r == q.r ? 0.f : fmaxf(b.r - q.r, -1e4f);
+  q.ref = fmaxf(a.ref, b.ref);
+  const float da = shift_of(a.ref, q.ref, c), db = shift_of(b.ref, q.ref, c);
   const float fa = ex2(da), fb = ex2(db);
   q.z = a.z * fa + b.z * fb;
   q.s = (a.s + da * a.z) * fa + (b.s + db * b.z) * fb;
@@ -165,6 +181,7 @@ __device__ __forceinline__ float2 lp_add2(float2 a, float2 b) {
 struct LpShared {
   Sums warp_sums[kLpWarps];
   int warp_rank[kLpWarps];
+  float ref[kLpThreads];        // each thread's own
   Sums sums[kLpMaxCluster];     // rank 0's, written by every CTA of the cluster
   int rank[kLpMaxCluster];
   uint64_t best[kLpMaxCluster][SD_TOP_MAX];
@@ -186,17 +203,61 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
-// A lane's running sums, in pairs, and how many entries come before the token.
+// A lane's running sums, in pairs, and how many entries come before the token; t = c l + nr. An entry
+// above `edge` moves the reference (kept in LpShared::ref).
 struct Lane {
-  float r;
+  float edge, nr;
   float2 z, s;
   int better;
 };
 
+// Moves a lane's reference up to gm.
+__device__ __forceinline__ void move_to(Lane& q, float& ref, float gm, const Heat& heat) {
+  if (!(gm < heat.to)) {
+    ref = q.edge = INFINITY;
+    return;
+  }
+  const float nr = -__fmul_rn(gm, heat.c);
+  const float d = ref == -INFINITY ? -1e4f : fmaxf(nr - q.nr, -1e4f);
+  const float f = ex2(d);
+  q.s = make_float2((q.s.x + d * q.z.x) * f, (q.s.y + d * q.z.y) * f);
+  q.z = make_float2(q.z.x * f, q.z.y * f);
+  q.nr = nr;
+  ref = gm;
+  // it moves only when it is 8 units behind (the sums have room, and a logarithm near 0 still comes from
+  // numbers near 0)
+  q.edge = fmaf(heat.to, 1.1920929e-7f, gm);  // (2^-23 of 2^26 units)
+}
+
+// Sums of a thread's logits of the whole row, whatever they are: the reference is their largest, what is
+// below it weighs nothing where it is beyond Heat's range (a step of bf16 is 2^18 units there).
+__device__ __noinline__ Sums extreme_sums(const uint16_t* x, int V, const Heat& heat) {
+  Sums q{-INFINITY, 0.f, 0.f};
+  for (int i = threadIdx.x; i < V; i += kLpThreads) {
+    const float v = __uint_as_float((uint32_t)__ldg(x + i) << 16);
+    if (v != v || v == INFINITY) q.z = nanf("");
+    if (!(v > -INFINITY) || v == INFINITY) continue;
+    if (v > q.ref) {
+      const float d = shift_of(q.ref, v, heat.c), f = ex2(d);
+      q.s = (q.s + d * q.z) * f;
+      q.z *= f;
+      q.ref = v;
+    }
+    if (fabsf(q.ref) < heat.to) {
+      const float t = fmaxf(fmaf(v, heat.c, -__fmul_rn(q.ref, heat.c)), -1e4f), p = ex2(t);
+      q.z += p;
+      q.s += t * p;
+    } else if (v == q.ref) {
+      q.z += 1.f;
+    }
+  }
+  return q;
+}
+
 // Takes in a group of U vectors a lane (entries g0 .. g0 + 256 U - 1); returns the lane's largest.
 template <int DT, int U>
-__device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], float c, float xt, int g0,
-                                      int token, int V, int lane) {
+__device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], const Heat& heat,
+                                      float& ref, float xt, int g0, int token, int V, int lane) {
   float gm;
   // a group that holds the token or ends the row is looked at entry by entry for the rank
   const bool edge = (token >= g0 && token < g0 + U * kVec) || g0 + U * kVec > V;
@@ -230,26 +291,15 @@ __device__ __forceinline__ float take(Lane& q, const Raw<DT> (&raw)[U], float c,
       }
       q.better += (int)(__low2float(n2) + __high2float(n2));
     }
-    // the reference moves only when it is some way behind (the sums have room, and a logarithm
-    // near 0 still comes from numbers near 0)
-    const float y = gm * c;
-    if (!(y - q.r <= 8.f) && gm > -INFINITY) {
-      const float d = q.r == -INFINITY ? 0.f : fmaxf(q.r - y, -1e4f);
-      const float f = ex2(d);
-      q.s = make_float2((q.s.x + d * q.z.x) * f, (q.s.y + d * q.z.y) * f);
-      q.z = make_float2(q.z.x * f, q.z.y * f);
-      q.r = y;
-    }
-    const float nr = q.r == -INFINITY ? 0.f : -q.r;
-    // -inf becomes a finite number far below (2^t is 0 and t 2^t, too); NaN stays
-    const __nv_bfloat162 low = __float2bfloat162_rn(-1e30f);
+    if (gm > q.edge) move_to(q, ref, gm, heat);
+    // (NaN stays)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t w[4] = {raw[u].a.x, raw[u].a.y, raw[u].a.z, raw[u].a.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(__hmax2_nan(as_bf162(w[i]), low));
-        const float2 t = lp_fma2(f, make_float2(c, c), make_float2(nr, nr));
+        const float2 f = __bfloat1622float2(__hmax2_nan(as_bf162(w[i]), heat.low));
+        const float2 t = lp_fma2(f, make_float2(heat.c, heat.c), make_float2(q.nr, q.nr));
         const float2 p = make_float2(ex2(t.x), ex2(t.y));
         q.z = lp_add2(q.z, p);
         q.s = lp_fma2(t, p, q.s);
@@ -421,27 +471,30 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P
                               : ((const float*)x)[token];
   float T = DT == SD_BF16_LOGITS && P.temperature ? P.temperature[row / P.J] : 1.f;
   if (!(T > 0.f)) T = 1.f;  // a greedy request's rows are reported at temperature 1
+  T = fminf(fmaxf(T, 7.8886090522101181e-31f), 1.2676506002282294e30f);  // 2^-100, 2^100
   const float c = kLog2e / T;
-  Lane q{-INFINITY, make_float2(0.f, 0.f), make_float2(0.f, 0.f), 0};
+  const Heat heat = heat_of(c);
+  sm.ref[tid] = -INFINITY;
+  Lane q{heat.from, 0.f, make_float2(0.f, 0.f), make_float2(0.f, 0.f), 0};
   float tm = nanf("");  // the largest entry of this thread
   for (int g = warp; g < groups; g += kLpWarps) {
     Raw<DT> now[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) now[u] = raw[u];
     fetch(g + kLpWarps);
-    const float gm = take<DT, U>(q, now, c, xt, begin + g * kGroup, token, P.V, lane);
+    const float gm = take<DT, U>(q, now, heat, sm.ref[tid], xt, begin + g * kGroup, token, P.V, lane);
     if (U == 1) tm = fmaxf(tm, gm);
     if (P.n_top > 0) {
       const uint32_t o = __reduce_max_sync(0xffffffffu, order_of(gm));
       if (lane == 0) gmax[g] = o;
     }
   }
-  Sums a{q.r, q.z.x + q.z.y, q.s.x + q.s.y};
+  Sums a{sm.ref[tid], q.z.x + q.z.y, q.s.x + q.s.y};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Sums b{__shfl_xor_sync(0xffffffffu, a.r, o), __shfl_xor_sync(0xffffffffu, a.z, o),
+    Sums b{__shfl_xor_sync(0xffffffffu, a.ref, o), __shfl_xor_sync(0xffffffffu, a.z, o),
            __shfl_xor_sync(0xffffffffu, a.s, o)};
-    if (DT == SD_BF16_LOGITS) a = join(a, b);
+    if (DT == SD_BF16_LOGITS) a = join(a, b, c);
     else a.s += b.s;
   }
   const int rank_part = __reduce_add_sync(0xffffffffu, q.better);
@@ -464,9 +517,9 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P
     int r = lane < kLpWarps ? sm.warp_rank[lane] : 0;
 #pragma unroll
     for (int o = kLpWarps / 2; o > 0; o >>= 1) {
-      Sums d{__shfl_xor_sync(0xffffffffu, b.r, o), __shfl_xor_sync(0xffffffffu, b.z, o),
+      Sums d{__shfl_xor_sync(0xffffffffu, b.ref, o), __shfl_xor_sync(0xffffffffu, b.z, o),
              __shfl_xor_sync(0xffffffffu, b.s, o)};
-      if (DT == SD_BF16_LOGITS) b = join(b, d);
+      if (DT == SD_BF16_LOGITS) b = join(b, d, c);
       else b.s += d.s;
     }
     r = __reduce_add_sync(0xffffffffu, r);
@@ -588,14 +641,27 @@ __global__ void __launch_bounds__(kLpThreads, 8) logprob_kernel(const LpParams P
   Sums t = sm.sums[0];
   int rank = sm.rank[0];
   for (int i = 1; i < C; ++i) {
-    if (DT == SD_BF16_LOGITS) t = join(t, sm.sums[i]);
+    if (DT == SD_BF16_LOGITS) t = join(t, sm.sums[i], c);
     else t.s += sm.sums[i].s;
     rank += sm.rank[i];
   }
+  if (DT == SD_BF16_LOGITS && isinf(t.ref)) {
+    t = extreme_sums((const uint16_t*)x, P.V, heat);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      t = join(t, Sums{__shfl_xor_sync(0xffffffffu, t.ref, o), __shfl_xor_sync(0xffffffffu, t.z, o),
+                       __shfl_xor_sync(0xffffffffu, t.s, o)}, c);
+    __syncthreads();
+    if (lane == 0) sm.warp_sums[warp] = t;
+    __syncthreads();
+    t = sm.warp_sums[0];
+    for (int i = 1; i < kLpWarps; ++i) t = join(t, sm.warp_sums[i], c);
+  }
   const float log2_z = DT == SD_BF16_LOGITS ? log2f(t.z) : 0.f;
-  auto lp = [&](float v) {
-    return DT == SD_BF16_LOGITS ? (fmaf(v, c, -t.r) - log2_z) * kLn2 : logf(v);
-  };
+  // z is in units of 2^r, r a rounded ref c: the rest of that comes off
+  const float ln_z =
+      (log2_z - (fabsf(t.ref) < heat.to ? fmaf(t.ref, c, -__fmul_rn(t.ref, c)) : 0.f)) * kLn2;
+  auto lp = [&](float v) { return DT == SD_BF16_LOGITS ? (v - t.ref) * (c * kLn2) - ln_z : logf(v); };
   if (tid == 0) {
     P.logprob[row] = in_range ? lp(xt) : -INFINITY;
     if (P.entropy)
