@@ -48,3 +48,51 @@ def test_scratch_at_any_multiple_of_16(n, G, D):
         assert torch.equal(c(workspace_buf=room[at:at + need]), want)
         assert torch.equal(room[:at], guard[:at])
         assert torch.equal(room[at + need:], guard[at + need:])
+
+
+def test_streams_without_scratch_of_their_own():
+    """Calls whose requests are shared by many CTAs, on two streams at once: each as it is alone."""
+    calls = [Call([40], [30000], 16, 2, 64, seed=1), Call([40], [28000], 16, 2, 64, seed=2),
+             Call([30, 30], [9000, 15000], 16, 2, 128, seed=3)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [[torch.zeros_like(c.q) for _ in range(8)] for c in calls]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j, (c, s) in enumerate(zip(calls, streams)):
+            if i % 2:
+                with torch.cuda.stream(s):
+                    c(outs[j][i])
+            else:
+                c(outs[j][i], stream=s if i % 4 else s.cuda_stream)
+    torch.cuda.synchronize()
+    for w, got in zip(want, outs):
+        for o in got:
+            assert torch.equal(o, w)
+
+
+def test_graphs_without_scratch_of_their_own():
+    """Two graphs captured one after another, replayed together and beside an eager call."""
+    calls = [Call([40], [30000], 16, 2, 64, seed=1), Call([60], [8000], 16, 2, 128, seed=2)]
+    want = [c() for c in calls]
+    outs = [torch.zeros_like(c.q) for c in calls]
+    graphs = []
+    for c, o in zip(calls, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c(o)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        eager = calls[0]()
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[0])
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+            o.zero_()
+        torch.cuda.synchronize()

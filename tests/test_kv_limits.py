@@ -59,3 +59,45 @@ def test_heads_that_one_token_cannot_have_are_refused(lib):
         assert lib.sd_kv_read(2, 3, Hkv, 64, *CACHE, P, 4, P, None, P, P, 128, 64, None, None) == -2
         assert lib.sd_kv_attend(2, 3, 8, Hkv, Hkv, 64, P, 256, 64, *CACHE, P, 4, P, P, 0.125, 1, P,
                                 256, 64, None, P, 1 << 40, None, None) == -2
+
+
+def test_calls_at_the_same_time_do_not_share_scratch(monkeypatch):
+    """Two threads inside sd_kv_attend, neither with a workspace of its own."""
+    import threading
+
+    import torch
+
+    inside, seen = threading.Barrier(2, timeout=60), []
+
+    class Fake:
+        @staticmethod
+        def sd_kv_attend_workspace_bytes(D):
+            return 4096
+
+        @staticmethod
+        def sd_kv_attend(*args):
+            ws, size = args[-4:-2]
+            seen.append((ws, size))
+            inside.wait()
+            return 0
+
+    monkeypatch.setattr(sd, "_lib", Fake)
+    monkeypatch.setattr(sd, "_attend_bytes", {}, raising=False)
+    monkeypatch.setattr(sd, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(sd, "_raw_stream", lambda t, stream: 0)
+    monkeypatch.setattr(sd, "_device", lambda t: t.device)
+    c = torch.zeros(2, 4, 16, 2, 64, dtype=torch.uint8)
+    s = torch.zeros(4, 2)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    table, lens, cu = (torch.zeros(n, dtype=torch.int32) for n in ((1, 4), (1,), (2,)))
+
+    def call():
+        sd.sd_kv_attend(q, c[0], c[1], s, s, table, lens, cu, torch.zeros_like(q))
+
+    threads = [threading.Thread(target=call) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    (a, size), (b, _) = seen
+    assert abs(a - b) >= size

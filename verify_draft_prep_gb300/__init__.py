@@ -649,20 +649,30 @@ def sd_kv_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_tokens, k_out
     _check(rc, "sd_kv_read")
 
 
-_attend_workspaces = {}
+def attend_workspace(device, D=128):
+    """A scratch buffer of sd_kv_attend on this device, for heads of up to D values."""
+    return _t().empty(sd_kv_attend_workspace_bytes(D), dtype=_t().uint8, device=device)
 
 
-def attend_workspace(device):
-    """Scratch of sd_kv_attend for this device, shared by calls that pass none (calls on
-    concurrent streams must pass their own)."""
-    import torch
+_attend_bytes = {}  # by D
 
-    key = torch.device(device)
-    ws = _attend_workspaces.get(key)
-    if ws is None:  # for the largest heads: it is never replaced, a captured graph may hold it
-        ws = torch.empty(_quick().sd_kv_attend_workspace_bytes(128), dtype=torch.uint8, device=key)
-        _attend_workspaces[key] = ws
-    return ws
+
+def _take_scratch(t, size, stream):
+    """Device memory for one call on one stream, and what gives it back: the allocator hands it out again
+    in that stream's order, and to a captured graph from the graph's own pool, so that no two calls
+    meet in it. (As a bare address, where torch gives one: a tensor takes 4 us more of each call.)"""
+    torch = _t()
+    take = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+    give = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+    if take is not None and give is not None and t.is_cuda:
+        return take(size, stream), give
+    device = _device(t)
+    if device.type != "cuda":
+        held = torch.empty(size, dtype=torch.uint8)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            held = torch.empty(size, dtype=torch.uint8, device=device)
+    return held.data_ptr(), lambda at, held=held: None
 
 
 def sd_kv_attend_workspace_bytes(D):
@@ -679,7 +689,8 @@ def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, c
     cu_q: [B+1] int32, the query tokens of each request; lse: [n, Hq] float32 or None; max_q: the
     most query tokens of a request that is expected (None: n); sm_scale: None for D ** -0.5;
     workspace_buf: uint8 device tensor of at least sd_kv_attend_workspace_bytes(D) bytes, or None
-    for this device's shared one.
+    for one that the call takes from the allocator and gives back (on its own stream, so that calls on
+    several streams, threads or graphs do not meet).
     """
     cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
     Hkv, D = k_cache.shape[2:]
@@ -696,12 +707,22 @@ def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, c
     if lse is not None and (lse.dtype != _t().float32 or lse.shape != (n, Hq)
                             or not lse.is_contiguous()):
         raise SDError("lse must be contiguous float32 [tokens, Hq]")
-    ws = workspace_buf if workspace_buf is not None else attend_workspace(k_cache.device)
-    rc = _quick().sd_kv_attend(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q), *sq,
-                             *cache, _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q),
-                             D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)),
-                             _ptr(out), *so, _ptr(lse), _ptr(ws), ws.numel(), _ptr(err),
-                             _raw_stream(k_cache, stream))
+    raw, give = _raw_stream(k_cache, stream), None
+    if workspace_buf is not None:
+        ws, size = _ptr(workspace_buf), workspace_buf.numel()
+    else:
+        size = _attend_bytes.get(D)
+        if size is None:
+            size = _attend_bytes[D] = sd_kv_attend_workspace_bytes(D)
+        ws, give = _take_scratch(k_cache, size, raw)
+    try:
+        rc = _quick().sd_kv_attend(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q),
+                                   *sq, *cache, _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q),
+                                   D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)),
+                                   _ptr(out), *so, _ptr(lse), ws, size, _ptr(err), raw)
+    finally:
+        if give is not None:
+            give(ws)
     _check(rc, "sd_kv_attend")
 
 
