@@ -56,12 +56,13 @@ class Step:
         self.table[col[None] < need[:, None]] = perm
         self.target_cache = Cache(pages, heads, dim, device)
         self.draft_cache = Cache(pages, heads, dim, device)
-        # the contexts so far, as a prompt would have written them
-        r = torch.arange(B, device=device).repeat_interleave(self.pos0.long())
-        start = torch.cumsum(self.pos0, 0) - self.pos0
-        p = torch.arange(r.numel(), device=device) - start[r]
-        slots = self.table[r, p // BLOCK] * BLOCK + (p % BLOCK).int()
-        for cache in (self.target_cache, self.draft_cache):
+        # the contexts so far, as a prompt would have written them: the target's positions 0..pos0-1 (its
+        # K+1 slots begin at pos0), the drafter's 0..pos0 (its rebuilt slots begin at pos0+1)
+        for cache, n in ((self.target_cache, self.pos0), (self.draft_cache, self.pos0 + 1)):
+            r = torch.arange(B, device=device).repeat_interleave(n.long())
+            start = torch.cumsum(n, 0) - n
+            p = torch.arange(r.numel(), device=device) - start[r]
+            slots = self.table[r, p // BLOCK] * BLOCK + (p % BLOCK).int()
             kv = self.randn(r.numel(), 2, heads, dim)
             sd.sd_kv_write(kv[:, 0], kv[:, 1], slots.int(), *cache.all())
         W = self.W = 2 * K
@@ -120,7 +121,7 @@ class Step:
         dq = self.randn(size, hq, self.dim)
         drafted = self.attend(self.draft_cache, dq, self.pos0 + 1 + self.W, self.cu_draft, self.W)
         return dict(out_tokens=out_tokens, accepted=accepted, logits=logits, attended=attended,
-                    q=q, k=k, v=v, slots=slots, draft_slots=slot, drafted=drafted, **said)
+                    q=q, k=k, v=v, slots=slots, draft_slots=slot, draft_q=dq, drafted=drafted, **said)
 
 
 def main():

@@ -474,7 +474,8 @@ SD_API int sd_hidden_gather(int capacity, int H, const int32_t* total_out, const
  *           value x that the call writes to the page;
  *   scale = max(old scale, need), the old scale counting as 0 when the call writes the page's
  *           slot 0 (the page then starts afresh: pages fill in order, so what a rewound or reused
- *           page held before is void);
+ *           page held before is void; a page given to a new owner is therefore first written with its
+ *           slot 0 among the tokens, or has its scales set to 0);
  *   the tokens written become e4m3(x / scale), to nearest even; infinities become +-448, NaN stays
  *   NaN; when the scale grew, what the page's other slots hold is rounded again to the new scale:
  *   e4m3(held * old / scale).
