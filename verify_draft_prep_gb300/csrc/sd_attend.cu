@@ -119,7 +119,7 @@ struct AttMisc {
   uint64_t k_full[12], k_empty[12], v_full[12], v_empty[12];
   uint64_t s_full[2], p_full[2], o_done[2], q_full[2], q_empty[2];
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
-  int sc_zero[kScaleSlots];   // bit e: entry e's V scale is zero
+  uint32_t sc_zero[kScaleSlots];  // bit e: entry e's V scale is zero, bit 16 + e: its K scale
   float row_scale[2 * kTile];
   float2 ml[2][kTile];        // (M, L) of both streams; before a unit's end (the largest M so far, -)
   int nan_first[2][128];      // first token with a NaN in dimension d of V, of a masked tile
@@ -262,6 +262,11 @@ __device__ __forceinline__ float q_factor(uint32_t mg, int& up) {
   return mg >= 0x7f80u ? nanf("") : __uint_as_float((uint32_t)(up + 127) << 23);
 }
 
+// What brings a row's scores back to sm_scale q . k, in binades; NaN for a row of NaN.
+__device__ __forceinline__ float row_scale_of(const AttendParams& P, float mul, int up) {
+  return mul != mul ? mul : P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
 // 8 bf16 times mul as two e4m3 terms: the leading 4 significant bits, and the rest.
 __device__ __forceinline__ void split8(const uint4& v, float mul, uint32_t* hi, uint32_t* lo) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -328,7 +333,7 @@ __device__ __forceinline__ void load_q(const AttendParams& P, const Segment& s, 
         *reinterpret_cast<uint2*>(at + k * (kTile / R) * DP + kTile * DP) =
             make_uint2(lo[0], lo[1]);
       }
-      if (c8 == 0) row_scale[r] = P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
+      if (c8 == 0) row_scale[r] = row_scale_of(P, mul, up);
     }
   }
 }
@@ -362,7 +367,7 @@ __device__ __forceinline__ float q_to_tmem(const AttendParams& P, const Segment&
     tmem_st8(dst + 16 + half * 8, o + 8);
   }
   tmem_wait_st();
-  return P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
+  return row_scale_of(P, mul, up);
 }
 
 // One row of Q (up to 128 values) by a thread of its own, into the swizzled operand in shared memory
@@ -393,7 +398,7 @@ __device__ __forceinline__ float q_to_smem(const AttendParams& P, const Segment&
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + kTile * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
-  return P.scale * __uint_as_float((uint32_t)(127 - up) << 23);
+  return row_scale_of(P, mul, up);
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -890,13 +895,16 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             sc.x, none ? -INFINITY : zero ? kZeroLog2 : sc.y != sc.y ? sc.y : __log2f(v),
             none ? 1.f : zero ? kZeroInv : __fdividef(1.f, v), 0.f);
         const uint32_t zeros = __ballot_sync(0xffffffffu, zero);
+        const uint32_t k_zeros = __ballot_sync(0xffffffffu, !none && sc.x == 0.f);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if (t0 + k >= s.b) break;
           ok = mbar_wait_warp(smem_u32(&m.sc_empty[slot]), sc_ph, gave_up);
           if (!ok) break;
           if (half == k) scales[slot * 16 + e] = f;
-          if (lane == 0) m.sc_zero[slot] = (int)(k ? zeros >> 16 : zeros & 0xffffu);
+          if (lane == 0)
+            m.sc_zero[slot] = k ? zeros >> 16 | (k_zeros & 0xffff0000u)
+                                : (zeros & 0xffffu) | k_zeros << 16;
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&m.sc_full[slot]));
           if (++slot == kScaleSlots) {
@@ -983,7 +991,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           continue;
         }
         const int t0 = (s.a + j) * kTile;
-        const int zero = m.sc_zero[slot];
+        const uint32_t zero = m.sc_zero[slot] & 0xffffu, k_zero = m.sc_zero[slot] >> 16;
         const bool masked = t0 + kTile > min_lim;
         if (kSFirst) {
           ok = mbar_wait_warp(smem_u32(&m.s_full[x]), done & 1, gave_up);
@@ -1034,15 +1042,19 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
           const float4* sc = scales + slot * 16 + copy * NC * 4;
           const int edge = lim - t0 - copy * NC * 32;  // columns from here on are masked
           const uint32_t tC = tS + copy * NC * 32;
-          if (masked) {  // rare: the masked columns of S become -inf where they lie
+          // rare: where they lie, the masked columns of S become -inf, and those of pages whose K is
+          // zeros 0, whatever the bytes (but for a row whose queries make every score NaN)
+          if (masked || k_zero) {
 #pragma unroll 1
             for (int c = 0; c < NC; ++c) {
               uint32_t v[32];
               tmem_ld32(tC + c * 32, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < 32; ++i) {
+                if ((k_zero >> ((copy * NC + c) * 4 + i / 8)) & 1 && rs == rs) v[i] = 0;
                 v[i] = c * 32 + i >= edge ? 0xff800000u : v[i];
+              }
               __syncwarp();
               tmem_st32(tC + c * 32, v);
             }

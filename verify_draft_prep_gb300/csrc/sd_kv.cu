@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
         if (my_row >= rows || it * rows + my_row >= slots || (have >> it) & 1) continue;
         uint2* dst =
             reinterpret_cast<uint2*>(base + (sub * 16 + it * rows + my_row) * P.st_tok);
-        const uint2 q = *dst;
+        // (a page of scale 0 holds zeros, whatever its bytes)
+        const uint2 q = s_old > 0.f ? *dst : make_uint2(0, 0);
         uint32_t o[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const KvReadParam
     }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t w[4] = {q[kv].x, q[kv].y, q[kv].z, q[kv].w};
+      const uint32_t keep = s[kv] == 0.f ? 0u : ~0u;  // a scale of 0: zeros, whatever the bytes
+      const uint32_t w[4] = {q[kv].x & keep, q[kv].y & keep, q[kv].z & keep, q[kv].w & keep};
       uint32_t o[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
