@@ -524,8 +524,9 @@ SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const v
  * down to 2^-12 of it; beside a token that dominates the row the steps are 2^-19 of its weight, and 3 bits
  * are kept down to 2^-24 of it. So the rest of a long context counts to 8 bits against a dominant
  * token, too. The V scales of the pages that one token sees lie within 2^80 of one another (a scale of
- * 0 counts as 2^-60). A token that sees nothing gets out = 0 and lse = -inf. NaN in tokens that a query token does not see has no effect on it. The
- * same call gives the same bits: parts of a request are joined in a fixed order.
+ * 0 counts as 2^-60). A token that sees nothing gets out = 0 and lse = -inf. NaN in tokens that a query
+ * token does not see has no effect on it, nor have the other queries of the request. The same call gives
+ * the same bits: parts of a request are joined in a fixed order.
  * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] (or beyond
  * 2^31 - 256) raises SD_ERR_KV_RANGE; those tokens are left out. cu_q has B+1 non-decreasing entries
  * in [0, n] (others are clamped, SD_ERR_KV_RANGE); tokens outside [cu_q[0], cu_q[B]) are not written.

@@ -1083,11 +1083,12 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
             }
           }
           const bool fall = mx < M - kFall && mx > -INFINITY;
-          const bool moved = __any_sync(0xffffffffu, mx > M + kSlack || fall);
+          const bool rise = mx > M + kSlack;
+          const bool moved = __any_sync(0xffffffffu, rise || fall);
           float fac = 1.f;
-          if (moved) {
+          if (moved) {  // (a row's own y alone decide on its reference)
             const float top = m.ml[x][wt].x;
-            float Mn = fall ? fmaxf(mx + kAbove, top - kDeepest) : fmaxf(M, mx);
+            float Mn = fall ? fmaxf(mx + kAbove, top - kDeepest) : rise ? mx : M;
             if (fall && !(Lsum * ex2f(M - Mn) < kMaxL)) Mn = M;
             m.ml[x][wt].x = fmaxf(top, Mn);
             fac = M == -INFINITY ? 0.f : ex2f(M - Mn);
