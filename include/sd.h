@@ -458,8 +458,9 @@ SD_API int sd_hidden_gather(int capacity, int H, const int32_t* total_out, const
  *     Hkv at most 2^22.
  *   - k_scale and v_scale [num_blocks, Hkv] fp32 hold one scale for each page and head: the byte q
  *     stands for e4m3(q) * scale. sd_kv_write makes powers of two, so that every product with a
- *     scale is exact; reads take any positive scale. A scale of 0 means that the page holds zeros
- *     (a cache may start as zeroed memory).
+ *     scale is exact; reads take any positive scale (sd_kv_attend V scales from 2^-100 to 2^120, which
+ *     holds all that sd_kv_write makes). A scale of 0 means that the page holds zeros (a cache may
+ *     start as zeroed memory, or as any with zeroed scales).
  *   - block_table [B, max_blocks] as for sd_pdraft_expand: position p of request r is slot
  *     p % block_size of page block_table[r][p / block_size].
  */

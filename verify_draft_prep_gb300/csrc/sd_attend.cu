@@ -38,6 +38,8 @@
 // Softmax beside a product that takes both operands from shared memory is 2.3 times slower; that is
 // why heads of 64 keep Q in tensor memory.
 
+#include <atomic>
+
 #include "sd_kv.cuh"
 #include "sd_tc.cuh"
 
@@ -890,7 +892,9 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
         const int far = entry(t0 + 4);
         const float2 sc_nxt = scales_of(nxt);
         const bool none = sc.y == -1.f, zero = !none && !(sc.y > 0.f) && sc.y == sc.y;
-        const float v = fmaxf(sc.y, kMinScale);  // (a NaN stays out of here)
+        // (a NaN stays out of here; the approximations are exact for powers of two, and off by 2^-22 of
+        // a weight at most for others)
+        const float v = fmaxf(sc.y, kMinScale);
         const float4 f = make_float4(
             sc.x, none ? -INFINITY : zero ? kZeroLog2 : sc.y != sc.y ? sc.y : __log2f(v),
             none ? 1.f : zero ? kZeroInv : __fdividef(1.f, v), 0.f);
@@ -1469,15 +1473,15 @@ static bool cache_map(CUtensorMap* map, const void* p, const KvCache& c, int DP)
 }
 
 static int sm_count() {
-  static int count[64];
+  static std::atomic<int> count[64];  // (threads that come first together all find the same)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (count[dev] == 0) {
-    int n = 0;
+  int n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    count[dev] = n;
+    count[dev].store(n, std::memory_order_relaxed);
   }
-  return count[dev];
+  return n;
 }
 
 template <int DP, int NS, int R>
@@ -1486,14 +1490,14 @@ static int launch_attend(const AttendParams& P, const CUtensorMap& km, const CUt
   using L = AttLayout<DP, NS, R>;
   constexpr int smem = L::kMisc + (int)sizeof(AttMisc) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  static bool set[64];  // per device
+  static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
-  if (!set[dev]) {
+  if (!set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(attend_kernel<DP, NS, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return SD_E_LAUNCH;
-    set[dev] = true;
+    set[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, 1, 1);
