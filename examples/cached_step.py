@@ -6,7 +6,8 @@ The target's K and V of the K+1 verify slots enter the cache, the slots attend t
 the (here: random) head gives logits, the drafts are verified, the answer gets its log
 probabilities, the drafter's batch is rebuilt, and its tokens enter the drafter's own cache and
 attend to it. The model parts between the calls are random matrices: the point is which arrays go
-from call to call, all of them on the device, without a synchronisation in between.
+from call to call, all of them on the device, without a synchronisation in between. At the end the
+step's tokens are read back from the target's cache, as a move to another precision would.
 """
 
 import argparse
@@ -81,6 +82,14 @@ class Step:
         sd.sd_kv_attend(q, *cache.all(), self.table, ctx, cu, out, max_q=max_q, err=self.err)
         return out
 
+    def read_back(self, cache, first, count):
+        """Tokens first[r] .. first[r] + count - 1 of every request as the cache holds them, bf16."""
+        cu = torch.arange(0, self.B * count + 1, count, **self.i32)
+        k, v = (torch.empty(self.B * count, self.heads, self.dim, dtype=torch.bfloat16,
+                            device=self.device) for _ in range(2))
+        sd.sd_kv_read(*cache.all(), self.table, cu, k, v, first_pos=first, err=self.err)
+        return k, v
+
     def run(self, drafts, draft_rows, seed=0, top=5):
         """drafts [B, K] and the drafter's logits [B*K, V] they came from. Returns what the step
         answers and the drafter's next batch."""
@@ -135,13 +144,15 @@ def main():
     drafts = torch.empty(a.requests, a.drafts, **step.i32)
     sd.sd_draft_sample(rows, drafts, seed=1, err=step.err)
     r = step.run(drafts, rows)
+    k, _ = step.read_back(step.target_cache, step.pos0, step.K + 1)
     torch.cuda.synchronize()
     if int(step.err):
         raise SystemExit(f"data errors: {int(step.err):#x}")
     live = r["out_tokens"] >= 0
     print(f"accepted {r['accepted'].float().mean():.2f} of {a.drafts} drafts; answer of "
           f"{int(live.sum())} tokens, mean log probability {float(r['logprob'][live].mean()):.3f}, "
-          f"mean entropy {float(r['entropy'][live].mean()):.3f}")
+          f"mean entropy {float(r['entropy'][live].mean()):.3f}; K in the cache is "
+          f"{float((k.float() - r['k'].float()).norm() / r['k'].float().norm()):.4f} off")
 
 
 if __name__ == "__main__":
