@@ -25,14 +25,15 @@
 // 128 rows each of the same tiles, which halves the traffic of K and V.
 //
 // What bounds it (measured, 8 heads of K and V, pages of 16):
-//   - 256 requests of 8 slots, 32 heads of 128, 1000 to 16000 tokens: 830 to 860 us, memory (79 to
-//     82% of the copy rate), and 910 to 960 once the power limit lowers the clocks after some tenths
-//     of a second.
-//   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 117 us against 40 of memory, 128
-//     drafter requests of 8 to 16 slots 374 us against 109: the softmax, 270 to 330 cycles for 32
-//     columns of 32 rows in each of an SM's four schedulers, while a tile of 48 rows costs as much as
-//     one of 64.
-//   - A prompt of 8192 tokens, 32 heads of 128: 578 us, 48% of the bf16 rate, softmax again.
+//   - 256 requests of 8 slots, 32 heads of 128, 1000 to 16000 tokens: 890 us in short runs, 76% of
+//     the copy rate, and 960 to 1020 once the power limit lowers the clocks after some tenths of a
+//     second.
+//   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 120 us against 40 of memory, 128
+//     drafter requests of 8 to 16 slots 411 us against 109, a prompt of 8192 tokens of 32 heads of 128
+//     640 us against 278 of products. No unit is half busy (64 requests: issue slots 42%, memory 28%,
+//     tensor cores 25%; prompt: 48%, 3%, 38%). What takes the time is a stream's chain S -> P -> PV ->
+//     next S: P takes the place of the only S, and only two streams cover for each other. A unit's
+//     own cost (kUnitCost) is a sixth of the line of 64 requests.
 //   - One token at 32000, 32 heads of 128: 31 us in a graph against 9.7 of memory: 14 tiles a CTA do
 //     not hide the setup, the first pages' latency and the join of 19 parts.
 // Softmax beside a product that takes both operands from shared memory is 2.3 times slower; that is
@@ -58,8 +59,10 @@ constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
 // 2^-14. A long context can hold thousands of weights far below one dominant token's, which together
 // are the answer where that token's V is small. So M follows the tiles both ways: up where a tile's
 // largest y passes M + kSlack, down where it lies below M - kFall, and every tile's largest P is
-// between 2^(kShift - kFall) = 2^-2 and 2^(kShift + kSlack) < 2^12. A window narrower than that has the
-// accumulator rescaled more often. M falls to kAbove above the tile's largest y, so that the next
+// between 2^(kShift - kFall) = 2^-2 and 2^(kShift + kSlack) < 2^12. The smaller kFall, the more bits the
+// small weights keep and the more often the accumulator is rescaled: with 9, 12, 14 and no fall 64
+// requests take 124, 122, 122, 120 us, 256 requests 896, 889, 884, 871, drafter batch 418, 413, 410, 404,
+// prompt 648, 640, 633, 608; at 12 the largest weight of every tile has all of its 8 bits. M falls to kAbove above the tile's largest y, so that the next
 // tiles find room on either side, and kDeepest at most below the largest M so far, so that the
 // accumulator (up to 2^21 a token at the largest M) stays within fp32; nor beyond kMaxL for L, which a
 // small V scale enlarges.
@@ -188,13 +191,13 @@ struct Segment {
 
 // Every unit takes kUnitCost places on the line before its tiles, for what it costs beside them (its
 // queries, its result), so that CTAs with many short units get fewer tiles. With 2, 4, 6, 8 and 16:
-// 64 requests 122, 120, 117, 117, 125 us; 256 requests 863, 861, 854, 853, 861; drafter batch 387, 373,
-// 374, 384, 429; prompt 833, 607, 578, 588, 631; one token 34 everywhere but 36 with 16.
+// 64 requests 127, 124, 122, 123, 131 us; 256 requests 897, 890, 890, 890, 894; drafter batch 417, 407,
+// 413, 423, 474; prompt 883, 640, 640, 651, 697; one token 34 everywhere but 36 with 16.
 constexpr int kUnitCost = 6;
 
 // The order of the line: heads outermost (requests, then their Q tiles inside), or, with two Q tiles,
-// innermost. Outermost against innermost: 64 requests 117 to 122 us, drafter batch 385 to 400, 256
-// requests 838 to 840, prompt (two Q tiles) 612 to 590.
+// innermost. Outermost against innermost: 64 requests 122 to 125 us, drafter batch 413 to 425, 256
+// requests 890 to 888, prompt (two Q tiles) 643 to 640.
 template <int NS>
 constexpr bool kHeadsInside = NS == 2;
 
@@ -934,11 +937,11 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap k_map,
     // A wait for V is for this tile's phase only if the one before in the same stage is known to have
     // ended. With an odd number of stages that one was the other stream's: S of this tile, which
     // comes after that stream's product with it, has to be there. Else it was this stream's own.
-    // (Waiting for S first everywhere: a prompt of 8192 tokens 602 instead of 588 us.)
+    // (Waiting for S first everywhere: 64 requests 129 instead of 122 us, a prompt 650 instead of 640.)
     constexpr bool kSFirst = NS == 1 && SV % 2 == 1;
     // The accumulator is rescaled before P is formed (heads of 64), or after, when S's registers are
-    // free and 64 columns go at a time. Before against after: 64 requests 120 to 123 us, drafter batch
-    // 408 to 413, prompt 663 to 639.
+    // free and 64 columns go at a time. Before against after: 64 requests 122 to 126 us, drafter batch
+    // 413 to 411, 256 requests 899 to 889, prompt 664 to 640.
     constexpr bool kLate = DP == 128;
     int it = 0, nq = 0, unit = 0;
     int done = 0;  // tiles of this stream so far
@@ -1567,7 +1570,7 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   P.ws = (unsigned char*)(((uintptr_t)workspace + 31) / 32 * 32);
   P.err = err;
   // A CTA's least share: a unit's cost and 4 tiles. With 1, 4 and 16 tiles one token at 500 tokens
-  // takes 16.2, 14.7, 21.5 us, at 1000 19.8, 19.1, 27.5, at 4000 20.9, 23.1, 30.8.
+  // takes 16.3, 15.7, 15.7 us, at 1000 19.6, 16.9, 19.2, at 4000 19.6, 21.5, 26.1.
   P.min_share = sdk::kUnitCost + 4;
   const int sms = sdk::sm_count();
   if (sms < 1) return SD_E_DEVICE;
@@ -1580,10 +1583,10 @@ extern "C" int sd_kv_attend_launch(int B, int n, int max_q, int Hq, int Hkv, int
   const bool join = ((long)max_blocks << log2_bs) > sdk::kTile;
   // The expected rows of a request choose the unit: 32 or 64 rows stand in the lanes four times or
   // twice, so that all softmax warps share a tile's columns; more than 128 make two Q tiles. Measured
-  // in us with units of 32, 64, 128 and 256 rows: heads of 64, 64 requests of 32 rows 95, 102, 131,
-  // 193; 48 rows 182, 113, 150, 200; 96 rows 262, 201, 152, 203; 192 rows 563, 338, 315, 279. Heads of
-  // 128, 256 requests of 32 rows 852, 860, 1087, 1691; 56 rows 1640, 910, 1161, 1659; 112 rows 3613,
-  // 1894, 1337, 1744; 64 requests of 240 rows 1693, 942, 697, 553.
+  // in us with units of 32, 64, 128 and 256 rows: heads of 64, 64 requests of 32 rows 102, 104, 148,
+  // 201; 48 rows 195, 118, 160, 219; 96 rows 279, 206, 161, 214; 192 rows 605, 351, 336, 297. Heads of
+  // 128, 256 requests of 32 rows 887, 923, 1184, 1877; 56 rows 1700, 950, 1262, 1845; 112 rows 3711,
+  // 1947, 1404, 1957; 64 requests of 240 rows 1788, 988, 749, 610.
   const long rows = (long)max_q * P.G;
   if (DP == 64) {
     if (rows <= 32) return sdk::launch_attend<64, 1, 4>(P, km, vm, ctas, join, stream);

@@ -1,8 +1,8 @@
 // sd_logprobs.cu -- log probabilities of given tokens, with the row's entropy, the token's rank and
 // the row's best alternatives (sd_token_logprobs), in one pass over each row.
 //
-// With y = l / T and m = max y: Z = sum e^(y - m), log p(x) = y_x - m - ln Z, and
-// H = -sum p ln p = ln Z - (sum e^(y - m) (y - m)) / Z. Sums are fp32, each thread's own and then a
+// With y = l / T and m a reference near the largest y: Z = sum e^(y - m), log p(x) = y_x - m - ln Z,
+// and H = -sum p ln p = ln Z - (sum e^(y - m) (y - m)) / Z. Sums are fp32, each thread's own and then a
 // tree's. Probability rows need no Z: log p = ln p_x, H = -sum p ln p.
 //
 // A warp takes 256 or 1024 neighbouring entries (a group) at a time. The group's maximum, one warp
@@ -13,10 +13,12 @@
 // values.
 //
 // Bound by memory on paper, the row once: 9216 rows of 201088 logits with 20 alternatives, 2.04 GB
-// of rows with a token, take 400 us, 75% of the copy rate. The rest goes to instructions: at 16 a clock
+// of rows with a token, take 405 us, 74% of the copy rate. The rest goes to instructions: at 16 a clock
 // and SM the exponentials alone take 220 us. CTAs of 128 threads, eight on an SM, so that one
 // row's tail (the selection, some 3 us) overlaps seven others' loads (434 instead of 396 us with 256
-// threads, four on an SM). 5 rows of 1024 probabilities with 5 alternatives: 4.5 us in a graph.
+// threads, four on an SM). 5 rows of 1024 probabilities with 5 alternatives: 4.5 us in a graph. 5
+// rows of 201088 logits, 2 MB, take 21 us: a row has 8 CTAs at most, a lane one load in flight, and
+// the selection up to 20 rounds in a row.
 
 #include "sd_common.cuh"
 
@@ -712,9 +714,9 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   P.err = err;
   // Few rows: a cluster of CTAs shares one, until the rows fill eight CTAs on every SM or a CTA has
   // few entries left, while there is a free SM for each fewer. Measured in us, 20 alternatives, 1, 2,
-  // 4 or 8 CTAs: 5 rows of 1024 logits 5.7, 7.0, 7.8, 10.6; of 8192 12.6, 9.2, 8.3, 10.0; of 32000
-  // 18.2, 16.0, 15.0, 12.2; of 201088 43, 32, 24, 21. 192 rows of 32000: 19.1, 17.4, 18.0, 21.2.
-  // 768 rows of 201088: 82, 71, 80, 109. 2304 rows of 131072: 104, 122, 158, 232.
+  // 4 or 8 CTAs: 5 rows of 1024 logits 5.7, 7.0, 7.2, 10.8; of 8192 12.7, 9.3, 8.2, 10.6; of 32000
+  // 17.7, 15.9, 14.6, 12.6; of 201088 43, 32, 23, 21. 192 rows of 32000: 20.9, 17.5, 17.9, 21.2.
+  // 768 rows of 201088: 81, 72, 79, 109. 2304 rows of 131072: 104, 120, 158, 233.
   int C = 1;
   while (C < sdk::kLpMaxCluster && (long)P.rows * C < 8 * 152 &&
          V / (2 * C) >= ((long)P.rows * 2 * C <= 152 ? 2048 : 4096))
@@ -722,8 +724,8 @@ extern "C" int sd_logprobs_launch(int B, int J, int V, int dtype, const void* ro
   while (C < sdk::kLpMaxCluster && V / C > SD_TOP_MAX_V / sdk::kLpMaxCluster) C *= 2;
   // Groups of one vector while there are few of them, so that the best n groups are few entries;
   // of logits else of four, which saves most of a group's own work. One against four vectors: 5
-  // rows of 201088 in CTAs of 25136 logits 21 to 26 us, 192 rows in CTAs of 50272 33.5 to 35.1, 2304
-  // rows of 131072 in CTAs of 65536 141 to 122, of 131072 152 to 104. Probabilities, which bring half
+  // rows of 201088 in CTAs of 25136 logits 21 to 26 us, 192 rows in CTAs of 50272 34.6 to 34.8, 2304
+  // rows of 131072 in CTAs of 65536 141 to 120, of 131072 152 to 104. Probabilities, which bring half
   // as many entries with each byte, gain nothing (2304 rows of 131072: 222 to 222 us with two).
   const int U = dtype == SD_BF16_LOGITS && V / C >= 65536 ? 4 : 1;
   const int group = U * sdk::kVec;
