@@ -519,15 +519,16 @@ SD_API int sd_kv_read(int B, int n, int Hkv, int D, const void* k_cache, const v
  * stands at position ctx_lens[r] - n_r + i and, when causal, sees the tokens up to its own
  * position; else all ctx_lens[r]. Head h of Hq reads head h / (Hq / Hkv) of the cache.
  *   S = sm_scale * q . k,  out = sum_j softmax(S)_j v_j,  lse = ln sum_j e^(S_j)
- * q is taken exactly but for what lies below 2^-17 of its largest magnitude; exponentials, sums and
- * products are fp32; out is rounded to bf16 once. The weights of v have 8 significant bits. Among 128
- * neighbouring tokens, weights far below the largest can have fewer, in steps of 2^-7 of it, but keep 3
- * down to 2^-12 of it; beside a token that dominates the row the steps are 2^-19 of its weight, and 3 bits
- * are kept down to 2^-24 of it. So the rest of a long context counts to 8 bits against a dominant
- * token, too. The V scales of the pages that one token sees lie within 2^80 of one another (a scale of
- * 0 counts as 2^-60). A token that sees nothing gets out = 0 and lse = -inf. NaN in tokens that a query
- * token does not see has no effect on it, nor have the other queries of the request. The same call gives
- * the same bits: parts of a request are joined in a fixed order.
+ * q is taken exactly but for what lies below 2^-17 of its largest magnitude; exponentials, sums
+ * and products are fp32; out is rounded to bf16 once. The weights of v have 8 significant bits. Among
+ * 128 neighbouring tokens, weights far below the largest can have fewer, in steps of 2^-7 of it,
+ * but keep 3 down to 2^-12 of it; beside a token that dominates the row the steps are 2^-19 of its
+ * weight, and 3 bits are kept down to 2^-24 of it. So the rest of a long context counts to 8 bits
+ * against a dominant token, too. The V scales of the pages that one token sees lie within 2^80 of
+ * one another (a scale of 0 counts as 2^-60). A token that sees nothing gets out = 0 and lse =
+ * -inf. NaN in tokens that a query token does not see has no effect on it, nor have the other
+ * queries of the request. The same call gives the same bits: parts of a request are joined in a
+ * fixed order.
  * A table entry outside [0, num_blocks) or a length outside [0, max_blocks*block_size] (or beyond
  * 2^31 - 256) raises SD_ERR_KV_RANGE; those tokens are left out. cu_q has B+1 non-decreasing entries
  * in [0, n] (others are clamped, SD_ERR_KV_RANGE); tokens outside [cu_q[0], cu_q[B]) are not written.

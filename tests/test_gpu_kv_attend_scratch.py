@@ -96,3 +96,24 @@ def test_graphs_without_scratch_of_their_own():
             assert torch.equal(o, w)
             o.zero_()
         torch.cuda.synchronize()
+
+
+def test_refused_calls_give_their_scratch_back():
+    """Head sizes and tensors that the call refuses, and calls without tokens."""
+    c = Call([4], [100], 8, 2, 64, seed=4)
+    c()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(3):
+        with pytest.raises(sd.SDError):  # heads of 72 values
+            sd.sd_kv_attend(torch.zeros(4, 8, 72, device=DEV).bfloat16(),
+                            *(torch.zeros(8, 16, 2, 72, dtype=torch.uint8, device=DEV) for _ in range(2)),
+                            *(torch.zeros(8, 2, device=DEV) for _ in range(2)), c.table, c.lens, c.cu,
+                            torch.zeros(4, 8, 72, device=DEV).bfloat16())
+        with pytest.raises(sd.SDError):  # more query heads than a multiple of the cache's
+            sd.sd_kv_attend(c.q[:, :7], *c.cache, c.table, c.lens, c.cu, torch.zeros_like(c.q)[:, :7])
+        with pytest.raises(sd.SDError):  # a tensor that the GPU cannot address
+            sd.sd_kv_attend(c.q, *c.cache, c.table, c.lens.cpu(), c.cu, torch.zeros_like(c.q))
+        sd.sd_kv_attend(c.q[:0], *c.cache, c.table, c.lens, c.cu, torch.zeros_like(c.q)[:0])
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before

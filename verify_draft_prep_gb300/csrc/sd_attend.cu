@@ -55,17 +55,17 @@ constexpr int kScaleSlots = 16;            // tiles of scales in flight
 constexpr float kZeroLog2 = -60.f, kZeroInv = 1152921504606846976.f;
 // P = 2^(y - M + kShift), M the row's reference, as P1 + P2: P1 is P to 3 significant bits (e5m2),
 // P2 the rest, at most 2^-3 of P's binade, to 4 (e4m3). Below 2^12 P2 stays within e4m3's 448. P has 8
-// significant bits down to 2^-2, where P2 reaches e4m3's finest step of 2^-9, and fewer below, 3 down to
-// 2^-14. A long context can hold thousands of weights far below one dominant token's, which together
-// are the answer where that token's V is small. So M follows the tiles both ways: up where a tile's
-// largest y passes M + kSlack, down where it lies below M - kFall, and every tile's largest P is
+// significant bits down to 2^-2, where P2 reaches e4m3's finest step of 2^-9, and fewer below, 3 down
+// to 2^-14. A long context can hold thousands of weights far below one dominant token's, which
+// together are the answer where that token's V is small. So M follows the tiles both ways: up where a
+// tile's largest y passes M + kSlack, down where it lies below M - kFall, and every tile's largest P is
 // between 2^(kShift - kFall) = 2^-2 and 2^(kShift + kSlack) < 2^12. The smaller kFall, the more bits the
 // small weights keep and the more often the accumulator is rescaled: with 9, 12, 14 and no fall 64
-// requests take 124, 122, 122, 120 us, 256 requests 896, 889, 884, 871, drafter batch 418, 413, 410, 404,
-// prompt 648, 640, 633, 608; at 12 the largest weight of every tile has all of its 8 bits. M falls to kAbove above the tile's largest y, so that the next
-// tiles find room on either side, and kDeepest at most below the largest M so far, so that the
-// accumulator (up to 2^21 a token at the largest M) stays within fp32; nor beyond kMaxL for L, which a
-// small V scale enlarges.
+// requests take 124, 122, 122, 120 us, 256 requests 896, 889, 884, 871, drafter batch 418, 413, 410,
+// 404, prompt 648, 640, 633, 608; at 12 the largest weight of every tile has all of its 8 bits. M
+// falls to kAbove above the tile's largest y, so that the next tiles find room on either side, and
+// kDeepest at most below the largest M so far, so that the accumulator (up to 2^21 a token at the
+// largest M) stays within fp32; nor beyond kMaxL for L, which a small V scale enlarges.
 constexpr float kShift = 10.f, kSlack = 1.9f, kFall = 12.f, kAbove = 2.f, kDeepest = 60.f;
 constexpr float kMaxL = 1e30f;
 constexpr float kTiny = 1.17549435e-38f;  // -inf times it is -inf, S times it is nothing

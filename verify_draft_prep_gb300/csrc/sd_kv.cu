@@ -17,8 +17,9 @@ namespace sdk {
 // magnitude and the quantisation: every value is read once. Larger pages take a team of warps, 16
 // tokens each, that meet over the magnitude. Per element 2 bytes are read and 1 is written; the
 // kernel is bound by memory for prompts (2 x 8192 tokens of 8 heads of 128: 18.7 us in a graph, 79%
-// of the copy rate; 1024 CTAs on 608 places, so that the second wave is not full) and by the chain slot -> token -> scale -> store for the few tokens of a step
-// (64 requests of 6 tokens of 8 heads of 64: 6.3 us in a graph).
+// of the copy rate; 1024 CTAs on 608 places, so that the second wave is not full) and by the chain
+// slot -> token -> scale -> store for the few tokens of a step (64 requests of 6 tokens of 8 heads
+// of 64: 6.3 us in a graph).
 // ---------------------------------------------------------------------------------------------
 struct KvWriteParams {
   const uint16_t* x[2];  // K, V rows
@@ -218,10 +219,10 @@ __global__ void __launch_bounds__(kWriteThreads, 4) kv_write_kernel(const KvWrit
 
 // ---------------------------------------------------------------------------------------------
 // Read back. Output row i is token i - cu[r] + first[r] of request r. A CTA takes 16 rows: their
-// pages are looked up once into shared memory (a binary search over the prefix), then every
-// thread moves 16 values at a time (16 bytes in, 32 out), four of them on their way. Bound by
-// memory, 1 byte read and 2 written for each value: 316000 tokens of 8 heads of 64 take 147 us, 97% of
-// the copy rate; one request of 32000 tokens of 8 heads of 128 36 us, 79%: 2000 CTAs on 912 places, the
+// pages are looked up once into shared memory (a binary search over the prefix), then every thread
+// moves 16 values at a time (16 bytes in, 32 out), four of them on their way. Bound by memory, 1
+// byte read and 2 written for each value: 316000 tokens of 8 heads of 64 take 147 us, 97% of the
+// copy rate; one request of 32000 tokens of 8 heads of 128 36 us, 79%: 2000 CTAs on 912 places, the
 // third wave a fifth full.
 // ---------------------------------------------------------------------------------------------
 struct KvReadParams {

@@ -135,10 +135,11 @@ struct Sums {
 };
 
 // The temperature of a row: c = log2(e) / T, and what of its logits is taken with it as it stands.
-// Where |ref| c passes 2^26, bf16 logits that differ from ref do so by 2^18 units or more, products can
-// overflow and r's rounding is no small part of a binade: a row with a logit from `to` on, or without
-// one above `from`, is taken by extreme_sums. `low`, 2^27 units below 0, stands for what is below it: 2^t
-// is 0 there under any reference, and t 2^t too because t stays finite (-inf would make it NaN).
+// Where |ref| c passes 2^26, bf16 logits that differ from ref do so by 2^18 units or more, products
+// can overflow and r's rounding is no small part of a binade: a row with a logit from `to` on, or
+// without one above `from`, is taken by extreme_sums. `low`, 2^27 units below 0, stands for what is
+// below it: 2^t is 0 there under any reference, and t 2^t too because t stays finite (-inf would
+// make it NaN).
 struct Heat {
   float c, from, to;
   __nv_bfloat162 low;
