@@ -553,6 +553,145 @@ SD_API int sd_kv_attend(int B, int n, int max_q, int Hq, int Hkv, int D, const v
 SD_API size_t sd_kv_attend_workspace_bytes(int D);
 
 /*
+ * sd_kv_weights -- the attention weight that each cached token gets from a call's queries.
+ *
+ * Queries, lengths and cache as for sd_kv_attend, whose lse is an input: of the query tokens of
+ * request r the first live[r] count (NULL: all; sd_verify's num_accepted + 1 leaves rejected drafts
+ * out). For each KV head h and token t < ctx_lens[r]:
+ *   w = sum over the tokens i that count and see t, and the heads of h's group, of
+ *       e^(sm_scale q_i . k_t - lse_i)
+ *   weights[t] = w                      for the request's own new tokens, or without `before`
+ *   weights[t] = w + decay * before[t]  for the others
+ * so that a token's number starts afresh in the call that brings it. weights and before are fp32
+ * [num_blocks, Hkv, block_size], as the cache's pages lie; before may be weights itself. Numbers of
+ * other slots are not written. A token whose page is not in the table is left out (SD_ERR_KV_RANGE, as
+ * for ctx_lens, cu_q and a live[r] outside [0, n_r], which are clamped). Rows with lse = -inf that see
+ * nothing add nothing. The same call gives the same bits; sums are fp32, q as for sd_kv_attend.
+ * Arguments: as for sd_kv_attend; lse [n, Hq] fp32; decay finite and >= 0; B and Hkv at most 65535.
+ *   Requests that share a page of the table race on its numbers.
+ */
+SD_API int sd_kv_weights(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q, long ld_q,
+                         long hs_q, const float* lse, const void* k_cache, long st_block,
+                         long st_tok, long st_head, const float* k_scale, int num_blocks,
+                         int block_size, const int32_t* block_table, int max_blocks,
+                         const int32_t* ctx_lens, const int32_t* cu_q, const int32_t* live,
+                         float sm_scale, int causal, float decay, const float* before,
+                         float* weights, int32_t* err, void* stream);
+
+/*
+ * sd_kv_evict -- a cache cut to a budget of tokens a request, by their weights.
+ *
+ * A request of more than `budget` tokens keeps the first `sink`, the last `recent`, and of those
+ * between them the ones with the largest weights (equal ones: the earlier; a NaN before all), so that
+ * `budget` stay, in their order. Every KV head chooses for itself: slot j of head h then holds its
+ * j-th token that stays. Shorter requests keep all.
+ *   kept[r][h][j] = the position that the j-th token had, -1 from new_lens[r] on
+ *   new_lens[r]   = min(ctx_lens[r], budget)
+ * The tokens' K, V and weights move to the pages that to_table lists (fresh ones: none of any
+ * request's table), or, to_table NULL, to the request's own from the first on (its pages not shared
+ * with another request; those behind new_lens are then free). A page's new scale is the largest of its
+ * tokens' old ones; a value becomes e4m3(held * old / new), to nearest even: unchanged but for what
+ * becomes subnormal. Pages and slots behind new_lens, and a table's pages that tokens leave, stay as they
+ * are. A position that a table does not cover raises SD_ERR_KV_RANGE: as a source it holds weight 0
+ * and zeros, as a place it is not written; lengths beyond the table are clamped, with the bit.
+ * Rotated keys keep the angle of the position they had: new tokens go on with positions of the text,
+ * while slots, ctx_lens and sd_kv_attend's causal order go by place.
+ * Arguments: cache as for sd_kv_write; weights fp32 [num_blocks, Hkv, block_size]; kept [B, Hkv,
+ *   budget] and new_lens [B] int32 outputs (new_lens is not ctx_lens); budget >= 1; sink, recent >= 0,
+ *   sink + recent <= budget; to_table [B, to_blocks]; B and Hkv at most 65535.
+ */
+SD_API int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long st_block,
+                       long st_tok, long st_head, float* k_scale, float* v_scale, int num_blocks,
+                       int block_size, float* weights, const int32_t* block_table, int max_blocks,
+                       const int32_t* to_table, int to_blocks, const int32_t* ctx_lens, int budget,
+                       int sink, int recent, int32_t* kept, int32_t* new_lens, int32_t* err,
+                       void* stream);
+
+/* ---- rotary positions ---- */
+#define SD_ROPE_HALVES 0      /* pair i of a head: values i and i + rot / 2 */
+#define SD_ROPE_NEIGHBOURS 1  /* pair i: values 2 i and 2 i + 1 */
+
+/* frequencies of pair i, in radians a position; f_i = base^(-2 i / rot) */
+#define SD_ROPE_PLAIN 0   /* f_i */
+#define SD_ROPE_LINEAR 1  /* f_i / factor */
+#define SD_ROPE_NTK 2     /* f_i of base * factor^(rot / (rot - 2)) */
+#define SD_ROPE_BANDS 3   /* from f_i / factor to f_i as the turns over original_len go from low to high */
+#define SD_ROPE_YARN 4    /* the same over the pairs between those that make `high` and `low` turns over
+                             original_len (whole pairs), and a scale of 0.1 ln(factor) + 1 */
+
+/*
+ * sd_rope -- rotary positions of queries and keys.
+ *
+ * The first `rot` values of every head of token i turn by its position p = positions[i] (any int32):
+ * with a = 2 pi p turns[j] / 2^64, pair j (x, y) becomes
+ *   scale * (x cos a - y sin a),  scale * (y cos a + x sin a),
+ * or, inverse, with -a: what sends a gradient back (or a rotated key to its unrotated one). The other
+ * values are copied. The angle is exact to 10^-7 at every position; values are fp32, rounded once.
+ * Arguments: n >= 0 tokens, n <= 2^31 - 1024; Hq, Hk >= 0 heads of queries and keys (0: none; their
+ *   pointers may then be NULL), Hq + Hk <= 2^20; D a multiple of 8 up to 512; rot even, 0 < rot <= D;
+ *   pairs SD_ROPE_HALVES or SD_ROPE_NEIGHBOURS; turns [rot / 2] (sd_rope_table's, on the device); scale
+ *   finite; q, k and their outputs bf16, value d of head h of token i at i*ld + h*hs + d (16-byte
+ *   aligned, strides multiples of 8). An output may be its input itself, with the same strides, and
+ *   else shares nothing with either input.
+ */
+SD_API int sd_rope(int n, int Hq, int Hk, int D, int rot, int pairs, const int32_t* positions,
+                   const uint64_t* turns, float scale, int inverse, const void* q, long ld_q,
+                   long hs_q, void* q_out, long ld_qo, long hs_qo, const void* k, long ld_k,
+                   long hs_k, void* k_out, long ld_ko, long hs_ko, void* stream);
+
+/*
+ * sd_rope_table -- the turns a position of every pair as fractions of 2^64, and the scale, for
+ * sd_rope. Host arithmetic: turns [rot / 2] and scale are HOST memory, and nothing is enqueued.
+ * Arguments: rot even, 2..512; base > 1; kind SD_ROPE_*; factor > 0 (SD_ROPE_YARN: >= 1); original_len
+ *   > 0 and 0 < low < high for SD_ROPE_BANDS and SD_ROPE_YARN (not looked at otherwise).
+ */
+SD_API int sd_rope_table(int rot, double base, int kind, double factor, double original_len,
+                         double low, double high, uint64_t* turns, float* scale);
+
+/* ---- rows cut by top-k, top-p and min-p ----
+ *
+ * A row's entries stand in order: larger first, equal ones by lower index. With their weights w (the
+ * probabilities for SD_F32_PROBS; exp(l / T_r) for SD_BF16_LOGITS, T_r within 2^-100 and 2^100) those
+ * kept are the first
+ *   top_k[r] of them (<= 0: all),
+ *   those of these before which less than top_p[r] of their sum lies (>= 1: all),
+ *   those with w >= min_p[r] w_max (<= 0: all; above 1 as 1),
+ * whichever is fewest, and the first entry always. T_r <= 0 (or NaN): the first entry alone. Entries of
+ * weight 0 are never kept: probabilities <= 0, logits of -inf, all beside a +inf, and NaN. A
+ * probability above 1 counts as 1. Which entries are kept, and which is drawn, is decided by sums with an
+ * error of 2^-40. temperature, top_k, top_p, min_p are [B] or NULL (1, and off).
+ */
+#define SD_CUT_MAX_V 524224
+
+/*
+ * sd_truncate -- rows cut as above, as probability rows: w / (the sum of those kept), else 0.
+ *
+ * The rows may serve as sd_verify's (target and draft rows cut by the same request's settings: the
+ * answer is then distributed as the cut target rows), sd_draft_sample's or sd_token_logprobs's.
+ * Arguments: B >= 0, J >= 1, 1 <= V <= SD_CUT_MAX_V; rows [B*J, V] of stride ld >= V (row r*J + j is
+ *   request r's); probs [B*J, V] fp32 of stride ld_out >= V, not overlapping rows; kept [B, J] int32
+ *   or NULL: how many entries are kept. A row that keeps none: zeros, kept 0, SD_ERR_ZERO_ROW.
+ *   B*J <= 2^27.
+ */
+SD_API int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld,
+                       const float* temperature, const int32_t* top_k, const float* top_p,
+                       const float* min_p, float* probs, long ld_out, int32_t* kept, int32_t* err,
+                       void* stream);
+
+/*
+ * sd_sample -- one token drawn from each row cut as above, by a given random number.
+ *
+ * tokens[r][j] = the first entry, in the order above, up to and with which more than u[r][j] of the
+ * sum of those kept lies (u taken within [0, 1]; NaN as 0).
+ * Arguments: as for sd_truncate; u [B, J] fp32; tokens [B, J] int32; prob [B, J] fp32 or NULL: the
+ *   token's probability among those kept. A row that keeps none: token 0, prob 0, SD_ERR_ZERO_ROW.
+ */
+SD_API int sd_sample(int B, int J, int V, int dtype, const void* rows, long ld,
+                     const float* temperature, const int32_t* top_k, const float* top_p,
+                     const float* min_p, const float* u, int32_t* tokens, float* prob,
+                     int32_t* kept, int32_t* err, void* stream);
+
+/*
  * sd_token_logprobs -- log probabilities of given tokens (a step's answer: sd_verify's
  * out_tokens on its target rows), with each row's entropy and best alternatives.
  *

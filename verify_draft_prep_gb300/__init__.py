@@ -33,6 +33,15 @@ SD_ERR_DRAFT_COUNT = 128
 SD_ERR_KV_SLOT = 256
 SD_ERR_KV_RANGE = 512
 
+SD_ROPE_HALVES = 0
+SD_ROPE_NEIGHBOURS = 1
+SD_ROPE_PLAIN = 0
+SD_ROPE_LINEAR = 1
+SD_ROPE_NTK = 2
+SD_ROPE_BANDS = 3
+SD_ROPE_YARN = 4
+
+SD_CUT_MAX_V = 524224
 SD_TOP_MAX = 32
 SD_TOP_MAX_V = 33554432
 
@@ -43,7 +52,8 @@ EXPORTED = ["sd_verify", "sd_verify_workspace_bytes", "sd_verify_kernels",
             "sd_verify_prepare", "sd_verify_prepare_workspace_bytes", "sd_verify_prepare_kernels",
             "sd_verify_prepare_ragged", "sd_diag_verify_prepare_withheld",
             "sd_verify_prepare_padded", "sd_kv_write", "sd_kv_read", "sd_kv_attend",
-            "sd_kv_attend_workspace_bytes", "sd_token_logprobs"]
+            "sd_kv_attend_workspace_bytes", "sd_token_logprobs", "sd_kv_weights", "sd_kv_evict",
+            "sd_rope", "sd_rope_table", "sd_truncate", "sd_sample"]
 
 _lock = threading.Lock()
 _lib = None
@@ -139,6 +149,23 @@ def load():
         lib.sd_token_logprobs.argtypes = [i32, i32, i32, i32, P, i64, P, P, i32, P, P, P, P, P, P,
                                           P]
         lib.sd_token_logprobs.restype = i32
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.sd_kv_weights.argtypes = [i32, i32, i32, i32, i32, i32, P, i64, i64, P, P, i64, i64, i64,
+                                      P, i32, i32, P, i32, P, P, P, f32, i32, f32, P, P, P, P]
+        lib.sd_kv_weights.restype = i32
+        lib.sd_kv_evict.argtypes = [i32, i32, i32] + cache + [P, P, i32, P, i32, P, i32, i32, i32, P,
+                                                              P, P, P]
+        lib.sd_kv_evict.restype = i32
+        lib.sd_rope.argtypes = [i32, i32, i32, i32, i32, i32, P, P, f32, i32, P, i64, i64, P, i64,
+                                i64, P, i64, i64, P, i64, i64, P]
+        lib.sd_rope.restype = i32
+        lib.sd_rope_table.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, P]
+        lib.sd_rope_table.restype = i32
+        rows = [i32, i32, i32, i32, P, i64, P, P, P, P]
+        lib.sd_truncate.argtypes = rows + [P, i64, P, P, P]
+        lib.sd_truncate.restype = i32
+        lib.sd_sample.argtypes = rows + [P, P, P, P, P, P]
+        lib.sd_sample.restype = i32
         lib.sd_status_string.argtypes = [i32]
         lib.sd_status_string.restype = ctypes.c_char_p
         lib.sd_version.argtypes = []
@@ -606,6 +633,11 @@ def _int32(t, shape, what):
         raise SDError(f"{what} must be contiguous int32 {list(shape)}")
 
 
+def _float32(t, shape, what):
+    if t.dtype != _t().float32 or t.shape != shape or not t.is_contiguous():
+        raise SDError(f"{what} must be contiguous float32 {list(shape)}")
+
+
 def sd_kv_write(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None, stream=None):
     """Quantise the K and V of n tokens into the pages that slot_mapping names (see include/sd.h).
 
@@ -724,6 +756,188 @@ def sd_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, c
         if give is not None:
             give(ws)
     _check(rc, "sd_kv_attend")
+
+
+def sd_kv_weights(q, lse, k_cache, k_scale, block_table, ctx_lens, cu_q, weights, before=None,
+                  live=None, max_q=None, sm_scale=None, causal=True, decay=1.0, err=None,
+                  stream=None):
+    """The attention weight that each cached token gets from a call's queries (see include/sd.h).
+
+    q, block_table, ctx_lens, cu_q, max_q, sm_scale, causal: as for sd_kv_attend, and lse its [n, Hq]
+    float32; live: [B] int32, how many of each request's query tokens count, or None for all; weights:
+    [num_blocks, Hkv, block_size] float32; before: the same, what tokens had so far (it may be weights
+    itself), or None.
+    """
+    # (K alone is read: its checks serve for both)
+    cache = _cache_args(k_cache, k_cache, k_scale, k_scale)
+    nb, bs, Hkv, D = k_cache.shape
+    B, mb = block_table.shape
+    if q.dim() != 3:
+        raise SDError("q must be [tokens, Hq, D]")
+    n, Hq = q.shape[:2]
+    _int32(block_table, (B, mb), "block_table")
+    _int32(ctx_lens, (B,), "ctx_lens")
+    _int32(cu_q, (B + 1,), "cu_q")
+    if live is not None:
+        _int32(live, (B,), "live")
+    _float32(lse, (n, Hq), "lse")
+    _float32(weights, (nb, Hkv, bs), "weights")
+    if before is not None:
+        _float32(before, (nb, Hkv, bs), "before")
+    rc = _quick().sd_kv_weights(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q),
+                                *_head_rows(q, Hq, D, "q"), _ptr(lse), cache[0], *cache[2:6], nb, bs,
+                                _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q), _ptr(live),
+                                D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)), decay,
+                                _ptr(before), _ptr(weights), _ptr(err), _raw_stream(k_cache, stream))
+    _check(rc, "sd_kv_weights")
+
+
+def sd_kv_evict(k_cache, v_cache, k_scale, v_scale, weights, block_table, ctx_lens, kept, new_lens,
+                to_table=None, sink=0, recent=0, err=None, stream=None):
+    """Cut a cache to kept.shape[2] tokens a request, by their weights (see include/sd.h).
+
+    weights: [num_blocks, Hkv, block_size] float32 (sd_kv_weights'); kept: [B, Hkv, budget] int32
+    output, the positions that stay; new_lens: [B] int32 output; to_table: [B, blocks] int32, fresh
+    pages for the tokens that stay, or None: they move to the front of the request's own.
+    """
+    cache = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    nb, bs, Hkv, D = k_cache.shape
+    B, mb = block_table.shape
+    _int32(block_table, (B, mb), "block_table")
+    _int32(ctx_lens, (B,), "ctx_lens")
+    _int32(new_lens, (B,), "new_lens")
+    if kept.dim() != 3:
+        raise SDError("kept must be [B, Hkv, budget]")
+    budget = kept.shape[2]
+    _int32(kept, (B, Hkv, budget), "kept")
+    _float32(weights, (nb, Hkv, bs), "weights")
+    to_blocks = 0
+    if to_table is not None:
+        to_blocks = to_table.shape[-1]
+        _int32(to_table, (B, to_blocks), "to_table")
+    rc = _quick().sd_kv_evict(B, Hkv, D, *cache, _ptr(weights), _ptr(block_table), mb,
+                              _ptr(to_table), to_blocks, _ptr(ctx_lens), budget, sink, recent,
+                              _ptr(kept), _ptr(new_lens), _ptr(err), _raw_stream(k_cache, stream))
+    _check(rc, "sd_kv_evict")
+
+
+_ROPE_PAIRS = {"halves": SD_ROPE_HALVES, "neighbours": SD_ROPE_NEIGHBOURS}
+_ROPE_KINDS = {"plain": SD_ROPE_PLAIN, "linear": SD_ROPE_LINEAR, "ntk": SD_ROPE_NTK,
+               "bands": SD_ROPE_BANDS, "yarn": SD_ROPE_YARN}
+
+
+def sd_rope_table(rot, base=10000.0, kind="plain", factor=1.0, original_len=0, low=1.0, high=32.0,
+                  device="cuda"):
+    """(turns, scale) for sd_rope, made once for a model (see include/sd.h): turns [rot / 2] int64 on
+    the device, the bits of fractions of 2^64; kind: "plain", "linear", "ntk", "bands" or "yarn"."""
+    torch = _t()
+    if kind not in _ROPE_KINDS:
+        raise SDError(f"kind must be one of {sorted(_ROPE_KINDS)}")
+    turns = torch.zeros(max(1, rot // 2), dtype=torch.int64)
+    scale = ctypes.c_float()
+    rc = _quick().sd_rope_table(rot, base, _ROPE_KINDS[kind], factor, original_len, low, high,
+                                turns.data_ptr(), ctypes.byref(scale))
+    _check(rc, "sd_rope_table")
+    return turns.to(device), scale.value
+
+
+def sd_rope(positions, turns, q=None, k=None, q_out=None, k_out=None, pairs="halves", scale=1.0,
+            inverse=False, stream=None):
+    """Rotary positions of queries and keys (see include/sd.h).
+
+    positions: [n] int32; turns: [rot / 2] int64 (sd_rope_table's): the first rot values of a head
+    turn; q, k: [n, heads, D] bfloat16 with contiguous heads (slices of one projection will do), either
+    may be None; q_out, k_out: the same shapes, or None to turn them in place; pairs: "halves" or
+    "neighbours"; inverse: turn back (a gradient).
+    """
+    if pairs not in _ROPE_PAIRS:
+        raise SDError("pairs must be 'halves' or 'neighbours'")
+    some = q if q is not None else k
+    if some is None or some.dim() != 3:
+        raise SDError("q and k must be [tokens, heads, D], one of them at least given")
+    if turns.dtype != _t().int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise SDError("turns must be contiguous int64 [rot / 2]")
+    n, _, D = some.shape
+    _int32(positions, (n,), "positions")
+    args = []
+    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise SDError(f"{what}_out comes with {what}")
+            args.append((0, None, 0, 0, None, 0, 0))
+            continue
+        if x.dim() != 3 or x.shape[0] != n:
+            raise SDError("q and k must hold the same tokens")
+        H = x.shape[1]
+        y = x if y is None else y
+        if y.shape != x.shape:
+            raise SDError(f"{what}_out must have {what}'s shape")
+        args.append((H, _ptr(x), *_head_rows(x, H, D, what), _ptr(y),
+                     *_head_rows(y, H, D, what + "_out")))
+    rc = _quick().sd_rope(n, args[0][0], args[1][0], D, 2 * turns.shape[0], _ROPE_PAIRS[pairs],
+                          _ptr(positions), _ptr(turns), scale, int(bool(inverse)), *args[0][1:],
+                          *args[1][1:], _raw_stream(some, stream))
+    _check(rc, "sd_rope")
+
+
+def _rows_args(rows, B, J, temperature, top_k, top_p, min_p):
+    """The arguments that sd_truncate and sd_sample share."""
+    torch = _t()
+    if rows.dtype == torch.float32:
+        dtype = SD_F32_PROBS
+    elif rows.dtype == torch.bfloat16:
+        dtype = SD_BF16_LOGITS
+    else:
+        raise SDError("rows must be float32 probabilities or bfloat16 logits")
+    if rows.dim() != 2 or rows.shape[0] != B * J:
+        raise SDError("rows must hold B*J rows")
+    for t, what in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None:
+            _float32(t, (B,), what)
+    if top_k is not None:
+        _int32(top_k, (B,), "top_k")
+    return (B, J, rows.shape[1], dtype, _ptr(rows), _row_stride(rows), _ptr(temperature), _ptr(top_k),
+            _ptr(top_p), _ptr(min_p))
+
+
+def sd_truncate(rows, probs, kept, temperature=None, top_k=None, top_p=None, min_p=None, err=None,
+                stream=None):
+    """Rows cut by top-k, top-p and min-p, as probability rows (see include/sd.h).
+
+    rows: [B*J, V] float32 probabilities or bfloat16 logits; probs: [B*J, V] float32 output; kept:
+    [B, J] int32 output, how many entries are kept (its shape says which rows are whose); temperature,
+    top_p, min_p: [B] float32 or None; top_k: [B] int32 or None.
+    """
+    B, J = kept.shape
+    args = _rows_args(rows, B, J, temperature, top_k, top_p, min_p)
+    _int32(kept, (B, J), "kept")
+    if probs.dtype != _t().float32 or probs.shape != rows.shape:
+        raise SDError("probs must be float32 of rows' shape")
+    rc = _quick().sd_truncate(*args, _ptr(probs), _row_stride(probs), _ptr(kept), _ptr(err),
+                              _raw_stream(rows, stream))
+    _check(rc, "sd_truncate")
+
+
+def sd_sample(rows, u, tokens, prob=None, kept=None, temperature=None, top_k=None, top_p=None,
+              min_p=None, err=None, stream=None):
+    """One token drawn from each row, cut by top-k, top-p and min-p, by a given random number (see
+    include/sd.h).
+
+    rows: [B*J, V] float32 probabilities or bfloat16 logits; u: [B, J] float32 in [0, 1); tokens:
+    [B, J] int32 output; prob: [B, J] float32 and kept: [B, J] int32 outputs or None; temperature,
+    top_p, min_p: [B] float32 or None; top_k: [B] int32 or None.
+    """
+    B, J = tokens.shape
+    args = _rows_args(rows, B, J, temperature, top_k, top_p, min_p)
+    _int32(tokens, (B, J), "tokens")
+    _float32(u, (B, J), "u")
+    if prob is not None:
+        _float32(prob, (B, J), "prob")
+    if kept is not None:
+        _int32(kept, (B, J), "kept")
+    rc = _quick().sd_sample(*args, _ptr(u), _ptr(tokens), _ptr(prob), _ptr(kept), _ptr(err),
+                            _raw_stream(rows, stream))
+    _check(rc, "sd_sample")
 
 
 def sd_token_logprobs(rows, tokens, logprob, entropy=None, rank=None, top_ids=None,

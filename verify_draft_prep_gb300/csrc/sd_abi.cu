@@ -64,6 +64,20 @@ int sd_kv_attend_launch(int, int, int, int, int, int, const void*, long, long, c
                         const void*, long, long, long, const float*, const float*, int, int,
                         const int32_t*, int, const int32_t*, const int32_t*, float, int, void*,
                         long, long, float*, void*, int32_t*, cudaStream_t);
+int sd_kv_weights_launch(int, int, int, int, int, int, const void*, long, long, const float*,
+                         const void*, long, long, long, const float*, int, int, const int32_t*,
+                         int, const int32_t*, const int32_t*, const int32_t*, float, int, float,
+                         const float*, float*, int32_t*, cudaStream_t);
+int sd_kv_evict_launch(int, int, int, void*, void*, long, long, long, float*, float*, int, int,
+                       float*, const int32_t*, int, const int32_t*, int, const int32_t*, int, int,
+                       int, int32_t*, int32_t*, int32_t*, cudaStream_t);
+int sd_rope_launch(int, int, int, int, int, int, const int32_t*, const uint64_t*, float, int,
+                   const void*, long, long, void*, long, long, const void*, long, long, void*, long,
+                   long, cudaStream_t);
+void sd_rope_table_make(int, double, int, double, double, double, double, uint64_t*, float*);
+int sd_rows_launch(int, int, int, int, const void*, long, const float*, const int32_t*,
+                   const float*, const float*, float*, long, const float*, int32_t*, float*,
+                   int32_t*, int32_t*, cudaStream_t);
 int sd_logprobs_launch(int, int, int, int, const void*, long, const int32_t*, const float*, int,
                        float*, float*, int32_t*, int32_t*, float*, int32_t*, cudaStream_t);
 }
@@ -709,6 +723,142 @@ int sd_token_logprobs(int B, int J, int V, int dtype, const void* rows, long ld,
   if (dev != SD_OK) return dev;
   return sd_logprobs_launch(B, J, V, dtype, rows, ld, tokens, temperature, n_top, logprob, entropy,
                             rank, top_ids, top_logprobs, err, (cudaStream_t)stream);
+}
+
+int sd_kv_weights(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q, long ld_q,
+                  long hs_q, const float* lse, const void* k_cache, long st_block, long st_tok,
+                  long st_head, const float* k_scale, int num_blocks, int block_size,
+                  const int32_t* block_table, int max_blocks, const int32_t* ctx_lens,
+                  const int32_t* cu_q, const int32_t* live, float sm_scale, int causal, float decay,
+                  const float* before, float* weights, int32_t* err, void* stream) {
+  if (B < 0 || n < 0 || max_q < 1 || max_blocks < 0 || Hq < 1 || ld_q < 0 || hs_q < 0)
+    return SD_E_SHAPE;
+  const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
+  if (rc != SD_OK) return rc;
+  if (Hq % Hkv || (long long)n * Hq > kMostCounted || B > 65535 || Hkv > 65535 || num_blocks < 1)
+    return SD_E_SHAPE;
+  if (!(sm_scale > 0.f && sm_scale <= 3.402823466e38f)) return SD_E_SHAPE;
+  if (!(decay >= 0.f && decay <= 3.402823466e38f)) return SD_E_SHAPE;
+  if (B == 0) return SD_OK;
+  if (!ctx_lens || !cu_q || !weights || (max_blocks > 0 && !block_table)) return SD_E_NULL;
+  if (n > 0 && (!q || !lse)) return SD_E_NULL;
+  if (!k_cache || !k_scale) return SD_E_NULL;
+  if (!aligned16(q) || !aligned16(k_cache) || ld_q % 8 || hs_q % 8) return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_kv_weights_launch(B, n, max_q, Hq, Hkv, D, q, ld_q, hs_q, lse, k_cache, st_block, st_tok,
+                              st_head, k_scale, num_blocks, cache_log2_bs(block_size), block_table,
+                              max_blocks, ctx_lens, cu_q, live, sm_scale, causal, decay, before,
+                              weights, err, (cudaStream_t)stream);
+}
+
+int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long st_block, long st_tok,
+                long st_head, float* k_scale, float* v_scale, int num_blocks, int block_size,
+                float* weights, const int32_t* block_table, int max_blocks, const int32_t* to_table,
+                int to_blocks, const int32_t* ctx_lens, int budget, int sink, int recent,
+                int32_t* kept, int32_t* new_lens, int32_t* err, void* stream) {
+  if (B < 0 || B > 65535 || max_blocks < 0 || to_blocks < 0) return SD_E_SHAPE;
+  const int rc = check_cache(Hkv, D, st_block, st_tok, st_head, num_blocks, block_size);
+  if (rc != SD_OK) return rc;
+  if (Hkv > 65535 || budget < 1 || budget > kMostCounted || sink < 0 || recent < 0 ||
+      (long long)sink + recent > budget)
+    return SD_E_SHAPE;
+  if (B == 0) return SD_OK;
+  if (!ctx_lens || !kept || !new_lens || (max_blocks > 0 && !block_table)) return SD_E_NULL;
+  if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale || !weights)) return SD_E_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_kv_evict_launch(B, Hkv, D, k_cache, v_cache, st_block, st_tok, st_head, k_scale, v_scale,
+                            num_blocks, cache_log2_bs(block_size), weights, block_table, max_blocks,
+                            to_table, to_blocks, ctx_lens, budget, sink, recent, kept, new_lens, err,
+                            (cudaStream_t)stream);
+}
+
+int sd_rope(int n, int Hq, int Hk, int D, int rot, int pairs, const int32_t* positions,
+            const uint64_t* turns, float scale, int inverse, const void* q, long ld_q, long hs_q,
+            void* q_out, long ld_qo, long hs_qo, const void* k, long ld_k, long hs_k, void* k_out,
+            long ld_ko, long hs_ko, void* stream) {
+  if (n < 0 || n > kMostCounted || Hq < 0 || Hk < 0 || (long long)Hq + Hk > 1 << 20)
+    return SD_E_SHAPE;
+  if (D < 8 || D > 512 || D % 8 || rot < 2 || rot > D || rot % 2) return SD_E_SHAPE;
+  if (pairs != SD_ROPE_HALVES && pairs != SD_ROPE_NEIGHBOURS) return SD_E_SHAPE;
+  if (!(scale >= -3.402823466e38f && scale <= 3.402823466e38f)) return SD_E_SHAPE;
+  if (ld_q < 0 || hs_q < 0 || ld_qo < 0 || hs_qo < 0 || ld_k < 0 || hs_k < 0 || ld_ko < 0 ||
+      hs_ko < 0)
+    return SD_E_SHAPE;
+  if (n == 0 || Hq + Hk == 0) return SD_OK;
+  if (!positions || !turns || (Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)))
+    return SD_E_NULL;
+  if (Hq > 0 && (!aligned16(q) || !aligned16(q_out) || ld_q % 8 || hs_q % 8 || ld_qo % 8 ||
+                 hs_qo % 8))
+    return SD_E_ALIGN;
+  if (Hk > 0 && (!aligned16(k) || !aligned16(k_out) || ld_k % 8 || hs_k % 8 || ld_ko % 8 ||
+                 hs_ko % 8))
+    return SD_E_ALIGN;
+  if ((uintptr_t)turns % 8) return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_rope_launch(n, Hq, Hk, D, rot, pairs, positions, turns, scale, inverse, q, ld_q, hs_q,
+                        q_out, ld_qo, hs_qo, k, ld_k, hs_k, k_out, ld_ko, hs_ko,
+                        (cudaStream_t)stream);
+}
+
+int sd_rope_table(int rot, double base, int kind, double factor, double original_len, double low,
+                  double high, uint64_t* turns, float* scale) {
+  if (rot < 2 || rot > 512 || rot % 2 || kind < SD_ROPE_PLAIN || kind > SD_ROPE_YARN)
+    return SD_E_SHAPE;
+  const double most = 1e30;  // (finite, and so are the products below)
+  if (!(base > 1 && base < most)) return SD_E_SHAPE;
+  if (kind != SD_ROPE_PLAIN && !(factor > 1 / most && factor < most)) return SD_E_SHAPE;
+  if (kind == SD_ROPE_YARN && !(factor >= 1)) return SD_E_SHAPE;
+  if (kind == SD_ROPE_BANDS || kind == SD_ROPE_YARN)
+    if (!(original_len > 0 && original_len < most && low > 0 && high > low && high < most))
+      return SD_E_SHAPE;
+  if (!turns || !scale) return SD_E_NULL;
+  sd_rope_table_make(rot, base, kind, factor, original_len, low, high, turns, scale);
+  return SD_OK;
+}
+
+namespace {
+
+// What sd_truncate and sd_sample check alike.
+int check_rows(int B, int J, int V, int dtype, long ld) {
+  if (dtype != SD_F32_PROBS && dtype != SD_BF16_LOGITS) return SD_E_DTYPE;
+  if (B < 0 || J < 1 || V < 1 || V > SD_CUT_MAX_V || ld < V) return SD_E_SHAPE;
+  if ((long long)B * J > 1LL << 27) return SD_E_SHAPE;
+  return SD_OK;
+}
+
+}  // namespace
+
+int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld, const float* temperature,
+                const int32_t* top_k, const float* top_p, const float* min_p, float* probs,
+                long ld_out, int32_t* kept, int32_t* err, void* stream) {
+  const int rc = check_rows(B, J, V, dtype, ld);
+  if (rc != SD_OK) return rc;
+  if (ld_out < V) return SD_E_SHAPE;
+  if (B == 0) return SD_OK;
+  if (!rows || !probs) return SD_E_NULL;
+  if ((uintptr_t)rows % (dtype == SD_F32_PROBS ? 4 : 2) || (uintptr_t)probs % 4) return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_rows_launch(B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p, probs, ld_out,
+                        nullptr, nullptr, nullptr, kept, err, (cudaStream_t)stream);
+}
+
+int sd_sample(int B, int J, int V, int dtype, const void* rows, long ld, const float* temperature,
+              const int32_t* top_k, const float* top_p, const float* min_p, const float* u,
+              int32_t* tokens, float* prob, int32_t* kept, int32_t* err, void* stream) {
+  const int rc = check_rows(B, J, V, dtype, ld);
+  if (rc != SD_OK) return rc;
+  if (B == 0) return SD_OK;
+  if (!rows || !u || !tokens) return SD_E_NULL;
+  if ((uintptr_t)rows % (dtype == SD_F32_PROBS ? 4 : 2)) return SD_E_ALIGN;
+  const int dev = check_device();
+  if (dev != SD_OK) return dev;
+  return sd_rows_launch(B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p, nullptr, 0, u,
+                        tokens, prob, kept, err, (cudaStream_t)stream);
 }
 
 }  // extern "C"

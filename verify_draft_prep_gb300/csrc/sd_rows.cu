@@ -1,0 +1,688 @@
+// sd_rows.cu -- rows cut by top-k, top-p and min-p: as probability rows (sd_truncate), or one token
+// drawn from each by a given random number (sd_sample).
+//
+// The entries of a row stand in order, larger first and equal ones by their index, and what is kept
+// is always a prefix of that order: the shortest of three. With weights w (the probabilities, or
+// exp((l - l_max) / T)) the first top_k entries, of those the ones before which less than top_p of
+// their sum lies, and the ones with w >= min_p w_max. A draw is a place in the running sum too. So
+// every question is one for a place in the order, by count or by sum, and the row is never sorted: a
+// histogram over its values answers them.
+//
+// Logits are bf16: a row has at most 65536 different values, so a histogram of all of them holds the
+// row exactly, and w is needed once for each value that occurs instead of once for each entry. That is
+// what lets the sums be exact enough for whole numbers to come out right: w in pairs of fp32 (2^-44),
+// sums in 64-bit integers. Probabilities have 32 bits: the histogram is over their upper 16, with the
+// sums of the lower 16 in whole numbers, and the one bin in question is resolved by reading the row
+// again (from L2), 8 bits at a time.
+//
+// A row is a cluster's work: each CTA counts its part into its own histogram (16-bit counts, so a part
+// is at most 65528 entries), then each scans its share of the bins over all of the cluster's
+// histograms through distributed shared memory.
+
+#include <atomic>
+
+#include "sd_kv.cuh"
+
+namespace sdk {
+
+constexpr int kRowThreads = 1024, kRowWarps = kRowThreads / 32;
+constexpr int kHistBytes = 131072;
+constexpr int kMostClusters = 8;
+// Sums are multiples of 2^-43 of the largest weight (logits) or of the power of two above it.
+constexpr int kSumBits = 43;
+constexpr double kSumUnit = 8796093022208.0;  // 2^43
+
+struct RowsParams {
+  const void* rows;
+  long ld;
+  int J, V, part, vec;  // entries of a CTA's part; whether rows allow 16-byte loads
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  float* probs;  // sd_truncate
+  long ld_out;
+  int vec_out;
+  const float* u;  // sd_sample
+  int32_t* tokens;
+  float* prob;
+  int32_t* kept;
+  int32_t* err;
+};
+
+// A value's place: entries of larger values and their sum, how many entries have the value, and the
+// weight of each (in units of the sums).
+struct Border {
+  uint32_t key, above, count;
+  double sum, w;
+};
+
+struct RowShared {
+  float2 two_to[64];               // 2^(j / 64) as pairs
+  uint32_t warp_count[kRowWarps];
+  unsigned long long warp_sum[kRowWarps];
+  uint32_t rank_count[kMostClusters];
+  unsigned long long rank_sum[kMostClusters];
+  uint32_t rank_top[kMostClusters];
+  uint32_t rank_eq[kMostClusters];
+  Border found, inside;             // a bin, by the CTA that holds it; an entry of it, by each CTA
+  uint32_t low[256];                // counts of the sub-bins
+  unsigned long long low_sum[256];  // sums of what lies below them
+  uint32_t merged[256];
+  unsigned long long merged_sum[256];
+  float2 per_unit;  // log2(e) / T as a pair
+  int index;
+};
+
+__device__ __forceinline__ FF ff_sum(float a, float b) { return ff_two_sum(a, b); }
+
+// 2^y for y = d c (pairs), y <= 0, as a count of 2^-63 (0 below 2^-63): k / 64 is y's nearest multiple
+// of 2^-6, 2^(k/64) from the table, and the rest e^u with |u| <= 0.0055, whose terms from the third on
+// need only fp32.
+__device__ __forceinline__ unsigned long long weight63(FF d, float2 c, const float2* two_to) {
+  const float p = d.hi * c.x;
+  if (!(p > -63.f)) return 0;
+  const float e = fmaf(d.hi, c.x, -p) + fmaf(d.hi, c.y, d.lo * c.x);
+  const int k = __float2int_rn(p * 64.f);
+  const FF g = ff_sum(fmaf((float)k, -0.015625f, p), e);
+  constexpr float kLn2Hi = 0.69314718055994531f;
+  constexpr float kLn2Lo = (float)(0.69314718055994530942 - (double)0.69314718055994531f);
+  const float uh = g.hi * kLn2Hi;
+  const float ul = fmaf(g.hi, kLn2Hi, -uh) + fmaf(g.hi, kLn2Lo, g.lo * kLn2Hi);
+  const float q = uh * uh;
+  const float ql = fmaf(uh, uh, -q) + 2.f * uh * ul;
+  const float cube = q * uh * fmaf(uh, fmaf(uh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f);
+  const FF r = ff_sum(uh, 0.5f * q);
+  const float rl = r.lo + (ul + fmaf(0.5f, ql, cube));
+  const float2 t = two_to[k & 63];
+  const float ph = t.x * r.hi;
+  const float pl = fmaf(t.x, r.hi, -ph) + fmaf(t.x, rl, t.y * r.hi);
+  const FF s = ff_sum(t.x, ph);
+  const float lo = s.lo + pl + t.y;
+  const float up = __uint_as_float((uint32_t)(127 + 63 + (k >> 6)) << 23);
+  return (unsigned long long)((long long)__float2ull_rz(s.hi * up) + __float2ll_rn(lo * up));
+}
+
+__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T warp_before(T v) {  // the sum over the lanes before this one
+  const int lane = threadIdx.x & 31;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x - v;
+}
+
+// Orderable keys. Logits: 16 bits, ascending with the value, both zeros alike; 0 for what is never
+// kept (-inf, NaN). Probabilities: their bits; 0 for what is not above 0, and 1 for what is above 1.
+__device__ __forceinline__ uint32_t logit_key(uint32_t b) {
+  if (b == 0x8000u) b = 0;
+  const uint32_t k = b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
+  return k <= 0x7fu || k > 0xff80u ? 0u : k;
+}
+__device__ __forceinline__ float logit_value(uint32_t k) {
+  return __uint_as_float((k & 0x8000u ? k & 0x7fffu : ~k & 0xffffu) << 16);
+}
+__device__ __forceinline__ uint32_t prob_key(uint32_t b) {
+  return b - 1u < 0x7f800000u ? min(b, 0x3f800000u) : 0u;
+}
+
+template <bool PROBS>
+struct RowReader {
+  const RowsParams& P;
+  const void* row;
+  int begin, end;  // this CTA's entries
+
+  __device__ __forceinline__ uint32_t key_at(int i) const {
+    return PROBS ? prob_key(__ldg((const uint32_t*)row + i))
+                 : logit_key(__ldg((const uint16_t*)row + i));
+  }
+
+  // f(index, key) for every entry of [a, b) that this thread takes, `step` vectors apart from `first`.
+  template <typename F>
+  __device__ __forceinline__ void each(int a, int b, int first, int step, F f) const {
+    constexpr int N = PROBS ? 4 : 8;
+    if (!P.vec) {
+      for (int i = a + first; i < b; i += step) f(i, key_at(i));
+      return;
+    }
+    const int vecs = (b - a) / N;
+    const uint4* p = reinterpret_cast<const uint4*>((const char*)row + (size_t)a * (PROBS ? 4 : 2));
+    auto one = [&](const uint4& v, int at) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (PROBS) {
+          f(at + j, prob_key(w[j]));
+        } else {
+          f(at + 2 * j, logit_key(w[j] & 0xffffu));
+          f(at + 2 * j + 1, logit_key(w[j] >> 16));
+        }
+      }
+    };
+    int v = first;
+    for (; v + 3 * step < vecs; v += 4 * step) {
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = __ldg(p + v + k * step);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) one(x[k], a + (v + k * step) * N);
+    }
+    for (; v < vecs; v += step) one(__ldg(p + v), a + v * N);
+    for (int i = a + vecs * N + first; i < b; i += step) f(i, key_at(i));
+  }
+};
+
+template <bool PROBS, bool WRITE>
+__global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P) {
+  extern __shared__ __align__(16) unsigned char s_hist[];
+  __shared__ RowShared sh;
+  uint32_t* hist = reinterpret_cast<uint32_t*>(s_hist);                       // logits: two counts
+  unsigned long long* hist64 = reinterpret_cast<unsigned long long*>(s_hist);  // count << 40 | sum
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x / C, req = row / P.J;
+  const float T = P.temperature ? P.temperature[req] : 1.f;
+  const bool greedy = !(T > 0.f);
+  RowReader<PROBS> in{P, (const char*)P.rows + (size_t)row * P.ld * (PROBS ? 4 : 2),
+                      min(P.V, rank * P.part), min(P.V, (rank + 1) * P.part)};
+
+  // ---- 1. this CTA's histogram and largest key ----
+  for (int i = tid; i < kHistBytes / 16; i += kRowThreads)
+    reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 64) {
+    const double t = exp2((double)tid / 64.0);
+    const float hi = (float)t;
+    sh.two_to[tid] = make_float2(hi, (float)(t - (double)hi));
+  } else if (tid == 64 && !PROBS) {
+    const double c = 1.4426950408889634074 / fmin(fmax((double)(greedy ? 1.f : T), 0x1p-100), 0x1p100);
+    const float hi = (float)c;
+    sh.per_unit = make_float2(hi, (float)(c - (double)hi));
+  }
+  if (tid == 65) sh.found = sh.inside = Border{0, 0, 0, 0.0, 0.0};
+  cluster.sync();  // (every CTA has begun: its shared memory may be written from here on)
+  uint32_t top = 0;
+  in.each(in.begin, in.end, tid, kRowThreads, [&](int, uint32_t k) {
+    if (!k) return;
+    top = max(top, k);
+    if (PROBS)  // (descending: bin 0 holds the largest; keys are at most 0x3f80 << 16)
+      atomicAdd(&hist64[0x3fff - (k >> 16)], 1ull << 40 | (k & 0xffffu));
+    else
+      atomicAdd(&hist[0x7fff - (k >> 1)], k & 1 ? 1u : 65536u);
+  });
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) sh.warp_count[warp] = top;
+  __syncthreads();
+  if (warp == 0) {
+    top = __reduce_max_sync(0xffffffffu, sh.warp_count[lane]);
+    if (lane < C) cluster.map_shared_rank(sh.rank_top, lane)[rank] = top;
+  }
+  cluster.sync();
+  top = 0;
+  for (int c = 0; c < C; ++c) top = max(top, sh.rank_top[c]);
+
+  // ---- 2. counts and sums before every row of 32 histogram words of this warp ----
+  const float top_value = PROBS ? 0.f : logit_value(top);
+  const int top_exp = PROBS ? max(1, (int)(top >> 23)) : 0;
+  const float2 per_unit = sh.per_unit;
+  // an entry's weight as a count of 2^-63 (logits)
+  auto weight = [&](uint32_t k) -> unsigned long long {
+    if (k == top) return 1ull << 63;
+    if (top == 0xff80u) return 0;  // beside +inf nothing weighs anything
+    return weight63(ff_sum(logit_value(k), -top_value), per_unit, sh.two_to);
+  };
+  auto sum_of = [&](uint32_t n, unsigned long long w63) -> unsigned long long {
+    // n w 2^-63 in units of 2^-43, rounded
+    const unsigned long long hi = __umul64hi(w63, (unsigned long long)n << 44);
+    return hi + ((w63 * ((unsigned long long)n << 44)) >> 63);
+  };
+  // exponent of a probability bin's (or key's) last place, relative to the units of the sums
+  auto place = [&](uint32_t k) { return max(1, (int)(k >> 23)) - top_exp + kSumBits - 24; };
+  auto bin_base = [&](uint32_t k) {  // the 24-bit significand with the lower 16 bits zero
+    return ((k >> 23) ? 0x800000u : 0u) | (k & 0x7f0000u);
+  };
+  auto shifted = [&](unsigned long long units, int by) -> unsigned long long {
+    if (by >= 0) return units << by;
+    return by < -62 ? 0 : ((units >> (-by - 1)) + 1) >> 1;
+  };
+  constexpr int kWords = PROBS ? kHistBytes / 8 : kHistBytes / 4;
+  const int my_rows = kWords / 32 / (C * kRowWarps);
+  const int word0 = (rank * kRowWarps + warp) * my_rows * 32;
+  // the entries of this lane's word of a row: two values (logits), the larger first, or one bin
+  struct Word {
+    uint32_t n0, n1;
+    unsigned long long s0, s1, w0, w1;
+  };
+  auto read_word = [&](int word) {
+    Word x = {0, 0, 0, 0, 0, 0};
+    if (PROBS) {
+      unsigned long long low = 0;
+      for (int c = 0; c < C; ++c) {
+        const unsigned long long v = *cluster.map_shared_rank(hist64 + word, c);
+        x.n0 += (uint32_t)(v >> 40);
+        low += v & 0xffffffffffull;
+      }
+      const uint32_t k = (uint32_t)(0x3fff - word) << 16;
+      x.s0 = shifted((unsigned long long)x.n0 * bin_base(k) + low, place(k));
+      x.w0 = low;
+    } else {
+      for (int c = 0; c < C; ++c) {
+        const uint32_t v = *cluster.map_shared_rank(hist + word, c);
+        x.n0 += v & 0xffffu;
+        x.n1 += v >> 16;
+      }
+      const uint32_t k = (uint32_t)(0x7fff - word) * 2 + 1;
+      if (x.n0) x.s0 = sum_of(x.n0, x.w0 = weight(k));
+      if (x.n1) x.s1 = sum_of(x.n1, x.w1 = weight(k - 1));
+    }
+    return x;
+  };
+  uint32_t row_count = 0;           // lane i: of row i, then of the rows before it
+  unsigned long long row_sum = 0;
+  for (int i = 0; i < my_rows; ++i) {
+    const Word x = read_word(word0 + i * 32 + lane);
+    const uint32_t n = __reduce_add_sync(0xffffffffu, x.n0 + x.n1);
+    if (n) {
+      const unsigned long long s = warp_sum64(x.s0 + x.s1);
+      if (lane == i) {
+        row_count = n;
+        row_sum = s;
+      }
+    }
+  }
+  uint32_t count_at = warp_before(row_count);
+  unsigned long long sum_at = warp_before(row_sum);
+  uint32_t my_count = __shfl_sync(0xffffffffu, count_at + row_count, 31);
+  unsigned long long my_sum = __shfl_sync(0xffffffffu, sum_at + row_sum, 31);
+  if (lane == 0) {
+    sh.warp_count[warp] = my_count;
+    sh.warp_sum[warp] = my_sum;
+  }
+  __syncthreads();
+  {
+    const uint32_t n = sh.warp_count[lane];
+    const unsigned long long s = sh.warp_sum[lane];
+    const uint32_t nb = warp_before(n);
+    const unsigned long long sb = warp_before(s);
+    if (warp == 0) {
+      const uint32_t all_n = __shfl_sync(0xffffffffu, nb + n, 31);
+      const unsigned long long all_s = __shfl_sync(0xffffffffu, sb + s, 31);
+      if (lane < C) {
+        cluster.map_shared_rank(sh.rank_count, lane)[rank] = all_n;
+        cluster.map_shared_rank(sh.rank_sum, lane)[rank] = all_s;
+      }
+    }
+    count_at += __shfl_sync(0xffffffffu, nb, warp);
+    sum_at += __shfl_sync(0xffffffffu, sb, warp);
+  }
+  cluster.sync();
+  uint32_t total = 0;
+  unsigned long long total_sum = 0;
+  for (int c = 0; c < C; ++c) {
+    if (c == rank) {
+      count_at += total;
+      sum_at += total_sum;
+    }
+    total += sh.rank_count[c];
+    total_sum += sh.rank_sum[c];
+  }
+  const uint32_t count0 = __shfl_sync(0xffffffffu, count_at, 0);  // before this warp
+  const unsigned long long sum0 = __shfl_sync(0xffffffffu, sum_at, 0);
+
+  // ---- 3. places in the order ----
+  // By count: the entry at place g (from 0). By sum: the one whose stretch of the running sum holds g.
+  // By key: the value `g`, whether it occurs or not. Every thread of the cluster calls this alike.
+  enum { kByCount, kBySum, kByKey };
+  auto find = [&](int by, unsigned long long g, double goal) -> Border {
+    const int key_word = by == kByKey ? (PROBS ? 0x3fff - (int)(g >> 16) : 0x7fff - (int)(g >> 1)) : 0;
+    bool mine = by == kByCount ? g >= count0 && g - count0 < my_count
+                : by == kBySum ? g >= sum0 && g - sum0 < my_sum
+                               : key_word >= word0 && key_word < word0 + my_rows * 32;
+    if (mine) {
+      uint32_t at;
+      if (by == kByKey) {
+        at = (key_word - word0) >> 5;
+      } else {
+        const bool before = by == kByCount ? count_at <= g : sum_at <= g;
+        // (rows beyond this warp's, and empty ones, stand where the next one begins)
+        at = 31 - __clz(__ballot_sync(0xffffffffu, before && lane < my_rows));
+        // of rows that begin at the same place the last one is not empty
+      }
+      const uint32_t base_n = __shfl_sync(0xffffffffu, count_at, at);
+      const unsigned long long base_s = __shfl_sync(0xffffffffu, sum_at, at);
+      const Word x = read_word(word0 + at * 32 + lane);
+      const uint32_t n = base_n + warp_before(x.n0 + x.n1);
+      const unsigned long long s = base_s + warp_before(x.s0 + x.s1);
+      bool here, second = false;
+      if (by == kByCount) {
+        here = g >= n && g < n + x.n0 + x.n1;
+        second = g >= n + x.n0;
+      } else if (by == kBySum) {
+        here = g >= s && g < s + x.s0 + x.s1;
+        second = g >= s + x.s0;
+      } else {
+        here = word0 + (int)at * 32 + lane == key_word;
+        second = !PROBS && !(g & 1);
+      }
+      if (here) {
+        Border b;
+        const int word = word0 + at * 32 + lane;
+        b.key = PROBS ? (uint32_t)(0x3fff - word) << 16 : (uint32_t)(0x7fff - word) * 2 + (second ? 0 : 1);
+        b.above = n + (second ? x.n0 : 0);
+        b.count = second ? x.n1 : x.n0;
+        b.sum = (double)(s + (second ? x.s0 : 0));
+        b.w = PROBS ? (double)x.w0 : (double)(second ? x.w1 : x.w0) * 0x1p-20;
+        for (int c = 0; c < C; ++c) *cluster.map_shared_rank(&sh.found, c) = b;
+      }
+    }
+    cluster.sync();
+    Border b = sh.found;
+    cluster.sync();
+    if (!PROBS) return b;
+    // A probability's bin holds 65536 values: two passes over the row find the one in question.
+    const double unit = exp2((double)place(b.key));
+    if (b.count == 1 && by != kByKey) {
+      b.key |= (uint32_t)b.w;  // the sum of the lower halves is that of the only entry
+      b.w = (double)(bin_base(b.key) | (b.key & 0xffffu)) * unit;
+      return b;
+    }
+    for (int level = 0; level < 2; ++level) {
+      const int shift = level ? 0 : 8;
+      if (tid < 256) {
+        sh.low[tid] = 0;
+        sh.low_sum[tid] = 0;
+      }
+      __syncthreads();
+      const uint32_t want = b.key >> (shift + 8);
+      in.each(in.begin, in.end, tid, kRowThreads, [&](int, uint32_t k) {
+        if (k >> (shift + 8) != want) return;
+        atomicAdd(&sh.low[255 - ((k >> shift) & 255u)], 1u);
+        if (!level) atomicAdd(&sh.low_sum[255 - ((k >> 8) & 255u)], (unsigned long long)(k & 255u));
+      });
+      cluster.sync();
+      uint32_t n = 0, before_n = 0;
+      unsigned long long s = 0, before_s = 0;
+      const uint32_t key = b.key | (255u - (uint32_t)tid) << shift;
+      if (tid < 256) {
+        for (int c = 0; c < C; ++c) {
+          n += *cluster.map_shared_rank(&sh.low[tid], c);
+          s += *cluster.map_shared_rank(&sh.low_sum[tid], c);
+        }
+        s += (unsigned long long)n * (bin_base(key) | (key & 0xffffu));
+        before_n = warp_before(n);
+        before_s = warp_before(s);
+        if (lane == 31) {
+          sh.merged[warp] = before_n + n;
+          sh.merged_sum[warp] = before_s + s;
+        }
+      }
+      __syncthreads();
+      if (tid < 256) {
+        for (int w = 0; w < warp; ++w) {
+          before_n += sh.merged[w];
+          before_s += sh.merged_sum[w];
+        }
+        const double from = b.sum + (double)before_s * unit, to = b.sum + (double)(before_s + s) * unit;
+        bool here;
+        if (by == kByCount) {
+          here = g >= b.above + before_n && g < (unsigned long long)b.above + before_n + n;
+        } else if (by == kBySum) {
+          // (the bin's own sum was rounded: what lies past its last entry is the last entry's)
+          here = n > 0 && (goal >= from || before_n == 0) &&
+                 (goal < to || before_n + n == b.count);
+        } else {
+          here = (uint32_t)(g >> shift) == key >> shift;
+        }
+        if (here)
+          sh.inside = Border{key, b.above + before_n, n, from,
+                             level ? (double)(bin_base(key) | (key & 0xffffu)) * unit : 0.0};
+      }
+      cluster.sync();
+      b = sh.inside;
+      __syncthreads();
+    }
+    return b;
+  };
+
+  if (total == 0) {
+    if (rank == 0 && tid == 0) {
+      raise_err(P.err, SD_ERR_ZERO_ROW);
+      if (P.kept) P.kept[row] = 0;
+      if (!WRITE) {
+        P.tokens[row] = 0;
+        if (P.prob) P.prob[row] = 0.f;
+      }
+    }
+    if (WRITE)
+      for (int i = in.begin + tid; i < in.end; i += kRowThreads) P.probs[row * P.ld_out + i] = 0.f;
+    cluster.sync();
+    return;
+  }
+
+  // The last entry kept, and the sum of those kept.
+  uint32_t n = total;
+  Border last = {0, 0, 0, 0.0, 0.0};
+  bool cut = false;
+  double kept_sum = (double)total_sum;
+  auto cut_at = [&](uint32_t m, const Border& b) {
+    n = m;
+    last = b;
+    cut = true;
+    kept_sum = b.sum + (double)(m - b.above) * b.w;
+  };
+  uint32_t k = 0x7fffffffu;
+  if (P.top_k && P.top_k[req] > 0) k = (uint32_t)P.top_k[req];
+  if (!PROBS && top == 0xff80u) k = min(k, find(kByKey, top, 0.0).count);
+  if (greedy) k = 1;
+  if (k < n) cut_at(k, find(kByCount, k - 1, 0.0));
+  const float top_p = P.top_p && !greedy ? P.top_p[req] : 1.f;
+  if (top_p < 1.f && n > 1) {
+    // the last entry before which less than top_p of the sum lies
+    const double goal = (double)fmaxf(top_p, 0.f) * kept_sum;
+    const double g = fmin(fmax(ceil(goal) - 1.0, 0.0), fmax(ceil(kept_sum) - 1.0, 0.0));
+    const Border b = find(kBySum, min((unsigned long long)g, total_sum - 1), g);
+    const double j = ceil((goal - b.sum) / b.w);
+    const uint32_t m = b.above + (j >= (double)b.count ? b.count : j >= 1.0 ? (uint32_t)j : 1u);
+    if (m < n) cut_at(m, b);
+  }
+  const float min_p = P.min_p && !greedy ? P.min_p[req] : 0.f;
+  if (min_p > 0.f && n > 1) {
+    uint32_t m;
+    if (min_p >= 1.f) {
+      m = find(kByKey, top, 0.0).count;
+    } else if (PROBS) {
+      const float t = __double2float_ru((double)min_p * (double)__uint_as_float(top));
+      const Border b = find(kByKey, max(1u, __float_as_uint(t)), 0.0);
+      m = b.above + b.count;
+    } else {
+      const double t = (double)top_value + fmin(fmax((double)T, 0x1p-100), 0x1p100) * log((double)min_p);
+      const uint32_t o = orderable(__double2float_ru(t));
+      const uint32_t key = o & 0x80000000u ? (o + 0xffffu) >> 16 : o >> 16;
+      const Border b = find(kByKey, min(max(key, 0x80u), top), 0.0);
+      m = b.above + b.count;
+    }
+    m = max(m, 1u);
+    if (m < n) cut_at(m, find(kByCount, m - 1, 0.0));
+  }
+  if (rank == 0 && tid == 0 && P.kept) P.kept[row] = (int32_t)n;
+
+  // ---- 4. the entry in question among those of its value, by index ----
+  // Index of entry number j (from 0) of those with this key. A warp goes over a stretch of its own.
+  auto nth = [&](uint32_t key, uint32_t j) -> int {
+    const int len = in.end - in.begin, seg = ((len + kRowWarps - 1) / kRowWarps + 7) & ~7;
+    const int a = in.begin + min(len, warp * seg), b = in.begin + min(len, (warp + 1) * seg);
+    uint32_t have = 0;
+    in.each(a, b, lane, 32, [&](int, uint32_t x) { have += x == key; });
+    have = __reduce_add_sync(0xffffffffu, have);
+    if (lane == 0) sh.warp_count[warp] = have;
+    __syncthreads();
+    const uint32_t v = sh.warp_count[lane];
+    const uint32_t vb = warp_before(v);
+    if (warp == 0) {
+      const uint32_t all = __shfl_sync(0xffffffffu, vb + v, 31);
+      if (lane < C) cluster.map_shared_rank(sh.rank_eq, lane)[rank] = all;
+    }
+    uint32_t before = __shfl_sync(0xffffffffu, vb, warp);
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) before += sh.rank_eq[c];
+    if (j >= before && j - before < have) {
+      uint32_t left = j - before;
+      for (int i = a; i < b; i += 32) {
+        const uint32_t m = __ballot_sync(0xffffffffu, i + lane < b && in.key_at(i + lane) == key);
+        const uint32_t c = __popc(m);
+        if (left < c) {
+          const int at = i + (int)__fns(m, 0, (int)left + 1);
+          if (lane < C) *cluster.map_shared_rank(&sh.index, lane) = at;
+          break;
+        }
+        left -= c;
+      }
+    }
+    cluster.sync();
+    return sh.index;
+  };
+
+  if (!WRITE) {
+    float u = P.u[row];
+    u = u > 0.f ? u : 0.f;
+    const double goal = fmin((double)u * kept_sum, kept_sum);
+    const double g = fmin(floor(goal), fmax(ceil((double)total_sum) - 1.0, 0.0));
+    Border b;
+    uint32_t j = 0;
+    if (n == 1) {
+      b = cut ? last : find(kByCount, 0, 0.0);
+    } else {
+      b = find(kBySum, min((unsigned long long)g, total_sum - 1), goal);
+      const double f = floor((goal - b.sum) / b.w);
+      j = f >= (double)(b.count - 1) ? b.count - 1 : f > 0.0 ? (uint32_t)f : 0u;
+      if (b.above + j >= n) {
+        b = cut ? last : find(kByCount, n - 1, 0.0);
+        j = n - 1 - b.above;
+      }
+    }
+    const int at = nth(b.key, j);
+    if (rank == 0 && tid == 0) {
+      P.tokens[row] = at;
+      if (P.prob) P.prob[row] = (float)(b.w / kept_sum);
+    }
+  } else {
+    int edge = 0x7fffffff;  // entries of the last value are kept up to here
+    if (cut && n - last.above < last.count) edge = nth(last.key, n - last.above - 1);
+    const uint32_t least = cut ? last.key : 1u;
+    const float inv = (float)(kSumUnit / kept_sum);
+    const float scale = PROBS ? __uint_as_float((uint32_t)(127 + 126 - top_exp) << 23) : 1.f;
+    float* out = P.probs + (size_t)row * P.ld_out;
+    auto value = [&](int i, uint32_t x) {
+      if (x < least || (x == least && i > edge)) return 0.f;
+      if (PROBS) return __uint_as_float(x) * scale * inv;
+      if (x == top) return inv;
+      if (top == 0xff80u) return 0.f;
+      const float d = logit_value(x) - top_value;
+      const float y = d * per_unit.x;
+      // (the product's rounding error goes into a factor: 2^y as exact as fp32 allows)
+      const float r = fmaf(d, per_unit.x, -y) + d * per_unit.y;
+      return y > -160.f ? exp2f(y) * fmaf(r, 0.69314718f, 1.f) * inv : 0.f;
+    };
+    constexpr int N = PROBS ? 4 : 8;
+    if (P.vec && P.vec_out) {
+      const int vecs = (in.end - in.begin) / N;
+      const uint4* p = reinterpret_cast<const uint4*>((const char*)in.row +
+                                                      (size_t)in.begin * (PROBS ? 4 : 2));
+      for (int v = tid; v < vecs; v += kRowThreads) {
+        const uint4 x = __ldg(p + v);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const int i = in.begin + v * N;
+        float4* o = reinterpret_cast<float4*>(out + i);
+        if (PROBS) {
+          __stcs(o, make_float4(value(i, prob_key(w[0])), value(i + 1, prob_key(w[1])),
+                                value(i + 2, prob_key(w[2])), value(i + 3, prob_key(w[3]))));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            __stcs(o + q, make_float4(value(i + 4 * q, logit_key(w[2 * q] & 0xffffu)),
+                                      value(i + 4 * q + 1, logit_key(w[2 * q] >> 16)),
+                                      value(i + 4 * q + 2, logit_key(w[2 * q + 1] & 0xffffu)),
+                                      value(i + 4 * q + 3, logit_key(w[2 * q + 1] >> 16))));
+        }
+      }
+      for (int i = in.begin + vecs * N + tid; i < in.end; i += kRowThreads)
+        out[i] = value(i, in.key_at(i));
+    } else {
+      for (int i = in.begin + tid; i < in.end; i += kRowThreads) out[i] = value(i, in.key_at(i));
+    }
+  }
+  cluster.sync();  // no CTA leaves while another may read its histogram
+}
+
+template <bool PROBS, bool WRITE>
+static int launch_rows(RowsParams& P, long n_rows, cudaStream_t stream) {
+  // CTAs of a row: a part fits 16-bit counts; long rows are shared by four, and by eight where there
+  // are few of them.
+  int C = P.V <= 8192 ? 1 : P.V <= 32768 ? 2 : P.V <= 262112 ? 4 : 8;
+  while (C < kMostClusters && C > 1 && n_rows * C * 2 <= 152) C *= 2;
+  P.part = ((P.V + C - 1) / C + 7) / 8 * 8;
+  static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
+  if (!set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(rows_kernel<PROBS, WRITE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kHistBytes) != cudaSuccess)
+      return SD_E_LAUNCH;
+    set[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n_rows * C), 1, 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.dynamicSmemBytes = kHistBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<PROBS, WRITE>, P) == cudaSuccess ? SD_OK
+                                                                              : SD_E_LAUNCH;
+}
+
+}  // namespace sdk
+
+extern "C" int sd_rows_launch(int B, int J, int V, int dtype, const void* rows, long ld,
+                              const float* temperature, const int32_t* top_k, const float* top_p,
+                              const float* min_p, float* probs, long ld_out, const float* u,
+                              int32_t* tokens, float* prob, int32_t* kept, int32_t* err,
+                              cudaStream_t stream) {
+  sdk::RowsParams P;
+  const int size = dtype == SD_F32_PROBS ? 4 : 2;
+  P.rows = rows;
+  P.ld = ld;
+  P.J = J;
+  P.V = V;
+  P.vec = (uintptr_t)rows % 16 == 0 && ld * size % 16 == 0;
+  P.temperature = temperature;
+  P.top_k = top_k;
+  P.top_p = top_p;
+  P.min_p = min_p;
+  P.probs = probs;
+  P.ld_out = ld_out;
+  P.vec_out = (uintptr_t)probs % 16 == 0 && ld_out % 4 == 0;
+  P.u = u;
+  P.tokens = tokens;
+  P.prob = prob;
+  P.kept = kept;
+  P.err = err;
+  const long n = (long)B * J;
+  if (dtype == SD_F32_PROBS)
+    return probs ? sdk::launch_rows<true, true>(P, n, stream)
+                 : sdk::launch_rows<true, false>(P, n, stream);
+  return probs ? sdk::launch_rows<false, true>(P, n, stream)
+               : sdk::launch_rows<false, false>(P, n, stream);
+}
