@@ -51,7 +51,8 @@ def weights_ref(q, lse, k, sm_scale, causal, live, decay, old):
         arg = 2.0 ** -22 * (x.abs() + lse[:, h, None].abs())
         w[:, h // (Hq // H)] += p.sum(0)
         tol[:, h // (Hq // H)] += torch.where(seen, p * (ds + arg + 2.0 ** -20), torch.zeros_like(x)).sum(0)
-    tol += rows * 2.0 ** -24 * w
+    # (fp32 may hold 0 for a number below its smallest normal one: 2^-126 a row)
+    tol += rows * (2.0 ** -24 * w + 2.0 ** -126)
     if old is not None:
         fresh = (pos >= T - n)[:, None]
         add = torch.where(fresh, torch.zeros_like(old), decay * old)

@@ -237,4 +237,4 @@ def test_after_attend():
     for r, T in enumerate(lens):
         t = torch.arange(T, device=DEV)
         got = w[c["table"][r].long()[t // bs], :, t % bs].double().sum(0)
-        assert torch.all((got - n_q * Hq // H).abs() < 1e-4 * n_q * Hq // H)
+        assert torch.all((got - n_q * Hq // H).abs() < 1e-4 * n_q * Hq / H)
