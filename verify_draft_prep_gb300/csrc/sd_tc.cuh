@@ -210,6 +210,20 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool 
       "r"(a), "r"(b), "r"((uint32_t)add), "n"(HI), "n"(IDESC)
       : "memory");
 }
+// A and B both bf16 and K-major, M = 128, N given, fp32 accumulator.
+__device__ __forceinline__ uint32_t mma_desc_bf16(int N) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
+}
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ss_bf16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %3, 0;\n"
+      " mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "n"(HI), "r"(idesc)
+      : "memory");
+}
 // Arrives on bar when every product issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(

@@ -1,18 +1,38 @@
 // sd_weights.cu -- the attention weight that each cached token gets from a call's queries
-// (sd_kv_weights).
+// (sd_kv_weights), on the fifth-generation tensor cores.
 //
 // w[t] = sum over the query tokens i that count and the heads g of the group, of those that see t,
 // e^(sm_scale q_ig . k_t - lse_ig), added to `decay` times what t had before (nothing for the call's
-// own tokens). A CTA has 128 tokens of one KV head, a token a thread, and goes over all rows (a row is
-// a query token and a head), so that every sum has one owner and a fixed order.
+// own tokens).
+//
+// The sums of the softmax are an input, so nothing runs along a row: a tile's tokens stand in the 128
+// lanes of the accumulator and the rows (a query token and one of the heads that share the KV head)
+// in its columns, S^T = K Q^T, and every token's sum stays in the registers of the one thread that
+// owns it. No maximum, no second product, no atomics, and the same call gives the same bits. Products are
+// bf16: an e4m3 value is one exactly, and so is q, which then needs neither scales nor a second term; K
+// is converted on its way to shared memory, where a byte waits for memory longer than for that.
+//
+// A unit is a pair of tiles (256 tokens) of one request and KV head; a chunk is up to 128 rows. Both
+// tiles use a chunk of Q in shared memory, and one group of four warps turns the S of each into sums.
+// Eight warps load: K a unit ahead in registers, and Q, which stays where a request has at most two
+// chunks. One thread issues the products.
+
+#include <atomic>
 
 #include "sd_kv.cuh"
+#include "sd_tc.cuh"
 
 namespace sdk {
 
+constexpr int kWTile = 128, kWPair = 2 * kWTile, kWRows = 128;
+constexpr int kWThreads = 544;      // 8 warps sum, 8 load, 1 issues
+constexpr int kWLoaders = 256;
+constexpr float kWLog2e = 1.4426950408889634f;
+
 struct WeightsParams {
   KvCache c;
-  int B, n, Hq, G, max_blocks, causal;
+  int B, n, Hq, G, max_blocks, causal, spread;
+  unsigned long long g_magic;  // ceil(2^64 / G); 0 for G = 1
   const uint16_t* q;
   long ld_q, hs_q;
   const float* lse;
@@ -27,93 +47,558 @@ struct WeightsParams {
   int32_t* err;
 };
 
-constexpr int kWTile = 128, kWRows = 32;
+template <int DP>
+struct WLayout {
+  static constexpr int kTileBytes = kWTile * DP * 2;  // K of a tile, or Q of a chunk, as bf16
+  static constexpr int kK = 0;                        // two pairs of tiles
+  static constexpr int kQ = kK + 4 * kTileBytes;      // two chunks
+  static constexpr int kMisc = kQ + 2 * kTileBytes;
+};
+
+struct WMisc {
+  uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2];
+  uint64_t s_full[2][2], s_empty[2][2];  // [tile of the pair][buffer]
+  float lse2[2][kWRows];                 // of the rows of a chunk of Q
+  int lim[2][kWRows];                    // tokens that they see
+  float k_scale[2][kWPair];              // of a pair's tokens, times sm_scale log2(e)
+  float before[2][kWPair];               // what they have so far
+  long at[2][kWPair];                    // where their number lies; -1: nowhere
+  long long warp_sum[kWThreads / 32];
+  int start_r;
+  long long start_in;
+  uint32_t tmem;
+  int gave_up;
+};
+
+struct WRequest {
+  int tok0, n_q, rows, len, off;  // rows: those that count
+};
+
+__device__ __forceinline__ int w_token(const WeightsParams& P, int row) {
+  return P.g_magic ? (int)__umul64hi((unsigned long long)row, P.g_magic) : row;
+}
+__device__ __forceinline__ long w_covered(const WeightsParams& P) {
+  return min((long)P.max_blocks << P.c.log2_bs, 2147483648L - 2 * kWPair);
+}
+__device__ __forceinline__ WRequest w_request(const WeightsParams& P, int r) {
+  WRequest q;
+  const int a = P.cu[r], b = P.cu[r + 1], ctx = P.ctx[r];
+  const int lo = min(max(a, 0), P.n), hi = min(max(b, lo), P.n);
+  q.tok0 = lo;
+  q.n_q = hi - lo;
+  q.rows = (P.live ? min(max(P.live[r], 0), q.n_q) : q.n_q) * P.G;
+  q.len = ctx < 0 ? 0 : (int)min((long)ctx, w_covered(P));
+  q.off = (int)max((long)ctx - q.n_q, -2147483647L);
+  return q;
+}
+__device__ __forceinline__ bool w_bad(const WeightsParams& P, int r) {
+  const int a = P.cu[r], b = P.cu[r + 1], ctx = P.ctx[r];
+  const bool bad = a < 0 || b < a || b > P.n || ctx < 0 || ctx > w_covered(P);
+  return bad || (P.live && (P.live[r] < 0 || P.live[r] > b - a));
+}
+__device__ __forceinline__ int w_sees(const WeightsParams& P, const WRequest& q, int row) {
+  if (!P.causal) return q.len;
+  return (int)max(0L, min((long)q.len, (long)q.off + w_token(P, row) + 1));
+}
+
+// A pair of tiles of one request and KV head, and the chunks of rows that see any of its tokens.
+struct WUnit {
+  WRequest q;
+  int r, h, pair, first, chunks;
+};
+// A chunk of Q stays for the next unit where the request has at most two of them.
+__device__ __forceinline__ bool w_stays(const WUnit& a, const WUnit& b, bool there) {
+  return there && a.chunks <= 2 && a.r == b.r && a.h == b.h;
+}
+
+// A CTA's units in their order. All units of a request lie one behind another; `spread`: pairs
+// outermost and every CTA takes each 152nd of the line, forwards and backwards in turn, so that a
+// prompt's units, which get cheaper along the context, even out; else heads outermost and every CTA
+// takes a stretch, so that it stays with a request's Q.
+struct WSchedule {
+  long long at, end;  // place on the line
+  int r, h, pair, pairs, round;
+
+  __device__ __forceinline__ int pairs_of(const WeightsParams& P, int rr) const {
+    return (w_request(P, rr).len + kWPair - 1) / kWPair;
+  }
+  // Settles `in` places behind the first unit of request r.
+  __device__ __forceinline__ void seek(const WeightsParams& P, long long in) {
+    for (;;) {
+      pairs = pairs_of(P, r);
+      const long long units = (long long)pairs * P.c.Hkv;
+      if (in < units) break;
+      in -= units;
+      ++r;
+    }
+    const int by = P.spread ? P.c.Hkv : pairs;
+    const int o = (int)(in / by), i = (int)(in - (long long)o * by);
+    pair = P.spread ? o : i;
+    h = P.spread ? i : o;
+  }
+  __device__ __forceinline__ WUnit unit(const WeightsParams& P) const {
+    WUnit u;
+    u.q = w_request(P, r);
+    u.r = r;
+    u.h = h;
+    u.pair = pair;
+    u.chunks = (u.q.rows + kWRows - 1) / kWRows;
+    u.first = 0;
+    if (P.causal && u.chunks > 2)
+      u.first = (int)min((long)u.chunks, max(0L, (long)pair * kWPair - u.q.off) * P.G / kWRows);
+    return u;
+  }
+  // On to the next unit; false: there is none.
+  __device__ __forceinline__ bool next(const WeightsParams& P) {
+    if (P.spread) {
+      const int n = gridDim.x, b = blockIdx.x;
+      const int by = round++ & 1 ? 2 * b + 1 : 2 * (n - 1 - b) + 1;
+      at += by;
+      if (at >= end) return false;
+      seek(P, (long long)pair * P.c.Hkv + h + by);
+      return true;
+    }
+    if (++at >= end) return false;
+    if (++pair == pairs) {
+      pair = 0;
+      if (++h == P.c.Hkv) {
+        h = 0;
+        ++r;
+        while ((pairs = pairs_of(P, r)) == 0) ++r;
+      }
+    }
+    return true;
+  }
+};
+
+// 16 e4m3 bytes as bf16 (two 16-byte parts), exactly.
+__device__ __forceinline__ void to_bf16(const uint4& v, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = e4m3x2_to_f32((uint16_t)w[i]), b = e4m3x2_to_f32((uint16_t)(w[i] >> 16));
+    // (the lower halves of these fp32 are zero)
+    o[2 * i] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x7632);
+    o[2 * i + 1] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x7632);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ float w_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 w_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&c)));
+  return d;
+}
+__device__ __forceinline__ float2 w_add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+  return d;
+}
 
 template <int DP>
-__global__ void __launch_bounds__(kWTile) weights_simple_kernel(const WeightsParams P) {
-  __shared__ float s_q[kWRows][DP];
-  __shared__ float s_lse[kWRows];
+__global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsParams P) {
+  using L = WLayout<DP>;
+  extern __shared__ unsigned char s_raw[];
+  unsigned char* smem = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
+  WMisc& m = *reinterpret_cast<WMisc*>(smem + L::kMisc);
   const KvCache& c = P.c;
-  const int tid = threadIdx.x, h = blockIdx.y, r = blockIdx.z, bs = 1 << c.log2_bs;
-  const int a = P.cu[r], b = P.cu[r + 1];
-  const int lo = min(max(a, 0), P.n), hi = min(max(b, lo), P.n), n_q = hi - lo;
-  const int ctx = P.ctx[r];
-  const long covered = min((long)P.max_blocks << c.log2_bs, 2147483648L - 256);
-  const int len = ctx < 0 ? 0 : (int)min((long)ctx, covered);
-  const long off = (long)ctx - n_q;
-  int live = P.live ? P.live[r] : n_q;
-  if (tid == 0 && blockIdx.x == 0 && h == 0 &&
-      (a < 0 || b < a || b > P.n || ctx < 0 || ctx > covered || live < 0 || live > n_q))
-    raise_err(P.err, SD_ERR_KV_RANGE);
-  live = min(max(live, 0), n_q);
-  if ((long)blockIdx.x * kWTile >= len) return;
-  const int t = blockIdx.x * kWTile + tid;
-  int page = -1;
-  if (t < len) {
-    page = P.table[(long)r * P.max_blocks + (t >> c.log2_bs)];
-    if ((unsigned)page >= (unsigned)c.num_blocks) {
-      page = -1;
-      raise_err(P.err, SD_ERR_KV_RANGE);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* gave_up = &m.gave_up;
+  const int bs = 1 << c.log2_bs;
+
+  if (tid < 2) {
+    mbar_init(smem_u32(&m.k_full[tid]), 8);
+    mbar_init(smem_u32(&m.k_empty[tid]), 9);
+    mbar_init(smem_u32(&m.q_full[tid]), 8);
+    mbar_init(smem_u32(&m.q_empty[tid]), 9);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&m.s_full[tid][b]), 1);
+      mbar_init(smem_u32(&m.s_empty[tid][b]), 4);
     }
+    m.gave_up = 0;
+    m.start_r = P.B;
   }
-  float k[DP];
-  float ks = 0.f;
-  if (page >= 0) ks = c.k_scale[(long)page * c.Hkv + h];
-#pragma unroll
-  for (int d = 0; d < DP; d += 16) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (page >= 0 && d < c.D && ks != 0.f)
-      v = __ldg(reinterpret_cast<const uint4*>(c.k + page * c.st_block + (t & (bs - 1)) * c.st_tok +
-                                               h * c.st_head + d));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = e4m3x2_to_f32((uint16_t)w[i]), y = e4m3x2_to_f32((uint16_t)(w[i] >> 16));
-      k[d + 4 * i] = x.x;
-      k[d + 4 * i + 1] = x.y;
-      k[d + 4 * i + 2] = y.x;
-      k[d + 4 * i + 3] = y.y;
-    }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (warp == 16) tmem_alloc(smem_u32(&m.tmem), 512);
+  // What comes before this call on its stream may still be running up to here.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this CTA's place on the line of units ----
+  const int per = (P.B + kWThreads - 1) / kWThreads;
+  const int r0 = min(P.B, tid * per), r1 = min(P.B, r0 + per);
+  long long mine = 0;
+  bool bad = false;
+  for (int r = r0; r < r1; ++r) {
+    mine += (long long)((w_request(P, r).len + kWPair - 1) / kWPair) * c.Hkv;
+    if (blockIdx.x == 0) bad |= w_bad(P, r);
   }
-  const float f = ks * P.scale;
-  float sum = 0.f, rest = 0.f;  // (compensated)
-  const int rows = live * P.G;
-  for (int r0 = 0; r0 < rows; r0 += kWRows) {
-    __syncthreads();
-    for (int i = tid; i < kWRows * DP; i += kWTile) {
-      const int row = r0 + i / DP, d = i % DP;
-      float x = 0.f;
-      if (row < rows && d < c.D)
-        x = bf16_bits_to_float(P.q[(long)(lo + row / P.G) * P.ld_q +
-                                   (long)(h * P.G + row % P.G) * P.hs_q + d]);
-      s_q[i / DP][d] = x;
-    }
-    if (tid < kWRows && r0 + tid < rows)
-      s_lse[tid] = P.lse[(long)(lo + (r0 + tid) / P.G) * P.Hq + h * P.G + (r0 + tid) % P.G];
-    __syncthreads();
-    const int m = min(kWRows, rows - r0);
-    float part = 0.f;
-    for (int i = 0; i < m; ++i) {
-      if (P.causal && t > off + (r0 + i) / P.G) continue;
-      float s = 0.f;
+  if (bad) raise_err(P.err, SD_ERR_KV_RANGE);
+  long long before = mine;
 #pragma unroll
-      for (int d = 0; d < DP; d += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(&s_q[i][d]);
-        s = fmaf(v.x, k[d], s);
-        s = fmaf(v.y, k[d + 1], s);
-        s = fmaf(v.z, k[d + 2], s);
-        s = fmaf(v.w, k[d + 3], s);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) m.warp_sum[warp] = before;
+  __syncthreads();
+  long long total = 0;
+  before -= mine;
+  for (int w = 0; w < kWThreads / 32; ++w) {
+    if (w < warp) before += m.warp_sum[w];
+    total += m.warp_sum[w];
+  }
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long g0 = P.spread ? blockIdx.x : min(total, share * blockIdx.x);
+  const long long g1 = P.spread ? total : min(total, g0 + share);
+  if (g0 < g1 && before <= g0 && g0 < before + mine) {
+    long long in = g0 - before;
+    int r = r0;
+    for (; r < r1; ++r) {
+      const long long u = (long long)((w_request(P, r).len + kWPair - 1) / kWPair) * c.Hkv;
+      if (in < u) break;
+      in -= u;
+    }
+    m.start_r = r;
+    m.start_in = in;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem;
+  WSchedule line;
+  line.r = m.start_r;
+  line.at = g0;
+  line.end = g1;
+  line.round = line.h = line.pair = line.pairs = 0;
+  bool some = g0 < g1;
+  WUnit s = {};
+  if (some) {
+    line.seek(P, m.start_in);
+    s = line.unit(P);
+  }
+
+  if (warp >= 8 && warp < 16) {
+    // ---- loads ----
+    const int t = tid - kWLoaders, lw = t >> 5;
+    constexpr int kParts = DP / 16, kPerPass = 32 / kParts;  // parts of a token; tokens of a pass
+    constexpr int kPasses = 32 / kPerPass;                   // of a warp's 32 tokens: 8 or 4
+    const int part = lane % kParts, sub = lane / kParts;
+    uint4 x[kPasses];
+    float ks = 0.f, was = 0.f;
+    long where = -1;
+    int page_next = -1;
+    auto page_of = [&](const WUnit& u) {
+      const int tok = u.pair * kWPair + t;
+      return tok < u.q.len ? __ldg(P.table + (long)u.r * P.max_blocks + (tok >> c.log2_bs)) : -2;
+    };
+    auto fetch = [&](const WUnit& u, int page) {  // this warp's tokens of a unit
+      const int tok = u.pair * kWPair + t;
+      ks = 0.f;
+      was = 0.f;
+      where = -1;
+      long src = -1;
+      if ((unsigned)page < (unsigned)c.num_blocks) {
+        const long slot = (long)page * c.Hkv + u.h;
+        ks = __ldg(c.k_scale + slot);
+        where = slot * bs + (tok & (bs - 1));
+        if (P.before && tok < u.q.off) was = P.before[where];
+        src = page * c.st_block + (tok & (bs - 1)) * c.st_tok + u.h * c.st_head;
+      } else if (page != -2) {
+        raise_err(P.err, SD_ERR_KV_RANGE);
       }
-      part += exp2f(s * f - s_lse[i] * 1.4426950408889634f);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const long from = __shfl_sync(0xffffffffu, src, i * kPerPass + sub);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (from >= 0 && part * 16 < c.D)
+          x[i] = ld_stream_u4(c.k + from + part * 16);
+      }
+    };
+    WUnit ahead = s;
+    bool more = some;
+    if (more) {
+      fetch(s, page_of(s));
+      more = line.next(P);
+      if (more) page_next = page_of(ahead = line.unit(P));
     }
-    const float y = part - rest, z = sum + y;
-    rest = (z - sum) - y;
-    sum = z;
+    int unit = 0, loads = 0;
+    bool ok = true, have_q = false;
+    while (some && ok) {
+      const int kb = unit & 1;
+      ok = mbar_wait_warp(smem_u32(&m.k_empty[kb]), ((unit >> 1) & 1) ^ 1, gave_up);
+      if (!ok) break;
+      // K of this unit, which is in registers
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int tok = lw * 32 + i * kPerPass + sub;
+        const float f = __shfl_sync(0xffffffffu, ks, i * kPerPass + sub);
+        uint4 lo, hi;
+        to_bf16(f == 0.f ? make_uint4(0, 0, 0, 0) : x[i], lo, hi);  // a scale of 0: zeros
+        const int row = tok & (kWTile - 1), ch = (2 * part) & 7;
+        unsigned char* at = smem + L::kK + (kb * 2 + (tok >> 7)) * L::kTileBytes +
+                            (part >> 2) * (kWTile * 128) + row * 128;
+        *reinterpret_cast<uint4*>(at + ((ch ^ (row & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (row & 7)) << 4)) = hi;
+      }
+      m.k_scale[kb][t] = ks * P.scale;
+      m.before[kb][t] = was;
+      m.at[kb][t] = where;
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&m.k_full[kb]));
+      // the next unit's K on its way
+      const WUnit after = ahead;
+      const bool next_there = more;
+      if (more) {
+        fetch(ahead, page_next);
+        more = line.next(P);
+        if (more) page_next = page_of(ahead = line.unit(P));
+      }
+      // Q, chunk by chunk
+      if (!have_q) {
+        for (int ch = s.first; ok && ch < s.chunks; ++ch, ++loads) {
+          const int qb = loads & 1;
+          const int row0 = ch * kWRows;
+          constexpr int kLanes = DP / 8, kRowsPass = kWLoaders / kLanes;
+          const int d8 = t % kLanes;
+          uint4 y[4];
+          auto q_rows = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = row0 + (i0 + i) * kRowsPass + t / kLanes;
+              y[i] = make_uint4(0, 0, 0, 0);
+              if (row < s.q.rows && d8 * 8 < c.D) {
+                const int tk = w_token(P, row);
+                y[i] = __ldg(reinterpret_cast<const uint4*>(
+                    P.q + (long)(s.q.tok0 + tk) * P.ld_q +
+                    (long)(s.h * P.G + row - tk * P.G) * P.hs_q + d8 * 8));
+              }
+            }
+          };
+          q_rows(0);
+          float l2 = INFINITY;
+          int lim = 0;
+          if (t < kWRows && row0 + t < s.q.rows) {
+            const int row = row0 + t, tk = w_token(P, row);
+            l2 = __ldg(P.lse + (long)(s.q.tok0 + tk) * P.Hq + s.h * P.G + row - tk * P.G) * kWLog2e;
+            lim = w_sees(P, s.q, row);
+          }
+          ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((loads >> 1) & 1) ^ 1, gave_up);
+          if (!ok) break;
+#pragma unroll
+          for (int i0 = 0; i0 < DP / 16; i0 += 4) {
+            if (i0) q_rows(i0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = (i0 + i) * kRowsPass + t / kLanes;
+              *reinterpret_cast<uint4*>(smem + L::kQ + qb * L::kTileBytes +
+                                        (d8 >> 3) * (kWRows * 128) + row * 128 +
+                                        (((d8 & 7) ^ (row & 7)) << 4)) = y[i];
+            }
+          }
+          if (t < kWRows) {
+            m.lse2[qb][t] = l2;
+            m.lim[qb][t] = lim;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&m.q_full[qb]));
+        }
+      }
+      have_q = w_stays(s, after, next_there);
+      s = after;
+      some = next_there;
+      ++unit;
+    }
+  } else if (warp == 16) {
+    // ---- products ----
+    constexpr uint32_t hi = desc_hi<128>();
+    const bool lead = elect_one();
+    const uint32_t k_lo = desc_lo<128>(base + L::kK), q_lo = desc_lo<128>(base + L::kQ);
+    int unit = 0, loads = 0, jobs[2] = {0, 0};
+    bool ok = true;
+    while (some && ok) {
+      const int kb = unit & 1;
+      const bool there = line.next(P);
+      const WUnit after = there ? line.unit(P) : s;
+      const bool keep = w_stays(s, after, there);
+      ok = mbar_wait_warp(smem_u32(&m.k_full[kb]), (unit >> 1) & 1, gave_up);
+      const bool two = (long)s.pair * kWPair + kWTile < s.q.len;
+      for (int ch = s.first; ok && ch < s.chunks; ++ch) {
+        const int load = loads + ch - s.first, qb = load & 1;
+        ok = mbar_wait_warp(smem_u32(&m.q_full[qb]), (load >> 1) & 1, gave_up);
+        const int cols = min(kWRows, (s.q.rows - ch * kWRows + 31) & ~31);
+        const uint32_t idesc = mma_desc_bf16(cols);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || (x && !two)) continue;
+          const int sb = jobs[x] & 1;
+          ok = mbar_wait_warp(smem_u32(&m.s_empty[x][sb]), ((jobs[x] >> 1) & 1) ^ 1, gave_up);
+          if (!ok) continue;
+          ++jobs[x];
+          tc_fence_after();
+          if (lead) {
+            const uint32_t d = tmem + (x * 2 + sb) * kWRows;
+            const uint32_t a = k_lo + (kb * 2 + x) * (L::kTileBytes / 16),
+                           b = q_lo + qb * (L::kTileBytes / 16);
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+              const uint32_t o = (kk >> 2) * (kWTile * 128 / 16) + (kk & 3) * 2;
+              mma_ss_bf16<hi>(d, a + o, b + o, idesc, kk > 0);
+            }
+            mma_commit(smem_u32(&m.s_full[x][sb]));
+          }
+        }
+        if (ok && lead && !keep) mma_commit(smem_u32(&m.q_empty[qb]));
+      }
+      if (ok && lead) mma_commit(smem_u32(&m.k_empty[kb]));
+      if (!keep) loads += s.chunks - s.first;
+      s = after;
+      some = there;
+      ++unit;
+      __syncwarp();
+    }
+    __syncwarp();
+  } else {
+    // ---- sums: group x has tile x of the pair, a token a lane ----
+    const int x = warp >> 2, wt = tid & (kWTile - 1);
+    const uint32_t tS = tmem + x * 2 * kWRows + ((uint32_t)(warp & 3) << 21);
+    int unit = 0, loads = 0, jobs = 0;
+    bool ok = true;
+    while (some && ok) {
+      const int kb = unit & 1;
+      const bool there = line.next(P);
+      const WUnit after = there ? line.unit(P) : s;
+      const bool keep = w_stays(s, after, there);
+      ok = mbar_wait_warp(smem_u32(&m.k_full[kb]), (unit >> 1) & 1, gave_up);
+      const int t0 = s.pair * kWPair + x * kWTile, tok = t0 + wt;
+      const bool mine_any = t0 < s.q.len;
+      const float f = m.k_scale[kb][x * kWTile + wt];
+      const float2 f2 = make_float2(f, f);
+      float sum = 0.f, rest = 0.f;  // (compensated from chunk to chunk)
+      for (int ch = s.first; ok && ch < s.chunks; ++ch) {
+        const int load = loads + ch - s.first, qb = load & 1;
+        ok = mbar_wait_warp(smem_u32(&m.q_full[qb]), (load >> 1) & 1, gave_up);
+        if (!ok) break;
+        if (mine_any) {
+          const int sb = jobs & 1;
+          ok = mbar_wait_warp(smem_u32(&m.s_full[x][sb]), (jobs >> 1) & 1, gave_up);
+          if (!ok) break;
+          ++jobs;
+          tc_fence_after();
+          const int cols = min(kWRows, (s.q.rows - ch * kWRows + 31) & ~31);
+          // rows see more along a chunk; the first sees the whole tile, or some tokens are masked
+          const bool masked = m.lim[qb][0] < t0 + kWTile;
+          const uint32_t tC = tS + sb * kWRows;
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          for (int c0 = 0; c0 < cols; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(tC + c0, v);
+            tmem_wait_ld();
+            const float4* l4 = reinterpret_cast<const float4*>(&m.lse2[qb][c0]);
+            if (!masked) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 l = l4[i];
+                const float2 a = w_fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                                        f2, make_float2(-l.x, -l.y));
+                const float2 b = w_fma2(
+                    make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), f2,
+                    make_float2(-l.z, -l.w));
+                acc[0] = w_add2(acc[0], make_float2(w_ex2(a.x), w_ex2(a.y)));
+                acc[1] = w_add2(acc[1], make_float2(w_ex2(b.x), w_ex2(b.y)));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float e = w_ex2(fmaf(__uint_as_float(v[i]), f, -m.lse2[qb][c0 + i]));
+                acc[i & 1].x += tok < m.lim[qb][c0 + i] ? e : 0.f;
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&m.s_empty[x][sb]));
+          const float part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+          const float y = part - rest, z = sum + y;
+          rest = (z - sum) - y;
+          sum = z;
+        }
+        __syncwarp();
+        if (lane == 0 && !keep) mbar_arrive(smem_u32(&m.q_empty[qb]));
+      }
+      if (ok) {
+        const long at = m.at[kb][x * kWTile + wt];
+        if (at >= 0) P.weights[at] = fmaf(P.decay, m.before[kb][x * kWTile + wt], sum);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&m.k_empty[kb]));
+      if (!keep) loads += s.chunks - s.first;
+      s = after;
+      some = there;
+      ++unit;
+    }
   }
-  if (page >= 0) {
-    const long at = ((long)page * c.Hkv + h) * bs + (t & (bs - 1));
-    P.weights[at] = P.before && t < off ? fmaf(P.decay, P.before[at], sum) : sum;
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (m.gave_up) {
+    // a wait ran out: the products in flight get some milliseconds before the memory is given up
+    if (tid == 0) raise_err(P.err, SD_ERR_WAIT);
+    const long long t = clock64();
+    while (clock64() - t < 20000000LL) __nanosleep(1000);
+    __syncthreads();
   }
+  tc_fence_after();
+  if (warp == 16) tmem_free(tmem, 512);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <int DP>
+static int launch_weights(const WeightsParams& P, cudaStream_t stream) {
+  constexpr int smem = WLayout<DP>::kMisc + (int)sizeof(WMisc) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+  static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
+  static std::atomic<int> sms[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
+  if (!set[dev].load(std::memory_order_acquire)) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+      return SD_E_DEVICE;
+    if (cudaFuncSetAttribute(weights_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             smem) != cudaSuccess)
+      return SD_E_LAUNCH;
+    sms[dev].store(n, std::memory_order_relaxed);
+    set[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms[dev].load(std::memory_order_relaxed), 1, 1);
+  cfg.blockDim = dim3(kWThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_kernel<DP>, P) == cudaSuccess ? SD_OK : SD_E_LAUNCH;
 }
 
 }  // namespace sdk
@@ -133,6 +618,7 @@ extern "C" int sd_kv_weights_launch(int B, int n, int max_q, int Hq, int Hkv, in
   P.n = n;
   P.Hq = Hq;
   P.G = Hq / Hkv;
+  P.g_magic = P.G > 1 ? ~0ull / (unsigned)P.G + 1 : 0;
   P.max_blocks = max_blocks;
   P.causal = causal;
   P.q = (const uint16_t*)q;
@@ -143,19 +629,12 @@ extern "C" int sd_kv_weights_launch(int B, int n, int max_q, int Hq, int Hkv, in
   P.ctx = ctx;
   P.cu = cu;
   P.live = live;
-  P.scale = sm_scale * 1.4426950408889634f;
+  P.scale = sm_scale * sdk::kWLog2e;
   P.decay = decay;
   P.before = before;
   P.weights = weights;
   P.err = err;
-  (void)max_q;
-  const long tiles = (((long)max_blocks << log2_bs) + sdk::kWTile - 1) / sdk::kWTile;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles > 0 ? tiles : 1), (unsigned)Hkv, (unsigned)B);
-  cfg.blockDim = dim3(sdk::kWTile, 1, 1);
-  cfg.stream = stream;
-  return (D <= 64 ? cudaLaunchKernelEx(&cfg, sdk::weights_simple_kernel<64>, P)
-                  : cudaLaunchKernelEx(&cfg, sdk::weights_simple_kernel<128>, P)) == cudaSuccess
-             ? SD_OK
-             : SD_E_LAUNCH;
+  // Requests of more chunks than stay in shared memory are prompts.
+  P.spread = (long)max_q * P.G > 2 * sdk::kWRows;
+  return D <= 64 ? sdk::launch_weights<64>(P, stream) : sdk::launch_weights<128>(P, stream);
 }
