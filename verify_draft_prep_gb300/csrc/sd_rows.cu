@@ -13,11 +13,15 @@
 // what lets the sums be exact enough for whole numbers to come out right: w in pairs of fp32 (2^-44),
 // sums in 64-bit integers. Probabilities have 32 bits: the histogram is over their upper 16, with the
 // sums of the lower 16 in whole numbers, and the one bin in question is resolved by reading the row
-// again (from L2), 8 bits at a time.
+// again (from L2).
 //
-// A row is a cluster's work: each CTA counts its part into its own histogram (16-bit counts, so a part
-// is at most 65528 entries), then each scans its share of the bins over all of the cluster's
-// histograms through distributed shared memory.
+// Two kernels. quick_kernel has 8192 bins, for logits of magnitude 2^-15 to 2^17 (and zero) and
+// probabilities from 2^-63 on: 32 or 64 KB, so that three or four rows are on an SM at a time and one
+// row's search hides behind another's reading. A row that needs more (a cut or a draw within values
+// that have no bin of their own, rows of odd scales) is marked, and rows_kernel, whose histogram has a
+// bin for every value, does the marked rows. A row is a CTA's work, or a cluster's where rows are few:
+// each CTA counts its part, then each scans its share of the bins over all of the cluster's histograms
+// through distributed shared memory, and one warp does the search.
 
 #include <atomic>
 
@@ -48,7 +52,12 @@ struct RowsParams {
   float* prob;
   int32_t* kept;
   int32_t* err;
+  int n_rows;
 };
+
+// What marks a row that quick_kernel leaves to rows_kernel, in its output.
+constexpr int32_t kMarkToken = -2147483647 - 1;
+constexpr float kMarkProb = -1.f;
 
 // A value's place: entries of larger values and their sum, how many entries have the value, and the
 // weight of each (in units of the sums).
@@ -145,6 +154,79 @@ struct RowReader {
                  : logit_key(__ldg((const uint16_t*)row + i));
   }
 
+  // f(bits) for every entry of the part, in any order.
+  template <typename F>
+  __device__ __forceinline__ void raw(int first, int step, F f) const {
+    constexpr int N = PROBS ? 4 : 8;
+    if (!P.vec) {
+      for (int i = begin + first; i < end; i += step)
+        f(PROBS ? __ldg((const uint32_t*)row + i) : (uint32_t)__ldg((const uint16_t*)row + i));
+      return;
+    }
+    const int vecs = (end - begin) / N;
+    const uint4* p = reinterpret_cast<const uint4*>((const char*)row + (size_t)begin * (PROBS ? 4 : 2));
+    auto one = [&](const uint4& v) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (PROBS) {
+          f(w[j]);
+        } else {
+          f(w[j] & 0xffffu);
+          f(w[j] >> 16);
+        }
+      }
+    };
+    constexpr int kAhead = 4;  // loads in flight
+    uint4 x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (first + k * step < vecs) x[k] = __ldg(p + first + k * step);
+    for (int v = first; v < vecs; v += kAhead * step) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int at = v + k * step;
+        if (at >= vecs) break;
+        const uint4 now = x[k];
+        if (at + kAhead * step < vecs) x[k] = __ldg(p + at + kAhead * step);
+        one(now);
+      }
+    }
+    for (int i = begin + vecs * N + first; i < end; i += step)
+      f(PROBS ? __ldg((const uint32_t*)row + i) : (uint32_t)__ldg((const uint16_t*)row + i));
+  }
+
+  // out[index] = value(index, key) for every entry of the part.
+  template <typename F>
+  __device__ __forceinline__ void write(float* out, int vec_out, int first, int step, F value) const {
+    constexpr int N = PROBS ? 4 : 8;
+    if (!P.vec || !vec_out) {
+      for (int i = begin + first; i < end; i += step) out[i] = value(i, key_at(i));
+      return;
+    }
+    const int vecs = (end - begin) / N;
+    const uint4* p = reinterpret_cast<const uint4*>((const char*)row + (size_t)begin * (PROBS ? 4 : 2));
+#pragma unroll 2
+    for (int v = first; v < vecs; v += step) {
+      const uint4 x = __ldg(p + v);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const int i = begin + v * N;
+      float4* o = reinterpret_cast<float4*>(out + i);
+      if (PROBS) {
+        __stcs(o, make_float4(value(i, prob_key(w[0])), value(i + 1, prob_key(w[1])),
+                              value(i + 2, prob_key(w[2])), value(i + 3, prob_key(w[3]))));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          __stcs(o + q, make_float4(value(i + 4 * q, logit_key(w[2 * q] & 0xffffu)),
+                                    value(i + 4 * q + 1, logit_key(w[2 * q] >> 16)),
+                                    value(i + 4 * q + 2, logit_key(w[2 * q + 1] & 0xffffu)),
+                                    value(i + 4 * q + 3, logit_key(w[2 * q + 1] >> 16))));
+      }
+    }
+    for (int i = begin + vecs * N + first; i < end; i += step) out[i] = value(i, key_at(i));
+  }
+
   // f(index, key) for every entry of [a, b) that this thread takes, `step` vectors apart from `first`.
   template <typename F>
   __device__ __forceinline__ void each(int a, int b, int first, int step, F f) const {
@@ -189,10 +271,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x / C, req = row / P.J;
+  // (quick_kernel's marks; the launch overlaps its end)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int row = blockIdx.x / C; row < P.n_rows; row += gridDim.x / C) {
+  if (WRITE ? P.probs[(size_t)row * P.ld_out] != kMarkProb : P.tokens[row] != kMarkToken) continue;
+  const int req = row / P.J;
   const float T = P.temperature ? P.temperature[req] : 1.f;
   const bool greedy = !(T > 0.f);
-  RowReader<PROBS> in{P, (const char*)P.rows + (size_t)row * P.ld * (PROBS ? 4 : 2),
+  const RowReader<PROBS> in{P, (const char*)P.rows + (size_t)row * P.ld * (PROBS ? 4 : 2),
                       min(P.V, rank * P.part), min(P.V, (rank + 1) * P.part)};
 
   // ---- 1. this CTA's histogram and largest key ----
@@ -462,9 +548,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
       }
     }
     if (WRITE)
-      for (int i = in.begin + tid; i < in.end; i += kRowThreads) P.probs[row * P.ld_out + i] = 0.f;
+      for (int i = in.begin + tid; i < in.end; i += kRowThreads) P.probs[(size_t)row * P.ld_out + i] = 0.f;
     cluster.sync();
-    return;
+    continue;
   }
 
   // The last entry kept, and the sum of those kept.
@@ -591,64 +677,661 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
       const float r = fmaf(d, per_unit.x, -y) + d * per_unit.y;
       return y > -160.f ? exp2f(y) * fmaf(r, 0.69314718f, 1.f) * inv : 0.f;
     };
-    constexpr int N = PROBS ? 4 : 8;
-    if (P.vec && P.vec_out) {
-      const int vecs = (in.end - in.begin) / N;
-      const uint4* p = reinterpret_cast<const uint4*>((const char*)in.row +
-                                                      (size_t)in.begin * (PROBS ? 4 : 2));
-      for (int v = tid; v < vecs; v += kRowThreads) {
-        const uint4 x = __ldg(p + v);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        const int i = in.begin + v * N;
-        float4* o = reinterpret_cast<float4*>(out + i);
-        if (PROBS) {
-          __stcs(o, make_float4(value(i, prob_key(w[0])), value(i + 1, prob_key(w[1])),
-                                value(i + 2, prob_key(w[2])), value(i + 3, prob_key(w[3]))));
-        } else {
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            __stcs(o + q, make_float4(value(i + 4 * q, logit_key(w[2 * q] & 0xffffu)),
-                                      value(i + 4 * q + 1, logit_key(w[2 * q] >> 16)),
-                                      value(i + 4 * q + 2, logit_key(w[2 * q + 1] & 0xffffu)),
-                                      value(i + 4 * q + 3, logit_key(w[2 * q + 1] >> 16))));
-        }
-      }
-      for (int i = in.begin + vecs * N + tid; i < in.end; i += kRowThreads)
-        out[i] = value(i, in.key_at(i));
-    } else {
-      for (int i = in.begin + tid; i < in.end; i += kRowThreads) out[i] = value(i, in.key_at(i));
-    }
+    in.write(out, P.vec_out, tid, kRowThreads, value);
   }
-  cluster.sync();  // no CTA leaves while another may read its histogram
+  cluster.sync();  // no CTA goes on while another may read its histogram
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// The quick kernel. Bins stand in the order of the values, larger first, as rows of 32 (a lane a bin):
+// logits have 128 rows of positive values, one for zero, 128 of negative ones; probabilities 256.
+// ---------------------------------------------------------------------------------------------
+constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQBins = 8192, kQRows = 257;
+constexpr int kQSmall = 256;    // logits below 2^-15 that a CTA may have
+constexpr int kQList = 2048;    // entries of one bin of probabilities
+constexpr double kQUnit = 17592186044416.0;  // sums of probabilities: multiples of 2^-44
+
+enum { kOpEnd, kOpNth, kOpCollect, kOpMark, kOpNothing };
+
+struct QuickShared {
+  float2 two_to[64];
+  uint32_t row_count[kQRows];  // of a row of bins, then of those before it (rank 0's)
+  unsigned long long row_sum[kQRows];
+  uint32_t rank_first[kMostClusters];  // the first bin in order that a CTA has anything in
+  uint32_t rank_zero[kMostClusters], rank_small[kMostClusters], rank_far[kMostClusters],
+      rank_bad[kMostClusters];
+  unsigned long long rank_small_sum[kMostClusters];
+  uint32_t zero, small, far, bad, first, eq[kQWarps], rank_eq[kMostClusters];
+  unsigned long long small_sum;
+  uint16_t small_at[kQSmall];
+  float2 per_unit;
+  // of rank 0's first warp to all: what to do, and the row's cut
+  int op;
+  uint32_t op_key, op_number;
+  int index, edge;
+  uint32_t least;
+  float inv;
+  // a bin's entries (lower halves), and counts and sums of them
+  uint32_t listed;
+  uint16_t list[kQList];
+  uint32_t sub[256], sub_sum[256];
+};
+
+// Bits of a logit by its place in the bins' order: row 128 is zero.
+__device__ __forceinline__ uint32_t quick_bits(int row, int lane) {
+  if (row == 128) return 0;
+  const int i = row < 128 ? 4095 - (row * 32 + lane) : (row - 129) * 32 + lane;
+  return (row < 128 ? 0u : 0x8000u) | (uint32_t)(0x4000 + i - 0x800);
+}
+// Its counter: the lower 12 bits of (bits + 0x800), the sign above them.
+__device__ __forceinline__ int quick_slot(uint32_t bits) {
+  const uint32_t t = bits + 0x800u;
+  return (int)((t & 0xfffu) | (t >> 3 & 0x1000u));
 }
 
 template <bool PROBS, bool WRITE>
-static int launch_rows(RowsParams& P, long n_rows, cudaStream_t stream) {
-  // CTAs of a row: a part fits 16-bit counts; long rows are shared by four, and by eight where there
-  // are few of them.
-  int C = P.V <= 8192 ? 1 : P.V <= 32768 ? 2 : P.V <= 262112 ? 4 : 8;
-  while (C < kMostClusters && C > 1 && n_rows * C * 2 <= 152) C *= 2;
-  P.part = ((P.V + C - 1) / C + 7) / 8 * 8;
-  static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
+__global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const RowsParams P) {
+  extern __shared__ __align__(16) unsigned char s_hist[];
+  __shared__ QuickShared sh;
+  uint32_t* count = reinterpret_cast<uint32_t*>(s_hist);
+  uint32_t* low = count + kQBins;  // probabilities: sums of the lower halves
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x / C, req = row / P.J;
+  const float T = P.temperature ? P.temperature[req] : 1.f;
+  const bool greedy = !(T > 0.f);
+  const RowReader<PROBS> in{P, (const char*)P.rows + (size_t)row * P.ld * (PROBS ? 4 : 2),
+                            min(P.V, rank * P.part), min(P.V, (rank + 1) * P.part)};
+
+  // ---- 1. this CTA's histogram ----
+  for (int i = tid; i < kQBins * (PROBS ? 2 : 1) / 4; i += kQThreads)
+    reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0, 0, 0, 0);
+  if (!PROBS && tid < 64) {
+    const double t = exp2((double)tid / 64.0);
+    const float hi = (float)t;
+    sh.two_to[tid] = make_float2(hi, (float)(t - (double)hi));
+  } else if (!PROBS && tid == 64) {
+    const double c = 1.4426950408889634074 / fmin(fmax((double)(greedy ? 1.f : T), 0x1p-100), 0x1p100);
+    const float hi = (float)c;
+    sh.per_unit = make_float2(hi, (float)(c - (double)hi));
+  } else if (tid == 96) {
+    sh.zero = sh.small = sh.far = sh.bad = 0;
+    sh.first = 0xffffffffu;
+    sh.small_sum = 0;
+  }
+  cluster.sync();  // (every CTA has begun: its shared memory may be written from here on)
+  {
+    uint32_t zeros = 0, far = 0, bad = 0;
+    in.raw(tid, kQThreads, [&](uint32_t b) {
+      if (PROBS) {
+        if (b >> 29 == 1) {
+          const int o = 0x3fff - (int)(b >> 16);
+          atomicAdd(&count[o], 1u);
+          atomicAdd(&low[o], b & 0xffffu);
+          if (b > 0x3f800000u) bad = 1;
+        } else if (b - 1u < 0x1fffffffu) {
+          ++far;  // below 2^-63
+        } else if (b - 1u < 0x7f800000u) {
+          bad = 1;
+        }
+      } else {
+        const uint32_t t = b + 0x800u;
+        if ((t & 0x7000u) == 0x4000u) {
+          atomicAdd(&count[(t & 0xfffu) | (t >> 3 & 0x1000u)], 1u);
+        } else if (b != 0xff80u) {
+          const uint32_t mag = b & 0x7fffu;
+          if (mag == 0) {
+            ++zeros;
+          } else if (mag < 0x3800u) {  // below 2^-15
+            const uint32_t i = atomicAdd(&sh.small, 1u);
+            if (i < kQSmall) sh.small_at[i] = (uint16_t)b;
+          } else if (mag <= 0x7f80u) {
+            if (b & 0x8000u) ++far;  // -2^17 or less
+            else bad = 1;
+          }
+        }
+      }
+    });
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    far = __reduce_add_sync(0xffffffffu, far);
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      if (zeros) atomicAdd(&sh.zero, zeros);
+      if (far) atomicAdd(&sh.far, far);
+      if (bad) sh.bad = 1;
+    }
+  }
+  __syncthreads();
+  // the first bin in order that is not empty
+  {
+    uint32_t first = 0xffffffffu;
+    constexpr int kPer = kQBins / kQThreads;
+    const uint4* c4 = reinterpret_cast<const uint4*>(count) + tid * (kPer / 4);
+    uint32_t some = 0;
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i) {
+      const uint4 v = c4[i];
+      some |= (v.x ? 1u : 0u) << (4 * i) | (v.y ? 2u : 0u) << (4 * i) | (v.z ? 4u : 0u) << (4 * i) |
+              (v.w ? 8u : 0u) << (4 * i);
+      if (PROBS && (v.x | v.y | v.z | v.w) > 0xffffu) sh.bad = 1;  // sums of 16 bits may have passed 32
+    }
+    if (some) {
+      const int at = tid * kPer;
+      if (PROBS) first = at + __ffs(some) - 1;
+      // positive counters ascend with the value; zero is place 4096, negative ones follow
+      else if (at < 4096) first = 4095 - (at + 31 - __clz(some));
+      else first = 1 + at + __ffs(some) - 1;
+    }
+    if (!PROBS && tid == 0 && sh.zero + sh.small) first = min(first, 4096u);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) atomicMin(&sh.first, first);
+  }
+  __syncthreads();
+  if (warp == 0 && lane < C) {
+    cluster.map_shared_rank(sh.rank_first, lane)[rank] = sh.first;
+    cluster.map_shared_rank(sh.rank_zero, lane)[rank] = sh.zero;
+    cluster.map_shared_rank(sh.rank_small, lane)[rank] = sh.small;
+    cluster.map_shared_rank(sh.rank_far, lane)[rank] = sh.far;
+    cluster.map_shared_rank(sh.rank_bad, lane)[rank] =
+        sh.bad | (uint32_t)(sh.small > kQSmall ? 1 : 0);
+  }
+  cluster.sync();
+  uint32_t first = 0xffffffffu, zeros = 0, smalls = 0, far = 0, bad = 0;
+  for (int c = 0; c < C; ++c) {
+    first = min(first, sh.rank_first[c]);
+    zeros += sh.rank_zero[c];
+    smalls += sh.rank_small[c];
+    far += sh.rank_far[c];
+    bad |= sh.rank_bad[c];
+  }
+  const bool some = first != 0xffffffffu;
+  // the largest logit (some small one, if there is none above: such rows are marked)
+  const uint32_t top_bits = !PROBS && some
+      ? first == 4096 ? 0u : first < 4096 ? quick_bits(first >> 5, first & 31)
+                                          : quick_bits(129 + ((first - 4097) >> 5), (first - 4097) & 31)
+      : 0u;
+  const float top_value = bf16_bits_to_float(top_bits);
+  const float2 per_unit = sh.per_unit;
+  // a logit's weight as a count of 2^-63
+  auto weight = [&](uint32_t bits) -> unsigned long long {
+    if (bits == top_bits) return 1ull << 63;
+    return weight63(ff_sum(bf16_bits_to_float(bits), -top_value), per_unit, sh.two_to);
+  };
+  auto sum_of = [&](uint32_t n, unsigned long long w63) -> unsigned long long {
+    // n w 2^-63 in units of 2^-43, rounded
+    const unsigned long long hi = __umul64hi(w63, (unsigned long long)n << 44);
+    return hi + ((w63 * ((unsigned long long)n << 44)) >> 63);
+  };
+  // a bin's entries, and their sum
+  auto read_bin = [&](int r, uint32_t& n, unsigned long long& s, unsigned long long& w) {
+    n = 0;
+    s = w = 0;
+    if (PROBS) {
+      const int o = r * 32 + lane;
+      unsigned long long l = 0;
+      for (int c = 0; c < C; ++c) {
+        n += *cluster.map_shared_rank(count + o, c);
+        l += *cluster.map_shared_rank(low + o, c);
+      }
+      if (n) {  // the significand's last place, in units of 2^-44
+        const uint32_t k = (uint32_t)(0x3fff - o);
+        const unsigned long long units =
+            (unsigned long long)n * ((0x80u | (k & 0x7fu)) << 16) + l;
+        const int by = (int)(k >> 7) - 150 + 44;
+        s = by >= 0 ? units << by : by < -62 ? 0 : ((units >> (-by - 1)) + 1) >> 1;
+        w = l;
+      }
+    } else {
+      const uint32_t bits = quick_bits(r, lane);
+      if (r == 128) {
+        n = lane == 0 ? zeros : 0;
+      } else {
+        const int at = quick_slot(bits);
+        for (int c = 0; c < C; ++c) n += *cluster.map_shared_rank(count + at, c);
+      }
+      if (n) s = sum_of(n, w = weight(bits));
+    }
+  };
+
+  // ---- 2. counts and sums of the rows of bins, into rank 0 ----
+  if (!PROBS) {  // small logits weigh for themselves, and stand beside zero
+    unsigned long long s = 0;
+    const uint32_t m = min(sh.small, (uint32_t)kQSmall);
+    if ((uint32_t)tid < m) s = sum_of(1, weight(sh.small_at[tid]));
+    if (m) {
+      s = warp_sum64(s);
+      if (lane == 0 && s) atomicAdd(&sh.small_sum, s);
+    }
+    __syncthreads();
+    if (tid == 0) cluster.map_shared_rank(sh.rank_small_sum, 0)[rank] = sh.small_sum;
+  }
+  constexpr int kRowsOf = PROBS ? 256 : 257;
+  for (int r = rank * kQWarps + warp; r < kRowsOf; r += C * kQWarps) {
+    uint32_t n;
+    unsigned long long s, w;
+    read_bin(r, n, s, w);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, n);
+    if (all) s = warp_sum64(s);
+    if (lane == 0) {
+      *cluster.map_shared_rank(&sh.row_count[r], 0) = all;
+      *cluster.map_shared_rank(&sh.row_sum[r], 0) = all ? s : 0;
+    }
+  }
+  cluster.sync();
+
+  // ---- 3. the search: rank 0's first warp, the others serve it ----
+  float* out = WRITE ? P.probs + (size_t)row * P.ld_out : nullptr;
+  auto nth = [&]() {  // index of entry number op_number of those with op_key
+    const uint32_t key = cluster.map_shared_rank(&sh, 0)->op_key;
+    const uint32_t j = cluster.map_shared_rank(&sh, 0)->op_number;
+    const int len = in.end - in.begin, seg = ((len + kQWarps - 1) / kQWarps + 7) & ~7;
+    const int a = in.begin + min(len, warp * seg), b = in.begin + min(len, (warp + 1) * seg);
+    uint32_t have = 0;
+    in.each(a, b, lane, 32, [&](int, uint32_t x) { have += x == key; });
+    have = __reduce_add_sync(0xffffffffu, have);
+    if (lane == 0) sh.eq[warp] = have;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (int w = 0; w < kQWarps; ++w) {
+      if (w < warp) before += sh.eq[w];
+      all += sh.eq[w];
+    }
+    if (warp == 0 && lane < C) cluster.map_shared_rank(sh.rank_eq, lane)[rank] = all;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) before += sh.rank_eq[c];
+    if (j >= before && j - before < have) {
+      uint32_t left = j - before;
+      for (int i = a; i < b; i += 32) {
+        const uint32_t m = __ballot_sync(0xffffffffu, i + lane < b && in.key_at(i + lane) == key);
+        const uint32_t c = __popc(m);
+        if (left < c) {
+          if (lane == 0)
+            cluster.map_shared_rank(&sh, 0)->index = i + (int)__fns(m, 0, (int)left + 1);
+          break;
+        }
+        left -= c;
+      }
+    }
+  };
+  auto collect = [&]() {  // the lower halves of a bin's entries
+    QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
+    const uint32_t bin = s0->op_key >> 16;
+    in.each(in.begin, in.end, tid, kQThreads, [&](int, uint32_t x) {
+      if (x >> 16 == bin) {
+        const uint32_t i = atomicAdd(&s0->listed, 1u);
+        if (i < kQList) s0->list[i] = (uint16_t)x;
+      }
+    });
+  };
+  auto serve = [&]() {
+    for (;;) {
+      cluster.sync();
+      const int op = cluster.map_shared_rank(&sh, 0)->op;
+      if (op == kOpNth) nth();
+      if (op == kOpCollect) collect();
+      if (op == kOpEnd || op == kOpMark || op == kOpNothing) break;
+      cluster.sync();
+    }
+  };
+  if (rank == 0 && warp == 0) {
+    // counts and sums before every row
+    constexpr int kPer = (kQRows + 31) / 32;
+    uint32_t n = 0;
+    unsigned long long s = 0;
+    if (!PROBS) {
+      for (int c = 0; c < C; ++c) s += sh.rank_small_sum[c];
+      if (lane == 0) {
+        sh.row_count[128] += smalls;
+        sh.row_sum[128] += s;
+      }
+      s = 0;
+      __syncwarp();
+    }
+    for (int i = 0; i < kPer; ++i)
+      if (lane * kPer + i < kRowsOf) {
+        n += sh.row_count[lane * kPer + i];
+        s += sh.row_sum[lane * kPer + i];
+      }
+    uint32_t n_at = warp_before(n);
+    unsigned long long s_at = warp_before(s);
+    const uint32_t binned = __shfl_sync(0xffffffffu, n_at + n, 31);
+    const unsigned long long total_sum = __shfl_sync(0xffffffffu, s_at + s, 31);
+    for (int i = 0; i < kPer; ++i)
+      if (lane * kPer + i < kRowsOf) {
+        const uint32_t a = sh.row_count[lane * kPer + i];
+        const unsigned long long b = sh.row_sum[lane * kPer + i];
+        sh.row_count[lane * kPer + i] = n_at;
+        sh.row_sum[lane * kPer + i] = s_at;
+        n_at += a;
+        s_at += b;
+      }
+    __syncwarp();
+    const uint32_t total = binned + far;
+    // far entries have to weigh nothing beside the others
+    bool mark = bad;
+    if (PROBS) mark |= total > 0 && total_sum < (unsigned long long)(kQUnit / 2);
+    else if (far) mark |= !some || !((-131072.f - top_value) * per_unit.x < -64.f);
+    if (!PROBS && some && first == 4096 && smalls) mark = true;
+
+    auto ask = [&](int op, uint32_t key, uint32_t number) {
+      if (lane == 0) {
+        sh.op = op;
+        sh.op_key = key;
+        sh.op_number = number;
+      }
+      cluster.sync();
+      if (op == kOpNth) nth();
+      if (op == kOpCollect) collect();
+      if (op == kOpNth || op == kOpCollect) cluster.sync();
+    };
+    // A probability's place in its bin: by count (g), by sum (goal), or by key.
+    auto inside = [&](Border b, int by, unsigned long long g, double goal, uint32_t key) -> Border {
+      const int e = (int)(b.key >> 23);
+      const double unit = exp2((double)(e - 150 + 44));
+      if (b.count == 1 && by != 2) {
+        b.key |= (uint32_t)b.w;
+        b.w = (double)(0x800000u | (b.key & 0x7fffffu)) * unit;
+        return b;
+      }
+      if (lane == 0) sh.listed = 0;
+      ask(kOpCollect, b.key, 0);
+      const uint32_t m = sh.listed;
+      if (m > kQList) {
+        mark = true;
+        return b;
+      }
+      for (int level = 0; level < 2; ++level) {
+        for (int i = lane; i < 256; i += 32) sh.sub[i] = sh.sub_sum[i] = 0;
+        __syncwarp();
+        for (uint32_t i = lane; i < m; i += 32) {
+          const uint32_t x = sh.list[i];
+          if (level && (x >> 8) != (b.key >> 8 & 0xffu)) continue;
+          atomicAdd(&sh.sub[255 - (level ? x & 255u : x >> 8)], 1u);
+          if (!level) atomicAdd(&sh.sub_sum[255 - (x >> 8)], x & 255u);
+        }
+        __syncwarp();
+        // 8 bins a lane
+        uint32_t bn = 0;
+        unsigned long long bsum = 0;
+        auto value = [&](int i) {
+          return b.key | (uint32_t)(255 - i) << (level ? 0 : 8);
+        };
+        auto units = [&](int i) {
+          return (unsigned long long)sh.sub[i] * (0x800000u | (value(i) & 0x7fffffu)) + sh.sub_sum[i];
+        };
+        for (int i = lane * 8; i < lane * 8 + 8; ++i) {
+          bn += sh.sub[i];
+          bsum += units(i);
+        }
+        uint32_t an = warp_before(bn);
+        unsigned long long as = warp_before(bsum);
+        bool hit = false;
+        Border got = b;
+        for (int i = lane * 8; i < lane * 8 + 8; ++i) {
+          const uint32_t c = sh.sub[i];
+          const unsigned long long u = units(i);
+          const double from = b.sum + (double)as * unit, to = b.sum + (double)(as + u) * unit;
+          bool here;
+          if (by == 0) here = g >= b.above + an && g < (unsigned long long)b.above + an + c;
+          else if (by == 1)
+            here = c > 0 && (goal >= from || an == 0) && (goal < to || an + c == b.count);
+          else here = (level ? key : key >> 8) == (level ? value(i) : value(i) >> 8);
+          if (here) {
+            hit = true;
+            got = Border{value(i), b.above + an, c, from,
+                         (double)(0x800000u | (value(i) & 0x7fffffu)) * unit};
+          }
+          an += c;
+          as += u;
+        }
+        const uint32_t who = __ballot_sync(0xffffffffu, hit);
+        const int src = who ? __ffs(who) - 1 : 0;
+        b.key = __shfl_sync(0xffffffffu, got.key, src);
+        b.above = __shfl_sync(0xffffffffu, got.above, src);
+        b.count = __shfl_sync(0xffffffffu, got.count, src);
+        b.sum = __shfl_sync(0xffffffffu, got.sum, src);
+        b.w = __shfl_sync(0xffffffffu, got.w, src);
+        __syncwarp();
+      }
+      return b;
+    };
+    // The entry at place g of the order (by 0), the one whose stretch of the running sum holds g (by
+    // 1), or a value, whether it occurs or not (by 2; g its place among the bins).
+    auto find = [&](int by, unsigned long long g, double goal, uint32_t key) -> Border {
+      Border b = {0, 0, 1, 0.0, 1.0};
+      if (by == 0 && g >= binned) {
+        mark = true;
+        return b;
+      }
+      int r;
+      if (by == 2) {
+        r = (int)(g >> 5);
+      } else {
+        int lo = 0, hi = kRowsOf;  // the last row that begins at g or before
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (by == 0 ? sh.row_count[mid] <= g : sh.row_sum[mid] <= g) lo = mid;
+          else hi = mid;
+        }
+        r = lo;
+      }
+      if (!PROBS && r == 128 && smalls) {
+        mark = true;
+        return b;
+      }
+      uint32_t n;
+      unsigned long long s, w;
+      read_bin(r, n, s, w);
+      const uint32_t an = sh.row_count[r] + warp_before(n);
+      const unsigned long long as = sh.row_sum[r] + warp_before(s);
+      const bool here = by == 0   ? g >= an && g < an + n
+                        : by == 1 ? g >= as && g < as + s
+                                  : lane == (int)(g & 31);
+      const uint32_t who = __ballot_sync(0xffffffffu, here);
+      const int src = who ? __ffs(who) - 1 : 0;
+      b.key = PROBS ? (uint32_t)(0x3fff - (r * 32 + src)) << 16 : logit_key(quick_bits(r, src));
+      b.above = __shfl_sync(0xffffffffu, an, src);
+      b.count = __shfl_sync(0xffffffffu, n, src);
+      b.sum = (double)__shfl_sync(0xffffffffu, as, src);
+      w = __shfl_sync(0xffffffffu, w, src);
+      b.w = PROBS ? (double)w : (double)w * 0x1p-20;
+      return PROBS ? inside(b, by, g, goal, key) : b;
+    };
+
+    uint32_t keep = total;
+    Border last = {0, 0, 0, 0.0, 0.0};
+    bool cut = false;
+    double kept_sum = (double)total_sum;
+    auto cut_at = [&](uint32_t m, const Border& b) {
+      keep = m;
+      last = b;
+      cut = true;
+      kept_sum = b.sum + (double)(m - b.above) * b.w;
+    };
+    int at = 0;
+    float prob = 0.f;
+    int edge = 0x7fffffff;
+    if (!mark && total > 0) {
+      uint32_t k = 0x7fffffffu;
+      if (P.top_k && P.top_k[req] > 0) k = (uint32_t)P.top_k[req];
+      if (greedy) k = 1;
+      if (k < keep) cut_at(k, find(0, k - 1, 0.0, 0));
+      const float top_p = P.top_p && !greedy ? P.top_p[req] : 1.f;
+      if (!mark && top_p < 1.f && keep > 1) {
+        // the last entry before which less than top_p of the sum lies
+        const double goal = (double)fmaxf(top_p, 0.f) * kept_sum;
+        const double g = fmin(fmax(ceil(goal) - 1.0, 0.0), fmax(ceil(kept_sum) - 1.0, 0.0));
+        const Border b = find(1, min((unsigned long long)g, total_sum - 1), g, 0);
+        const double j = ceil((goal - b.sum) / b.w);
+        const uint32_t m = b.above + (j >= (double)b.count ? b.count : j >= 1.0 ? (uint32_t)j : 1u);
+        if (m < keep) cut_at(m, b);
+      }
+      const float min_p = P.min_p && !greedy ? P.min_p[req] : 0.f;
+      if (!mark && min_p > 0.f && keep > 1) {
+        uint32_t m = keep;
+        if (PROBS) {
+          const Border t = find(0, 0, 0.0, 0);  // the largest
+          if (min_p >= 1.f) {
+            m = t.count;
+          } else if (!mark) {
+            const uint32_t key =
+                __float_as_uint(__double2float_ru((double)min_p * (double)__uint_as_float(t.key)));
+            if (key >> 29 == 1) {
+              const Border b = find(2, 0x3fff - (key >> 16), 0.0, key);
+              m = b.above + b.count;
+            } else if (far) {
+              mark = true;
+            }
+          }
+        } else if (min_p >= 1.f) {
+          m = find(0, 0, 0.0, 0).count;
+        } else {
+          const double t =
+              (double)top_value + fmin(fmax((double)T, 0x1p-100), 0x1p100) * log((double)min_p);
+          const uint32_t o = orderable(__double2float_ru(t));
+          // the smallest logit that stays, as bits
+          const uint32_t key = min(o & 0x80000000u ? (o + 0xffffu) >> 16 : o >> 16, logit_key(top_bits));
+          const uint32_t bits = key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu;
+          const uint32_t mag = bits & 0x7fffu;
+          if (mag >= 0x4800u) {  // beyond the bins: -2^17 or less (a larger one is not below the top)
+            m = far ? (mark = true, keep) : keep;
+          } else if (mag < 0x3800u && (mag || smalls)) {
+            // between the bins: zero stays or goes
+            if (smalls) mark = true;
+            else m = bits & 0x8000u ? sh.row_count[129] : sh.row_count[128];
+          } else {
+            const uint32_t i = mag - 0x3800u;
+            const Border b = find(2, mag == 0 ? 128 * 32 : bits & 0x8000u ? 129 * 32 + i : 4095 - i, 0.0, 0);
+            m = b.above + b.count;
+          }
+        }
+        m = max(m, 1u);
+        if (!mark && m < keep) cut_at(m, find(0, m - 1, 0.0, 0));
+      }
+      if (!mark && !WRITE) {
+        float u = P.u[row];
+        u = u > 0.f ? u : 0.f;
+        Border b;
+        uint32_t j = 0;
+        if (keep == 1) {
+          b = cut ? last : find(0, 0, 0.0, 0);
+        } else {
+          const double goal = fmin((double)u * kept_sum, kept_sum);
+          const double g = fmin(floor(goal), fmax(ceil((double)total_sum) - 1.0, 0.0));
+          b = find(1, min((unsigned long long)g, total_sum - 1), goal, 0);
+          const double f = floor((goal - b.sum) / b.w);
+          j = f >= (double)(b.count - 1) ? b.count - 1 : f > 0.0 ? (uint32_t)f : 0u;
+          if (!mark && b.above + j >= keep) {
+            b = cut ? last : find(0, keep - 1, 0.0, 0);
+            j = keep - 1 - b.above;
+          }
+        }
+        if (!mark) {
+          ask(kOpNth, b.key, j);
+          at = sh.index;
+          prob = (float)(b.w / kept_sum);
+        }
+      }
+      if (!mark && WRITE && cut && keep - last.above < last.count) {
+        ask(kOpNth, last.key, keep - last.above - 1);
+        edge = sh.index;
+      }
+    }
+    if (lane == 0) {
+      sh.edge = edge;
+      sh.least = cut ? last.key : 1u;
+      sh.inv = (float)((PROBS ? kQUnit : kSumUnit) / kept_sum);
+      if (!mark) {
+        if (total == 0) raise_err(P.err, SD_ERR_ZERO_ROW);
+        if (P.kept) P.kept[row] = (int32_t)keep;
+        if (!WRITE) {
+          P.tokens[row] = at;
+          if (P.prob) P.prob[row] = prob;
+        }
+      } else if (WRITE) {
+        out[0] = kMarkProb;
+      } else {
+        P.tokens[row] = kMarkToken;
+      }
+    }
+    ask(mark ? kOpMark : total == 0 ? kOpNothing : kOpEnd, 0, 0);
+  } else {
+    serve();
+  }
+  if (WRITE) {
+    const QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
+    const int op = s0->op, edge = s0->edge;
+    const uint32_t least = op == kOpNothing ? 0xffffffffu : s0->least;
+    const float inv = s0->inv;
+    if (op != kOpMark) {
+      auto value = [&](int i, uint32_t x) {
+        if (x < least || (x == least && i > edge)) return 0.f;
+        if (PROBS) return __uint_as_float(x) * inv;
+        const float d = logit_value(x) - top_value;
+        const float y = d * per_unit.x;
+        // (the product's rounding error goes into a factor: 2^y as exact as fp32 allows)
+        const float r = fmaf(d, per_unit.x, -y) + d * per_unit.y;
+        return y > -160.f ? exp2f(y) * fmaf(r, 0.69314718f, 1.f) * inv : 0.f;
+      };
+      in.write(out, P.vec_out, tid, kQThreads, value);
+    }
+  }
+  cluster.sync();  // no CTA leaves while another may read its shared memory
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <bool PROBS, bool WRITE>
+static int launch_rows(RowsParams& P, cudaStream_t stream) {
+  constexpr int kQuickBytes = kQBins * 4 * (PROBS ? 2 : 1);
+  static std::atomic<bool> set[64];  // per device; true only once the attributes are in force
+  static std::atomic<int> sms[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
   if (!set[dev].load(std::memory_order_acquire)) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+      return SD_E_DEVICE;
     if (cudaFuncSetAttribute(rows_kernel<PROBS, WRITE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kHistBytes) != cudaSuccess)
+                             kHistBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(quick_kernel<PROBS, WRITE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kQuickBytes) != cudaSuccess)
       return SD_E_LAUNCH;
+    sms[dev].store(n, std::memory_order_relaxed);
     set[dev].store(true, std::memory_order_release);
   }
+  const int n_sm = sms[dev].load(std::memory_order_relaxed);
+  auto parts = [&](int C) { return ((P.V + C - 1) / C + 7) / 8 * 8; };
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(n_rows * C), 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+
+  // CTAs of a row: more while the SMs have room for them, and a CTA some thousands of entries.
+  int C = 1;
+  while (C < kMostClusters && P.n_rows * 2L * C <= 4L * n_sm && P.V > 4096 * C) C *= 2;
+  P.part = parts(C);
+  attr[0].val.clusterDim.x = (unsigned)C;
+  cfg.gridDim = dim3((unsigned)(P.n_rows * C), 1, 1);
+  cfg.blockDim = dim3(kQThreads, 1, 1);
+  cfg.dynamicSmemBytes = kQuickBytes;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, quick_kernel<PROBS, WRITE>, P) != cudaSuccess) return SD_E_LAUNCH;
+
+  // A part's counts have 16 bits there.
+  C = P.V <= 8192 ? 1 : P.V <= 32768 ? 2 : P.V <= 262112 ? 4 : 8;
+  P.part = parts(C);
+  attr[0].val.clusterDim.x = (unsigned)C;
+  const int clusters = n_sm / C < P.n_rows ? n_sm / C : P.n_rows;
+  cfg.gridDim = dim3((unsigned)(clusters * C), 1, 1);
   cfg.blockDim = dim3(kRowThreads, 1, 1);
   cfg.dynamicSmemBytes = kHistBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, rows_kernel<PROBS, WRITE>, P) == cudaSuccess ? SD_OK
                                                                               : SD_E_LAUNCH;
 }
@@ -679,10 +1362,8 @@ extern "C" int sd_rows_launch(int B, int J, int V, int dtype, const void* rows, 
   P.prob = prob;
   P.kept = kept;
   P.err = err;
-  const long n = (long)B * J;
+  P.n_rows = B * J;
   if (dtype == SD_F32_PROBS)
-    return probs ? sdk::launch_rows<true, true>(P, n, stream)
-                 : sdk::launch_rows<true, false>(P, n, stream);
-  return probs ? sdk::launch_rows<false, true>(P, n, stream)
-               : sdk::launch_rows<false, false>(P, n, stream);
+    return probs ? sdk::launch_rows<true, true>(P, stream) : sdk::launch_rows<true, false>(P, stream);
+  return probs ? sdk::launch_rows<false, true>(P, stream) : sdk::launch_rows<false, false>(P, stream);
 }
