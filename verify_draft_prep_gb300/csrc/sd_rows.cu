@@ -117,6 +117,13 @@ __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// The same for v < 2^62, by the warp's integer reduction.
+__device__ __forceinline__ unsigned long long warp_sum62(unsigned long long v) {
+  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x1fffffu);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 21) & 0x1fffffu);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 42));
+  return a + ((unsigned long long)b << 21) + ((unsigned long long)c << 42);
+}
 template <typename T>
 __device__ __forceinline__ T warp_before(T v) {  // the sum over the lanes before this one
   const int lane = threadIdx.x & 31;
@@ -194,6 +201,51 @@ struct RowReader {
     }
     for (int i = begin + vecs * N + first; i < end; i += step)
       f(PROBS ? __ldg((const uint32_t*)row + i) : (uint32_t)__ldg((const uint16_t*)row + i));
+  }
+
+  // f(index) for every entry of the part with this (not zero) key, in any order.
+  template <typename F>
+  __device__ __forceinline__ void matches(uint32_t key, int first, int step, F f) const {
+    constexpr int N = PROBS ? 4 : 8;
+    int i0 = begin + first;
+    if (P.vec) {
+      const int vecs = (end - begin) / N;
+      const uint4* p = reinterpret_cast<const uint4*>((const char*)row + (size_t)begin * (PROBS ? 4 : 2));
+      // two logits at a time: the words' halves that are zero after the exclusive or
+      const bool zero = !PROBS && key == 0x8000u;
+      const uint32_t bits = PROBS ? key : (key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu) * 0x10001u;
+      const uint32_t mask = zero ? 0x7fff7fffu : 0xffffffffu;
+      auto one = [&](const uint4& v, int at) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hit = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (PROBS) {
+            // (what is above 1 counts as 1)
+            hit |= (key == 0x3f800000u ? prob_key(w[j]) : w[j]) == bits;
+          } else {
+            const uint32_t x = (w[j] & mask) ^ bits;
+            hit |= (x - 0x00010001u) & ~x & 0x80008000u;
+          }
+        }
+        if (hit)
+          for (int j = 0; j < N; ++j)
+            if (key_at(at + j) == key) f(at + j);
+      };
+      constexpr int kAhead = 4;
+      for (int v = first; v < vecs; v += kAhead * step) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (v + k * step < vecs) x[k] = __ldg(p + v + k * step);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (v + k * step < vecs) one(x[k], begin + (v + k * step) * N);
+      }
+      i0 += vecs * N;
+    }
+    for (int i = i0; i < end; i += step)
+      if (key_at(i) == key) f(i);
   }
 
   // out[index] = value(index, key) for every entry of the part.
@@ -708,13 +760,16 @@ struct QuickShared {
   float2 per_unit;
   // of rank 0's first warp to all: what to do, and the row's cut
   int op;
-  uint32_t op_key, op_number;
+  uint32_t op_key, op_number, op_count;
   int index, edge;
   uint32_t least;
   float inv;
   // a bin's entries (lower halves), and counts and sums of them
   uint32_t listed;
-  uint16_t list[kQList];
+  union {
+    uint16_t list[kQList];
+    int at[kQList];  // or indices of entries of one value
+  };
   uint32_t sub[256], sub_sum[256];
 };
 
@@ -871,9 +926,14 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     if (PROBS) {
       const int o = r * 32 + lane;
       unsigned long long l = 0;
-      for (int c = 0; c < C; ++c) {
-        n += *cluster.map_shared_rank(count + o, c);
-        l += *cluster.map_shared_rank(low + o, c);
+      if (C == 1) {
+        n = count[o];
+        l = low[o];
+      } else {
+        for (int c = 0; c < C; ++c) {
+          n += *cluster.map_shared_rank(count + o, c);
+          l += *cluster.map_shared_rank(low + o, c);
+        }
       }
       if (n) {  // the significand's last place, in units of 2^-44
         const uint32_t k = (uint32_t)(0x3fff - o);
@@ -889,7 +949,9 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         n = lane == 0 ? zeros : 0;
       } else {
         const int at = quick_slot(bits);
-        for (int c = 0; c < C; ++c) n += *cluster.map_shared_rank(count + at, c);
+        if (C == 1) n = count[at];
+        else
+          for (int c = 0; c < C; ++c) n += *cluster.map_shared_rank(count + at, c);
       }
       if (n) s = sum_of(n, w = weight(bits));
     }
@@ -907,25 +969,52 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     __syncthreads();
     if (tid == 0) cluster.map_shared_rank(sh.rank_small_sum, 0)[rank] = sh.small_sum;
   }
-  constexpr int kRowsOf = PROBS ? 256 : 257;
-  for (int r = rank * kQWarps + warp; r < kRowsOf; r += C * kQWarps) {
-    uint32_t n;
-    unsigned long long s, w;
-    read_bin(r, n, s, w);
-    const uint32_t all = __reduce_add_sync(0xffffffffu, n);
-    if (all) s = warp_sum64(s);
-    if (lane == 0) {
-      *cluster.map_shared_rank(&sh.row_count[r], 0) = all;
-      *cluster.map_shared_rank(&sh.row_sum[r], 0) = all ? s : 0;
+  constexpr int kRowsOf = PROBS ? 256 : 257, kTogether = 4;
+  for (int r0 = rank * kQWarps + warp; r0 < kRowsOf; r0 += kTogether * C * kQWarps) {
+    uint32_t n[kTogether];
+    unsigned long long s[kTogether], w;
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      const int r = r0 + k * C * kQWarps;
+      n[k] = 0;
+      s[k] = 0;
+      if (r < kRowsOf) read_bin(r, n[k], s[k], w);
+    }
+#pragma unroll
+    for (int k = 0; k < kTogether; ++k) {
+      const int r = r0 + k * C * kQWarps;
+      if (r >= kRowsOf) break;
+      const uint32_t all = __reduce_add_sync(0xffffffffu, n[k]);
+      if (all) s[k] = warp_sum62(s[k]);
+      if (lane == 0) {
+        *cluster.map_shared_rank(&sh.row_count[r], 0) = all;
+        *cluster.map_shared_rank(&sh.row_sum[r], 0) = s[k];
+      }
     }
   }
   cluster.sync();
 
   // ---- 3. the search: rank 0's first warp, the others serve it ----
   float* out = WRITE ? P.probs + (size_t)row * P.ld_out : nullptr;
-  auto nth = [&]() {  // index of entry number op_number of those with op_key
-    const uint32_t key = cluster.map_shared_rank(&sh, 0)->op_key;
-    const uint32_t j = cluster.map_shared_rank(&sh, 0)->op_number;
+  // Index of entry number op_number of those with op_key: up to kQList of them are listed and the
+  // one with so many smaller ones is found; more are counted along the row.
+  auto nth = [&]() {
+    QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
+    const uint32_t key = s0->op_key, j = s0->op_number;
+    if (s0->op_count <= kQList) {
+      in.matches(key, tid, kQThreads, [&](int i) { s0->at[atomicAdd(&s0->listed, 1u)] = i; });
+      cluster.sync();
+      if (rank == 0) {
+        const int m = (int)sh.listed;
+        for (int a = tid; a < m; a += kQThreads) {
+          const int mine = sh.at[a];
+          uint32_t less = 0;
+          for (int i = 0; i < m; ++i) less += sh.at[i] < mine;
+          if (less == j) sh.index = mine;
+        }
+      }
+      return;
+    }
     const int len = in.end - in.begin, seg = ((len + kQWarps - 1) / kQWarps + 7) & ~7;
     const int a = in.begin + min(len, warp * seg), b = in.begin + min(len, (warp + 1) * seg);
     uint32_t have = 0;
@@ -943,15 +1032,28 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     for (int c = 0; c < rank; ++c) before += sh.rank_eq[c];
     if (j >= before && j - before < have) {
       uint32_t left = j - before;
-      for (int i = a; i < b; i += 32) {
-        const uint32_t m = __ballot_sync(0xffffffffu, i + lane < b && in.key_at(i + lane) == key);
-        const uint32_t c = __popc(m);
-        if (left < c) {
-          if (lane == 0)
-            cluster.map_shared_rank(&sh, 0)->index = i + (int)__fns(m, 0, (int)left + 1);
-          break;
+      for (int i = a; i < b;) {  // 256 entries at a time, then the 32 with the one in question
+        uint32_t x[8], n = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = i + k * 32 + lane < b ? in.key_at(i + k * 32 + lane) : 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) n += __popc(__ballot_sync(0xffffffffu, x[k] == key));
+        if (left >= n) {
+          left -= n;
+          i += 256;
+          continue;
         }
-        left -= c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t m = __ballot_sync(0xffffffffu, x[k] == key), c = __popc(m);
+          if (left < c && n) {
+            if (lane == 0) s0->index = i + k * 32 + (int)__fns(m, 0, (int)left + 1);
+            n = 0;
+          } else if (n) {
+            left -= c;
+          }
+        }
+        break;
       }
     }
   };
@@ -1015,11 +1117,13 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     else if (far) mark |= !some || !((-131072.f - top_value) * per_unit.x < -64.f);
     if (!PROBS && some && first == 4096 && smalls) mark = true;
 
-    auto ask = [&](int op, uint32_t key, uint32_t number) {
+    auto ask = [&](int op, uint32_t key, uint32_t number, uint32_t of) {
       if (lane == 0) {
         sh.op = op;
         sh.op_key = key;
         sh.op_number = number;
+        sh.op_count = of;
+        sh.listed = 0;
       }
       cluster.sync();
       if (op == kOpNth) nth();
@@ -1035,8 +1139,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         b.w = (double)(0x800000u | (b.key & 0x7fffffu)) * unit;
         return b;
       }
-      if (lane == 0) sh.listed = 0;
-      ask(kOpCollect, b.key, 0);
+      ask(kOpCollect, b.key, 0, b.count);
       const uint32_t m = sh.listed;
       if (m > kQList) {
         mark = true;
@@ -1229,13 +1332,13 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
           }
         }
         if (!mark) {
-          ask(kOpNth, b.key, j);
+          ask(kOpNth, b.key, j, b.count);
           at = sh.index;
           prob = (float)(b.w / kept_sum);
         }
       }
       if (!mark && WRITE && cut && keep - last.above < last.count) {
-        ask(kOpNth, last.key, keep - last.above - 1);
+        ask(kOpNth, last.key, keep - last.above - 1, last.count);
         edge = sh.index;
       }
     }
@@ -1256,7 +1359,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         P.tokens[row] = kMarkToken;
       }
     }
-    ask(mark ? kOpMark : total == 0 ? kOpNothing : kOpEnd, 0, 0);
+    ask(mark ? kOpMark : total == 0 ? kOpNothing : kOpEnd, 0, 0, 0);
   } else {
     serve();
   }
