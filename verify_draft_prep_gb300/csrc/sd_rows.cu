@@ -90,7 +90,6 @@ __device__ __forceinline__ FF ff_sum(float a, float b) { return ff_two_sum(a, b)
 // need only fp32.
 __device__ __forceinline__ unsigned long long weight63(FF d, float2 c, const float2* two_to) {
   const float p = d.hi * c.x;
-  if (!(p > -63.f)) return 0;
   const float e = fmaf(d.hi, c.x, -p) + fmaf(d.hi, c.y, d.lo * c.x);
   const int k = __float2int_rn(p * 64.f);
   const FF g = ff_sum(fmaf((float)k, -0.015625f, p), e);
@@ -109,7 +108,8 @@ __device__ __forceinline__ unsigned long long weight63(FF d, float2 c, const flo
   const FF s = ff_sum(t.x, ph);
   const float lo = s.lo + pl + t.y;
   const float up = __uint_as_float((uint32_t)(127 + 63 + (k >> 6)) << 23);
-  return (unsigned long long)((long long)__float2ull_rz(s.hi * up) + __float2ll_rn(lo * up));
+  const long long w = (long long)__float2ull_rz(s.hi * up) + __float2ll_rn(lo * up);
+  return p > -63.f ? (unsigned long long)w : 0;
 }
 
 __device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
@@ -161,46 +161,67 @@ struct RowReader {
                  : logit_key(__ldg((const uint16_t*)row + i));
   }
 
-  // f(bits) for every entry of the part, in any order.
+  // f(words, n) for the part in any order: 16 bytes at a time, or one entry (n = 1, in the word's
+  // lower half for logits).
   template <typename F>
   __device__ __forceinline__ void raw(int first, int step, F f) const {
     constexpr int N = PROBS ? 4 : 8;
-    if (!P.vec) {
-      for (int i = begin + first; i < end; i += step)
-        f(PROBS ? __ldg((const uint32_t*)row + i) : (uint32_t)__ldg((const uint16_t*)row + i));
-      return;
-    }
-    const int vecs = (end - begin) / N;
-    const uint4* p = reinterpret_cast<const uint4*>((const char*)row + (size_t)begin * (PROBS ? 4 : 2));
-    auto one = [&](const uint4& v) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    int i0 = begin + first;
+    if (P.vec) {
+      const int vecs = (end - begin) / N;
+      const uint4* p = reinterpret_cast<const uint4*>((const char*)row + (size_t)begin * (PROBS ? 4 : 2));
+      constexpr int kAhead = 4;  // loads in flight
+      uint4 x[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (PROBS) {
-          f(w[j]);
-        } else {
-          f(w[j] & 0xffffu);
-          f(w[j] >> 16);
+      for (int k = 0; k < kAhead; ++k)
+        if (first + k * step < vecs) x[k] = __ldg(p + first + k * step);
+      for (int v = first; v < vecs; v += kAhead * step) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int at = v + k * step;
+          if (at >= vecs) break;
+          const uint32_t now[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          if (at + kAhead * step < vecs) x[k] = __ldg(p + at + kAhead * step);
+          f(now, N);
         }
       }
-    };
-    constexpr int kAhead = 4;  // loads in flight
-    uint4 x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (first + k * step < vecs) x[k] = __ldg(p + first + k * step);
-    for (int v = first; v < vecs; v += kAhead * step) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int at = v + k * step;
-        if (at >= vecs) break;
-        const uint4 now = x[k];
-        if (at + kAhead * step < vecs) x[k] = __ldg(p + at + kAhead * step);
-        one(now);
-      }
+      i0 += vecs * N;
     }
-    for (int i = begin + vecs * N + first; i < end; i += step)
-      f(PROBS ? __ldg((const uint32_t*)row + i) : (uint32_t)__ldg((const uint16_t*)row + i));
+    for (int i = i0; i < end; i += step) {
+      const uint32_t now[4] = {
+          PROBS ? __ldg((const uint32_t*)row + i) : (uint32_t)__ldg((const uint16_t*)row + i), 0, 0, 0};
+      f(now, 1);
+    }
+  }
+
+  // f(key) for every probability whose upper half this is.
+  template <typename F>
+  __device__ __forceinline__ void in_bin(uint32_t bin, int first, int step, F f) const {
+    int i0 = begin + first;
+    if (P.vec) {
+      const int vecs = (end - begin) / 4;
+      const uint4* p = reinterpret_cast<const uint4*>((const uint32_t*)row + begin);
+      constexpr int kAhead = 4;
+      for (int v = first; v < vecs; v += kAhead * step) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (v + k * step < vecs) x[k] = __ldg(p + v + k * step);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (v + k * step >= vecs) break;
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (w[j] >> 16 == bin) f(w[j]);
+        }
+      }
+      i0 += vecs * 4;
+    }
+    for (int i = i0; i < end; i += step) {
+      const uint32_t w = __ldg((const uint32_t*)row + i);
+      if (w >> 16 == bin) f(w);
+    }
   }
 
   // f(index) for every entry of the part with this (not zero) key, in any order.
@@ -750,11 +771,14 @@ struct QuickShared {
   float2 two_to[64];
   uint32_t row_count[kQRows];  // of a row of bins, then of those before it (rank 0's)
   unsigned long long row_sum[kQRows];
+  uint8_t filled[kQThreads];
+  uint16_t todo[kQRows];
+  int n_todo;
   uint32_t rank_first[kMostClusters];  // the first bin in order that a CTA has anything in
   uint32_t rank_zero[kMostClusters], rank_small[kMostClusters], rank_far[kMostClusters],
       rank_bad[kMostClusters];
   unsigned long long rank_small_sum[kMostClusters];
-  uint32_t zero, small, far, bad, first, eq[kQWarps], rank_eq[kMostClusters];
+  uint32_t zero, small, far, bad, first, eq[kQWarps];
   unsigned long long small_sum;
   uint16_t small_at[kQSmall];
   float2 per_unit;
@@ -779,21 +803,28 @@ __device__ __forceinline__ uint32_t quick_bits(int row, int lane) {
   const int i = row < 128 ? 4095 - (row * 32 + lane) : (row - 129) * 32 + lane;
   return (row < 128 ? 0u : 0x8000u) | (uint32_t)(0x4000 + i - 0x800);
 }
-// Its counter: the lower 12 bits of (bits + 0x800), the sign above them.
+// Its counter: the lower 12 bits and the sign above them. (Exponents of 2^-15 to 2^16 are those whose
+// upper bit differs from the three below it, so that the lower 12 bits and the sign say it all; the
+// fourth of them, upside down, is the value's order.)
 __device__ __forceinline__ int quick_slot(uint32_t bits) {
-  const uint32_t t = bits + 0x800u;
-  return (int)((t & 0xfffu) | (t >> 3 & 0x1000u));
+  return (int)((bits & 0xfffu) | (bits >> 3 & 0x1000u));
+}
+__device__ __forceinline__ bool quick_has(uint32_t bits) {
+  return ((bits ^ bits << 1) & 0x7000u) == 0x4000u;
 }
 
 template <bool PROBS, bool WRITE>
 __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const RowsParams P) {
   extern __shared__ __align__(16) unsigned char s_hist[];
   __shared__ QuickShared sh;
-  uint32_t* count = reinterpret_cast<uint32_t*>(s_hist);
-  uint32_t* low = count + kQBins;  // probabilities: sums of the lower halves
+  uint32_t* count = reinterpret_cast<uint32_t*>(s_hist);  // probabilities: then sums of the lower halves
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto meet = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
   const int row = blockIdx.x / C, req = row / P.J;
   const float T = P.temperature ? P.temperature[req] : 1.f;
   const bool greedy = !(T > 0.f);
@@ -816,39 +847,69 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     sh.first = 0xffffffffu;
     sh.small_sum = 0;
   }
-  cluster.sync();  // (every CTA has begun: its shared memory may be written from here on)
+  meet();  // (every CTA has begun: its shared memory may be written from here on)
   {
-    uint32_t zeros = 0, far = 0, bad = 0;
-    in.raw(tid, kQThreads, [&](uint32_t b) {
-      if (PROBS) {
-        if (b >> 29 == 1) {
-          const int o = 0x3fff - (int)(b >> 16);
-          atomicAdd(&count[o], 1u);
-          atomicAdd(&low[o], b & 0xffffu);
-          if (b > 0x3f800000u) bad = 1;
-        } else if (b - 1u < 0x1fffffffu) {
-          ++far;  // below 2^-63
-        } else if (b - 1u < 0x7f800000u) {
-          bad = 1;
-        }
+    uint32_t zeros = 0, far = 0, bad = 0, largest = 0;
+    char* at = reinterpret_cast<char*>(count);
+    auto odd_logit = [&](uint32_t b) {  // one without a counter
+      const uint32_t mag = b & 0x7fffu;
+      if (b == 0xff80u || mag > 0x7f80u) return;
+      if (mag == 0) {
+        ++zeros;
+      } else if (mag < 0x3800u) {  // below 2^-15
+        const uint32_t i = atomicAdd(&sh.small, 1u);
+        if (i < kQSmall) sh.small_at[i] = (uint16_t)b;
+      } else if (b & 0x8000u) {
+        ++far;  // -2^17 or less
       } else {
-        const uint32_t t = b + 0x800u;
-        if ((t & 0x7000u) == 0x4000u) {
-          atomicAdd(&count[(t & 0xfffu) | (t >> 3 & 0x1000u)], 1u);
-        } else if (b != 0xff80u) {
-          const uint32_t mag = b & 0x7fffu;
-          if (mag == 0) {
-            ++zeros;
-          } else if (mag < 0x3800u) {  // below 2^-15
-            const uint32_t i = atomicAdd(&sh.small, 1u);
-            if (i < kQSmall) sh.small_at[i] = (uint16_t)b;
-          } else if (mag <= 0x7f80u) {
-            if (b & 0x8000u) ++far;  // -2^17 or less
-            else bad = 1;
+        bad = 1;
+      }
+    };
+    in.raw(tid, kQThreads, [&](const uint32_t (&w)[4], int n) {
+      if (PROBS) {
+        bool odd = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j && n == 1) break;
+          if (w[j] >> 29 == 1) {
+            uint32_t* c = reinterpret_cast<uint32_t*>(at + (w[j] >> 14 & 0x7ffcu));
+            atomicAdd(c, 1u);
+            atomicAdd(c + kQBins, w[j] & 0xffffu);
+            largest = max(largest, w[j]);
+          } else {
+            odd |= w[j] != 0;
+          }
+        }
+        if (odd)
+          for (int j = 0; j < 4; ++j) {
+            if (j && n == 1) break;
+            if (w[j] - 1u < 0x1fffffffu) ++far;  // below 2^-63
+            else if (w[j] >> 29 != 1 && w[j] - 1u < 0x7f800000u) bad = 1;
+          }
+      } else if (n == 1) {
+        if (quick_has(w[0])) atomicAdd(&count[quick_slot(w[0])], 1u);
+        else odd_logit(w[0]);
+      } else {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t y = ((w[j] ^ w[j] << 1) & 0x70007000u) ^ 0x40004000u;
+          const bool lo = !(y & 0xffffu), hi = !(y >> 16);
+          if (lo) atomicAdd(reinterpret_cast<uint32_t*>(at + ((w[j] << 2 & 0x3ffcu) | (w[j] >> 1 & 0x4000u))), 1u);
+          if (hi) atomicAdd(reinterpret_cast<uint32_t*>(at + ((w[j] >> 14 & 0x3ffcu) | (w[j] >> 17 & 0x4000u))), 1u);
+          odd |= y;
+        }
+        if (odd) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // (most are -inf)
+            const uint32_t x = w[j] ^ 0xff80ff80u;
+            if (x & 0xffffu && !quick_has(w[j] & 0xffffu)) odd_logit(w[j] & 0xffffu);
+            if (x >> 16 && !quick_has(w[j] >> 16)) odd_logit(w[j] >> 16);
           }
         }
       }
     });
+    if (largest > 0x3f800000u) bad = 1;
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     far = __reduce_add_sync(0xffffffffu, far);
     bad = __reduce_or_sync(0xffffffffu, bad);
@@ -872,10 +933,11 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
               (v.w ? 8u : 0u) << (4 * i);
       if (PROBS && (v.x | v.y | v.z | v.w) > 0xffffu) sh.bad = 1;  // sums of 16 bits may have passed 32
     }
+    sh.filled[tid] = some != 0;
     if (some) {
-      const int at = tid * kPer;
-      if (PROBS) first = at + __ffs(some) - 1;
-      // positive counters ascend with the value; zero is place 4096, negative ones follow
+      // counters ascend with the magnitude; zero is place 4096, negative logits follow
+      const int at = PROBS ? tid * kPer : tid * kPer ^ 0x800;
+      if (PROBS) first = 8191 - (at + 31 - __clz(some));
       else if (at < 4096) first = 4095 - (at + 31 - __clz(some));
       else first = 1 + at + __ffs(some) - 1;
     }
@@ -892,7 +954,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     cluster.map_shared_rank(sh.rank_bad, lane)[rank] =
         sh.bad | (uint32_t)(sh.small > kQSmall ? 1 : 0);
   }
-  cluster.sync();
+  meet();
   uint32_t first = 0xffffffffu, zeros = 0, smalls = 0, far = 0, bad = 0;
   for (int c = 0; c < C; ++c) {
     first = min(first, sh.rank_first[c]);
@@ -919,42 +981,32 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     const unsigned long long hi = __umul64hi(w63, (unsigned long long)n << 44);
     return hi + ((w63 * ((unsigned long long)n << 44)) >> 63);
   };
-  // a bin's entries, and their sum
-  auto read_bin = [&](int r, uint32_t& n, unsigned long long& s, unsigned long long& w) {
-    n = 0;
-    s = w = 0;
-    if (PROBS) {
-      const int o = r * 32 + lane;
-      unsigned long long l = 0;
-      if (C == 1) {
-        n = count[o];
-        l = low[o];
-      } else {
-        for (int c = 0; c < C; ++c) {
-          n += *cluster.map_shared_rank(count + o, c);
-          l += *cluster.map_shared_rank(low + o, c);
-        }
-      }
-      if (n) {  // the significand's last place, in units of 2^-44
-        const uint32_t k = (uint32_t)(0x3fff - o);
-        const unsigned long long units =
-            (unsigned long long)n * ((0x80u | (k & 0x7fu)) << 16) + l;
-        const int by = (int)(k >> 7) - 150 + 44;
-        s = by >= 0 ? units << by : by < -62 ? 0 : ((units >> (-by - 1)) + 1) >> 1;
-        w = l;
-      }
+  // a bin's entries (and, of probabilities, the sum of their lower halves)
+  auto count_of = [&](int r, unsigned long long& lows) -> uint32_t {
+    uint32_t n = 0;
+    lows = 0;
+    if (!PROBS && r == 128) return lane == 0 ? zeros : 0;
+    const int at = PROBS ? 8191 - (r * 32 + lane) : quick_slot(quick_bits(r, lane));
+    if (C == 1) {
+      n = count[at];
+      if (PROBS) lows = count[at + kQBins];
     } else {
-      const uint32_t bits = quick_bits(r, lane);
-      if (r == 128) {
-        n = lane == 0 ? zeros : 0;
-      } else {
-        const int at = quick_slot(bits);
-        if (C == 1) n = count[at];
-        else
-          for (int c = 0; c < C; ++c) n += *cluster.map_shared_rank(count + at, c);
+      for (int c = 0; c < C; ++c) {
+        const uint32_t* from = cluster.map_shared_rank(count + at, c);
+        n += from[0];
+        if (PROBS) lows += from[kQBins];
       }
-      if (n) s = sum_of(n, w = weight(bits));
     }
+    return n;
+  };
+  // their sum; w: the weight of each (logits)
+  auto bin_sum = [&](int r, uint32_t n, unsigned long long lows, unsigned long long& w) {
+    if (!PROBS) return sum_of(n, w = weight(quick_bits(r, lane)));
+    if (n == 0) return 0ull;
+    const uint32_t k = (uint32_t)(0x3fff - (r * 32 + lane));
+    const unsigned long long units = (unsigned long long)n * ((0x80u | (k & 0x7fu)) << 16) + lows;
+    const int by = (int)(k >> 7) - 150 + 44;  // the significand's last place, in units of 2^-44
+    return by >= 0 ? units << by : by < -62 ? 0ull : ((units >> (-by - 1)) + 1) >> 1;
   };
 
   // ---- 2. counts and sums of the rows of bins, into rank 0 ----
@@ -969,44 +1021,76 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     __syncthreads();
     if (tid == 0) cluster.map_shared_rank(sh.rank_small_sum, 0)[rank] = sh.small_sum;
   }
-  constexpr int kRowsOf = PROBS ? 256 : 257, kTogether = 4;
-  for (int r0 = rank * kQWarps + warp; r0 < kRowsOf; r0 += kTogether * C * kQWarps) {
+  constexpr int kRowsOf = PROBS ? 256 : 257, kTogether = 2;
+  // A CTA alone has noted which of its rows are empty (its threads looked at one each).
+  auto filled = [&](int r) {
+    if (C > 1 || (!PROBS && r == 128)) return true;
+    return (bool)sh.filled[PROBS ? 255 - r : (r < 128 ? 127 - r : r - 1) ^ 64];
+  };
+  if (C == 1) {
+    if (warp == 0) {  // the others, one behind another
+      int n = 0;
+      for (int r0 = 0; r0 < kRowsOf; r0 += 32) {
+        const int r = r0 + lane;
+        const bool take = r < kRowsOf && filled(r);
+        const uint32_t m = __ballot_sync(0xffffffffu, take);
+        if (take) sh.todo[n + __popc(m & ((1u << lane) - 1))] = (uint16_t)r;
+        else if (r < kRowsOf) {
+          sh.row_count[r] = 0;
+          sh.row_sum[r] = 0;
+        }
+        n += __popc(m);
+      }
+      if (lane == 0) sh.n_todo = n;
+    }
+    __syncthreads();
+  }
+  const int rows_todo = C == 1 ? sh.n_todo : kRowsOf;
+  for (int i0 = rank * kQWarps + warp; i0 < rows_todo; i0 += kTogether * C * kQWarps) {
     uint32_t n[kTogether];
     unsigned long long s[kTogether], w;
+    int r[kTogether];
+    bool any = false;
 #pragma unroll
     for (int k = 0; k < kTogether; ++k) {
-      const int r = r0 + k * C * kQWarps;
+      const int i = i0 + k * C * kQWarps;
+      r[k] = i < rows_todo ? C == 1 ? sh.todo[i] : i : -1;
       n[k] = 0;
       s[k] = 0;
-      if (r < kRowsOf) read_bin(r, n[k], s[k], w);
+      if (r[k] >= 0) n[k] = count_of(r[k], s[k]);
+      any |= n[k] != 0;
+    }
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+      for (int k = 0; k < kTogether; ++k) s[k] = bin_sum(max(r[k], 0), n[k], s[k], w);
     }
 #pragma unroll
     for (int k = 0; k < kTogether; ++k) {
-      const int r = r0 + k * C * kQWarps;
-      if (r >= kRowsOf) break;
       const uint32_t all = __reduce_add_sync(0xffffffffu, n[k]);
       if (all) s[k] = warp_sum62(s[k]);
-      if (lane == 0) {
-        *cluster.map_shared_rank(&sh.row_count[r], 0) = all;
-        *cluster.map_shared_rank(&sh.row_sum[r], 0) = s[k];
+      if (lane == 0 && r[k] >= 0) {
+        QuickShared* s0 = C == 1 ? &sh : cluster.map_shared_rank(&sh, 0);
+        s0->row_count[r[k]] = all;
+        s0->row_sum[r[k]] = all ? s[k] : 0;
       }
     }
   }
-  cluster.sync();
+  meet();
 
   // ---- 3. the search: rank 0's first warp, the others serve it ----
   float* out = WRITE ? P.probs + (size_t)row * P.ld_out : nullptr;
+  const int worker = tid - (rank ? 0 : 32), workers = kQThreads - (rank ? 0 : 32);
   // Index of entry number op_number of those with op_key: up to kQList of them are listed and the
   // one with so many smaller ones is found; more are counted along the row.
   auto nth = [&]() {
     QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
     const uint32_t key = s0->op_key, j = s0->op_number;
     if (s0->op_count <= kQList) {
-      in.matches(key, tid, kQThreads, [&](int i) { s0->at[atomicAdd(&s0->listed, 1u)] = i; });
-      cluster.sync();
+      in.matches(key, worker, workers, [&](int i) { s0->at[atomicAdd(&s0->listed, 1u)] = i; });
+      meet();
       if (rank == 0) {
         const int m = (int)sh.listed;
-        for (int a = tid; a < m; a += kQThreads) {
+        for (int a = worker; a < m; a += workers) {
           const int mine = sh.at[a];
           uint32_t less = 0;
           for (int i = 0; i < m; ++i) less += sh.at[i] < mine;
@@ -1015,21 +1099,18 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       }
       return;
     }
-    const int len = in.end - in.begin, seg = ((len + kQWarps - 1) / kQWarps + 7) & ~7;
-    const int a = in.begin + min(len, warp * seg), b = in.begin + min(len, (warp + 1) * seg);
+    const int w0 = worker >> 5, len = in.end - in.begin;
+    const int seg = ((len + workers / 32 - 1) / (workers / 32) + 7) & ~7;
+    const int a = in.begin + min(len, w0 * seg), b = in.begin + min(len, (w0 + 1) * seg);
     uint32_t have = 0;
     in.each(a, b, lane, 32, [&](int, uint32_t x) { have += x == key; });
     have = __reduce_add_sync(0xffffffffu, have);
-    if (lane == 0) sh.eq[warp] = have;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-    for (int w = 0; w < kQWarps; ++w) {
-      if (w < warp) before += sh.eq[w];
-      all += sh.eq[w];
-    }
-    if (warp == 0 && lane < C) cluster.map_shared_rank(sh.rank_eq, lane)[rank] = all;
-    cluster.sync();
-    for (int c = 0; c < rank; ++c) before += sh.rank_eq[c];
+    if (lane == 0) sh.eq[w0] = have;
+    meet();
+    uint32_t before = 0;
+    for (int c = 0; c <= rank; ++c)
+      for (int w = 0; w < (c == rank ? w0 : c ? kQWarps : kQWarps - 1); ++w)
+        before += cluster.map_shared_rank(&sh, c)->eq[w];
     if (j >= before && j - before < have) {
       uint32_t left = j - before;
       for (int i = a; i < b;) {  // 256 entries at a time, then the 32 with the one in question
@@ -1057,24 +1138,22 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       }
     }
   };
-  auto collect = [&]() {  // the lower halves of a bin's entries
-    QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
-    const uint32_t bin = s0->op_key >> 16;
-    in.each(in.begin, in.end, tid, kQThreads, [&](int, uint32_t x) {
-      if (x >> 16 == bin) {
-        const uint32_t i = atomicAdd(&s0->listed, 1u);
-        if (i < kQList) s0->list[i] = (uint16_t)x;
-      }
-    });
-  };
   auto serve = [&]() {
     for (;;) {
-      cluster.sync();
-      const int op = cluster.map_shared_rank(&sh, 0)->op;
-      if (op == kOpNth) nth();
-      if (op == kOpCollect) collect();
-      if (op == kOpEnd || op == kOpMark || op == kOpNothing) break;
-      cluster.sync();
+      meet();
+      QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
+      const int op = s0->op;
+      if (op == kOpNth) {
+        nth();
+      } else if (op == kOpCollect) {  // the lower halves of a bin's entries
+        in.in_bin(s0->op_key >> 16, worker, workers, [&](uint32_t x) {
+          const uint32_t i = atomicAdd(&s0->listed, 1u);
+          if (i < kQList) s0->list[i] = (uint16_t)x;
+        });
+      } else {
+        break;
+      }
+      meet();
     }
   };
   if (rank == 0 && warp == 0) {
@@ -1125,10 +1204,9 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         sh.op_count = of;
         sh.listed = 0;
       }
-      cluster.sync();
-      if (op == kOpNth) nth();
-      if (op == kOpCollect) collect();
-      if (op == kOpNth || op == kOpCollect) cluster.sync();
+      meet();
+      if (op == kOpNth) meet();  // (nth's own)
+      if (op == kOpNth || op == kOpCollect) meet();
     };
     // A probability's place in its bin: by count (g), by sum (goal), or by key.
     auto inside = [&](Border b, int by, unsigned long long g, double goal, uint32_t key) -> Border {
@@ -1224,9 +1302,10 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         mark = true;
         return b;
       }
-      uint32_t n;
-      unsigned long long s, w;
-      read_bin(r, n, s, w);
+      unsigned long long lows, w = 0;
+      const uint32_t n = count_of(r, lows);
+      const unsigned long long s = bin_sum(r, n, lows, w);
+      if (PROBS) w = lows;
       const uint32_t an = sh.row_count[r] + warp_before(n);
       const unsigned long long as = sh.row_sum[r] + warp_before(s);
       const bool here = by == 0   ? g >= an && g < an + n
@@ -1381,7 +1460,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       in.write(out, P.vec_out, tid, kQThreads, value);
     }
   }
-  cluster.sync();  // no CTA leaves while another may read its shared memory
+  meet();  // no CTA leaves while another may read its shared memory
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
