@@ -761,11 +761,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
 // logits have 128 rows of positive values, one for zero, 128 of negative ones; probabilities 256.
 // ---------------------------------------------------------------------------------------------
 constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQBins = 8192, kQRows = 257;
+constexpr uint16_t kLeast = 0xc7ff;  // the least logit that has a counter, -130560
 constexpr int kQSmall = 256;    // logits below 2^-15 that a CTA may have
 constexpr int kQList = 2048;    // entries of one bin of probabilities
 constexpr double kQUnit = 17592186044416.0;  // sums of probabilities: multiples of 2^-44
 
-enum { kOpEnd, kOpNth, kOpCollect, kOpMark, kOpNothing };
+enum { kOpEnd, kOpNth, kOpCollect, kOpCount, kOpMark, kOpNothing };
 
 struct QuickShared {
   float2 two_to[64];
@@ -851,20 +852,18 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
   {
     uint32_t zeros = 0, far = 0, bad = 0, largest = 0;
     char* at = reinterpret_cast<char*>(count);
-    auto odd_logit = [&](uint32_t b) {  // one without a counter
-      const uint32_t mag = b & 0x7fffu;
-      if (b == 0xff80u || mag > 0x7f80u) return;
-      if (mag == 0) {
+    auto odd_logit = [&](uint32_t b) {  // one of magnitude below 2^-15
+      if ((b & 0x7fffu) == 0) {
         ++zeros;
-      } else if (mag < 0x3800u) {  // below 2^-15
+      } else {
         const uint32_t i = atomicAdd(&sh.small, 1u);
         if (i < kQSmall) sh.small_at[i] = (uint16_t)b;
-      } else if (b & 0x8000u) {
-        ++far;  // -2^17 or less
-      } else {
-        bad = 1;
       }
     };
+    // Logits of -2^17 and less, -inf and NaN become the least that has a counter, and are told apart
+    // only if it matters how many there are. One above 2^17 shows in the maximum.
+    __nv_bfloat162 most = __halves2bfloat162(__ushort_as_bfloat16(kLeast), __ushort_as_bfloat16(kLeast));
+    const __nv_bfloat162 least2 = most;
     in.raw(tid, kQThreads, [&](const uint32_t (&w)[4], int n) {
       if (PROBS) {
         bool odd = false;
@@ -886,30 +885,35 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
             if (w[j] - 1u < 0x1fffffffu) ++far;  // below 2^-63
             else if (w[j] >> 29 != 1 && w[j] - 1u < 0x7f800000u) bad = 1;
           }
-      } else if (n == 1) {
-        if (quick_has(w[0])) atomicAdd(&count[quick_slot(w[0])], 1u);
-        else odd_logit(w[0]);
       } else {
-        uint32_t odd = 0;
+        uint32_t v[4], odd = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t y = ((w[j] ^ w[j] << 1) & 0x70007000u) ^ 0x40004000u;
-          const bool lo = !(y & 0xffffu), hi = !(y >> 16);
-          if (lo) atomicAdd(reinterpret_cast<uint32_t*>(at + ((w[j] << 2 & 0x3ffcu) | (w[j] >> 1 & 0x4000u))), 1u);
-          if (hi) atomicAdd(reinterpret_cast<uint32_t*>(at + ((w[j] >> 14 & 0x3ffcu) | (w[j] >> 17 & 0x4000u))), 1u);
-          odd |= y;
+          const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), least2);
+          most = __hmax2(most, x);
+          v[j] = *reinterpret_cast<const uint32_t*>(&x);
+          odd |= ((v[j] ^ v[j] << 1) & 0x70007000u) ^ 0x40004000u;
         }
-        if (odd) {
+        if (n == 1) {  // (its word's upper half is no entry)
+          if (quick_has(v[0] & 0xffffu)) atomicAdd(&count[quick_slot(v[0] & 0xffffu)], 1u);
+          else odd_logit(v[0] & 0xffffu);
+        } else if (!odd) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // (most are -inf)
-            const uint32_t x = w[j] ^ 0xff80ff80u;
-            if (x & 0xffffu && !quick_has(w[j] & 0xffffu)) odd_logit(w[j] & 0xffffu);
-            if (x >> 16 && !quick_has(w[j] >> 16)) odd_logit(w[j] >> 16);
+          for (int j = 0; j < 4; ++j) {
+            atomicAdd(reinterpret_cast<uint32_t*>(at + ((v[j] << 2 & 0x3ffcu) | (v[j] >> 1 & 0x4000u))), 1u);
+            atomicAdd(reinterpret_cast<uint32_t*>(at + ((v[j] >> 14 & 0x3ffcu) | (v[j] >> 17 & 0x4000u))), 1u);
+          }
+        } else {
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t b = j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu;
+            if (quick_has(b)) atomicAdd(&count[quick_slot(b)], 1u);
+            else if ((b & 0x7fffu) < 0x3800u) odd_logit(b);
           }
         }
       }
     });
     if (largest > 0x3f800000u) bad = 1;
+    if (!PROBS && (__low2float(most) >= 131072.f || __high2float(most) >= 131072.f)) bad = 1;
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     far = __reduce_add_sync(0xffffffffu, far);
     bad = __reduce_or_sync(0xffffffffu, bad);
@@ -918,6 +922,11 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       if (far) atomicAdd(&sh.far, far);
       if (bad) sh.bad = 1;
     }
+  }
+  __syncthreads();
+  if (!PROBS && tid == 0) {
+    sh.far = count[quick_slot(kLeast)];
+    count[quick_slot(kLeast)] = 0;
   }
   __syncthreads();
   // the first bin in order that is not empty
@@ -1150,6 +1159,12 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
           const uint32_t i = atomicAdd(&s0->listed, 1u);
           if (i < kQList) s0->list[i] = (uint16_t)x;
         });
+      } else if (op == kOpCount) {  // the logits without a counter below that are numbers
+        uint32_t n = 0;
+        in.each(in.begin, in.end, worker, workers,
+                [&](int, uint32_t x) { n += x && x <= logit_key(kLeast); });
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0 && n) atomicAdd(&s0->listed, n);
       } else {
         break;
       }
@@ -1193,7 +1208,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     // far entries have to weigh nothing beside the others
     bool mark = bad;
     if (PROBS) mark |= total > 0 && total_sum < (unsigned long long)(kQUnit / 2);
-    else if (far) mark |= !some || !((-131072.f - top_value) * per_unit.x < -64.f);
+    else if (far) mark |= !some || !((-130560.f - top_value) * per_unit.x < -64.f);
     if (!PROBS && some && first == 4096 && smalls) mark = true;
 
     auto ask = [&](int op, uint32_t key, uint32_t number, uint32_t of) {
@@ -1206,7 +1221,15 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       }
       meet();
       if (op == kOpNth) meet();  // (nth's own)
-      if (op == kOpNth || op == kOpCollect) meet();
+      if (op == kOpNth || op == kOpCollect || op == kOpCount) meet();
+    };
+    // The whole number at or below d / w, d >= 0 (a quotient of fp32, put right).
+    auto quotient = [](double d, double w) -> double {
+      double q = (double)floorf(__fdividef((float)d, (float)w));
+      const double r = fma(-q, w, d);
+      if (r < 0.0) q -= 1.0;
+      else if (r >= w) q += 1.0;
+      return q;
     };
     // A probability's place in its bin: by count (g), by sum (goal), or by key.
     auto inside = [&](Border b, int by, unsigned long long g, double goal, uint32_t key) -> Border {
@@ -1339,14 +1362,15 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       uint32_t k = 0x7fffffffu;
       if (P.top_k && P.top_k[req] > 0) k = (uint32_t)P.top_k[req];
       if (greedy) k = 1;
-      if (k < keep) cut_at(k, find(0, k - 1, 0.0, 0));
+      if (k < keep && k <= binned) cut_at(k, find(0, k - 1, 0.0, 0));
       const float top_p = P.top_p && !greedy ? P.top_p[req] : 1.f;
       if (!mark && top_p < 1.f && keep > 1) {
         // the last entry before which less than top_p of the sum lies
         const double goal = (double)fmaxf(top_p, 0.f) * kept_sum;
         const double g = fmin(fmax(ceil(goal) - 1.0, 0.0), fmax(ceil(kept_sum) - 1.0, 0.0));
         const Border b = find(1, min((unsigned long long)g, total_sum - 1), g, 0);
-        const double j = ceil((goal - b.sum) / b.w);
+        double j = quotient(fmax(goal - b.sum, 0.0), b.w);
+        if (fma(-j, b.w, goal - b.sum) > 0.0) j += 1.0;
         const uint32_t m = b.above + (j >= (double)b.count ? b.count : j >= 1.0 ? (uint32_t)j : 1u);
         if (m < keep) cut_at(m, b);
       }
@@ -1370,11 +1394,18 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         } else if (min_p >= 1.f) {
           m = find(0, 0, 0.0, 0).count;
         } else {
-          const double t =
-              (double)top_value + fmin(fmax((double)T, 0x1p-100), 0x1p100) * log((double)min_p);
-          const uint32_t o = orderable(__double2float_ru(t));
-          // the smallest logit that stays, as bits
-          const uint32_t key = min(o & 0x80000000u ? (o + 0xffffu) >> 16 : o >> 16, logit_key(top_bits));
+          // the least logit that stays: near an estimate in fp32, 32 of them are weighed
+          const float unit = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
+          const uint32_t topk = logit_key(top_bits);
+          const uint32_t near = orderable(fmaf(unit, __logf(min_p), top_value)) >> 16;
+          const uint32_t mine = min(max((int)near - 16 + lane, 1), (int)topk);
+          const unsigned long long least_w = __float2ull_rn(min_p * 0x1p63f);
+          const uint32_t mine_bits = mine & 0x8000u ? mine & 0x7fffu : ~mine & 0xffffu;
+          const uint32_t stays = __ballot_sync(0xffffffffu, weight(mine_bits) >= least_w);
+          // (the weights ascend with the lane; the estimate is good to a few values, or all is marked)
+          const int at0 = stays ? __ffs(stays) - 1 : 32;
+          const uint32_t key = __shfl_sync(0xffffffffu, mine, at0 & 31);
+          if ((at0 == 0 && near > 16) || (at0 == 32 && near + 16 < topk)) mark = true;
           const uint32_t bits = key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu;
           const uint32_t mag = bits & 0x7fffu;
           if (mag >= 0x4800u) {  // beyond the bins: -2^17 or less (a larger one is not below the top)
@@ -1392,6 +1423,13 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         m = max(m, 1u);
         if (!mark && m < keep) cut_at(m, find(0, m - 1, 0.0, 0));
       }
+      if (!mark && !cut && far) {  // all that is a number is kept, or as many as top_k
+        if (!PROBS) {
+          ask(kOpCount, 0, 0, 0);
+          keep = binned + sh.listed;
+        }
+        if (k < keep) mark = true;
+      }
       if (!mark && !WRITE) {
         float u = P.u[row];
         u = u > 0.f ? u : 0.f;
@@ -1403,7 +1441,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
           const double goal = fmin((double)u * kept_sum, kept_sum);
           const double g = fmin(floor(goal), fmax(ceil((double)total_sum) - 1.0, 0.0));
           b = find(1, min((unsigned long long)g, total_sum - 1), goal, 0);
-          const double f = floor((goal - b.sum) / b.w);
+          const double f = quotient(fmax(goal - b.sum, 0.0), b.w);
           j = f >= (double)(b.count - 1) ? b.count - 1 : f > 0.0 ? (uint32_t)f : 0u;
           if (!mark && b.above + j >= keep) {
             b = cut ? last : find(0, keep - 1, 0.0, 0);
@@ -1413,7 +1451,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         if (!mark) {
           ask(kOpNth, b.key, j, b.count);
           at = sh.index;
-          prob = (float)(b.w / kept_sum);
+          prob = __fdiv_rn((float)b.w, (float)kept_sum);
         }
       }
       if (!mark && WRITE && cut && keep - last.above < last.count) {
@@ -1424,7 +1462,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     if (lane == 0) {
       sh.edge = edge;
       sh.least = cut ? last.key : 1u;
-      sh.inv = (float)((PROBS ? kQUnit : kSumUnit) / kept_sum);
+      sh.inv = __fdiv_rn((float)(PROBS ? kQUnit : kSumUnit), (float)kept_sum);
       if (!mark) {
         if (total == 0) raise_err(P.err, SD_ERR_ZERO_ROW);
         if (P.kept) P.kept[row] = (int32_t)keep;
