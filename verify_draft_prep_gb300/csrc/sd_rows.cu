@@ -1231,6 +1231,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       else if (r >= w) q += 1.0;
       return q;
     };
+    uint32_t listed_bin = 0;
     // A probability's place in its bin: by count (g), by sum (goal), or by key.
     auto inside = [&](Border b, int by, unsigned long long g, double goal, uint32_t key) -> Border {
       const int e = (int)(b.key >> 23);
@@ -1240,7 +1241,9 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         b.w = (double)(0x800000u | (b.key & 0x7fffffu)) * unit;
         return b;
       }
-      ask(kOpCollect, b.key, 0, b.count);
+      // (the last bin's entries are still listed, if it was this one)
+      if (b.key != listed_bin) ask(kOpCollect, b.key, 0, b.count);
+      listed_bin = b.key;
       const uint32_t m = sh.listed;
       if (m > kQList) {
         mark = true;
@@ -1532,8 +1535,11 @@ static int launch_rows(RowsParams& P, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
 
-  // CTAs of a row: more while the SMs have room for them, and a CTA some thousands of entries.
-  int C = 1;
+  // CTAs of a row: more while the SMs have room for them, and a CTA some thousands of entries. Long
+  // rows of probabilities are read again for every place that is looked for: with four CTAs a row
+  // those on the SMs at a time stay within L2. With 1, 2, 4 CTAs 384 rows of 201088 probabilities cut
+  // take 556, 546, 488 us, 2048 of logits 956, 970, 1048, one token of each of 1024 rows 330, 342, 379.
+  int C = PROBS && P.V > 65536 ? 4 : 1;
   while (C < kMostClusters && P.n_rows * 2L * C <= 4L * n_sm && P.V > 4096 * C) C *= 2;
   P.part = parts(C);
   attr[0].val.clusterDim.x = (unsigned)C;
