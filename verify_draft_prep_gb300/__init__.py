@@ -766,7 +766,7 @@ def sd_kv_weights(q, lse, k_cache, k_scale, block_table, ctx_lens, cu_q, weights
     q, block_table, ctx_lens, cu_q, max_q, sm_scale, causal: as for sd_kv_attend, and lse its [n, Hq]
     float32; live: [B] int32, how many of each request's query tokens count, or None for all; weights:
     [num_blocks, Hkv, block_size] float32; before: the same, what tokens had so far (it may be weights
-    itself), or None.
+    itself), or None; max_q: None for n / B, rounded up.
     """
     # (K alone is read: its checks serve for both)
     cache = _cache_args(k_cache, k_cache, k_scale, k_scale)
@@ -784,7 +784,9 @@ def sd_kv_weights(q, lse, k_cache, k_scale, block_table, ctx_lens, cu_q, weights
     _float32(weights, (nb, Hkv, bs), "weights")
     if before is not None:
         _float32(before, (nb, Hkv, bs), "before")
-    rc = _quick().sd_kv_weights(B, n, max(1, n) if max_q is None else max_q, Hq, Hkv, D, _ptr(q),
+    if max_q is None:
+        max_q = max(1, -(-n // max(1, B)))
+    rc = _quick().sd_kv_weights(B, n, max_q, Hq, Hkv, D, _ptr(q),
                                 *_head_rows(q, Hq, D, "q"), _ptr(lse), cache[0], *cache[2:6], nb, bs,
                                 _ptr(block_table), mb, _ptr(ctx_lens), _ptr(cu_q), _ptr(live),
                                 D ** -0.5 if sm_scale is None else sm_scale, int(bool(causal)), decay,

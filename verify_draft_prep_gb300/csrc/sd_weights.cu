@@ -25,13 +25,14 @@
 namespace sdk {
 
 constexpr int kWTile = 128, kWPair = 2 * kWTile, kWRows = 128;
-constexpr int kWThreads = 544;      // 8 warps sum, 8 load, 1 issues
+constexpr int kWThreads = 576;      // 8 warps sum, 8 load, one issues, one fetches ahead
 constexpr int kWLoaders = 256;
+constexpr int kWAhead = 5;  // units that are fetched ahead into L2
 constexpr float kWLog2e = 1.4426950408889634f;
 
 struct WeightsParams {
   KvCache c;
-  int B, n, Hq, G, max_blocks, causal, spread;
+  int B, n, Hq, G, max_blocks, causal;
   unsigned long long g_magic;  // ceil(2^64 / G); 0 for G = 1
   const uint16_t* q;
   long ld_q, hs_q;
@@ -47,19 +48,22 @@ struct WeightsParams {
   int32_t* err;
 };
 
-template <int DP>
+// Long: requests of many chunks (prompts), whose Q streams by while K stays.
+template <int DP, bool LONG>
 struct WLayout {
   static constexpr int kTileBytes = kWTile * DP * 2;  // K of a tile, or Q of a chunk, as bf16
-  static constexpr int kK = 0;                        // two pairs of tiles
-  static constexpr int kQ = kK + 4 * kTileBytes;      // two chunks
-  static constexpr int kMisc = kQ + 2 * kTileBytes;
+  static constexpr int kNK = LONG ? 1 : 2;            // pairs of tiles
+  static constexpr int kNQ = LONG ? 4 : 2;            // chunks
+  static constexpr int kK = 0;
+  static constexpr int kQ = kK + 2 * kNK * kTileBytes;
+  static constexpr int kMisc = kQ + kNQ * kTileBytes;
 };
 
 struct WMisc {
-  uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2];
+  uint64_t k_full[2], k_empty[2], q_full[4], q_empty[4];
   uint64_t s_full[2][2], s_empty[2][2];  // [tile of the pair][buffer]
-  float lse2[2][kWRows];                 // of the rows of a chunk of Q
-  int lim[2][kWRows];                    // tokens that they see
+  float lse2[4][kWRows];                 // of the rows of a chunk of Q
+  int lim[4][kWRows];                    // tokens that they see
   float k_scale[2][kWPair];              // of a pair's tokens, times sm_scale log2(e)
   float before[2][kWPair];               // what they have so far
   long at[2][kWPair];                    // where their number lies; -1: nowhere
@@ -68,10 +72,11 @@ struct WMisc {
   long long start_in;
   uint32_t tmem;
   int gave_up;
+  int loaded;  // units that are on their way to shared memory
 };
 
 struct WRequest {
-  int tok0, n_q, rows, len, off;  // rows: those that count
+  int tok0, rows, len, off;  // rows: those that count
 };
 
 __device__ __forceinline__ int w_token(const WeightsParams& P, int row) {
@@ -84,11 +89,11 @@ __device__ __forceinline__ WRequest w_request(const WeightsParams& P, int r) {
   WRequest q;
   const int a = P.cu[r], b = P.cu[r + 1], ctx = P.ctx[r];
   const int lo = min(max(a, 0), P.n), hi = min(max(b, lo), P.n);
+  const int n_q = hi - lo;
   q.tok0 = lo;
-  q.n_q = hi - lo;
-  q.rows = (P.live ? min(max(P.live[r], 0), q.n_q) : q.n_q) * P.G;
+  q.rows = (P.live ? min(max(P.live[r], 0), n_q) : n_q) * P.G;
   q.len = ctx < 0 ? 0 : (int)min((long)ctx, w_covered(P));
-  q.off = (int)max((long)ctx - q.n_q, -2147483647L);
+  q.off = (int)max((long)ctx - n_q, -2147483647L);
   return q;
 }
 __device__ __forceinline__ bool w_bad(const WeightsParams& P, int r) {
@@ -115,57 +120,67 @@ __device__ __forceinline__ bool w_stays(const WUnit& a, const WUnit& b, bool the
 // outermost and every CTA takes each 152nd of the line, forwards and backwards in turn, so that a
 // prompt's units, which get cheaper along the context, even out; else heads outermost and every CTA
 // takes a stretch, so that it stays with a request's Q.
+template <bool SPREAD>
 struct WSchedule {
   long long at, end;  // place on the line
-  int r, h, pair, pairs, round;
+  int pairs, round;
 
-  __device__ __forceinline__ int pairs_of(const WeightsParams& P, int rr) const {
-    return (w_request(P, rr).len + kWPair - 1) / kWPair;
-  }
-  // Settles `in` places behind the first unit of request r.
-  __device__ __forceinline__ void seek(const WeightsParams& P, long long in) {
-    for (;;) {
-      pairs = pairs_of(P, r);
-      const long long units = (long long)pairs * P.c.Hkv;
-      if (in < units) break;
-      in -= units;
-      ++r;
-    }
-    const int by = P.spread ? P.c.Hkv : pairs;
-    const int o = (int)(in / by), i = (int)(in - (long long)o * by);
-    pair = P.spread ? o : i;
-    h = P.spread ? i : o;
-  }
-  __device__ __forceinline__ WUnit unit(const WeightsParams& P) const {
-    WUnit u;
-    u.q = w_request(P, r);
-    u.r = r;
+  __device__ __forceinline__ void place(const WeightsParams& P, WUnit& u, int h, int pair) const {
     u.h = h;
     u.pair = pair;
-    u.chunks = (u.q.rows + kWRows - 1) / kWRows;
     u.first = 0;
     if (P.causal && u.chunks > 2)
       u.first = (int)min((long)u.chunks, max(0L, (long)pair * kWPair - u.q.off) * P.G / kWRows);
+  }
+  __device__ __forceinline__ void request(const WeightsParams& P, WUnit& u, int r) {
+    u.r = r;
+    u.q = w_request(P, r);
+    u.chunks = (u.q.rows + kWRows - 1) / kWRows;
+    pairs = (u.q.len + kWPair - 1) / kWPair;
+  }
+  // `in` places behind the first unit of u's request.
+  __device__ __forceinline__ void seek(const WeightsParams& P, WUnit& u, long long in) {
+    for (;;) {
+      const long long units = (long long)pairs * P.c.Hkv;
+      if (in < units) break;
+      in -= units;
+      request(P, u, u.r + 1);
+    }
+    const int by = SPREAD ? P.c.Hkv : pairs;
+    const int o = (int)(in / by), i = (int)(in - (long long)o * by);
+    place(P, u, SPREAD ? i : o, SPREAD ? o : i);
+  }
+  __device__ __forceinline__ WUnit begin(const WeightsParams& P, long long from, long long to, int r,
+                                         long long in) {
+    at = from;
+    end = to;
+    round = pairs = 0;
+    WUnit u = {};
+    if (from < to) {
+      request(P, u, r);
+      seek(P, u, in);
+    }
     return u;
   }
   // On to the next unit; false: there is none.
-  __device__ __forceinline__ bool next(const WeightsParams& P) {
-    if (P.spread) {
+  __device__ __forceinline__ bool next(const WeightsParams& P, WUnit& u) {
+    if (SPREAD) {
       const int n = gridDim.x, b = blockIdx.x;
       const int by = round++ & 1 ? 2 * b + 1 : 2 * (n - 1 - b) + 1;
       at += by;
       if (at >= end) return false;
-      seek(P, (long long)pair * P.c.Hkv + h + by);
+      seek(P, u, (long long)u.pair * P.c.Hkv + u.h + by);
       return true;
     }
     if (++at >= end) return false;
-    if (++pair == pairs) {
-      pair = 0;
-      if (++h == P.c.Hkv) {
-        h = 0;
-        ++r;
-        while ((pairs = pairs_of(P, r)) == 0) ++r;
-      }
+    if (u.pair + 1 < pairs) {
+      place(P, u, u.h, u.pair + 1);
+    } else if (u.h + 1 < P.c.Hkv) {
+      place(P, u, u.h + 1, 0);
+    } else {
+      do request(P, u, u.r + 1);
+      while (pairs == 0);
+      place(P, u, 0, 0);
     }
     return true;
   }
@@ -209,9 +224,15 @@ __device__ __forceinline__ float2 w_add2(float2 a, float2 b) {
   return d;
 }
 
-template <int DP>
+__device__ __forceinline__ void w_copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+template <int DP, bool LONG>
 __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsParams P) {
-  using L = WLayout<DP>;
+  using L = WLayout<DP, LONG>;
   extern __shared__ unsigned char s_raw[];
   unsigned char* smem = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
   WMisc& m = *reinterpret_cast<WMisc*>(smem + L::kMisc);
@@ -221,17 +242,17 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
   volatile int* gave_up = &m.gave_up;
   const int bs = 1 << c.log2_bs;
 
-  if (tid < 2) {
-    mbar_init(smem_u32(&m.k_full[tid]), 8);
-    mbar_init(smem_u32(&m.k_empty[tid]), 9);
+  if (tid < 4) {
     mbar_init(smem_u32(&m.q_full[tid]), 8);
     mbar_init(smem_u32(&m.q_empty[tid]), 9);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&m.s_full[tid][b]), 1);
-      mbar_init(smem_u32(&m.s_empty[tid][b]), 4);
+    mbar_init(smem_u32(&m.s_full[tid >> 1][tid & 1]), 1);
+    mbar_init(smem_u32(&m.s_empty[tid >> 1][tid & 1]), 4);
+    if (tid < 2) {
+      mbar_init(smem_u32(&m.k_full[tid]), 8);
+      mbar_init(smem_u32(&m.k_empty[tid]), 9);
     }
     m.gave_up = 0;
+    m.loaded = 0;
     m.start_r = P.B;
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -264,8 +285,8 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     total += m.warp_sum[w];
   }
   const long long share = (total + gridDim.x - 1) / gridDim.x;
-  const long long g0 = P.spread ? blockIdx.x : min(total, share * blockIdx.x);
-  const long long g1 = P.spread ? total : min(total, g0 + share);
+  const long long g0 = LONG ? blockIdx.x : min(total, share * blockIdx.x);
+  const long long g1 = LONG ? total : min(total, g0 + share);
   if (g0 < g1 && before <= g0 && g0 < before + mine) {
     long long in = g0 - before;
     int r = r0;
@@ -281,17 +302,9 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = m.tmem;
-  WSchedule line;
-  line.r = m.start_r;
-  line.at = g0;
-  line.end = g1;
-  line.round = line.h = line.pair = line.pairs = 0;
+  WSchedule<LONG> line;
+  WUnit s = line.begin(P, g0, g1, m.start_r, m.start_in);
   bool some = g0 < g1;
-  WUnit s = {};
-  if (some) {
-    line.seek(P, m.start_in);
-    s = line.unit(P);
-  }
 
   if (warp >= 8 && warp < 16) {
     // ---- loads ----
@@ -303,6 +316,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     float ks = 0.f, was = 0.f;
     long where = -1;
     int page_next = -1;
+    volatile int* loaded = &m.loaded;
     auto page_of = [&](const WUnit& u) {
       const int tok = u.pair * kWPair + t;
       return tok < u.q.len ? __ldg(P.table + (long)u.r * P.max_blocks + (tok >> c.log2_bs)) : -2;
@@ -334,14 +348,14 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     bool more = some;
     if (more) {
       fetch(s, page_of(s));
-      more = line.next(P);
-      if (more) page_next = page_of(ahead = line.unit(P));
+      more = line.next(P, ahead);
+      if (more) page_next = page_of(ahead);
     }
     int unit = 0, loads = 0;
     bool ok = true, have_q = false;
     while (some && ok) {
-      const int kb = unit & 1;
-      ok = mbar_wait_warp(smem_u32(&m.k_empty[kb]), ((unit >> 1) & 1) ^ 1, gave_up);
+      const int kb = unit % L::kNK;
+      ok = mbar_wait_warp(smem_u32(&m.k_empty[kb]), ((unit / L::kNK) & 1) ^ 1, gave_up);
       if (!ok) break;
       // K of this unit, which is in registers
 #pragma unroll
@@ -367,11 +381,67 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
       const bool next_there = more;
       if (more) {
         fetch(ahead, page_next);
-        more = line.next(P);
-        if (more) page_next = page_of(ahead = line.unit(P));
+        more = line.next(P, ahead);
+        if (more) page_next = page_of(ahead);
       }
+      if (t == 0) *loaded = unit + 1;
       // Q, chunk by chunk
-      if (!have_q) {
+      if (LONG) {
+        // by asynchronous copies, two chunks on their way behind the one that is waited for
+        constexpr int kLanes = DP / 8, kRowsPass = kWLoaders / kLanes;
+        const int d8 = t % kLanes;
+        auto of_row = [&](int ch, float& l2, int& lim) {
+          l2 = INFINITY;
+          lim = 0;
+          const int row = ch * kWRows + t;
+          if (t < kWRows && row < s.q.rows && ch < s.chunks) {
+            const int tk = w_token(P, row);
+            l2 = __ldg(P.lse + (long)(s.q.tok0 + tk) * P.Hq + s.h * P.G + row - tk * P.G) * kWLog2e;
+            lim = w_sees(P, s.q, row);
+          }
+        };
+        auto there = [&](int load) {
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&m.q_full[load % L::kNQ]));
+        };
+        float l2;
+        int lim;
+        of_row(s.first, l2, lim);
+        for (int ch = s.first; ok && ch < s.chunks; ++ch, ++loads) {
+          const int qb = loads % L::kNQ;
+          ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((loads / L::kNQ) & 1) ^ 1, gave_up);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) {
+            const int at = i * kRowsPass + t / kLanes, row = ch * kWRows + at;
+            const bool is = row < s.q.rows && d8 * 8 < c.D;
+            const int tk = is ? w_token(P, row) : 0;
+            const uint16_t* from = is ? P.q + (long)(s.q.tok0 + tk) * P.ld_q +
+                                            (long)(s.h * P.G + row - tk * P.G) * P.hs_q + d8 * 8
+                                      : P.q;
+            w_copy16(base + L::kQ + qb * L::kTileBytes + (d8 >> 3) * (kWRows * 128) + at * 128 +
+                         (((d8 & 7) ^ (at & 7)) << 4),
+                     from, is);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (t < kWRows) {
+            m.lse2[qb][t] = l2;
+            m.lim[qb][t] = lim;
+          }
+          of_row(ch + 1, l2, lim);
+          if (ch - s.first >= 2) {
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+            there(loads - 2);
+          }
+        }
+        if (ok && s.chunks - s.first >= 2) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          there(loads - 2);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok && s.chunks > s.first) there(loads - 1);
+      } else if (!have_q) {
         for (int ch = s.first; ok && ch < s.chunks; ++ch, ++loads) {
           const int qb = loads & 1;
           const int row0 = ch * kWRows;
@@ -421,7 +491,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
           if (lane == 0) mbar_arrive(smem_u32(&m.q_full[qb]));
         }
       }
-      have_q = w_stays(s, after, next_there);
+      have_q = !LONG && w_stays(s, after, next_there);
       s = after;
       some = next_there;
       ++unit;
@@ -434,15 +504,15 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     int unit = 0, loads = 0, jobs[2] = {0, 0};
     bool ok = true;
     while (some && ok) {
-      const int kb = unit & 1;
-      const bool there = line.next(P);
-      const WUnit after = there ? line.unit(P) : s;
-      const bool keep = w_stays(s, after, there);
-      ok = mbar_wait_warp(smem_u32(&m.k_full[kb]), (unit >> 1) & 1, gave_up);
+      const int kb = unit % L::kNK;
+      WUnit after = s;
+      const bool there = line.next(P, after);
+      const bool keep = !LONG && w_stays(s, after, there);
+      ok = mbar_wait_warp(smem_u32(&m.k_full[kb]), (unit / L::kNK) & 1, gave_up);
       const bool two = (long)s.pair * kWPair + kWTile < s.q.len;
       for (int ch = s.first; ok && ch < s.chunks; ++ch) {
-        const int load = loads + ch - s.first, qb = load & 1;
-        ok = mbar_wait_warp(smem_u32(&m.q_full[qb]), (load >> 1) & 1, gave_up);
+        const int load = loads + ch - s.first, qb = load % L::kNQ;
+        ok = mbar_wait_warp(smem_u32(&m.q_full[qb]), (load / L::kNQ) & 1, gave_up);
         const int cols = min(kWRows, (s.q.rows - ch * kWRows + 31) & ~31);
         const uint32_t idesc = mma_desc_bf16(cols);
 #pragma unroll
@@ -475,6 +545,33 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
       __syncwarp();
     }
     __syncwarp();
+  } else if (warp == 17) {
+    // ---- K of the units to come into L2: a unit's registers alone do not keep memory busy ----
+    if (!LONG) {
+      volatile int* loaded = &m.loaded;
+      const long long t0 = clock64();
+      for (int unit = 0; some; ++unit) {
+        int page[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = s.pair * kWPair + i * 32 + lane;
+          page[i] = tok < s.q.len ? __ldg(P.table + (long)s.r * P.max_blocks + (tok >> c.log2_bs)) : -1;
+        }
+        while (unit - *loaded > kWAhead && !*gave_up && clock64() - t0 < kWaitClocks) __nanosleep(100);
+        if (*gave_up || clock64() - t0 >= kWaitClocks) break;
+        if (unit > *loaded) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if ((unsigned)page[i] >= (unsigned)c.num_blocks) continue;
+            const int tok = s.pair * kWPair + i * 32 + lane;
+            const uint8_t* at = c.k + page[i] * c.st_block + (tok & (bs - 1)) * c.st_tok + s.h * c.st_head;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+          }
+        }
+        __syncwarp();
+        some = line.next(P, s);
+      }
+    }
   } else {
     // ---- sums: group x has tile x of the pair, a token a lane ----
     const int x = warp >> 2, wt = tid & (kWTile - 1);
@@ -482,19 +579,19 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     int unit = 0, loads = 0, jobs = 0;
     bool ok = true;
     while (some && ok) {
-      const int kb = unit & 1;
-      const bool there = line.next(P);
-      const WUnit after = there ? line.unit(P) : s;
-      const bool keep = w_stays(s, after, there);
-      ok = mbar_wait_warp(smem_u32(&m.k_full[kb]), (unit >> 1) & 1, gave_up);
+      const int kb = unit % L::kNK;
+      WUnit after = s;
+      const bool there = line.next(P, after);
+      const bool keep = !LONG && w_stays(s, after, there);
+      ok = mbar_wait_warp(smem_u32(&m.k_full[kb]), (unit / L::kNK) & 1, gave_up);
       const int t0 = s.pair * kWPair + x * kWTile, tok = t0 + wt;
       const bool mine_any = t0 < s.q.len;
       const float f = m.k_scale[kb][x * kWTile + wt];
       const float2 f2 = make_float2(f, f);
       float sum = 0.f, rest = 0.f;  // (compensated from chunk to chunk)
       for (int ch = s.first; ok && ch < s.chunks; ++ch) {
-        const int load = loads + ch - s.first, qb = load & 1;
-        ok = mbar_wait_warp(smem_u32(&m.q_full[qb]), (load >> 1) & 1, gave_up);
+        const int load = loads + ch - s.first, qb = load % L::kNQ;
+        ok = mbar_wait_warp(smem_u32(&m.q_full[qb]), (load / L::kNQ) & 1, gave_up);
         if (!ok) break;
         if (mine_any) {
           const int sb = jobs & 1;
@@ -507,10 +604,8 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
           const bool masked = m.lim[qb][0] < t0 + kWTile;
           const uint32_t tC = tS + sb * kWRows;
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          for (int c0 = 0; c0 < cols; c0 += 32) {
-            uint32_t v[32];
-            tmem_ld32(tC + c0, v);
-            tmem_wait_ld();
+          // 32 columns at a time
+          auto add = [&](const uint32_t (&v)[32], int c0) {
             const float4* l4 = reinterpret_cast<const float4*>(&m.lse2[qb][c0]);
             if (!masked) {
 #pragma unroll
@@ -531,6 +626,12 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
                 acc[i & 1].x += tok < m.lim[qb][c0 + i] ? e : 0.f;
               }
             }
+          };
+          for (int c0 = 0; c0 < cols; c0 += 32) {
+            uint32_t v[32];
+            tmem_ld32(tC + c0, v);
+            tmem_wait_ld();
+            add(v, c0);
           }
           tc_fence_before();
           __syncwarp();
@@ -570,9 +671,9 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-template <int DP>
+template <int DP, bool LONG>
 static int launch_weights(const WeightsParams& P, cudaStream_t stream) {
-  constexpr int smem = WLayout<DP>::kMisc + (int)sizeof(WMisc) + 1024;
+  constexpr int smem = WLayout<DP, LONG>::kMisc + (int)sizeof(WMisc) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
   static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
   static std::atomic<int> sms[64];
@@ -582,7 +683,7 @@ static int launch_weights(const WeightsParams& P, cudaStream_t stream) {
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
       return SD_E_DEVICE;
-    if (cudaFuncSetAttribute(weights_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(weights_kernel<DP, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return SD_E_LAUNCH;
     sms[dev].store(n, std::memory_order_relaxed);
@@ -598,7 +699,7 @@ static int launch_weights(const WeightsParams& P, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weights_kernel<DP>, P) == cudaSuccess ? SD_OK : SD_E_LAUNCH;
+  return cudaLaunchKernelEx(&cfg, weights_kernel<DP, LONG>, P) == cudaSuccess ? SD_OK : SD_E_LAUNCH;
 }
 
 }  // namespace sdk
@@ -635,6 +736,9 @@ extern "C" int sd_kv_weights_launch(int B, int n, int max_q, int Hq, int Hkv, in
   P.weights = weights;
   P.err = err;
   // Requests of more chunks than stay in shared memory are prompts.
-  P.spread = (long)max_q * P.G > 2 * sdk::kWRows;
-  return D <= 64 ? sdk::launch_weights<64>(P, stream) : sdk::launch_weights<128>(P, stream);
+  if ((long)max_q * P.G > 2 * sdk::kWRows)
+    return D <= 64 ? sdk::launch_weights<64, true>(P, stream)
+                   : sdk::launch_weights<128, true>(P, stream);
+  return D <= 64 ? sdk::launch_weights<64, false>(P, stream)
+                 : sdk::launch_weights<128, false>(P, stream);
 }
