@@ -412,17 +412,22 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
           const int qb = loads % L::kNQ;
           ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((loads / L::kNQ) & 1) ^ 1, gave_up);
           if (!ok) break;
+          // a warp's 16 rows: a lane finds one, all lanes copy
+          long mine = -1;
+          const int at0 = (t >> 5) * (32 / kLanes) + (lane & 15) % (32 / kLanes) +
+                          (lane & 15) / (32 / kLanes) * kRowsPass;
+          if (lane < 16 && ch * kWRows + at0 < s.q.rows) {
+            const int row = ch * kWRows + at0, tk = w_token(P, row);
+            mine = (long)(s.q.tok0 + tk) * P.ld_q + (long)(s.h * P.G + row - tk * P.G) * P.hs_q;
+          }
 #pragma unroll
           for (int i = 0; i < DP / 16; ++i) {
-            const int at = i * kRowsPass + t / kLanes, row = ch * kWRows + at;
-            const bool is = row < s.q.rows && d8 * 8 < c.D;
-            const int tk = is ? w_token(P, row) : 0;
-            const uint16_t* from = is ? P.q + (long)(s.q.tok0 + tk) * P.ld_q +
-                                            (long)(s.h * P.G + row - tk * P.G) * P.hs_q + d8 * 8
-                                      : P.q;
+            const long from = __shfl_sync(0xffffffffu, mine, i * (32 / kLanes) + lane / kLanes);
+            const int at = i * kRowsPass + t / kLanes;
+            const bool is = from >= 0 && d8 * 8 < c.D;
             w_copy16(base + L::kQ + qb * L::kTileBytes + (d8 >> 3) * (kWRows * 128) + at * 128 +
                          (((d8 & 7) ^ (at & 7)) << 4),
-                     from, is);
+                     P.q + (is ? from + d8 * 8 : 0), is);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (t < kWRows) {
