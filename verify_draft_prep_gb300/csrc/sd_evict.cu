@@ -28,7 +28,7 @@ struct EvictParams {
   int32_t* err;
 };
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelCluster = 8;
 
 // Tokens that a request's table covers.
 __device__ __forceinline__ long evict_covered(const EvictParams& P) {
@@ -40,67 +40,104 @@ __device__ __forceinline__ int evict_len(const EvictParams& P, int r) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Choice: one CTA a request and head. The weights become orderable keys in shared memory (where they
-// fit, 200 KB; else they are read again), three passes of 11, 11 and 10 bits find the last key that
-// stays, and a pass in the tokens' order writes down the places.
+// Choice: one request and head by a CTA, or by a cluster where there are few of them. The weights become
+// orderable keys in shared memory (where they fit, 200 KB; else they are read again), three passes of 11,
+// 11 and 10 bits over counts of all CTAs find the last key that stays, and a pass in the tokens' order
+// writes down the places. What takes the time is latency: a page and then a weight behind it (eight of
+// each on their way a thread), and a dozen barriers.
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictParams P) {
   extern __shared__ uint32_t s_key[];
-  __shared__ uint32_t s_bin[2048];
+  __shared__ uint32_t s_bin[2][2048];  // counts, by turns of the passes
   __shared__ uint32_t s_warp[kSelWarps], s_warp2[kSelWarps];
-  __shared__ uint32_t s_found[2];
+  __shared__ uint32_t s_found[2], s_stay[kSelCluster], s_tied[kSelCluster];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  auto meet = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x, r = blockIdx.y;
+  const int h = blockIdx.x / C, r = blockIdx.y;
   const int n = evict_len(P, r), ctx = P.ctx[r];
   const int keep = min(n, P.budget);
   int32_t* kept = P.kept + ((long)r * P.c.Hkv + h) * P.budget;
-  if (tid == 0 && h == 0) {
+  if (tid == 0 && h == 0 && rank == 0) {
     P.new_lens[r] = keep;
     if (ctx < 0 || ctx > evict_covered(P)) raise_err(P.err, SD_ERR_KV_RANGE);
   }
-  for (int i = keep + tid; i < P.budget; i += kSelThreads) kept[i] = -1;
+  const int all = C * kSelThreads, me = rank * kSelThreads + tid;
+  for (int i = keep + me; i < P.budget; i += all) kept[i] = -1;
   if (n <= P.budget) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
+    for (int i = me; i < n; i += all) kept[i] = i;
     return;
   }
+  if (C > 1) cluster.sync();  // (every CTA has begun: its shared memory may be written from here on)
   const int32_t* table = P.table + (long)r * P.max_blocks;
   const int bs = 1 << P.c.log2_bs, first = P.sink, m = n - P.sink - P.recent;
+  // this CTA's tokens [a0, a1) of those in question
+  const int part = (m + C - 1) / C, a0 = min(m, rank * part), a1 = min(m, a0 + part);
   bool bad = false;
   // A token's weight as a key: larger ones first, a NaN before all; one without a page counts as 0.
-  auto load = [&](int i) -> uint32_t {
-    const int t = first + i;
-    const int page = __ldg(table + (t >> P.c.log2_bs));
-    if ((unsigned)page >= (unsigned)P.c.num_blocks) {
-      bad = true;
-      return orderable(0.f);
-    }
-    const float w = P.weights[((long)page * P.c.Hkv + h) * bs + (t & (bs - 1))];
+  auto page_of = [&](int i) { return __ldg(table + ((first + i) >> P.c.log2_bs)); };
+  auto key_of = [&](int i, int page) -> uint32_t {
+    const bool is = (unsigned)page < (unsigned)P.c.num_blocks;
+    bad |= !is;
+    float w = 0.f;
+    if (is) w = __ldg(P.weights + ((long)page * P.c.Hkv + h) * bs + ((first + i) & (bs - 1)));
     return w != w ? 0xffffffffu : orderable(w);
   };
-  const bool held = P.in_smem >= m;
+  const bool held = P.in_smem >= part;
   if (held) {
-#pragma unroll 8
-    for (int i = tid; i < m; i += kSelThreads) s_key[i] = load(i);
+    for (int i0 = a0 + tid; i0 < a1; i0 += 8 * kSelThreads) {
+      int page[8];
+      uint32_t k[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) page[j] = i0 + j * kSelThreads < a1 ? page_of(i0 + j * kSelThreads) : 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k[j] = i0 + j * kSelThreads < a1 ? key_of(i0 + j * kSelThreads, page[j]) : 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * kSelThreads < a1) s_key[i0 + j * kSelThreads - a0] = k[j];
+    }
   }
-  auto key = [&](int i) { return held ? s_key[i] : load(i); };
+  auto key = [&](int i) { return held ? s_key[i - a0] : key_of(i, page_of(i)); };
 
   uint32_t need = (uint32_t)(P.budget - P.sink - P.recent);  // < m
   uint32_t prefix = 0;
-  bool any = need > 0;
+  const bool any = need > 0;
   for (int level = 0; any && level < 3; ++level) {
     const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
     const uint32_t high = level == 0 ? 0u : 0xffffffffu << (shift + bits);
-    for (int i = tid; i < 2048; i += kSelThreads) s_bin[i] = 0;
+    uint32_t* bin = s_bin[level & 1];
+    for (int i = tid; i < 2048; i += kSelThreads) bin[i] = 0;
     __syncthreads();
-    for (int i = tid; i < m; i += kSelThreads) {
+    for (int i = a0 + tid; i < a1; i += kSelThreads) {
       const uint32_t k = key(i);
-      if ((k & high) == prefix) atomicAdd(&s_bin[2047 - ((k >> shift) & ((1u << bits) - 1))], 1u);
+      if ((k & high) == prefix) atomicAdd(&bin[2047 - ((k >> shift) & ((1u << bits) - 1))], 1u);
     }
-    __syncthreads();
-    // the bin in which number `need` from the largest lies: 4 bins a thread
+    meet();
+    // the bin in which number `need` from the largest lies: 4 bins a thread, of all CTAs
     uint32_t c[4], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum += c[j] = s_bin[tid * 4 + j];
+    {
+      uint4 v = reinterpret_cast<const uint4*>(bin)[tid];
+      if (C > 1) {
+        v = make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < C; ++k) {
+          const uint4 x = reinterpret_cast<const uint4*>(cluster.map_shared_rank(bin, k))[tid];
+          v.x += x.x;
+          v.y += x.y;
+          v.z += x.z;
+          v.w += x.w;
+        }
+      }
+      c[0] = v.x;
+      c[1] = v.y;
+      c[2] = v.z;
+      c[3] = v.w;
+      sum = v.x + v.y + v.z + v.w;
+    }
     uint32_t at = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -126,9 +163,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictPa
   }
   const uint32_t ties = need;  // of the tokens whose key is `prefix`, so many stay: the first
 
-  // the places, in order: a warp goes over a stretch of its own
-  const int seg = (n + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
-  const int a = min(n, warp * seg), b = min(n, a + seg);
+  // the places, in order: a warp goes over a stretch of its own, of this CTA's part with the tokens
+  // before it (the first CTA) and behind it (the last one)
+  const int b0 = rank == 0 ? 0 : first + a0, b1 = rank == C - 1 ? n : first + a1;
+  const int seg = (b1 - b0 + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;
+  const int a = min(b1, b0 + warp * seg), b = min(b1, a + seg);
   // 0: goes, 1: stays, 2: stays if it is among the first `ties` of its key
   auto kind = [&](int t) {
     if (t < P.sink || t >= n - P.recent) return 1;
@@ -137,22 +176,42 @@ __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictPa
     return k > prefix ? 1 : k == prefix ? 2 : 0;
   };
   uint32_t stay = 0, tied = 0;
+#pragma unroll 4
   for (int i = a; i < b; i += 32) {
     const int x = i + lane < b ? kind(i + lane) : 0;
-    stay += __popc(__ballot_sync(0xffffffffu, x == 1));
-    tied += __popc(__ballot_sync(0xffffffffu, x == 2));
+    stay += x == 1;
+    tied += x == 2;
   }
+  stay = __reduce_add_sync(0xffffffffu, stay);
+  tied = __reduce_add_sync(0xffffffffu, tied);
   if (lane == 0) {
     s_warp[warp] = stay;
     s_warp2[warp] = tied;
   }
   __syncthreads();
+  if (C > 1) {
+    if (tid < C) {
+      uint32_t x = 0, y = 0;
+      for (int w = 0; w < kSelWarps; ++w) {
+        x += s_warp[w];
+        y += s_warp2[w];
+      }
+      cluster.map_shared_rank(s_stay, tid)[rank] = x;
+      cluster.map_shared_rank(s_tied, tid)[rank] = y;
+    }
+    cluster.sync();
+  }
   stay = tied = 0;
+  for (int k = 0; k < rank; ++k) {
+    stay += s_stay[k];
+    tied += s_tied[k];
+  }
   for (int w = 0; w < warp; ++w) {
     stay += s_warp[w];
     tied += s_warp2[w];
   }
   const uint32_t below = (1u << lane) - 1;
+#pragma unroll 2
   for (int i = a; i < b; i += 32) {
     const int x = i + lane < b ? kind(i + lane) : 0;
     const uint32_t one = __ballot_sync(0xffffffffu, x == 1), two = __ballot_sync(0xffffffffu, x == 2);
@@ -166,20 +225,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictPa
 }
 
 // ---------------------------------------------------------------------------------------------
-// Move: a CTA takes 128 places (whole pages) of one head, K and V together, into registers and then
-// to their new pages. A new page's scale is the largest of its tokens' (their sources' pages'), so that
+// Move: a CTA takes 128 places (whole pages; 256 of heads of up to 64) of one head, first K and then V,
+// into registers and then to their new pages. A new page's scale is the largest of its tokens' (their sources' pages'), so that
 // values only ever lose what becomes subnormal, and a page of tokens that do not move stays as it is.
 // Within the request's own pages a token only moves towards the front: a cluster goes over the
 // places in rounds, and nothing is written before all of the round's tokens are read.
 // ---------------------------------------------------------------------------------------------
-constexpr int kMoveThreads = 256, kMoveTokens = 128, kMoveCluster = 8;
+constexpr int kMoveThreads = 256, kMoveCluster = 8;
 
-template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams P) {
+template <bool IN_PLACE, int kMoveTokens>
+__global__ void __launch_bounds__(kMoveThreads, 5) evict_move_kernel(const EvictParams P) {
   __shared__ long s_src[kMoveTokens], s_dst[kMoveTokens];  // elements; -1: no page, -2: no token
   __shared__ float s_scale[2][kMoveTokens];
   __shared__ unsigned s_max[2][kMoveTokens];  // of each page, in its first token's place
   __shared__ float s_ratio[2][kMoveTokens];   // -1: stays as it is
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the places)
   const KvCache& c = P.c;
   const int tid = threadIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int n = min(evict_len(P, r), P.budget), bs = 1 << c.log2_bs;
@@ -188,6 +248,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   const int32_t* to = IN_PLACE ? table : P.to + (long)r * P.to_blocks;
   const int to_blocks = IN_PLACE ? P.max_blocks : P.to_blocks;
   const int parts = c.D / 16;  // 16-byte parts of a token's head
+  if (!IN_PLACE && (long)blockIdx.x * kMoveTokens >= n) return;
   const int step = IN_PLACE ? kMoveCluster * kMoveTokens : 0x7fffffff;
   for (long j0 = 0; j0 < n; j0 += step) {
     const long base = j0 + (long)blockIdx.x * kMoveTokens;
@@ -247,39 +308,37 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
       }
     }
     __syncthreads();
-    // 2. the tokens' bytes: up to 8 parts a thread
-    uint4 x[8];
-    const int all = 2 * kMoveTokens * parts;
+    // 2. the tokens' bytes, 4 parts a thread, and on to their pages
+    const int all = kMoveTokens * parts;
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv) {
+      uint8_t* cache = kv ? P.v : P.k;
+      uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = tid + i * kMoveThreads;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (u >= all) continue;
-      const int kv = u >= kMoveTokens * parts, v = kv ? u - kMoveTokens * parts : u;
-      const int t = v / parts, p = v - t * parts;
-      if (s_dst[t] >= 0 && (s_ratio[kv][t] > 0.f || s_ratio[kv][t] != s_ratio[kv][t]))
-        x[i] = __ldcs(reinterpret_cast<const uint4*>((kv ? P.v : P.k) + s_src[t] + p * 16));
-    }
-    if (IN_PLACE) cluster_barrier();
-    // 3. to their pages
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int u = tid + i * kMoveThreads;
-      if (u >= all) continue;
-      const int kv = u >= kMoveTokens * parts, v = kv ? u - kMoveTokens * parts : u;
-      const int t = v / parts, p = v - t * parts;
-      const float ratio = s_ratio[kv][t];
-      if (s_dst[t] < 0 || ratio == -1.f) continue;
-      if (ratio != 1.f && ratio != 0.f) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 a = e4m3x2_to_f32((uint16_t)w[q]), b = e4m3x2_to_f32((uint16_t)(w[q] >> 16));
-          w[q] = f32_to_e4m3x2(a.x * ratio, a.y * ratio) |
-                 (uint32_t)f32_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int u = tid + i * kMoveThreads, t = u / parts;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (u < all && s_dst[t] >= 0 && (s_ratio[kv][t] > 0.f || s_ratio[kv][t] != s_ratio[kv][t]))
+          x[i] = __ldcs(reinterpret_cast<const uint4*>(cache + s_src[t] + (u - t * parts) * 16));
       }
-      *reinterpret_cast<uint4*>((kv ? P.v : P.k) + s_dst[t] + p * 16) = x[i];
+      if (IN_PLACE) cluster_barrier();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = tid + i * kMoveThreads, t = u / parts;
+        if (u >= all) continue;
+        const float ratio = s_ratio[kv][t];
+        if (s_dst[t] < 0 || ratio == -1.f) continue;
+        if (ratio != 1.f && ratio != 0.f) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 a = e4m3x2_to_f32((uint16_t)w[q]), b = e4m3x2_to_f32((uint16_t)(w[q] >> 16));
+            w[q] = f32_to_e4m3x2(a.x * ratio, a.y * ratio) |
+                   (uint32_t)f32_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
+          }
+        }
+        *reinterpret_cast<uint4*>(cache + s_dst[t] + (u - t * parts) * 16) = x[i];
+      }
     }
     if (tid < kMoveTokens && weight_to >= 0) {
       P.weights[weight_to] = weight;
@@ -291,6 +350,33 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     if (!IN_PLACE) break;
     __syncthreads();  // (the arrays in shared memory are read)
   }
+}
+
+template <int TOKENS>
+static int launch_move(const EvictParams& P, long most, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kMoveThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (P.to) {
+    const long places = most < P.budget ? most : P.budget;
+    const unsigned chunks = (unsigned)((places + TOKENS - 1) / TOKENS);
+    if (chunks == 0) return SD_OK;
+    cfg.gridDim = dim3(chunks, (unsigned)P.c.Hkv, (unsigned)P.B);
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<false, TOKENS>, P) == cudaSuccess ? SD_OK
+                                                                                       : SD_E_LAUNCH;
+  }
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kMoveCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(kMoveCluster, (unsigned)P.c.Hkv, (unsigned)P.B);
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel<true, TOKENS>, P) == cudaSuccess ? SD_OK
+                                                                                     : SD_E_LAUNCH;
 }
 
 }  // namespace sdk
@@ -333,31 +419,22 @@ extern "C" int sd_kv_evict_launch(int B, int Hkv, int D, void* k_cache, void* v_
     set[dev].store(true, std::memory_order_release);
   }
   const long most = (long)max_blocks << log2_bs;
-  P.in_smem = (int)(most < kMostSmem / 4 ? most : kMostSmem / 4);
+  // CTAs of a request and head: more while the SMs have room for them and each has 1000 tokens.
+  int C = 1;
+  while (C < sdk::kSelCluster && (long)B * Hkv * C * 2 <= 304 && most > 2048L * C) C *= 2;
+  const long part = (most + C - 1) / C;
+  P.in_smem = (int)(part < kMostSmem / 4 ? part : kMostSmem / 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)Hkv, (unsigned)B, 1);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(Hkv * C), (unsigned)B, 1);
   cfg.blockDim = dim3(sdk::kSelThreads, 1, 1);
   cfg.dynamicSmemBytes = (size_t)P.in_smem * 4;
   cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, sdk::evict_choose_kernel, P) != cudaSuccess) return SD_E_LAUNCH;
-  cudaLaunchConfig_t mv = {};
-  mv.blockDim = dim3(sdk::kMoveThreads, 1, 1);
-  mv.stream = stream;
-  if (to_table) {
-    const long places = most < budget ? most : budget;
-    const unsigned chunks = (unsigned)((places + sdk::kMoveTokens - 1) / sdk::kMoveTokens);
-    if (chunks == 0) return SD_OK;
-    mv.gridDim = dim3(chunks, (unsigned)Hkv, (unsigned)B);
-    return cudaLaunchKernelEx(&mv, sdk::evict_move_kernel<false>, P) == cudaSuccess ? SD_OK
-                                                                                   : SD_E_LAUNCH;
-  }
-  mv.gridDim = dim3(sdk::kMoveCluster, (unsigned)Hkv, (unsigned)B);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = sdk::kMoveCluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  mv.attrs = attr;
-  mv.numAttrs = 1;
-  return cudaLaunchKernelEx(&mv, sdk::evict_move_kernel<true>, P) == cudaSuccess ? SD_OK
-                                                                                : SD_E_LAUNCH;
+  return D <= 64 ? sdk::launch_move<256>(P, most, stream) : sdk::launch_move<128>(P, most, stream);
 }
