@@ -85,6 +85,48 @@ def test_sizes(kind, V):
 
 
 @pytest.mark.parametrize("kind", ["probs", "logits"])
+@pytest.mark.parametrize("V", [255, 256, 257, 511, 512, 513, 4097])
+def test_sizes_where_kernels_change(kind, V):
+    """Rows that a warp sorts, and those that a CTA or several count."""
+    check(rows_of(24, V, kind, V, spread=4.0), 12, 2, settings(12, V + 1))
+    check(rows_of(3, V, kind, V, ld=V + 5), 3, 1, settings(3, V + 2), pad=1)
+
+
+@pytest.mark.parametrize("kind", ["probs", "logits"])
+@pytest.mark.parametrize("V", [300, 3000])
+def test_many_rows(kind, V):
+    """More rows than fit on the GPU at a time: tokens, counts and sums of all of them."""
+    n = 3000
+    rows, s = rows_of(n, V, kind, 19), settings(n, 19)
+    probs, kept, tokens, prob, u = run(rows, n, 1, s)
+    for i in range(0, n, 37):
+        get = lambda f: float(s[f][i])  # noqa: E731
+        order, p, m = stepref.cut_ref(rows[i].double().cpu(), kind == "logits", get("temperature"),
+                                      int(s["top_k"][i]), get("top_p"), get("min_p"))
+        assert int(kept[i]) == m and int(tokens[i]) == stepref.draw_ref(order, p, m, float(u[i]))[0]
+    assert torch.equal((probs > 0).sum(1).int(), kept[:, 0])
+    assert torch.all((probs.double().sum(1) - 1).abs() < 2.0 ** -18)
+    assert torch.all((probs.gather(1, tokens.long()) - prob).abs() <= prob * 2.0 ** -18)
+
+
+@pytest.mark.parametrize("V", [1500, 201088])
+def test_grammar_masks(V):
+    """Nearly every entry -inf or the type's lowest number: fewer numbers than top_k, draws and counts
+    among what is left, with and without another cut."""
+    low = torch.finfo(torch.bfloat16).min
+    x = rows_of(8, V, "logits", 20)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(21)
+    hide = torch.rand(8, V, generator=g, device=DEV) < 0.99
+    hide[:, 7] = False
+    x[:4] = x[:4].masked_fill(hide[:4], -math.inf)
+    x[4:] = x[4:].masked_fill(hide[4:], low)
+    s = dict(temperature=torch.full((8,), 0.9), top_k=torch.tensor([0, 50, 0, 5000] * 2).int(),
+             top_p=torch.tensor([1.0, 1.0, 0.8, 1.0] * 2), min_p=None)
+    check(x, 8, 1, s)
+
+
+@pytest.mark.parametrize("kind", ["probs", "logits"])
 @pytest.mark.parametrize("V,ld", [(8193, 8193), (20000, 20001), (32768, 32776), (50001, 50004),
                                   (201088, 201088), (262113, 262120)])
 def test_large(kind, V, ld):

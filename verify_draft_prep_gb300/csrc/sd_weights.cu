@@ -62,7 +62,7 @@ struct WLayout {
 struct WMisc {
   uint64_t k_full[2], k_empty[2], q_full[4], q_empty[4];
   uint64_t s_full[2][2], s_empty[2][2];  // [tile of the pair][buffer]
-  float lse2[4][kWRows];                 // of the rows of a chunk of Q
+  float lse2[4][kWRows];                 // -lse log2(e) of the rows of a chunk of Q
   int lim[4][kWRows];                    // tokens that they see
   float k_scale[2][kWPair];              // of a pair's tokens, times sm_scale log2(e)
   float before[2][kWPair];               // what they have so far
@@ -391,12 +391,12 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
         constexpr int kLanes = DP / 8, kRowsPass = kWLoaders / kLanes;
         const int d8 = t % kLanes;
         auto of_row = [&](int ch, float& l2, int& lim) {
-          l2 = INFINITY;
+          l2 = -INFINITY;
           lim = 0;
           const int row = ch * kWRows + t;
           if (t < kWRows && row < s.q.rows && ch < s.chunks) {
             const int tk = w_token(P, row);
-            l2 = __ldg(P.lse + (long)(s.q.tok0 + tk) * P.Hq + s.h * P.G + row - tk * P.G) * kWLog2e;
+            l2 = __ldg(P.lse + (long)(s.q.tok0 + tk) * P.Hq + s.h * P.G + row - tk * P.G) * -kWLog2e;
             lim = w_sees(P, s.q, row);
           }
         };
@@ -467,11 +467,11 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
             }
           };
           q_rows(0);
-          float l2 = INFINITY;
+          float l2 = -INFINITY;
           int lim = 0;
           if (t < kWRows && row0 + t < s.q.rows) {
             const int row = row0 + t, tk = w_token(P, row);
-            l2 = __ldg(P.lse + (long)(s.q.tok0 + tk) * P.Hq + s.h * P.G + row - tk * P.G) * kWLog2e;
+            l2 = __ldg(P.lse + (long)(s.q.tok0 + tk) * P.Hq + s.h * P.G + row - tk * P.G) * -kWLog2e;
             lim = w_sees(P, s.q, row);
           }
           ok = mbar_wait_warp(smem_u32(&m.q_empty[qb]), ((loads >> 1) & 1) ^ 1, gave_up);
@@ -617,17 +617,17 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
               for (int i = 0; i < 8; ++i) {
                 const float4 l = l4[i];
                 const float2 a = w_fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
-                                        f2, make_float2(-l.x, -l.y));
+                                        f2, make_float2(l.x, l.y));
                 const float2 b = w_fma2(
                     make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), f2,
-                    make_float2(-l.z, -l.w));
+                    make_float2(l.z, l.w));
                 acc[0] = w_add2(acc[0], make_float2(w_ex2(a.x), w_ex2(a.y)));
                 acc[1] = w_add2(acc[1], make_float2(w_ex2(b.x), w_ex2(b.y)));
               }
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float e = w_ex2(fmaf(__uint_as_float(v[i]), f, -m.lse2[qb][c0 + i]));
+                const float e = w_ex2(fmaf(__uint_as_float(v[i]), f, m.lse2[qb][c0 + i]));
                 acc[i & 1].x += tok < m.lim[qb][c0 + i] ? e : 0.f;
               }
             }
