@@ -44,7 +44,8 @@ __device__ __forceinline__ int evict_len(const EvictParams& P, int r) {
 // orderable keys in shared memory (where they fit, 200 KB; else they are read again), three passes of 11,
 // 11 and 10 bits over counts of all CTAs find the last key that stays, and a pass in the tokens' order
 // writes down the places. What takes the time is latency: a page and then a weight behind it (eight of
-// each on their way a thread), and a dozen barriers.
+// each on their way a thread), and a dozen barriers. One request of 32000 tokens of 8 heads: 24 us with
+// clusters of 8, 69 with a CTA a head; 64 requests of 512 to 8192: 37 us.
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictParams P) {
   extern __shared__ uint32_t s_key[];
@@ -229,7 +230,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictPa
 // into registers and then to their new pages. A new page's scale is the largest of its tokens' (their sources' pages'), so that
 // values only ever lose what becomes subnormal, and a page of tokens that do not move stays as it is.
 // Within the request's own pages a token only moves towards the front: a cluster goes over the
-// places in rounds, and nothing is written before all of the round's tokens are read.
+// places in rounds, and nothing is written before all of the round's tokens are read. Bound by memory
+// behind a chain of three loads (place, page, scale): 64 requests of up to 2048 tokens of 8 heads of 64
+// take 60 us, 66% of the copy rate (K and V together in registers, four CTAs an SM instead of five: 79);
+// one request of 16000 of 128 16 us.
 // ---------------------------------------------------------------------------------------------
 constexpr int kMoveThreads = 256, kMoveCluster = 8;
 

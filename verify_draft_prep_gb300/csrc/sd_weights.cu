@@ -15,7 +15,19 @@
 // A unit is a pair of tiles (256 tokens) of one request and KV head; a chunk is up to 128 rows. Both
 // tiles use a chunk of Q in shared memory, and one group of four warps turns the S of each into sums.
 // Eight warps load: K a unit ahead in registers, and Q, which stays where a request has at most two
-// chunks. One thread issues the products.
+// chunks (else it streams by, asynchronously copied, two chunks ahead). One thread issues the
+// products, and one warp has the K of units further on fetched into L2.
+//
+// What bounds it (pages of 16, 8 heads of K):
+//   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 96 us against 22 of memory. Issue
+//     slots 44%, memory 18%, exponentials 10%, tensor cores 5%: a unit of 256 tokens is some 6000
+//     instructions of warps, half of them the conversion of K and the loads' addresses.
+//   - A prompt of 8192 tokens of 32 heads of 128: 357 us against 146 of products. The exponentials
+//     alone take 276; tensor cores 37%, issue slots 46%. (With a quarter or an eighth of the exponentials
+//     by a polynomial it took 519 and 480 us, without 437, when the loads took more of the slots.)
+//   - One token at 32000, 32 heads of 128: 25 us against 5: 7 units a CTA, each as long as its loads.
+// S read 16 columns at a time with the next ones on their way: 64 requests 102 against 95 us, a prompt
+// 502 against 437 (registers); three warps that fetch ahead, or 8 and 12 units: no change.
 
 #include <atomic>
 
