@@ -24,8 +24,8 @@
  *     asserts. One kernel waits on a value written by another CTA of the same launch: the
  *     single launch of sd_verify_prepare (see there), whose wait is bounded by time (20 ms on
  *     the GPU clock) and ends with SD_ERR_WAIT, never with a hang. The warps of a CTA of
- *     sd_kv_attend wait for one another and for its loads, each time about a second at most;
- *     SD_ERR_WAIT there too means that the call's output is incomplete.
+ *     sd_kv_attend and of sd_kv_weights wait for one another and for their loads, each time about a
+ *     second at most; SD_ERR_WAIT there too means that the call's output is incomplete.
  *
  * Notation: B requests, K drafts per request (1 <= K <= SD_K_MAX), V vocabulary entries,
  * H hidden size. Target rows p_0..p_K of request r are rows r*(K+1)+j of `target`; draft rows
@@ -64,18 +64,19 @@ extern "C" {
 #define SD_ERR_BLOCK_TABLE 2    /* drafter position not covered by the block table: slot -1 */
 #define SD_ERR_NUM_ACCEPTED 4   /* num_accepted outside [0, K]: clamped */
 #define SD_ERR_MAP_RANGE 8      /* hidden_map row >= n_in_rows: h_shared written instead */
-#define SD_ERR_ZERO_ROW 16      /* a race row without a positive key even on p: token 0 */
+#define SD_ERR_ZERO_ROW 16      /* a race row without a positive key even on p, or a row to be cut
+                                   without an entry to keep: token 0 */
 #define SD_ERR_TOTAL_RANGE 32   /* total_out outside [0, capacity]: clamped */
 #define SD_ERR_WAIT 64          /* sd_verify_prepare: a request's first drafter slot was not
                                    published within the bounded wait (20 ms); its final token is
-                                   not written to input_ids. sd_kv_attend: a wait inside the
-                                   kernel ran out, outputs are incomplete */
+                                   not written to input_ids. sd_kv_attend, sd_kv_weights: a wait
+                                   inside the kernel ran out, outputs are incomplete */
 #define SD_ERR_DRAFT_COUNT 128  /* cu_drafts gives a request a draft count outside [0, K_max]:
                                    clamped (sd_verify_ragged) */
 #define SD_ERR_KV_SLOT 256      /* a slot beyond the cache: that token is not written */
 #define SD_ERR_KV_RANGE 512     /* a length, a prefix entry or a block-table entry of a cache read
                                    is out of range: those tokens are left out (sd_kv_read writes
-                                   zeros for them) */
+                                   zeros for them, sd_kv_evict takes them as such) */
 
 /* input kinds for sd_verify */
 #define SD_F32_PROBS 0    /* fp32 probabilities, already at the sampling temperature */
@@ -654,8 +655,8 @@ SD_API int sd_rope_table(int rot, double base, int kind, double factor, double o
  * probabilities for SD_F32_PROBS; exp(l / T_r) for SD_BF16_LOGITS, T_r within 2^-100 and 2^100) those
  * kept are the first
  *   top_k[r] of them (<= 0: all),
- *   those of these before which less than top_p[r] of their sum lies (>= 1: all),
- *   those with w >= min_p[r] w_max (<= 0: all; above 1 as 1),
+ *   those of these before which less than top_p[r] of their sum lies (>= 1 or NaN: all),
+ *   those with w >= min_p[r] w_max (<= 0 or NaN: all; above 1 as 1),
  * whichever is fewest, and the first entry always. T_r <= 0 (or NaN): the first entry alone. Entries of
  * weight 0 are never kept: probabilities <= 0, logits of -inf, all beside a +inf, and NaN. A
  * probability above 1 counts as 1. Which entries are kept, and which is drawn, is decided by sums with an

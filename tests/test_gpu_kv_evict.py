@@ -200,3 +200,30 @@ def test_attention_goes_on_over_what_stayed():
             assert torch.all((x - y).abs() <= lim[..., None])
         o, _, tol, _ = kvref.attend_ref(q[r:r + 1].double(), kk, vv, D ** -0.5, False)
         assert torch.all((out[r:r + 1].double() - o).abs() <= tol)
+
+
+@pytest.mark.parametrize("lens,H,bs", [([5000, 4097], 32, 16), ([9000, 100, 3000], 16, 32), ([430000], 1, 128),
+                                       ([60000] * 2, 80, 128)])
+def test_choice_of_long_requests(lens, H, bs):
+    """One CTA a request and head, clusters of several, keys that fit shared memory and keys that do not:
+    the tokens that stay are those of a sort."""
+    budget, sink, recent, D = 777, 3, 50, 16
+    c = make(lens, H, D, bs, budget, seed=13, ties=True)
+    c["w"] += torch.rand(c["w"].shape, device=DEV).mul(64).floor() / 64
+    was = c["w"].clone()
+    kept, out = run(c, budget, sink, recent)
+    for r, n in enumerate(lens):
+        assert int(out[r]) == min(n, budget)
+        t = torch.arange(n, device=DEV)
+        w = was[c["table"][r].long()[t // bs], :, t % bs]  # [n, H]
+        if n <= budget:
+            assert torch.all(kept[r, :, :n] == t) and torch.all(kept[r, :, n:] == -1)
+            continue
+        mid = torch.sort(w[sink:n - recent], dim=0, descending=True, stable=True).indices
+        mid = torch.sort(mid[:budget - sink - recent] + sink, dim=0).values
+        want = torch.cat([t[:sink, None].expand(-1, H), mid, t[n - recent:, None].expand(-1, H)]).T
+        assert torch.equal(kept[r].long(), want)
+        # and their weights stand where they went
+        j = torch.arange(budget, device=DEV)
+        for h in (0, H - 1):
+            assert torch.equal(c["w"][c["to"][r].long()[j // bs], h, j % bs], w[want[h], h])

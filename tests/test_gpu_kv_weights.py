@@ -238,3 +238,38 @@ def test_after_attend():
         t = torch.arange(T, device=DEV)
         got = w[c["table"][r].long()[t // bs], :, t % bs].double().sum(0)
         assert torch.all((got - n_q * Hq // H).abs() < 1e-4 * n_q * Hq / H)
+
+
+@pytest.mark.parametrize("max_q", [1, 40, 600])
+def test_any_number_expected(max_q):
+    """max_q only chooses the kernel: many chunks of rows in the one for few, few in the one for many."""
+    c = make([600, 333], [500, 3], 8, 2, 64, 16, seed=16)
+    lse = lse_of(c, 0.125)
+    out = torch.full_like(c["before"], -3.0)
+    call(c, out, lse, before=c["before"], max_q=max_q)
+    check(c, out, lse, 0.125)
+
+
+@pytest.mark.parametrize("D,bs", [(128, 16), (64, 128), (96, 8)])
+def test_long_contexts(D, bs):
+    """Many units a CTA, among them those of neighbours that have none or one."""
+    c = make([20000, 0, 1, 7001], [4, 0, 1, 6], 16, 8, D, bs, seed=17)
+    lse = lse_of(c, D ** -0.5)
+    out, err = torch.full_like(c["before"], -3.0), torch.zeros(1, dtype=torch.int32, device=DEV)
+    call(c, out, lse, err, before=c["before"], max_q=6)
+    check(c, out, lse, D ** -0.5)
+    assert int(err) == 0
+
+
+def test_many_requests():
+    """More requests than threads find their places."""
+    g = torch.Generator()
+    g.manual_seed(18)
+    lens = torch.randint(0, 60, (1500,), generator=g).tolist()
+    n_q = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 4, (1500,), generator=g))]
+    c = make(lens, n_q, 4, 1, 32, 8, seed=18)
+    lse = torch.zeros(sum(n_q), 4, device=DEV)
+    out, err = torch.full_like(c["before"], -3.0), torch.zeros(1, dtype=torch.int32, device=DEV)
+    call(c, out, lse, err, before=c["before"], max_q=3, sm_scale=2.0 ** -6)
+    check(c, out, lse, 2.0 ** -6)
+    assert int(err) == 0
