@@ -324,21 +324,29 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     constexpr int kParts = DP / 16, kPerPass = 32 / kParts;  // parts of a token; tokens of a pass
     constexpr int kPasses = 32 / kPerPass;                   // of a warp's 32 tokens: 8 or 4
     const int part = lane % kParts, sub = lane / kParts;
-    uint4 x[kPasses];
+    constexpr int kHeld = 4;  // passes whose bytes are in registers at a time
+    uint4 x[kHeld];
     float ks = 0.f, was = 0.f;
-    long where = -1;
+    long where = -1, src = -1;
     int page_next = -1;
     volatile int* loaded = &m.loaded;
     auto page_of = [&](const WUnit& u) {
       const int tok = u.pair * kWPair + t;
       return tok < u.q.len ? __ldg(P.table + (long)u.r * P.max_blocks + (tok >> c.log2_bs)) : -2;
     };
+    auto bytes = [&](int first) {  // of kHeld passes
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const long from = __shfl_sync(0xffffffffu, src, (first + i) * kPerPass + sub);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (from >= 0 && part * 16 < c.D) x[i] = ld_stream_u4(c.k + from + part * 16);
+      }
+    };
     auto fetch = [&](const WUnit& u, int page) {  // this warp's tokens of a unit
       const int tok = u.pair * kWPair + t;
       ks = 0.f;
       was = 0.f;
-      where = -1;
-      long src = -1;
+      where = src = -1;
       if ((unsigned)page < (unsigned)c.num_blocks) {
         const long slot = (long)page * c.Hkv + u.h;
         ks = __ldg(c.k_scale + slot);
@@ -348,13 +356,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
       } else if (page != -2) {
         raise_err(P.err, SD_ERR_KV_RANGE);
       }
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const long from = __shfl_sync(0xffffffffu, src, i * kPerPass + sub);
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (from >= 0 && part * 16 < c.D)
-          x[i] = ld_stream_u4(c.k + from + part * 16);
-      }
+      bytes(0);
     };
     WUnit ahead = s;
     bool more = some;
@@ -372,10 +374,12 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
       // K of this unit, which is in registers
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
+        // (heads of 128: the second half is in L2 by now)
+        if (i > 0 && i % kHeld == 0) bytes(i);
         const int tok = lw * 32 + i * kPerPass + sub;
         const float f = __shfl_sync(0xffffffffu, ks, i * kPerPass + sub);
         uint4 lo, hi;
-        to_bf16(f == 0.f ? make_uint4(0, 0, 0, 0) : x[i], lo, hi);  // a scale of 0: zeros
+        to_bf16(f == 0.f ? make_uint4(0, 0, 0, 0) : x[i % kHeld], lo, hi);  // a scale of 0: zeros
         const int row = tok & (kWTile - 1), ch = (2 * part) & 7;
         unsigned char* at = smem + L::kK + (kb * 2 + (tok >> 7)) * L::kTileBytes +
                             (part >> 2) * (kWTile * 128) + row * 128;
