@@ -14,18 +14,21 @@
 //
 // A unit is a pair of tiles (256 tokens) of one request and KV head; a chunk is up to 128 rows. Both
 // tiles use a chunk of Q in shared memory, and one group of four warps turns the S of each into sums.
-// Eight warps load: K a unit ahead in registers, and Q, which stays where a request has at most two
-// chunks (else it streams by, asynchronously copied, two chunks ahead). One thread issues the
-// products, and one warp has the K of units further on fetched into L2.
+// Eight warps load: K (three units ahead through a ring in shared memory for heads of up to 64, else
+// one ahead in registers, with one warp that has the units further on fetched into L2), and Q, which
+// stays where a request has at most two chunks and else streams by, asynchronously copied, two chunks
+// ahead. One thread issues the products.
 //
 // What bounds it (pages of 16, 8 heads of K):
-//   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 96 us against 22 of memory. Issue
-//     slots 44%, memory 18%, exponentials 10%, tensor cores 5%: a unit of 256 tokens is some 6000
-//     instructions of warps, half of them the conversion of K and the loads' addresses.
-//   - A prompt of 8192 tokens of 32 heads of 128: 357 us against 146 of products. The exponentials
+//   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 85 us against 22 of memory. Nothing is
+//     full (issue slots 44%, memory 18%, exponentials 10%, tensor cores 5%): the loading warps' own chain,
+//     some 450 instructions a unit each, is what the others wait for. K a unit ahead in registers: 95;
+//     two units ahead in registers: 134 (spills).
+//   - A prompt of 8192 tokens of 32 heads of 128: 362 us against 146 of products. The exponentials
 //     alone take 276; tensor cores 37%, issue slots 46%. (With a quarter or an eighth of the exponentials
 //     by a polynomial it took 519 and 480 us, without 437, when the loads took more of the slots.)
-//   - One token at 32000, 32 heads of 128: 25 us against 5: 7 units a CTA, each as long as its loads.
+//   - One token at 32000, 32 heads of 128: 20 us against 5: 7 units a CTA, each as long as its loads; 26
+//     with all of a unit's K in registers, some of which were spilled.
 // S read 16 columns at a time with the next ones on their way: 64 requests 102 against 95 us, a prompt
 // 502 against 437 (registers); three warps that fetch ahead, or 8 and 12 units: no change.
 
@@ -66,9 +69,14 @@ struct WLayout {
   static constexpr int kTileBytes = kWTile * DP * 2;  // K of a tile, or Q of a chunk, as bf16
   static constexpr int kNK = LONG ? 1 : 2;            // pairs of tiles
   static constexpr int kNQ = LONG ? 4 : 2;            // chunks
+  // Heads of up to 64 leave room for K's bytes on their way: a ring of units, which no thread holds in
+  // registers.
+  static constexpr int kRing = DP == 64 && !LONG ? 4 : 0;
+  static constexpr int kRingUnit = kWPair * (DP + 16);  // bytes, scale, number so far and its place
   static constexpr int kK = 0;
   static constexpr int kQ = kK + 2 * kNK * kTileBytes;
-  static constexpr int kMisc = kQ + kNQ * kTileBytes;
+  static constexpr int kStage = kQ + kNQ * kTileBytes;
+  static constexpr int kMisc = kStage + kRing * kRingUnit;
 };
 
 struct WMisc {
@@ -236,6 +244,10 @@ __device__ __forceinline__ float2 w_add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ void w_copy4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void w_copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(there ? 16 : 0)
@@ -360,7 +372,39 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     };
     WUnit ahead = s;
     bool more = some;
-    if (more) {
+    // The ring: every thread copies for itself and waits for its own copies alone.
+    constexpr int kRing = L::kRing > 0 ? L::kRing : 1;
+    WSchedule<LONG> far = line;
+    auto stage_of = [&](int u) { return (uint32_t)(L::kStage + u % kRing * L::kRingUnit); };
+    auto issue = [&](int u) {  // unit number u, which is `ahead`
+      if (more) {
+        const uint32_t st = base + stage_of(u);
+        const int tok = ahead.pair * kWPair + t, page = page_next;
+        const bool is = (unsigned)page < (unsigned)c.num_blocks;
+        if (!is && page != -2) raise_err(P.err, SD_ERR_KV_RANGE);
+        const long slot = is ? (long)page * c.Hkv + ahead.h : 0;
+        const long to = is ? slot * bs + (tok & (bs - 1)) : -1;
+        const long from = is ? page * c.st_block + (tok & (bs - 1)) * c.st_tok + ahead.h * c.st_head : -1;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const long at = __shfl_sync(0xffffffffu, from, i * kPerPass + sub);
+          const bool there = at >= 0 && part * 16 < c.D;
+          w_copy16(st + (i * kWLoaders + t) * 16, c.k + (there ? at + part * 16 : 0), there);
+        }
+        const uint32_t meta = st + kWPair * DP + t * 4;
+        w_copy4(meta, c.k_scale + slot, is);
+        const bool old = is && P.before && tok < ahead.q.off;
+        w_copy4(meta + kWPair * 4, old ? P.before + to : c.k_scale, old);
+        *reinterpret_cast<long*>(smem + stage_of(u) + kWPair * (DP + 8) + t * 8) = to;
+        more = far.next(P, ahead);
+        if (more) page_next = page_of(ahead);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (L::kRing > 0) {
+      if (more) page_next = page_of(ahead);
+      for (int u = 0; u + 1 < kRing; ++u) issue(u);
+    } else if (more) {
       fetch(s, page_of(s));
       more = line.next(P, ahead);
       if (more) page_next = page_of(ahead);
@@ -369,13 +413,24 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     bool ok = true, have_q = false;
     while (some && ok) {
       const int kb = unit % L::kNK;
+      if (L::kRing > 0) {
+        issue(unit + kRing - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        const unsigned char* st = smem + stage_of(unit);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          x[i % kHeld] = *reinterpret_cast<const uint4*>(st + (i * kWLoaders + t) * 16);
+        ks = *reinterpret_cast<const float*>(st + kWPair * DP + t * 4);
+        was = *reinterpret_cast<const float*>(st + kWPair * (DP + 4) + t * 4);
+        where = *reinterpret_cast<const long*>(st + kWPair * (DP + 8) + t * 8);
+      }
       ok = mbar_wait_warp(smem_u32(&m.k_empty[kb]), ((unit / L::kNK) & 1) ^ 1, gave_up);
       if (!ok) break;
       // K of this unit, which is in registers
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         // (heads of 128: the second half is in L2 by now)
-        if (i > 0 && i % kHeld == 0) bytes(i);
+        if (L::kRing == 0 && i > 0 && i % kHeld == 0) bytes(i);
         const int tok = lw * 32 + i * kPerPass + sub;
         const float f = __shfl_sync(0xffffffffu, ks, i * kPerPass + sub);
         uint4 lo, hi;
@@ -393,9 +448,12 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&m.k_full[kb]));
       // the next unit's K on its way
-      const WUnit after = ahead;
-      const bool next_there = more;
-      if (more) {
+      WUnit after = ahead;
+      bool next_there = more;
+      if (L::kRing > 0) {
+        after = s;
+        next_there = line.next(P, after);
+      } else if (more) {
         fetch(ahead, page_next);
         more = line.next(P, ahead);
         if (more) page_next = page_of(ahead);
@@ -568,7 +626,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weights_kernel(const WeightsPara
     __syncwarp();
   } else if (warp == 17) {
     // ---- K of the units to come into L2: a unit's registers alone do not keep memory busy ----
-    if (!LONG) {
+    if (!LONG && L::kRing == 0) {
       volatile int* loaded = &m.loaded;
       const long long t0 = clock64();
       for (int unit = 0; some; ++unit) {
