@@ -670,7 +670,7 @@ SD_API int sd_rope_table(int rot, double base, int kind, double factor, double o
  * The rows may serve as sd_verify's (target and draft rows cut by the same request's settings: the
  * answer is then distributed as the cut target rows), sd_draft_sample's or sd_token_logprobs's.
  * Arguments: B >= 0, J >= 1, 1 <= V <= SD_CUT_MAX_V; rows [B*J, V] of stride ld >= V (row r*J + j is
- *   request r's); probs [B*J, V] fp32 of stride ld_out >= V, not overlapping rows; kept [B, J] int32
+ *   request r's); probs [B*J, V] fp32 of stride ld_out >= V, in memory apart from rows'; kept [B, J] int32
  *   or NULL: how many entries are kept. A row that keeps none: zeros, kept 0, SD_ERR_ZERO_ROW.
  *   B*J <= 2^27.
  */

@@ -31,7 +31,7 @@ def weights_args(**over):
 def evict_args(**over):
     a = dict(B=2, Hkv=2, D=64, k_cache=P, v_cache=P, st_block=2048, st_tok=128, st_head=64, k_scale=P,
              v_scale=P, num_blocks=4, block_size=16, weights=P, table=P, max_blocks=4, to=None,
-             to_blocks=0, ctx=P, budget=8, sink=2, recent=3, kept=P, new_lens=P, err=None, stream=None)
+             to_blocks=0, ctx=P, budget=8, sink=2, recent=3, kept=P, new_lens=2 * P, err=None, stream=None)
     assert set(over) <= set(a)
     a.update(over)
     return list(a.values())
@@ -49,7 +49,7 @@ def rope_args(**over):
 def cut_args(draw, **over):
     a = dict(B=2, J=3, V=100, dtype=1, rows=P, ld=100, temperature=None, top_k=None, top_p=None,
              min_p=None)
-    a.update(dict(u=P, tokens=P, prob=None) if draw else dict(probs=P, ld_out=100))
+    a.update(dict(u=P, tokens=P, prob=None) if draw else dict(probs=1 << 30, ld_out=100))
     a.update(kept=None, err=None, stream=None)
     assert set(over) <= set(a)
     a.update(over)
@@ -109,9 +109,19 @@ def test_cut_rows_refuse(lib, draw, over, rc):
 def test_cut_rows_refuse_their_own(lib):
     assert lib.sd_truncate(*cut_args(False, ld_out=99)) == -2
     assert lib.sd_truncate(*cut_args(False, probs=None)) == -1
-    assert lib.sd_truncate(*cut_args(False, probs=P + 2)) == -4
+    assert lib.sd_truncate(*cut_args(False, probs=(1 << 30) + 2)) == -4
     assert lib.sd_sample(*cut_args(True, u=None)) == -1
     assert lib.sd_sample(*cut_args(True, tokens=None)) == -1
+
+
+def test_memory_that_may_not_be_shared(lib):
+    """An output that is its input keeps the strides; lengths and rows that are read again stay."""
+    assert lib.sd_rope(*rope_args(q_out=P, ld_qo=512)) == -2
+    assert lib.sd_rope(*rope_args(k_out=P, hs_ko=128)) == -2
+    assert lib.sd_kv_evict(*evict_args(new_lens=P, ctx=P)) == -2
+    assert lib.sd_truncate(*cut_args(False, rows=4096, probs=4096)) == -2
+    assert lib.sd_truncate(*cut_args(False, rows=4096, probs=4096 + 600 * 2 - 4)) == -2
+    assert lib.sd_truncate(*cut_args(False, rows=4096, probs=4096 - 600 * 4 + 4)) == -2
 
 
 @pytest.mark.parametrize("over", [

@@ -765,6 +765,7 @@ int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long st_blo
     return SD_E_SHAPE;
   if (B == 0) return SD_OK;
   if (!ctx_lens || !kept || !new_lens || (max_blocks > 0 && !block_table)) return SD_E_NULL;
+  if (new_lens == ctx_lens) return SD_E_SHAPE;  // (every head reads the old ones)
   if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale || !weights)) return SD_E_NULL;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return SD_E_ALIGN;
   const int dev = check_device();
@@ -797,6 +798,9 @@ int sd_rope(int n, int Hq, int Hk, int D, int rot, int pairs, const int32_t* pos
                  hs_ko % 8))
     return SD_E_ALIGN;
   if ((uintptr_t)turns % 8) return SD_E_ALIGN;
+  // an output that is its input has its strides
+  if (Hq > 0 && q == q_out && (ld_q != ld_qo || hs_q != hs_qo)) return SD_E_SHAPE;
+  if (Hk > 0 && k == k_out && (ld_k != ld_ko || hs_k != hs_ko)) return SD_E_SHAPE;
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_rope_launch(n, Hq, Hk, D, rot, pairs, positions, turns, scale, inverse, q, ld_q, hs_q,
@@ -840,7 +844,13 @@ int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld, const
   if (ld_out < V) return SD_E_SHAPE;
   if (B == 0) return SD_OK;
   if (!rows || !probs) return SD_E_NULL;
-  if ((uintptr_t)rows % (dtype == SD_F32_PROBS ? 4 : 2) || (uintptr_t)probs % 4) return SD_E_ALIGN;
+  const uintptr_t size = dtype == SD_F32_PROBS ? 4 : 2;
+  if ((uintptr_t)rows % size || (uintptr_t)probs % 4) return SD_E_ALIGN;
+  // rows are read again after some of probs is written
+  const uintptr_t last = (uintptr_t)B * J - 1;
+  const uintptr_t rows_end = (uintptr_t)rows + (last * ld + V) * size;
+  const uintptr_t probs_end = (uintptr_t)probs + (last * ld_out + V) * 4;
+  if ((uintptr_t)probs < rows_end && (uintptr_t)rows < probs_end) return SD_E_SHAPE;
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_rows_launch(B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p, probs, ld_out,
