@@ -83,6 +83,10 @@ struct RowShared {
   int index;
 };
 
+// 2^n in fp64, n from -1000 to 1000.
+__device__ __forceinline__ double two_to_the(int n) {
+  return __longlong_as_double((long long)(1023 + n) << 52);
+}
 __device__ __forceinline__ FF ff_sum(float a, float b) { return ff_two_sum(a, b); }
 
 // 2^y for y = d c (pairs), y <= 0, as a count of 2^-63 (0 below 2^-63): k / 64 is y's nearest multiple
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
     cluster.sync();
     if (!PROBS) return b;
     // A probability's bin holds 65536 values: two passes over the row find the one in question.
-    const double unit = exp2((double)place(b.key));
+    const double unit = two_to_the(place(b.key));
     if (b.count == 1 && by != kByKey) {
       b.key |= (uint32_t)b.w;  // the sum of the lower halves is that of the only entry
       b.w = (double)(bin_base(b.key) | (b.key & 0xffffu)) * unit;
@@ -1242,7 +1246,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     // A probability's place in its bin: by count (g), by sum (goal), or by key.
     auto inside = [&](Border b, int by, unsigned long long g, double goal, uint32_t key) -> Border {
       const int e = (int)(b.key >> 23);
-      const double unit = exp2((double)(e - 150 + 44));
+      const double unit = two_to_the(e - 150 + 44);
       if (b.count == 1 && by != 2) {
         b.key |= (uint32_t)b.w;
         b.w = (double)(0x800000u | (b.key & 0x7fffffu)) * unit;
@@ -1257,6 +1261,9 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         return b;
       }
       for (int level = 0; level < 2; ++level) {
+        // where the goal lies behind the sum before the bin, in its last places
+        const unsigned long long behind =
+            (unsigned long long)fmax((goal - b.sum) * two_to_the(150 - 44 - e), 0.0);
         for (int i = lane; i < 256; i += 32) sh.sub[i] = sh.sub_sum[i] = 0;
         __syncwarp();
         for (uint32_t i = lane; i < m; i += 32) {
@@ -1286,15 +1293,14 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         for (int i = lane * 8; i < lane * 8 + 8; ++i) {
           const uint32_t c = sh.sub[i];
           const unsigned long long u = units(i);
-          const double from = b.sum + (double)as * unit, to = b.sum + (double)(as + u) * unit;
           bool here;
           if (by == 0) here = g >= b.above + an && g < (unsigned long long)b.above + an + c;
           else if (by == 1)
-            here = c > 0 && (goal >= from || an == 0) && (goal < to || an + c == b.count);
+            here = c > 0 && (behind >= as || an == 0) && (behind < as + u || an + c == b.count);
           else here = (level ? key : key >> 8) == (level ? value(i) : value(i) >> 8);
           if (here) {
             hit = true;
-            got = Border{value(i), b.above + an, c, from,
+            got = Border{value(i), b.above + an, c, b.sum + (double)as * unit,
                          (double)(0x800000u | (value(i) & 0x7fffffu)) * unit};
           }
           an += c;
@@ -1666,7 +1672,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
       if (P.prob) {
         const double w = PROBS ? (double)__uint_as_float(key(j)) : (double)weight(key(j));
         // (in the sums' units: a probability's is 2^-50 of the power of two above the largest)
-        const double unit = PROBS ? exp2((double)(126 - top_exp + kSmallBits)) : 0x1p-13;
+        const double unit = PROBS ? two_to_the(126 - top_exp + kSmallBits) : 0x1p-13;
         P.prob[row] = (float)(w * unit / kept_sum);
       }
     }
