@@ -273,3 +273,17 @@ def test_many_requests():
     call(c, out, lse, err, before=c["before"], max_q=3, sm_scale=2.0 ** -6)
     check(c, out, lse, 2.0 ** -6)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 4), (80, 7)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_the_kernel_for_prompts(D, G, causal):
+    """Prompts in earnest and, by what is expected, single tokens and requests without any."""
+    c = make([700, 0, 1200, 31, 130], [700, 0, 650, 1, 0], 2 * G, 2, D, 16, seed=D)
+    lse = lse_of(c, D ** -0.5, causal=causal)
+    out, err = torch.full_like(c["before"], -3.0), torch.zeros(1, dtype=torch.int32, device=DEV)
+    live = [700, 0, 301, 1, 0]
+    call(c, out, lse, err, before=c["before"], max_q=1 << 20, causal=causal, decay=0.5,
+         live=torch.tensor(live, dtype=torch.int32, device=DEV))
+    check(c, out, lse, D ** -0.5, causal=causal, decay=0.5, live=live)
+    assert int(err) == 0

@@ -423,7 +423,8 @@ extern "C" int sd_kv_evict_launch(int B, int Hkv, int D, void* k_cache, void* v_
     set[dev].store(true, std::memory_order_release);
   }
   const long most = (long)max_blocks << log2_bs;
-  // CTAs of a request and head: more while the SMs have room for them and each has 1000 tokens.
+  // CTAs of a request and head: more while the SMs have room for them and each has 1000 tokens. (512
+  // requests and heads with 1, 2, 4: the call 102, 120, 168 us; 8 with 1 and 8: 85 and 39.)
   int C = 1;
   while (C < sdk::kSelCluster && (long)B * Hkv * C * 2 <= 304 && most > 2048L * C) C *= 2;
   const long part = (most + C - 1) / C;

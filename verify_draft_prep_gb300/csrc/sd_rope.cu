@@ -75,8 +75,8 @@ __device__ __forceinline__ typename RopeVec<W>::T pack(const float (&f)[W]) {
 // per_head threads has one unit each of the same head and goes over neighbouring heads, so that its
 // factors stay in registers until the token ends. 2 bytes are read and 2 written for each value, and
 // nothing else is large: bound by memory. 16384 tokens of 40 heads of 128: 60 us, 82% of the copy rate;
-// half of each head turned, neighbours paired, 8192 tokens: 33 us, 75%; a step's 384 tokens of 72 heads
-// of 64: 4.9 us in a graph, a launch and three dependent latencies.
+// half of each head turned, neighbours paired, 8192 tokens: 31 us, 80%; a step's 384 tokens of 72 heads
+// of 64: 3.9 us in a graph, a launch and three dependent latencies.
 template <int W, bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) {
   using T = typename RopeVec<W>::T;
@@ -206,8 +206,10 @@ extern "C" int sd_rope_launch(int n, int Hq, int Hk, int D, int rot, int pairs,
   P.hs_y[0] = hs_qo;
   P.ld_y[1] = ld_ko;
   P.hs_y[1] = hs_ko;
-  // A step's few tokens spread over the SMs, a prompt's share their CTA's setup.
-  P.chunk = n / (152 * 8) < 1 ? 1 : n / (152 * 8) > 8 ? 8 : n / (152 * 8);
+  // Tokens of a CTA: a step's few spread over the SMs, a prompt's share their CTA's setup. With 1, 2, 4,
+  // 8, 16: 384 tokens 4.9, 3.9, 4.1, 5.3, 7.7 us, 8192 42.9, 36.0, 32.7, 31.7, 30.8, 16384 124.7, 84.1,
+  // 68.9, 60.3, 60.0.
+  P.chunk = n / 304 < 2 ? 2 : n / 304 > 16 ? 16 : n / 304;
   // The widest accesses that every part of a head allows: 16 bytes, else 8 (halves) or a pair.
   if (pairs == SD_ROPE_HALVES) {
     if (rot % 16 == 0) return sdk::launch_rope<8, true>(P, stream);

@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
 // us): reading and counting 53 us (8 instructions an entry; a shared atomic of 32 different
 // addresses takes 2.5 cycles), the sums of the bins 12, the search 18, the drawn value's entries 38: 608
 // rows do not stay in L2, so they come from memory a second time. 1024 rows are two rounds of those
-// places, 331 us against 61 of memory. 2048 rows of logits cut: 964 us against 364; 384 of probabilities 488
+// places, 331 us against 61 of memory. 2048 rows of logits cut: 964 us against 364; 384 of probabilities 476
 // against 91 (each place that is looked for reads the row again). One row of 1024: 27 us, latency.
 // ---------------------------------------------------------------------------------------------
 constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQBins = 8192, kQRows = 257;

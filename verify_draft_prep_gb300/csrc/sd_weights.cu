@@ -63,7 +63,7 @@ struct WeightsParams {
   int32_t* err;
 };
 
-// Long: requests of many chunks (prompts), whose Q streams by while K stays.
+// LONG: requests of many chunks (prompts), whose Q streams by while K stays.
 template <int DP, bool LONG>
 struct WLayout {
   static constexpr int kTileBytes = kWTile * DP * 2;  // K of a tile, or Q of a chunk, as bf16
@@ -814,8 +814,11 @@ extern "C" int sd_kv_weights_launch(int B, int n, int max_q, int Hq, int Hkv, in
   P.before = before;
   P.weights = weights;
   P.err = err;
-  // Requests of more chunks than stay in shared memory are prompts.
-  if ((long)max_q * P.G > 2 * sdk::kWRows)
+  // Prompts of many chunks. The kernel for few against the one for many, in us: heads of 128, one token of
+  // 32000 19 to 30, 4 requests of 512, 1024, 2048 rows 38 to 44, 88 to 97, 158 to 165, 2 of 4096 and 8192
+  // rows 153 to 149, 293 to 281, a prompt of 32768 rows 751 to 362 (its units get cheaper along the
+  // context); heads of 64, 64 requests of 48 rows 85 to 204, 4 of 4096 rows 261 to 285.
+  if ((long)max_q * P.G > 4096)
     return D <= 64 ? sdk::launch_weights<64, true>(P, stream)
                    : sdk::launch_weights<128, true>(P, stream);
   return D <= 64 ? sdk::launch_weights<64, false>(P, stream)
