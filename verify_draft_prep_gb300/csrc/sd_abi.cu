@@ -622,8 +622,8 @@ int check_cache(int Hkv, int D, long st_block, long st_tok, long st_head, int nu
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// The kernels step over tokens, rows and requests in int, some hundreds at a time: their numbers stay
-// this far below 2^31.
+// The kernels step over tokens, rows and requests in int, up to 1023 at a time (in 64 bits where a step is
+// larger): their numbers stay this far below 2^31.
 constexpr long long kMostCounted = 2147483647LL - 1023;
 
 }  // namespace

@@ -68,10 +68,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_choose_kernel(const EvictPa
     P.new_lens[r] = keep;
     if (ctx < 0 || ctx > evict_covered(P)) raise_err(P.err, SD_ERR_KV_RANGE);
   }
-  const int all = C * kSelThreads, me = rank * kSelThreads + tid;
-  for (int i = keep + me; i < P.budget; i += all) kept[i] = -1;
+  // (budgets and lengths reach 2^31 - 1024, and a cluster's step is up to 4096: 64 bits)
+  const long all = C * kSelThreads, me = rank * kSelThreads + tid;
+  for (long i = keep + me; i < P.budget; i += all) kept[i] = -1;
   if (n <= P.budget) {
-    for (int i = me; i < n; i += all) kept[i] = i;
+    for (long i = me; i < n; i += all) kept[i] = (int)i;
     return;
   }
   if (C > 1) cluster.sync();  // (every CTA has begun: its shared memory may be written from here on)
