@@ -659,8 +659,9 @@ SD_API int sd_rope_table(int rot, double base, int kind, double factor, double o
  *   those with w >= min_p[r] w_max (<= 0 or NaN: all; above 1 as 1),
  * whichever is fewest, and the first entry always. T_r <= 0 (or NaN): the first entry alone. Entries of
  * weight 0 are never kept: probabilities <= 0, logits of -inf, all beside a +inf, and NaN. A
- * probability above 1 counts as 1. Which entries are kept, and which is drawn, is decided by sums with an
- * error of 2^-40. temperature, top_k, top_p, min_p are [B] or NULL (1, and off).
+ * probability above 1 counts as 1. Which entries are kept, and which is drawn, is decided by sums that
+ * are off by 2^-40 of the row's sum at most, however many entries and values there are. temperature,
+ * top_k, top_p, min_p are [B] or NULL (1, and off).
  */
 #define SD_CUT_MAX_V 524224
 

@@ -10,10 +10,11 @@
 //
 // Logits are bf16: a row has at most 65536 different values, so a histogram of all of them holds the
 // row exactly, and w is needed once for each value that occurs instead of once for each entry. That is
-// what lets the sums be exact enough for whole numbers to come out right: w in pairs of fp32 (2^-44),
-// sums in 64-bit integers. Probabilities have 32 bits: the histogram is over their upper 16, with the
-// sums of the lower 16 in whole numbers, and the one bin in question is resolved by reading the row
-// again (from L2).
+// what lets the sums be exact enough for whole numbers to come out right: w in pairs of fp32 (2^-43), and
+// from there on whole numbers of 2^-62 of the largest weight (81 bits), products with top-p and the
+// drawn number among them, so that nothing is rounded however many bins there are. Probabilities have 32
+// bits: the histogram is over their upper 16, with the sums of the lower 16 in whole numbers, and the
+// one bin in question is resolved by reading the row again (from L2).
 //
 // Two kernels. quick_kernel has 8192 bins, for logits of magnitude 2^-15 to 2^17 (and zero) and
 // probabilities from 2^-63 on: 32 or 64 KB, so that three or four rows are on an SM at a time and one
@@ -32,9 +33,13 @@ namespace sdk {
 constexpr int kRowThreads = 1024, kRowWarps = kRowThreads / 32;
 constexpr int kHistBytes = 131072;
 constexpr int kMostClusters = 8;
-// Sums are multiples of 2^-43 of the largest weight (logits) or of the power of two above it.
-constexpr int kSumBits = 43;
-constexpr double kSumUnit = 8796093022208.0;  // 2^43
+// Sums are multiples of 2^-62 of the largest weight (logits), of the power of two above it or of one
+// (probabilities): with up to 2^19 entries they have up to 81 bits, three numbers of 27 for a warp's
+// reduction. (As multiples of 2^-43 in 64 bits every bin was rounded by up to 2^-44, and thousands of
+// bins made it 2^-36 of a sum. With four numbers, of 2^-63: one token of each of 1024 rows 347 us
+// against 345.)
+constexpr int kSumBits = 62;
+constexpr double kSumUnit = 0x1p62;
 
 struct RowsParams {
   const void* rows;
@@ -59,19 +64,22 @@ struct RowsParams {
 constexpr int32_t kMarkToken = -2147483647 - 1;
 constexpr float kMarkProb = -1.f;
 
+typedef unsigned __int128 u128;
+
 // A value's place: entries of larger values and their sum, how many entries have the value, and the
 // weight of each (in units of the sums).
 struct Border {
   uint32_t key, above, count;
-  double sum, w;
+  unsigned long long w;
+  u128 sum;
 };
 
 struct RowShared {
   float2 two_to[64];               // 2^(j / 64) as pairs
   uint32_t warp_count[kRowWarps];
-  unsigned long long warp_sum[kRowWarps];
+  u128 warp_sum[kRowWarps];
   uint32_t rank_count[kMostClusters];
-  unsigned long long rank_sum[kMostClusters];
+  u128 rank_sum[kMostClusters];
   uint32_t rank_top[kMostClusters];
   uint32_t rank_eq[kMostClusters];
   Border found, inside;             // a bin, by the CTA that holds it; an entry of it, by each CTA
@@ -89,10 +97,10 @@ __device__ __forceinline__ double two_to_the(int n) {
 }
 __device__ __forceinline__ FF ff_sum(float a, float b) { return ff_two_sum(a, b); }
 
-// 2^y for y = d c (pairs), y <= 0, as a count of 2^-63 (0 below 2^-63): k / 64 is y's nearest multiple
+// 2^y for y = d c (pairs), y <= 0, as a count of 2^-62 (0 below 2^-62): k / 64 is y's nearest multiple
 // of 2^-6, 2^(k/64) from the table, and the rest e^u with |u| <= 0.0055, whose terms from the third on
 // need only fp32.
-__device__ __forceinline__ unsigned long long weight63(FF d, float2 c, const float2* two_to) {
+__device__ __forceinline__ unsigned long long weight62(FF d, float2 c, const float2* two_to) {
   const float p = d.hi * c.x;
   const float e = fmaf(d.hi, c.x, -p) + fmaf(d.hi, c.y, d.lo * c.x);
   const int k = __float2int_rn(p * 64.f);
@@ -111,22 +119,34 @@ __device__ __forceinline__ unsigned long long weight63(FF d, float2 c, const flo
   const float pl = fmaf(t.x, r.hi, -ph) + fmaf(t.x, rl, t.y * r.hi);
   const FF s = ff_sum(t.x, ph);
   const float lo = s.lo + pl + t.y;
-  const float up = __uint_as_float((uint32_t)(127 + 63 + (k >> 6)) << 23);
+  const float up = __uint_as_float((uint32_t)(127 + kSumBits + (k >> 6)) << 23);
   const long long w = (long long)__float2ull_rz(s.hi * up) + __float2ll_rn(lo * up);
-  return p > -63.f ? (unsigned long long)w : 0;
+  return p > (float)-kSumBits ? (unsigned long long)w : 0;
 }
 
-__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// The warp's sum by its integer reduction; the sum is below 2^81.
+__device__ __forceinline__ u128 warp_sum(u128 v) {
+  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7ffffffu);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27) & 0x7ffffffu);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 54));
+  return (u128)(a + ((unsigned long long)b << 27)) + ((u128)c << 54);
 }
-// The same for v < 2^62, by the warp's integer reduction.
-__device__ __forceinline__ unsigned long long warp_sum62(unsigned long long v) {
-  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x1fffffu);
-  const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 21) & 0x1fffffu);
-  const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 42));
-  return a + ((unsigned long long)b << 21) + ((unsigned long long)c << 42);
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
+  return __shfl_sync(0xffffffffu, v, lane);
+}
+__device__ __forceinline__ u128 from_lane(u128 v, int lane) {
+  return (u128)__shfl_sync(0xffffffffu, (unsigned long long)(v >> 64), lane) << 64 |
+         __shfl_sync(0xffffffffu, (unsigned long long)v, lane);
+}
+__device__ __forceinline__ uint32_t from_below(uint32_t v, int by) {
+  return __shfl_up_sync(0xffffffffu, v, by);
+}
+__device__ __forceinline__ unsigned long long from_below(unsigned long long v, int by) {
+  return __shfl_up_sync(0xffffffffu, v, by);
+}
+__device__ __forceinline__ u128 from_below(u128 v, int by) {
+  return (u128)__shfl_up_sync(0xffffffffu, (unsigned long long)(v >> 64), by) << 64 |
+         __shfl_up_sync(0xffffffffu, (unsigned long long)v, by);
 }
 template <typename T>
 __device__ __forceinline__ T warp_before(T v) {  // the sum over the lanes before this one
@@ -134,10 +154,49 @@ __device__ __forceinline__ T warp_before(T v) {  // the sum over the lanes befor
   T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = from_below(x, o);
     if (lane >= o) x += y;
   }
   return x - v;
+}
+
+__device__ __forceinline__ double sum_double(u128 v) {
+  return fma((double)(unsigned long long)(v >> 64), 0x1p64, (double)(unsigned long long)v);
+}
+// x * sum for 0 <= x <= 1, exact but for the places below 1, which are cut (and said to be there).
+__device__ __forceinline__ u128 share_of(float x, u128 sum, bool& more) {
+  const uint32_t b = __float_as_uint(x);
+  const int down = 150 - max(1, (int)(b >> 23));  // x is its 24-bit significand times 2^-down
+  const u128 all = sum * ((b >> 23 ? 0x800000u : 0u) | (b & 0x7fffffu));
+  more = down > 127 ? all != 0 : (all & (((u128)1 << down) - 1)) != 0;
+  return down > 127 ? (u128)0 : all >> down;
+}
+// The places in a running sum of `total` that a draw (u) and a top-p ask for: where u * kept lies, and the
+// last one before top_p * kept.
+__device__ __forceinline__ u128 draw_place(float u, u128 kept, u128 total) {
+  bool more;
+  const u128 g = share_of(u > 0.f ? fminf(u, 1.f) : 0.f, kept, more);
+  return g < total ? g : total - 1;
+}
+__device__ __forceinline__ u128 last_place(float top_p, u128 kept, u128 total) {
+  bool more;
+  const u128 g = share_of(fmaxf(top_p, 0.f), kept, more);
+  return more ? (g < total ? g : total - 1) : g == 0 ? (u128)0 : g - 1;
+}
+// d / w in whole numbers, most + 1 <= 2^19 or less: a quotient of fp32, put right.
+__device__ __forceinline__ uint32_t quotient(u128 d, unsigned long long w, uint32_t most) {
+  w = max(w, 1ull);
+  const float f = fmaf((float)(unsigned long long)(d >> 32), 0x1p32f, (float)(uint32_t)d);
+  uint32_t q = (uint32_t)fminf(__fdividef(f, (float)w), (float)most);
+  const u128 p = (u128)w * q;
+  if (p > d) --q;
+  else if (d - p >= w) ++q;
+  return min(q, most);
+}
+// `units` < 2^44 of 2^by, to nearest.
+__device__ __forceinline__ u128 shifted(unsigned long long units, int by) {
+  if (by >= 0) return (u128)units << by;
+  return by < -62 ? 0 : ((units >> (-by - 1)) + 1) >> 1;
 }
 
 // Orderable keys. Logits: 16 bits, ascending with the value, both zeros alike; 0 for what is never
@@ -370,7 +429,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
     const float hi = (float)c;
     sh.per_unit = make_float2(hi, (float)(c - (double)hi));
   }
-  if (tid == 65) sh.found = sh.inside = Border{0, 0, 0, 0.0, 0.0};
+  if (tid == 65) sh.found = sh.inside = Border{0, 0, 0, 0, 0};
   cluster.sync();  // (every CTA has begun: its shared memory may be written from here on)
   uint32_t top = 0;
   in.each(in.begin, in.end, tid, kRowThreads, [&](int, uint32_t k) {
@@ -396,25 +455,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
   const float top_value = PROBS ? 0.f : logit_value(top);
   const int top_exp = PROBS ? max(1, (int)(top >> 23)) : 0;
   const float2 per_unit = sh.per_unit;
-  // an entry's weight as a count of 2^-63 (logits)
+  // an entry's weight as a count of 2^-62 (logits)
   auto weight = [&](uint32_t k) -> unsigned long long {
-    if (k == top) return 1ull << 63;
+    if (k == top) return 1ull << kSumBits;
     if (top == 0xff80u) return 0;  // beside +inf nothing weighs anything
-    return weight63(ff_sum(logit_value(k), -top_value), per_unit, sh.two_to);
-  };
-  auto sum_of = [&](uint32_t n, unsigned long long w63) -> unsigned long long {
-    // n w 2^-63 in units of 2^-43, rounded
-    const unsigned long long hi = __umul64hi(w63, (unsigned long long)n << 44);
-    return hi + ((w63 * ((unsigned long long)n << 44)) >> 63);
+    return weight62(ff_sum(logit_value(k), -top_value), per_unit, sh.two_to);
   };
   // exponent of a probability bin's (or key's) last place, relative to the units of the sums
   auto place = [&](uint32_t k) { return max(1, (int)(k >> 23)) - top_exp + kSumBits - 24; };
   auto bin_base = [&](uint32_t k) {  // the 24-bit significand with the lower 16 bits zero
     return ((k >> 23) ? 0x800000u : 0u) | (k & 0x7f0000u);
-  };
-  auto shifted = [&](unsigned long long units, int by) -> unsigned long long {
-    if (by >= 0) return units << by;
-    return by < -62 ? 0 : ((units >> (-by - 1)) + 1) >> 1;
   };
   constexpr int kWords = PROBS ? kHistBytes / 8 : kHistBytes / 4;
   const int my_rows = kWords / 32 / (C * kRowWarps);
@@ -422,7 +472,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
   // the entries of this lane's word of a row: two values (logits), the larger first, or one bin
   struct Word {
     uint32_t n0, n1;
-    unsigned long long s0, s1, w0, w1;
+    u128 s0, s1;
+    unsigned long long w0, w1;
   };
   auto read_word = [&](int word) {
     Word x = {0, 0, 0, 0, 0, 0};
@@ -443,18 +494,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
         x.n1 += v >> 16;
       }
       const uint32_t k = (uint32_t)(0x7fff - word) * 2 + 1;
-      if (x.n0) x.s0 = sum_of(x.n0, x.w0 = weight(k));
-      if (x.n1) x.s1 = sum_of(x.n1, x.w1 = weight(k - 1));
+      if (x.n0) x.s0 = (u128)(x.w0 = weight(k)) * x.n0;
+      if (x.n1) x.s1 = (u128)(x.w1 = weight(k - 1)) * x.n1;
     }
     return x;
   };
   uint32_t row_count = 0;           // lane i: of row i, then of the rows before it
-  unsigned long long row_sum = 0;
+  u128 row_sum = 0;
   for (int i = 0; i < my_rows; ++i) {
     const Word x = read_word(word0 + i * 32 + lane);
     const uint32_t n = __reduce_add_sync(0xffffffffu, x.n0 + x.n1);
     if (n) {
-      const unsigned long long s = warp_sum64(x.s0 + x.s1);
+      const u128 s = warp_sum(x.s0 + x.s1);
       if (lane == i) {
         row_count = n;
         row_sum = s;
@@ -462,9 +513,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
     }
   }
   uint32_t count_at = warp_before(row_count);
-  unsigned long long sum_at = warp_before(row_sum);
-  uint32_t my_count = __shfl_sync(0xffffffffu, count_at + row_count, 31);
-  unsigned long long my_sum = __shfl_sync(0xffffffffu, sum_at + row_sum, 31);
+  u128 sum_at = warp_before(row_sum);
+  uint32_t my_count = from_lane(count_at + row_count, 31);
+  u128 my_sum = from_lane(sum_at + row_sum, 31);
   if (lane == 0) {
     sh.warp_count[warp] = my_count;
     sh.warp_sum[warp] = my_sum;
@@ -472,23 +523,23 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
   __syncthreads();
   {
     const uint32_t n = sh.warp_count[lane];
-    const unsigned long long s = sh.warp_sum[lane];
+    const u128 s = sh.warp_sum[lane];
     const uint32_t nb = warp_before(n);
-    const unsigned long long sb = warp_before(s);
+    const u128 sb = warp_before(s);
     if (warp == 0) {
-      const uint32_t all_n = __shfl_sync(0xffffffffu, nb + n, 31);
-      const unsigned long long all_s = __shfl_sync(0xffffffffu, sb + s, 31);
+      const uint32_t all_n = from_lane(nb + n, 31);
+      const u128 all_s = from_lane(sb + s, 31);
       if (lane < C) {
         cluster.map_shared_rank(sh.rank_count, lane)[rank] = all_n;
         cluster.map_shared_rank(sh.rank_sum, lane)[rank] = all_s;
       }
     }
-    count_at += __shfl_sync(0xffffffffu, nb, warp);
-    sum_at += __shfl_sync(0xffffffffu, sb, warp);
+    count_at += from_lane(nb, warp);
+    sum_at += from_lane(sb, warp);
   }
   cluster.sync();
   uint32_t total = 0;
-  unsigned long long total_sum = 0;
+  u128 total_sum = 0;
   for (int c = 0; c < C; ++c) {
     if (c == rank) {
       count_at += total;
@@ -497,40 +548,40 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
     total += sh.rank_count[c];
     total_sum += sh.rank_sum[c];
   }
-  const uint32_t count0 = __shfl_sync(0xffffffffu, count_at, 0);  // before this warp
-  const unsigned long long sum0 = __shfl_sync(0xffffffffu, sum_at, 0);
+  const uint32_t count0 = from_lane(count_at, 0);  // before this warp
+  const u128 sum0 = from_lane(sum_at, 0);
 
   // ---- 3. places in the order ----
-  // By count: the entry at place g (from 0). By sum: the one whose stretch of the running sum holds g.
-  // By key: the value `g`, whether it occurs or not. Every thread of the cluster calls this alike.
+  // By count: the entry at place g (from 0). By sum: the one whose stretch of the running sum holds place
+  // at_sum. By key: the value `g`, whether it occurs or not. Every thread of the cluster calls this alike.
   enum { kByCount, kBySum, kByKey };
-  auto find = [&](int by, unsigned long long g, double goal) -> Border {
+  auto find = [&](int by, uint32_t g, u128 at_sum) -> Border {
     const int key_word = by == kByKey ? (PROBS ? 0x3fff - (int)(g >> 16) : 0x7fff - (int)(g >> 1)) : 0;
     bool mine = by == kByCount ? g >= count0 && g - count0 < my_count
-                : by == kBySum ? g >= sum0 && g - sum0 < my_sum
+                : by == kBySum ? at_sum >= sum0 && at_sum - sum0 < my_sum
                                : key_word >= word0 && key_word < word0 + my_rows * 32;
     if (mine) {
       uint32_t at;
       if (by == kByKey) {
         at = (key_word - word0) >> 5;
       } else {
-        const bool before = by == kByCount ? count_at <= g : sum_at <= g;
+        const bool before = by == kByCount ? count_at <= g : sum_at <= at_sum;
         // (rows beyond this warp's, and empty ones, stand where the next one begins)
         at = 31 - __clz(__ballot_sync(0xffffffffu, before && lane < my_rows));
         // of rows that begin at the same place the last one is not empty
       }
-      const uint32_t base_n = __shfl_sync(0xffffffffu, count_at, at);
-      const unsigned long long base_s = __shfl_sync(0xffffffffu, sum_at, at);
+      const uint32_t base_n = from_lane(count_at, at);
+      const u128 base_s = from_lane(sum_at, at);
       const Word x = read_word(word0 + at * 32 + lane);
       const uint32_t n = base_n + warp_before(x.n0 + x.n1);
-      const unsigned long long s = base_s + warp_before(x.s0 + x.s1);
+      const u128 s = base_s + warp_before(x.s0 + x.s1);
       bool here, second = false;
       if (by == kByCount) {
         here = g >= n && g < n + x.n0 + x.n1;
         second = g >= n + x.n0;
       } else if (by == kBySum) {
-        here = g >= s && g < s + x.s0 + x.s1;
-        second = g >= s + x.s0;
+        here = at_sum >= s && at_sum < s + x.s0 + x.s1;
+        second = at_sum >= s + x.s0;
       } else {
         here = word0 + (int)at * 32 + lane == key_word;
         second = !PROBS && !(g & 1);
@@ -541,8 +592,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
         b.key = PROBS ? (uint32_t)(0x3fff - word) << 16 : (uint32_t)(0x7fff - word) * 2 + (second ? 0 : 1);
         b.above = n + (second ? x.n0 : 0);
         b.count = second ? x.n1 : x.n0;
-        b.sum = (double)(s + (second ? x.s0 : 0));
-        b.w = PROBS ? (double)x.w0 : (double)(second ? x.w1 : x.w0) * 0x1p-20;
+        b.sum = s + (second ? x.s0 : 0);
+        b.w = second ? x.w1 : x.w0;
         for (int c = 0; c < C; ++c) *cluster.map_shared_rank(&sh.found, c) = b;
       }
     }
@@ -551,10 +602,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
     cluster.sync();
     if (!PROBS) return b;
     // A probability's bin holds 65536 values: two passes over the row find the one in question.
-    const double unit = two_to_the(place(b.key));
+    const int up = place(b.key);
+    auto one = [&](uint32_t k) {
+      return (unsigned long long)shifted(bin_base(k) | (k & 0xffffu), up);
+    };
     if (b.count == 1 && by != kByKey) {
       b.key |= (uint32_t)b.w;  // the sum of the lower halves is that of the only entry
-      b.w = (double)(bin_base(b.key) | (b.key & 0xffffu)) * unit;
+      b.w = one(b.key);
       return b;
     }
     for (int level = 0; level < 2; ++level) {
@@ -593,20 +647,18 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
           before_n += sh.merged[w];
           before_s += sh.merged_sum[w];
         }
-        const double from = b.sum + (double)before_s * unit, to = b.sum + (double)(before_s + s) * unit;
+        const u128 from = b.sum + shifted(before_s, up), to = b.sum + shifted(before_s + s, up);
         bool here;
         if (by == kByCount) {
           here = g >= b.above + before_n && g < (unsigned long long)b.above + before_n + n;
         } else if (by == kBySum) {
-          // (the bin's own sum was rounded: what lies past its last entry is the last entry's)
-          here = n > 0 && (goal >= from || before_n == 0) &&
-                 (goal < to || before_n + n == b.count);
+          // (the bin's own sum may have been rounded: what lies past its last entry is the last entry's)
+          here = n > 0 && (at_sum >= from || before_n == 0) && (at_sum < to || before_n + n == b.count);
         } else {
           here = (uint32_t)(g >> shift) == key >> shift;
         }
         if (here)
-          sh.inside = Border{key, b.above + before_n, n, from,
-                             level ? (double)(bin_base(key) | (key & 0xffffu)) * unit : 0.0};
+          sh.inside = Border{key, b.above + before_n, n, level ? one(key) : 0, from};
       }
       cluster.sync();
       b = sh.inside;
@@ -632,48 +684,46 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
 
   // The last entry kept, and the sum of those kept.
   uint32_t n = total;
-  Border last = {0, 0, 0, 0.0, 0.0};
+  Border last = {0, 0, 0, 0, 0};
   bool cut = false;
-  double kept_sum = (double)total_sum;
+  u128 kept_sum = total_sum;
   auto cut_at = [&](uint32_t m, const Border& b) {
     n = m;
     last = b;
     cut = true;
-    kept_sum = b.sum + (double)(m - b.above) * b.w;
+    kept_sum = b.sum + (u128)b.w * (m - b.above);
   };
   uint32_t k = 0x7fffffffu;
   if (P.top_k && P.top_k[req] > 0) k = (uint32_t)P.top_k[req];
-  if (!PROBS && top == 0xff80u) k = min(k, find(kByKey, top, 0.0).count);
+  if (!PROBS && top == 0xff80u) k = min(k, find(kByKey, top, 0).count);
   if (greedy) k = 1;
-  if (k < n) cut_at(k, find(kByCount, k - 1, 0.0));
+  if (k < n) cut_at(k, find(kByCount, k - 1, 0));
   const float top_p = P.top_p && !greedy ? P.top_p[req] : 1.f;
   if (top_p < 1.f && n > 1) {
     // the last entry before which less than top_p of the sum lies
-    const double goal = (double)fmaxf(top_p, 0.f) * kept_sum;
-    const double g = fmin(fmax(ceil(goal) - 1.0, 0.0), fmax(ceil(kept_sum) - 1.0, 0.0));
-    const Border b = find(kBySum, min((unsigned long long)g, total_sum - 1), g);
-    const double j = ceil((goal - b.sum) / b.w);
-    const uint32_t m = b.above + (j >= (double)b.count ? b.count : j >= 1.0 ? (uint32_t)j : 1u);
+    const u128 at = last_place(top_p, kept_sum, total_sum);
+    const Border b = find(kBySum, 0, at);
+    const uint32_t m = b.above + 1 + quotient(at > b.sum ? at - b.sum : 0, b.w, b.count - 1);
     if (m < n) cut_at(m, b);
   }
   const float min_p = P.min_p && !greedy ? P.min_p[req] : 0.f;
   if (min_p > 0.f && n > 1) {
     uint32_t m;
     if (min_p >= 1.f) {
-      m = find(kByKey, top, 0.0).count;
+      m = find(kByKey, top, 0).count;
     } else if (PROBS) {
       const float t = __double2float_ru((double)min_p * (double)__uint_as_float(top));
-      const Border b = find(kByKey, max(1u, __float_as_uint(t)), 0.0);
+      const Border b = find(kByKey, max(1u, __float_as_uint(t)), 0);
       m = b.above + b.count;
     } else {
       const double t = (double)top_value + fmin(fmax((double)T, 0x1p-100), 0x1p100) * log((double)min_p);
       const uint32_t o = orderable(__double2float_ru(t));
       const uint32_t key = o & 0x80000000u ? (o + 0xffffu) >> 16 : o >> 16;
-      const Border b = find(kByKey, min(max(key, 0x80u), top), 0.0);
+      const Border b = find(kByKey, min(max(key, 0x80u), top), 0);
       m = b.above + b.count;
     }
     m = max(m, 1u);
-    if (m < n) cut_at(m, find(kByCount, m - 1, 0.0));
+    if (m < n) cut_at(m, find(kByCount, m - 1, 0));
   }
   if (rank == 0 && tid == 0 && P.kept) P.kept[row] = (int32_t)n;
 
@@ -714,33 +764,29 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
   };
 
   if (!WRITE) {
-    float u = P.u[row];
-    u = u > 0.f ? u : 0.f;
-    const double goal = fmin((double)u * kept_sum, kept_sum);
-    const double g = fmin(floor(goal), fmax(ceil((double)total_sum) - 1.0, 0.0));
     Border b;
     uint32_t j = 0;
     if (n == 1) {
-      b = cut ? last : find(kByCount, 0, 0.0);
+      b = cut ? last : find(kByCount, 0, 0);
     } else {
-      b = find(kBySum, min((unsigned long long)g, total_sum - 1), goal);
-      const double f = floor((goal - b.sum) / b.w);
-      j = f >= (double)(b.count - 1) ? b.count - 1 : f > 0.0 ? (uint32_t)f : 0u;
+      const u128 at = draw_place(P.u[row], kept_sum, total_sum);
+      b = find(kBySum, 0, at);
+      j = quotient(at > b.sum ? at - b.sum : 0, b.w, b.count - 1);
       if (b.above + j >= n) {
-        b = cut ? last : find(kByCount, n - 1, 0.0);
+        b = cut ? last : find(kByCount, n - 1, 0);
         j = n - 1 - b.above;
       }
     }
     const int at = nth(b.key, j);
     if (rank == 0 && tid == 0) {
       P.tokens[row] = at;
-      if (P.prob) P.prob[row] = (float)(b.w / kept_sum);
+      if (P.prob) P.prob[row] = (float)((double)b.w / sum_double(kept_sum));
     }
   } else {
     int edge = 0x7fffffff;  // entries of the last value are kept up to here
     if (cut && n - last.above < last.count) edge = nth(last.key, n - last.above - 1);
     const uint32_t least = cut ? last.key : 1u;
-    const float inv = (float)(kSumUnit / kept_sum);
+    const float inv = (float)(kSumUnit / sum_double(kept_sum));
     const float scale = PROBS ? __uint_as_float((uint32_t)(127 + 126 - top_exp) << 23) : 1.f;
     float* out = P.probs + (size_t)row * P.ld_out;
     auto value = [&](int i, uint32_t x) {
@@ -775,24 +821,22 @@ constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQBins = 8192, kQRows =
 constexpr uint16_t kLeast = 0xc7ff;  // the least logit that has a counter, -130560
 constexpr int kQSmall = 256;    // logits below 2^-15 that a CTA may have
 constexpr int kQList = 2048;    // entries of one bin of probabilities
-constexpr double kQUnit = 17592186044416.0;  // sums of probabilities: multiples of 2^-44
 
 enum { kOpEnd, kOpNth, kOpCollect, kOpCount, kOpMark, kOpNothing };
 
+// (At most 16 KB: four CTAs with their counters in 196 KB leave 60 KB of L1 for the row's second reading.
+// With 17 KB, and so 28 KB of L1, that takes 80000 cycles a row instead of 70000.)
 struct QuickShared {
   float2 two_to[64];
   uint32_t row_count[kQRows];  // of a row of bins, then of those before it (rank 0's)
-  unsigned long long row_sum[kQRows];
-  uint8_t filled[kQThreads];
-  uint16_t todo[kQRows];
+  u128 row_sum[kQRows];
   int n_todo;
   uint32_t rank_first[kMostClusters];  // the first bin in order that a CTA has anything in
   uint32_t rank_zero[kMostClusters], rank_small[kMostClusters], rank_far[kMostClusters],
       rank_bad[kMostClusters];
-  unsigned long long rank_small_sum[kMostClusters];
+  unsigned long long rank_small_sum[kMostClusters];  // (of 256 weights at most, in units of 2^-54)
   uint32_t zero, small, far, bad, first, eq[kQWarps];
   unsigned long long small_sum;
-  uint16_t small_at[kQSmall];
   float2 per_unit;
   // of rank 0's first warp to all: what to do, and the row's cut
   int op;
@@ -805,6 +849,11 @@ struct QuickShared {
   union {
     uint16_t list[kQList];
     int at[kQList];  // or indices of entries of one value
+    struct {         // or, before the search, which rows of bins hold anything, and the small logits
+      uint8_t filled[kQThreads];
+      uint16_t todo[kQRows];
+      uint16_t small_at[kQSmall];
+    };
   };
   uint32_t sub[256], sub_sum[256];
 };
@@ -824,6 +873,8 @@ __device__ __forceinline__ int quick_slot(uint32_t bits) {
 __device__ __forceinline__ bool quick_has(uint32_t bits) {
   return ((bits ^ bits << 1) & 0x7000u) == 0x4000u;
 }
+
+static_assert(sizeof(QuickShared) <= 16384, "shared memory of four CTAs");
 
 template <bool PROBS, bool WRITE>
 __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const RowsParams P) {
@@ -991,15 +1042,10 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       : 0u;
   const float top_value = bf16_bits_to_float(top_bits);
   const float2 per_unit = sh.per_unit;
-  // a logit's weight as a count of 2^-63
+  // a logit's weight as a count of 2^-62
   auto weight = [&](uint32_t bits) -> unsigned long long {
-    if (bits == top_bits) return 1ull << 63;
-    return weight63(ff_sum(bf16_bits_to_float(bits), -top_value), per_unit, sh.two_to);
-  };
-  auto sum_of = [&](uint32_t n, unsigned long long w63) -> unsigned long long {
-    // n w 2^-63 in units of 2^-43, rounded
-    const unsigned long long hi = __umul64hi(w63, (unsigned long long)n << 44);
-    return hi + ((w63 * ((unsigned long long)n << 44)) >> 63);
+    if (bits == top_bits) return 1ull << kSumBits;
+    return weight62(ff_sum(bf16_bits_to_float(bits), -top_value), per_unit, sh.two_to);
   };
   // a bin's entries (and, of probabilities, the sum of their lower halves)
   auto count_of = [&](int r, unsigned long long& lows) -> uint32_t {
@@ -1020,22 +1066,22 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     return n;
   };
   // their sum; w: the weight of each (logits)
-  auto bin_sum = [&](int r, uint32_t n, unsigned long long lows, unsigned long long& w) {
-    if (!PROBS) return sum_of(n, w = weight(quick_bits(r, lane)));
-    if (n == 0) return 0ull;
+  auto bin_sum = [&](int r, uint32_t n, unsigned long long lows, unsigned long long& w) -> u128 {
+    if (!PROBS) return (u128)(w = weight(quick_bits(r, lane))) * n;
+    if (n == 0) return 0;
     const uint32_t k = (uint32_t)(0x3fff - (r * 32 + lane));
     const unsigned long long units = (unsigned long long)n * ((0x80u | (k & 0x7fu)) << 16) + lows;
-    const int by = (int)(k >> 7) - 150 + 44;  // the significand's last place, in units of 2^-44
-    return by >= 0 ? units << by : by < -62 ? 0ull : ((units >> (-by - 1)) + 1) >> 1;
+    // (the significand's last place, in units of 2^-62)
+    return shifted(units, (int)(k >> 7) - 150 + kSumBits);
   };
 
   // ---- 2. counts and sums of the rows of bins, into rank 0 ----
   if (!PROBS) {  // small logits weigh for themselves, and stand beside zero
     unsigned long long s = 0;
     const uint32_t m = min(sh.small, (uint32_t)kQSmall);
-    if ((uint32_t)tid < m) s = sum_of(1, weight(sh.small_at[tid]));
+    if ((uint32_t)tid < m) s = ((weight(sh.small_at[tid]) >> 7) + 1) >> 1;
     if (m) {
-      s = warp_sum64(s);
+      s = (unsigned long long)warp_sum(s);
       if (lane == 0 && s) atomicAdd(&sh.small_sum, s);
     }
     __syncthreads();
@@ -1068,7 +1114,8 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
   const int rows_todo = C == 1 ? sh.n_todo : kRowsOf;
   for (int i0 = rank * kQWarps + warp; i0 < rows_todo; i0 += kTogether * C * kQWarps) {
     uint32_t n[kTogether];
-    unsigned long long s[kTogether], w;
+    unsigned long long low[kTogether], w;
+    u128 s[kTogether];
     int r[kTogether];
     bool any = false;
 #pragma unroll
@@ -1076,22 +1123,22 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       const int i = i0 + k * C * kQWarps;
       r[k] = i < rows_todo ? C == 1 ? sh.todo[i] : i : -1;
       n[k] = 0;
-      s[k] = 0;
-      if (r[k] >= 0) n[k] = count_of(r[k], s[k]);
+      s[k] = low[k] = 0;
+      if (r[k] >= 0) n[k] = count_of(r[k], low[k]);
       any |= n[k] != 0;
     }
     if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-      for (int k = 0; k < kTogether; ++k) s[k] = bin_sum(max(r[k], 0), n[k], s[k], w);
+      for (int k = 0; k < kTogether; ++k) s[k] = bin_sum(max(r[k], 0), n[k], low[k], w);
     }
 #pragma unroll
     for (int k = 0; k < kTogether; ++k) {
       const uint32_t all = __reduce_add_sync(0xffffffffu, n[k]);
-      if (all) s[k] = warp_sum62(s[k]);
+      if (all) s[k] = warp_sum(s[k]);
       if (lane == 0 && r[k] >= 0) {
         QuickShared* s0 = C == 1 ? &sh : cluster.map_shared_rank(&sh, 0);
         s0->row_count[r[k]] = all;
-        s0->row_sum[r[k]] = all ? s[k] : 0;
+        s0->row_sum[r[k]] = all ? s[k] : (u128)0;
       }
     }
   }
@@ -1186,12 +1233,12 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     // counts and sums before every row
     constexpr int kPer = (kQRows + 31) / 32;
     uint32_t n = 0;
-    unsigned long long s = 0;
+    u128 s = 0;
     if (!PROBS) {
       for (int c = 0; c < C; ++c) s += sh.rank_small_sum[c];
       if (lane == 0) {
         sh.row_count[128] += smalls;
-        sh.row_sum[128] += s;
+        sh.row_sum[128] += s << 8;
       }
       s = 0;
       __syncwarp();
@@ -1202,13 +1249,13 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         s += sh.row_sum[lane * kPer + i];
       }
     uint32_t n_at = warp_before(n);
-    unsigned long long s_at = warp_before(s);
-    const uint32_t binned = __shfl_sync(0xffffffffu, n_at + n, 31);
-    const unsigned long long total_sum = __shfl_sync(0xffffffffu, s_at + s, 31);
+    u128 s_at = warp_before(s);
+    const uint32_t binned = from_lane(n_at + n, 31);
+    const u128 total_sum = from_lane(s_at + s, 31);
     for (int i = 0; i < kPer; ++i)
       if (lane * kPer + i < kRowsOf) {
         const uint32_t a = sh.row_count[lane * kPer + i];
-        const unsigned long long b = sh.row_sum[lane * kPer + i];
+        const u128 b = sh.row_sum[lane * kPer + i];
         sh.row_count[lane * kPer + i] = n_at;
         sh.row_sum[lane * kPer + i] = s_at;
         n_at += a;
@@ -1218,7 +1265,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     const uint32_t total = binned + far;
     // far entries have to weigh nothing beside the others
     bool mark = bad;
-    if (PROBS) mark |= total > 0 && total_sum < (unsigned long long)(kQUnit / 2);
+    if (PROBS) mark |= total > 0 && total_sum < (u128)1 << (kSumBits - 1);
     else if (far) mark |= !some || !((-130560.f - top_value) * per_unit.x < -64.f);
     if (!PROBS && some && first == 4096 && smalls) mark = true;
 
@@ -1234,22 +1281,16 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       if (op == kOpNth) meet();  // (nth's own)
       if (op == kOpNth || op == kOpCollect || op == kOpCount) meet();
     };
-    // The whole number at or below d / w, d >= 0 (a quotient of fp32, put right).
-    auto quotient = [](double d, double w) -> double {
-      double q = (double)floorf(__fdividef((float)d, (float)w));
-      const double r = fma(-q, w, d);
-      if (r < 0.0) q -= 1.0;
-      else if (r >= w) q += 1.0;
-      return q;
-    };
     uint32_t listed_bin = 0;
-    // A probability's place in its bin: by count (g), by sum (goal), or by key.
-    auto inside = [&](Border b, int by, unsigned long long g, double goal, uint32_t key) -> Border {
-      const int e = (int)(b.key >> 23);
-      const double unit = two_to_the(e - 150 + 44);
+    // A probability's place in its bin: by count (g), by sum (at_sum), or by key.
+    auto inside = [&](Border b, int by, uint32_t g, u128 at_sum, uint32_t key) -> Border {
+      const int up = (int)(b.key >> 23) - 150 + kSumBits;  // of its last place, in units of the sums
+      auto one = [&](uint32_t k) {
+        return (unsigned long long)shifted(0x800000u | (k & 0x7fffffu), up);
+      };
       if (b.count == 1 && by != 2) {
         b.key |= (uint32_t)b.w;
-        b.w = (double)(0x800000u | (b.key & 0x7fffffu)) * unit;
+        b.w = one(b.key);
         return b;
       }
       // (the last bin's entries are still listed, if it was this one)
@@ -1261,9 +1302,9 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         return b;
       }
       for (int level = 0; level < 2; ++level) {
-        // where the goal lies behind the sum before the bin, in its last places
-        const unsigned long long behind =
-            (unsigned long long)fmax((goal - b.sum) * two_to_the(150 - 44 - e), 0.0);
+        // how far behind the sum before the bin the place lies, in the bin's last places
+        const u128 d = at_sum > b.sum ? at_sum - b.sum : 0;
+        const unsigned long long behind = (unsigned long long)(up >= 0 ? d >> up : d << -up);
         for (int i = lane; i < 256; i += 32) sh.sub[i] = sh.sub_sum[i] = 0;
         __syncwarp();
         for (uint32_t i = lane; i < m; i += 32) {
@@ -1300,8 +1341,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
           else here = (level ? key : key >> 8) == (level ? value(i) : value(i) >> 8);
           if (here) {
             hit = true;
-            got = Border{value(i), b.above + an, c, b.sum + (double)as * unit,
-                         (double)(0x800000u | (value(i) & 0x7fffffu)) * unit};
+            got = Border{value(i), b.above + an, c, one(value(i)), b.sum + shifted(as, up)};
           }
           an += c;
           as += u;
@@ -1311,16 +1351,16 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         b.key = __shfl_sync(0xffffffffu, got.key, src);
         b.above = __shfl_sync(0xffffffffu, got.above, src);
         b.count = __shfl_sync(0xffffffffu, got.count, src);
-        b.sum = __shfl_sync(0xffffffffu, got.sum, src);
+        b.sum = from_lane(got.sum, src);
         b.w = __shfl_sync(0xffffffffu, got.w, src);
         __syncwarp();
       }
       return b;
     };
-    // The entry at place g of the order (by 0), the one whose stretch of the running sum holds g (by
-    // 1), or a value, whether it occurs or not (by 2; g its place among the bins).
-    auto find = [&](int by, unsigned long long g, double goal, uint32_t key) -> Border {
-      Border b = {0, 0, 1, 0.0, 1.0};
+    // The entry at place g of the order (by 0), the one whose stretch of the running sum holds place at_sum
+    // (by 1), or a value, whether it occurs or not (by 2; g its place among the bins).
+    auto find = [&](int by, uint32_t g, u128 at_sum, uint32_t key) -> Border {
+      Border b = {0, 0, 1, 1, 0};
       if (by == 0 && g >= binned) {
         mark = true;
         return b;
@@ -1332,7 +1372,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         int lo = 0, hi = kRowsOf;  // the last row that begins at g or before
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (by == 0 ? sh.row_count[mid] <= g : sh.row_sum[mid] <= g) lo = mid;
+          if (by == 0 ? sh.row_count[mid] <= g : sh.row_sum[mid] <= at_sum) lo = mid;
           else hi = mid;
         }
         r = lo;
@@ -1343,33 +1383,32 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       }
       unsigned long long lows, w = 0;
       const uint32_t n = count_of(r, lows);
-      const unsigned long long s = bin_sum(r, n, lows, w);
+      const u128 s = bin_sum(r, n, lows, w);
       if (PROBS) w = lows;
       const uint32_t an = sh.row_count[r] + warp_before(n);
-      const unsigned long long as = sh.row_sum[r] + warp_before(s);
+      const u128 as = sh.row_sum[r] + warp_before(s);
       const bool here = by == 0   ? g >= an && g < an + n
-                        : by == 1 ? g >= as && g < as + s
-                                  : lane == (int)(g & 31);
+                        : by == 2 ? lane == (int)(g & 31)
+                                  : at_sum >= as && at_sum < as + s;
       const uint32_t who = __ballot_sync(0xffffffffu, here);
       const int src = who ? __ffs(who) - 1 : 0;
       b.key = PROBS ? (uint32_t)(0x3fff - (r * 32 + src)) << 16 : logit_key(quick_bits(r, src));
       b.above = __shfl_sync(0xffffffffu, an, src);
       b.count = __shfl_sync(0xffffffffu, n, src);
-      b.sum = (double)__shfl_sync(0xffffffffu, as, src);
-      w = __shfl_sync(0xffffffffu, w, src);
-      b.w = PROBS ? (double)w : (double)w * 0x1p-20;
-      return PROBS ? inside(b, by, g, goal, key) : b;
+      b.sum = from_lane(as, src);
+      b.w = __shfl_sync(0xffffffffu, w, src);
+      return PROBS ? inside(b, by, g, at_sum, key) : b;
     };
 
     uint32_t keep = total;
-    Border last = {0, 0, 0, 0.0, 0.0};
+    Border last = {0, 0, 0, 0, 0};
     bool cut = false;
-    double kept_sum = (double)total_sum;
+    u128 kept_sum = total_sum;
     auto cut_at = [&](uint32_t m, const Border& b) {
       keep = m;
       last = b;
       cut = true;
-      kept_sum = b.sum + (double)(m - b.above) * b.w;
+      kept_sum = b.sum + (u128)b.w * (m - b.above);
     };
     int at = 0;
     float prob = 0.f;
@@ -1378,44 +1417,41 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
       uint32_t k = 0x7fffffffu;
       if (P.top_k && P.top_k[req] > 0) k = (uint32_t)P.top_k[req];
       if (greedy) k = 1;
-      if (k < keep && k <= binned) cut_at(k, find(0, k - 1, 0.0, 0));
+      if (k < keep && k <= binned) cut_at(k, find(0, k - 1, 0, 0));
       const float top_p = P.top_p && !greedy ? P.top_p[req] : 1.f;
       if (!mark && top_p < 1.f && keep > 1) {
         // the last entry before which less than top_p of the sum lies
-        const double goal = (double)fmaxf(top_p, 0.f) * kept_sum;
-        const double g = fmin(fmax(ceil(goal) - 1.0, 0.0), fmax(ceil(kept_sum) - 1.0, 0.0));
-        const Border b = find(1, min((unsigned long long)g, total_sum - 1), g, 0);
-        double j = quotient(fmax(goal - b.sum, 0.0), b.w);
-        if (fma(-j, b.w, goal - b.sum) > 0.0) j += 1.0;
-        const uint32_t m = b.above + (j >= (double)b.count ? b.count : j >= 1.0 ? (uint32_t)j : 1u);
+        const u128 at = last_place(top_p, kept_sum, total_sum);
+        const Border b = find(1, 0, at, 0);
+        const uint32_t m = b.above + 1 + quotient(at > b.sum ? at - b.sum : 0, b.w, b.count - 1);
         if (m < keep) cut_at(m, b);
       }
       const float min_p = P.min_p && !greedy ? P.min_p[req] : 0.f;
       if (!mark && min_p > 0.f && keep > 1) {
         uint32_t m = keep;
         if (PROBS) {
-          const Border t = find(0, 0, 0.0, 0);  // the largest
+          const Border t = find(0, 0, 0, 0);  // the largest
           if (min_p >= 1.f) {
             m = t.count;
           } else if (!mark) {
             const uint32_t key =
                 __float_as_uint(__double2float_ru((double)min_p * (double)__uint_as_float(t.key)));
             if (key >> 29 == 1) {
-              const Border b = find(2, 0x3fff - (key >> 16), 0.0, key);
+              const Border b = find(2, 0x3fff - (key >> 16), 0, key);
               m = b.above + b.count;
             } else if (far) {
               mark = true;
             }
           }
         } else if (min_p >= 1.f) {
-          m = find(0, 0, 0.0, 0).count;
+          m = find(0, 0, 0, 0).count;
         } else {
           // the least logit that stays: near an estimate in fp32, 32 of them are weighed
           const float unit = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
           const uint32_t topk = logit_key(top_bits);
           const uint32_t near = orderable(fmaf(unit, __logf(min_p), top_value)) >> 16;
           const uint32_t mine = min(max((int)near - 16 + lane, 1), (int)topk);
-          const unsigned long long least_w = __float2ull_rn(min_p * 0x1p63f);
+          const unsigned long long least_w = __float2ull_rn(min_p * (float)kSumUnit);
           const uint32_t mine_bits = mine & 0x8000u ? mine & 0x7fffu : ~mine & 0xffffu;
           const uint32_t stays = __ballot_sync(0xffffffffu, weight(mine_bits) >= least_w);
           // (the weights ascend with the lane; the estimate is good to a few values, or all is marked)
@@ -1432,12 +1468,12 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
             else m = bits & 0x8000u ? sh.row_count[129] : sh.row_count[128];
           } else {
             const uint32_t i = mag - 0x3800u;
-            const Border b = find(2, mag == 0 ? 128 * 32 : bits & 0x8000u ? 129 * 32 + i : 4095 - i, 0.0, 0);
+            const Border b = find(2, mag == 0 ? 128 * 32 : bits & 0x8000u ? 129 * 32 + i : 4095 - i, 0, 0);
             m = b.above + b.count;
           }
         }
         m = max(m, 1u);
-        if (!mark && m < keep) cut_at(m, find(0, m - 1, 0.0, 0));
+        if (!mark && m < keep) cut_at(m, find(0, m - 1, 0, 0));
       }
       if (!mark && !cut && far) {  // all that is a number is kept, or as many as top_k
         if (!PROBS) {
@@ -1447,27 +1483,23 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         if (k < keep) mark = true;
       }
       if (!mark && !WRITE) {
-        float u = P.u[row];
-        u = u > 0.f ? u : 0.f;
         Border b;
         uint32_t j = 0;
         if (keep == 1) {
-          b = cut ? last : find(0, 0, 0.0, 0);
+          b = cut ? last : find(0, 0, 0, 0);
         } else {
-          const double goal = fmin((double)u * kept_sum, kept_sum);
-          const double g = fmin(floor(goal), fmax(ceil((double)total_sum) - 1.0, 0.0));
-          b = find(1, min((unsigned long long)g, total_sum - 1), goal, 0);
-          const double f = quotient(fmax(goal - b.sum, 0.0), b.w);
-          j = f >= (double)(b.count - 1) ? b.count - 1 : f > 0.0 ? (uint32_t)f : 0u;
+          const u128 at_sum = draw_place(P.u[row], kept_sum, total_sum);
+          b = find(1, 0, at_sum, 0);
+          j = quotient(at_sum > b.sum ? at_sum - b.sum : 0, b.w, b.count - 1);
           if (!mark && b.above + j >= keep) {
-            b = cut ? last : find(0, keep - 1, 0.0, 0);
+            b = cut ? last : find(0, keep - 1, 0, 0);
             j = keep - 1 - b.above;
           }
         }
         if (!mark) {
           ask(kOpNth, b.key, j, b.count);
           at = sh.index;
-          prob = __fdiv_rn((float)b.w, (float)kept_sum);
+          prob = __fdiv_rn((float)b.w, (float)sum_double(kept_sum));
         }
       }
       if (!mark && WRITE && cut && keep - last.above < last.count) {
@@ -1478,7 +1510,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     if (lane == 0) {
       sh.edge = edge;
       sh.least = cut ? last.key : 1u;
-      sh.inv = __fdiv_rn((float)(PROBS ? kQUnit : kSumUnit), (float)kept_sum);
+      sh.inv = __fdiv_rn((float)kSumUnit, (float)sum_double(kept_sum));
       if (!mark) {
         if (total == 0) raise_err(P.err, SD_ERR_ZERO_ROW);
         if (P.kept) P.kept[row] = (int32_t)keep;
@@ -1602,13 +1634,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
     per_unit.x = (float)c;
     per_unit.y = (float)(c - (double)per_unit.x);
   }
-  // a logit's weight as a count of 2^-63
+  // a logit's weight as a count of 2^-62
   auto weight = [&](uint32_t k) -> unsigned long long {
-    if (k == top) return 1ull << 63;
-    return weight63(ff_sum(logit_value(k), -top_value), per_unit, s_two_to);
+    if (k == top) return 1ull << kSumBits;
+    return weight62(ff_sum(logit_value(k), -top_value), per_unit, s_two_to);
   };
   auto units = [&](uint32_t k) -> unsigned long long {  // of 2^-50
-    if (!PROBS) return ((weight(k) >> (62 - kSmallBits)) + 1) >> 1;
+    if (!PROBS) return ((weight(k) >> (kSumBits - 1 - kSmallBits)) + 1) >> 1;
     const unsigned long long sig = (k >> 23 ? 0x800000u : 0u) | (k & 0x7fffffu);
     const int by = max(1, (int)(k >> 23)) - top_exp + kSmallBits - 24;
     return by >= 0 ? sig << by : by < -62 ? 0ull : ((sig >> (-by - 1)) + 1) >> 1;
@@ -1647,7 +1679,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
       const float t = __double2float_ru((double)min_p * (double)__uint_as_float(top));
       n = max(1, at_least(max(1u, __float_as_uint(t)), n));
     } else {  // 32 places at a time, by their weights
-      const double least = (double)min_p * 0x1p63;
+      const double least = (double)min_p * kSumUnit;
       int lo = 0, hi = n;  // the first that goes lies in (lo, hi]; the first of all stays
       while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, at = min(hi - 1, lo + (lane + 1) * step);
@@ -1672,7 +1704,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
       if (P.prob) {
         const double w = PROBS ? (double)__uint_as_float(key(j)) : (double)weight(key(j));
         // (in the sums' units: a probability's is 2^-50 of the power of two above the largest)
-        const double unit = PROBS ? two_to_the(126 - top_exp + kSmallBits) : 0x1p-13;
+        const double unit = PROBS ? two_to_the(126 - top_exp + kSmallBits) : two_to_the(kSmallBits - kSumBits);
         P.prob[row] = (float)(w * unit / kept_sum);
       }
     }
