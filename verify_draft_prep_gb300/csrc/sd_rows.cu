@@ -27,6 +27,7 @@
 #include <atomic>
 
 #include "sd_kv.cuh"
+#include "sd_tc.cuh"
 
 namespace sdk {
 
@@ -884,9 +885,11 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the search and those that serve it meet from different places of the program, which __syncthreads and
+  // a group's sync do not allow: barriers that count warps and threads)
   auto meet = [&]() {
-    if (C == 1) __syncthreads();
-    else cluster.sync();
+    if (C == 1) named_bar(1, kQThreads);
+    else asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
   };
   const int row = blockIdx.x / C, req = row / P.J;
   const float T = P.temperature ? P.temperature[req] : 1.f;
