@@ -564,10 +564,10 @@ SD_API size_t sd_kv_attend_workspace_bytes(int D);
  *   weights[t] = w                      for the request's own new tokens, or without `before`
  *   weights[t] = w + decay * before[t]  for the others
  * so that a token's number starts afresh in the call that brings it. weights and before are fp32
- * [num_blocks, Hkv, block_size], as the cache's pages lie; before may be weights itself. Numbers of
- * other slots are not written. A token whose page is not in the table is left out (SD_ERR_KV_RANGE, as
- * for ctx_lens, cu_q and a live[r] outside [0, n_r], which are clamped). Rows with lse = -inf that see
- * nothing add nothing. The same call gives the same bits; sums are fp32, q as for sd_kv_attend.
+ * [num_blocks, Hkv, block_size], as the cache's pages lie; before may be weights itself (and else
+ * shares nothing with it). Numbers of other slots are not written. A token whose page is not in the
+ * table is left out (SD_ERR_KV_RANGE, as for ctx_lens, cu_q and a live[r] outside [0, n_r], which are
+ * clamped). Rows with lse = -inf that see nothing add nothing. The same call gives the same bits; sums are fp32, q as for sd_kv_attend.
  * Arguments: as for sd_kv_attend; lse [n, Hq] fp32; decay finite and >= 0; B and Hkv at most 65535.
  *   Requests that share a page of the table race on its numbers.
  */
@@ -598,8 +598,10 @@ SD_API int sd_kv_weights(int B, int n, int max_q, int Hq, int Hkv, int D, const 
  * Rotated keys keep the angle of the position they had: new tokens go on with positions of the text,
  * while slots, ctx_lens and sd_kv_attend's causal order go by place.
  * Arguments: cache as for sd_kv_write; weights fp32 [num_blocks, Hkv, block_size]; kept [B, Hkv,
- *   budget] and new_lens [B] int32 outputs (new_lens is not ctx_lens); budget >= 1; sink, recent >= 0,
- *   sink + recent <= budget; to_table [B, to_blocks]; B and Hkv at most 65535.
+ *   budget] and new_lens [B] int32 outputs, apart from each other, ctx_lens and the tables; budget >= 1;
+ *   sink, recent >= 0, sink + recent <= budget; to_table [B, to_blocks], apart from block_table (in place:
+ *   NULL); k_cache is not v_cache, nor k_scale v_scale, but for one cache and its scales given twice with
+ *   to_table; B and Hkv at most 65535.
  */
 SD_API int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long st_block,
                        long st_tok, long st_head, float* k_scale, float* v_scale, int num_blocks,
@@ -633,7 +635,8 @@ SD_API int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long
  *   pairs SD_ROPE_HALVES or SD_ROPE_NEIGHBOURS; turns [rot / 2] (sd_rope_table's, on the device); scale
  *   finite; q, k and their outputs bf16, value d of head h of token i at i*ld + h*hs + d (16-byte
  *   aligned, strides multiples of 8). An output may be its input itself, with the same strides, and
- *   else shares nothing with either input.
+ *   else shares nothing with either input or the other output (slices of one array may lie side by side);
+ *   no two of its own values share memory.
  */
 SD_API int sd_rope(int n, int Hq, int Hk, int D, int rot, int pairs, const int32_t* positions,
                    const uint64_t* turns, float scale, int inverse, const void* q, long ld_q,
@@ -671,9 +674,9 @@ SD_API int sd_rope_table(int rot, double base, int kind, double factor, double o
  * The rows may serve as sd_verify's (target and draft rows cut by the same request's settings: the
  * answer is then distributed as the cut target rows), sd_draft_sample's or sd_token_logprobs's.
  * Arguments: B >= 0, J >= 1, 1 <= V <= SD_CUT_MAX_V; rows [B*J, V] of stride ld >= V (row r*J + j is
- *   request r's); probs [B*J, V] fp32 of stride ld_out >= V, in memory apart from rows'; kept [B, J] int32
- *   or NULL: how many entries are kept. A row that keeps none: zeros, kept 0, SD_ERR_ZERO_ROW.
- *   B*J <= 2^27.
+ *   request r's); probs [B*J, V] fp32 of stride ld_out >= V; kept [B, J] int32 or NULL: how many entries
+ *   are kept; outputs in memory apart from each other, the rows and the settings. A row that keeps none:
+ *   zeros, kept 0, SD_ERR_ZERO_ROW. B*J <= 2^27.
  */
 SD_API int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld,
                        const float* temperature, const int32_t* top_k, const float* top_p,
@@ -686,7 +689,8 @@ SD_API int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld
  * tokens[r][j] = the first entry, in the order above, up to and with which more than u[r][j] of the
  * sum of those kept lies (u taken within [0, 1]; NaN as 0).
  * Arguments: as for sd_truncate; u [B, J] fp32; tokens [B, J] int32; prob [B, J] fp32 or NULL: the
- *   token's probability among those kept. A row that keeps none: token 0, prob 0, SD_ERR_ZERO_ROW.
+ *   token's probability among those kept (it may be u itself; outputs share nothing else). A row that
+ *   keeps none: token 0, prob 0, SD_ERR_ZERO_ROW.
  */
 SD_API int sd_sample(int B, int J, int V, int dtype, const void* rows, long ld,
                      const float* temperature, const int32_t* top_k, const float* top_p,

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "sd.h"
+#include "sd_overlap.cuh"
 
 extern "C" {
 int sd_verify_launch(int, int, int, int, const void*, long, const void*, long, const int32_t*,
@@ -744,6 +745,8 @@ int sd_kv_weights(int B, int n, int max_q, int Hq, int Hkv, int D, const void* q
   if (n > 0 && (!q || !lse)) return SD_E_NULL;
   if (!k_cache || !k_scale) return SD_E_NULL;
   if (!aligned16(q) || !aligned16(k_cache) || ld_q % 8 || hs_q % 8) return SD_E_ALIGN;
+  const size_t numbers = (size_t)num_blocks * Hkv * block_size * 4;
+  if (before != weights && share(before, numbers, weights, numbers)) return SD_E_SHAPE;
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_kv_weights_launch(B, n, max_q, Hq, Hkv, D, q, ld_q, hs_q, lse, k_cache, st_block, st_tok,
@@ -765,9 +768,23 @@ int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long st_blo
     return SD_E_SHAPE;
   if (B == 0) return SD_OK;
   if (!ctx_lens || !kept || !new_lens || (max_blocks > 0 && !block_table)) return SD_E_NULL;
-  if (new_lens == ctx_lens) return SD_E_SHAPE;  // (every head reads the old ones)
   if (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale || !weights)) return SD_E_NULL;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return SD_E_ALIGN;
+  // Places are chosen while other heads read the lengths and tables; a table that is its own list of fresh
+  // pages would have the move write what others still read; K and V move one after the other.
+  const size_t lens = (size_t)B * 4, places = lens * Hkv * budget, table = lens * max_blocks,
+               to = lens * to_blocks;
+  const struct {
+    const void* p;
+    size_t n;
+  } out[] = {{kept, places}, {new_lens, lens}}, in[] = {{ctx_lens, lens}, {block_table, table}, {to_table, to}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (share(o.p, o.n, i.p, i.n)) return SD_E_SHAPE;
+  if (share(kept, places, new_lens, lens) || share(block_table, table, to_table, to)) return SD_E_SHAPE;
+  if (num_blocks > 0 && (k_cache == v_cache || k_scale == v_scale) &&
+      (!to_table || k_cache != v_cache || k_scale != v_scale))
+    return SD_E_SHAPE;
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_kv_evict_launch(B, Hkv, D, k_cache, v_cache, st_block, st_tok, st_head, k_scale, v_scale,
@@ -801,6 +818,16 @@ int sd_rope(int n, int Hq, int Hk, int D, int rot, int pairs, const int32_t* pos
   // an output that is its input has its strides
   if (Hq > 0 && q == q_out && (ld_q != ld_qo || hs_q != hs_qo)) return SD_E_SHAPE;
   if (Hk > 0 && k == k_out && (ld_k != ld_ko || hs_k != hs_ko)) return SD_E_SHAPE;
+  // and else shares nothing with either input, the other output or itself
+  const HeadRows in[2] = {{q, ld_q, hs_q, Hq}, {k, ld_k, hs_k, Hk}};
+  const HeadRows out[2] = {{q_out, ld_qo, hs_qo, Hq}, {k_out, ld_ko, hs_ko, Hk}};
+  for (int i = 0; i < 2; ++i) {
+    if (out[i].H == 0) continue;
+    if (heads_overlap(out[i], n, D)) return SD_E_SHAPE;
+    if (out[i].p != in[i].p && heads_share(out[i], in[i], n, D)) return SD_E_SHAPE;
+    if (in[1 - i].H > 0 && heads_share(out[i], in[1 - i], n, D)) return SD_E_SHAPE;
+  }
+  if (Hq > 0 && Hk > 0 && heads_share(out[0], out[1], n, D)) return SD_E_SHAPE;
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_rope_launch(n, Hq, Hk, D, rot, pairs, positions, turns, scale, inverse, q, ld_q, hs_q,
@@ -834,6 +861,17 @@ int check_rows(int B, int J, int V, int dtype, long ld) {
   return SD_OK;
 }
 
+// Whether an output of the two shares memory with what they read: a marked row is read again, with its
+// settings, after other rows' outputs (and its own mark) are written.
+bool cut_shares(const void* out, size_t n_out, int B, int J, int V, int dtype, const void* rows, long ld,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p) {
+  const size_t n_rows = (((size_t)B * J - 1) * ld + V) * (dtype == SD_F32_PROBS ? 4 : 2);
+  const size_t each = (size_t)B * 4;
+  return share(out, n_out, rows, n_rows) || share(out, n_out, temperature, each) ||
+         share(out, n_out, top_k, each) || share(out, n_out, top_p, each) ||
+         share(out, n_out, min_p, each);
+}
+
 }  // namespace
 
 int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld, const float* temperature,
@@ -846,11 +884,11 @@ int sd_truncate(int B, int J, int V, int dtype, const void* rows, long ld, const
   if (!rows || !probs) return SD_E_NULL;
   const uintptr_t size = dtype == SD_F32_PROBS ? 4 : 2;
   if ((uintptr_t)rows % size || (uintptr_t)probs % 4) return SD_E_ALIGN;
-  // rows are read again after some of probs is written
-  const uintptr_t last = (uintptr_t)B * J - 1;
-  const uintptr_t rows_end = (uintptr_t)rows + (last * ld + V) * size;
-  const uintptr_t probs_end = (uintptr_t)probs + (last * ld_out + V) * 4;
-  if ((uintptr_t)probs < rows_end && (uintptr_t)rows < probs_end) return SD_E_SHAPE;
+  const size_t n_probs = (((size_t)B * J - 1) * ld_out + V) * 4, n_kept = (size_t)B * J * 4;
+  if (cut_shares(probs, n_probs, B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p) ||
+      cut_shares(kept, n_kept, B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p) ||
+      share(probs, n_probs, kept, n_kept))
+    return SD_E_SHAPE;
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_rows_launch(B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p, probs, ld_out,
@@ -865,6 +903,15 @@ int sd_sample(int B, int J, int V, int dtype, const void* rows, long ld, const f
   if (B == 0) return SD_OK;
   if (!rows || !u || !tokens) return SD_E_NULL;
   if ((uintptr_t)rows % (dtype == SD_F32_PROBS ? 4 : 2)) return SD_E_ALIGN;
+  const void* out[] = {tokens, prob, kept};
+  const size_t each = (size_t)B * J * 4;
+  for (int i = 0; i < 3; ++i) {
+    if (cut_shares(out[i], each, B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p) ||
+        share(out[i], each, out[(i + 1) % 3], each))
+      return SD_E_SHAPE;
+    // (a row's number is read before its probability is written: that may take its place)
+    if (!(out[i] == prob && prob == u) && share(out[i], each, u, each)) return SD_E_SHAPE;
+  }
   const int dev = check_device();
   if (dev != SD_OK) return dev;
   return sd_rows_launch(B, J, V, dtype, rows, ld, temperature, top_k, top_p, min_p, nullptr, 0, u,
