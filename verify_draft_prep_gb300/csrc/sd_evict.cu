@@ -6,8 +6,6 @@
 // chooses for itself: the heads of a page need not hold the same tokens, only the same number. What
 // stays keeps its order; it fills new pages (or the request's own from the first on).
 
-#include <atomic>
-
 #include "sd_kv.cuh"
 
 namespace sdk {
@@ -413,10 +411,11 @@ extern "C" int sd_kv_evict_launch(int B, int Hkv, int D, void* k_cache, void* v_
   P.kept = kept;
   P.new_lens = new_lens;
   P.err = err;
-  static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
+  static std::atomic<bool> set[sdk::kMostDevices];  // per device; true only once the attribute is in force
   constexpr int kMostSmem = 200 * 1024;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
+  const int sms = sdk::device_sms(dev);
+  if (sms == 0) return SD_E_DEVICE;
   if (!set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(sdk::evict_choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMostSmem) != cudaSuccess)
@@ -427,7 +426,7 @@ extern "C" int sd_kv_evict_launch(int B, int Hkv, int D, void* k_cache, void* v_
   // CTAs of a request and head: more while the SMs have room for them and each has 1000 tokens. (512
   // requests and heads with 1, 2, 4: the call 102, 120, 168 us; 8 with 1 and 8: 85 and 39.)
   int C = 1;
-  while (C < sdk::kSelCluster && (long)B * Hkv * C * 2 <= 304 && most > 2048L * C) C *= 2;
+  while (C < sdk::kSelCluster && (long)B * Hkv * C * 2 <= 2 * sms && most > 2048L * C) C *= 2;
   const long part = (most + C - 1) / C;
   P.in_smem = (int)(part < kMostSmem / 4 ? part : kMostSmem / 4);
   cudaLaunchConfig_t cfg = {};

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "sd_common.cuh"
 
 namespace sdk {
@@ -20,6 +22,21 @@ struct KvCache {
   long st_block, st_tok, st_head;
   int num_blocks, log2_bs, Hkv, D;
 };
+
+// Devices that the launchers keep something for (attributes that are set once), and the current one's
+// number of SMs; 0: there is none such.
+constexpr int kMostDevices = 64;
+inline int device_sms(int& dev) {
+  static std::atomic<int> sms[kMostDevices];
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMostDevices) return 0;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+      return 0;
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 constexpr float kMinScale = 7.8886090522101181e-31f;  // 2^-100, the smallest scale a page is given
 

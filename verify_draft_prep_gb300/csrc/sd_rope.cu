@@ -209,7 +209,10 @@ extern "C" int sd_rope_launch(int n, int Hq, int Hk, int D, int rot, int pairs,
   // Tokens of a CTA: a step's few spread over the SMs, a prompt's share their CTA's setup. With 1, 2, 4,
   // 8, 16: 384 tokens 4.9, 3.9, 4.1, 5.3, 7.7 us, 8192 42.9, 36.0, 32.7, 31.7, 30.8, 16384 124.7, 84.1,
   // 68.9, 60.3, 60.0.
-  P.chunk = n / 304 < 2 ? 2 : n / 304 > 16 ? 16 : n / 304;
+  int dev = 0;
+  const int places = 2 * sdk::device_sms(dev);
+  if (places == 0) return SD_E_DEVICE;
+  P.chunk = n / places < 2 ? 2 : n / places > 16 ? 16 : n / places;
   // The widest accesses that every part of a head allows: 16 bytes, else 8 (halves) or a pair.
   if (pairs == SD_ROPE_HALVES) {
     if (rot % 16 == 0) return sdk::launch_rope<8, true>(P, stream);

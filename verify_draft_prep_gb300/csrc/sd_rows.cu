@@ -24,8 +24,6 @@
 // each CTA counts its part, then each scans its share of the bins over all of the cluster's histograms
 // through distributed shared memory, and one warp does the search.
 
-#include <atomic>
-
 #include "sd_kv.cuh"
 #include "sd_tc.cuh"
 
@@ -1738,14 +1736,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
 template <bool PROBS, bool WRITE>
 static int launch_rows(RowsParams& P, cudaStream_t stream) {
   constexpr int kQuickBytes = kQBins * 4 * (PROBS ? 2 : 1);
-  static std::atomic<bool> set[64];  // per device; true only once the attributes are in force
-  static std::atomic<int> sms[64];
+  static std::atomic<bool> set[kMostDevices];  // true only once the attributes are in force
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
+  const int n_sm = device_sms(dev);
+  if (n_sm == 0) return SD_E_DEVICE;
   if (!set[dev].load(std::memory_order_acquire)) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-      return SD_E_DEVICE;
     if (cudaFuncSetAttribute(rows_kernel<PROBS, WRITE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kHistBytes) != cudaSuccess ||
         cudaFuncSetAttribute(quick_kernel<PROBS, WRITE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1754,11 +1749,10 @@ static int launch_rows(RowsParams& P, cudaStream_t stream) {
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmallWarps * kSmallProbsV * 16) != cudaSuccess)
       return SD_E_LAUNCH;
-    sms[dev].store(n, std::memory_order_relaxed);
     set[dev].store(true, std::memory_order_release);
   }
   // (probabilities take the quick kernel longer: with many rows the warps' sorting pays up to 1024)
-  if (P.V <= kSmallV || (PROBS && P.V <= kSmallProbsV && P.n_rows > 600)) {
+  if (P.V <= kSmallV || (PROBS && P.V <= kSmallProbsV && P.n_rows >= 4 * n_sm)) {
     int size = 2;
     while (size < P.V) size *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -1770,7 +1764,6 @@ static int launch_rows(RowsParams& P, cudaStream_t stream) {
                ? SD_OK
                : SD_E_LAUNCH;
   }
-  const int n_sm = sms[dev].load(std::memory_order_relaxed);
   auto parts = [&](int C) { return ((P.V + C - 1) / C + 7) / 8 * 8; };
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -32,8 +32,6 @@
 // S read 16 columns at a time with the next ones on their way: 64 requests 102 against 95 us, a prompt
 // 502 against 437 (registers); three warps that fetch ahead, or 8 and 12 units: no change.
 
-#include <atomic>
-
 #include "sd_kv.cuh"
 #include "sd_tc.cuh"
 
@@ -137,7 +135,7 @@ __device__ __forceinline__ bool w_stays(const WUnit& a, const WUnit& b, bool the
 }
 
 // A CTA's units in their order. All units of a request lie one behind another; `spread`: pairs
-// outermost and every CTA takes each 152nd of the line, forwards and backwards in turn, so that a
+// outermost and every CTA takes one of each gridDim.x units, forwards and backwards in turn, so that a
 // prompt's units, which get cheaper along the context, even out; else heads outermost and every CTA
 // takes a stretch, so that it stays with a request's Q.
 template <bool SPREAD>
@@ -754,22 +752,18 @@ template <int DP, bool LONG>
 static int launch_weights(const WeightsParams& P, cudaStream_t stream) {
   constexpr int smem = WLayout<DP, LONG>::kMisc + (int)sizeof(WMisc) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-  static std::atomic<bool> set[64];  // per device; true only once the attribute is in force
-  static std::atomic<int> sms[64];
+  static std::atomic<bool> set[kMostDevices];  // true only once the attribute is in force
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SD_E_DEVICE;
+  const int sms = device_sms(dev);
+  if (sms == 0) return SD_E_DEVICE;
   if (!set[dev].load(std::memory_order_acquire)) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-      return SD_E_DEVICE;
     if (cudaFuncSetAttribute(weights_kernel<DP, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return SD_E_LAUNCH;
-    sms[dev].store(n, std::memory_order_relaxed);
     set[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms[dev].load(std::memory_order_relaxed), 1, 1);
+  cfg.gridDim = dim3((unsigned)sms, 1, 1);
   cfg.blockDim = dim3(kWThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
