@@ -1,11 +1,12 @@
-"""sd_kv_evict at the largest budgets and lengths that it accepts: places are counted up to 2^31 - 1024 by
-clusters whose step is up to 4096."""
+"""sd_kv_evict where it counts far: the largest budgets and lengths that it accepts (places up to 2^31 - 1024,
+by clusters whose step is up to 4096), and moves within a request's own pages that take several rounds."""
 
 import pytest
 import torch
 
 import kvref
 import verify_draft_prep_gb300 as sd
+from test_gpu_kv_evict import bits, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,41 @@ def test_largest_length():
     assert int(lens) == MOST
     check_places(whole, MOST)
     assert int(c[0].view(torch.uint8).sum()) == 0 and int(c[4].sum()) == 0
+
+
+@pytest.mark.parametrize("H,D,bs,n,budget", [(2, 128, 16, 9000, 3500), (1, 128, 128, 7000, 3000), (3, 96, 32, 6000, 4111),
+                                             (2, 64, 16, 9000, 5000)])
+def test_rounds_of_a_move_in_place(H, D, bs, n, budget):
+    """More places than a cluster takes at a time (1024, or 2048 of heads of up to 64): what stays is where
+    a move into fresh pages puts it, and where a sort of the weights says."""
+    sink, recent = 5, 300
+    c = make([n], H, D, bs, budget, seed=n, fresh=True)
+    was = {f: c[f].clone() for f in ("k", "v", "ks", "vs", "w")}
+    kept, lens = run(c, budget, sink, recent)
+    mine = {**{f: was[f].clone() for f in was}, "table": c["table"], "to": None, "ctx": c["ctx"]}
+    kept2, lens2 = run(mine, budget, sink, recent)
+    assert torch.equal(kept, kept2) and int(lens) == int(lens2) == budget
+    t, j = torch.arange(n, device=DEV), torch.arange(budget, device=DEV)
+    page = c["table"][0].long()
+    fresh, own = c["to"][0].long()[j // bs], page[j // bs]
+    for h in range(H):
+        w = was["w"][page[t // bs], h, t % bs]
+        mid = torch.sort(w[sink:n - recent], descending=True, stable=True).indices[:budget - sink - recent]
+        want = torch.cat([t[:sink], torch.sort(mid + sink).values, t[n - recent:]])
+        assert torch.equal(kept[0, h].long(), want)
+        src = page[want // bs]
+        assert torch.equal(mine["w"][own, h, j % bs], was["w"][src, h, want % bs])
+        for x, s in (("k", "ks"), ("v", "vs")):
+            assert torch.equal(mine[s][own, h], c[s][fresh, h])
+            got, same = (bits(y[x])[p, j % bs, h] for y, p in ((mine, own), (c, fresh)))
+            assert torch.equal(got, same)
+            # powers of two: a value is what it was but for what became subnormal
+            step = mine[s][own, h].double() * 2.0 ** -10
+            a = got.view(kvref.E4M3).double() * mine[s][own, h].double()[:, None]
+            b = bits(was[x])[src, want % bs, h].view(kvref.E4M3).double() * was[s][src, h].double()[:, None]
+            assert torch.all((a - b).abs() <= step[:, None])
+    # pages behind the kept ones, and pages of no request, stay as they are
+    rest = torch.ones(mine["k"].shape[0], dtype=torch.bool, device=DEV)
+    rest[own] = False
+    for f in was:
+        assert torch.equal(bits(mine[f])[rest], bits(was[f])[rest])
