@@ -212,6 +212,35 @@ __device__ __forceinline__ uint32_t prob_key(uint32_t b) {
   return b - 1u < 0x7f800000u ? min(b, 0x3f800000u) : 0u;
 }
 
+// What a kept entry's probability is made with: 1 over the sum of those kept, a pair, for weights in units of
+// the largest (logits) or as they are but for a power of two (probabilities). A probability is rounded
+// once (2^-24). A logit's distance from the largest is rounded to fp32 (2^-24 of it, which is as much of
+// the result for each nat), its exponential is fp32's (2^-22), and two products: 2048 rows of 201088
+// logits take 975 us so, 997 with the distance as a pair.
+struct KeptValue {
+  float2 inv;
+  float2 per_unit;
+  float top_value, scale;
+
+  template <bool PROBS>
+  __device__ __forceinline__ float of(uint32_t key) const {
+    if (PROBS) {
+      const float x = __uint_as_float(key) * scale;
+      return fmaf(x, inv.x, x * inv.y);
+    }
+    const float d = logit_value(key) - top_value;
+    const float y = d * per_unit.x;
+    // (the product's rounding error goes into a factor)
+    const float r = fmaf(d, per_unit.x, -y) + d * per_unit.y;
+    const float x = exp2f(y) * fmaf(r, 0.69314718f, 1.f);
+    return y > -160.f ? fmaf(x, inv.x, x * inv.y) : 0.f;
+  }
+};
+__device__ __forceinline__ float2 pair_of(double x) {
+  const float hi = (float)x;
+  return make_float2(hi, (float)(x - (double)hi));
+}
+
 template <bool PROBS>
 struct RowReader {
   const RowsParams& P;
@@ -785,19 +814,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
     int edge = 0x7fffffff;  // entries of the last value are kept up to here
     if (cut && n - last.above < last.count) edge = nth(last.key, n - last.above - 1);
     const uint32_t least = cut ? last.key : 1u;
-    const float inv = (float)(kSumUnit / sum_double(kept_sum));
-    const float scale = PROBS ? __uint_as_float((uint32_t)(127 + 126 - top_exp) << 23) : 1.f;
+    const KeptValue v = {pair_of(kSumUnit / sum_double(kept_sum)), per_unit, top_value,
+                         PROBS ? __uint_as_float((uint32_t)(127 + 126 - top_exp) << 23) : 1.f};
     float* out = P.probs + (size_t)row * P.ld_out;
     auto value = [&](int i, uint32_t x) {
-      if (x < least || (x == least && i > edge)) return 0.f;
-      if (PROBS) return __uint_as_float(x) * scale * inv;
-      if (x == top) return inv;
-      if (top == 0xff80u) return 0.f;
-      const float d = logit_value(x) - top_value;
-      const float y = d * per_unit.x;
-      // (the product's rounding error goes into a factor: 2^y as exact as fp32 allows)
-      const float r = fmaf(d, per_unit.x, -y) + d * per_unit.y;
-      return y > -160.f ? exp2f(y) * fmaf(r, 0.69314718f, 1.f) * inv : 0.f;
+      // (of entries beside +inf only those that are +inf are kept)
+      return x < least || (x == least && i > edge) ? 0.f : !PROBS && x == top ? v.inv.x : v.of<PROBS>(x);
     };
     in.write(out, P.vec_out, tid, kRowThreads, value);
   }
@@ -842,7 +864,7 @@ struct QuickShared {
   uint32_t op_key, op_number, op_count;
   int index, edge;
   uint32_t least;
-  float inv;
+  float2 inv;
   // a bin's entries (lower halves), and counts and sums of them
   uint32_t listed;
   union {
@@ -1500,7 +1522,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         if (!mark) {
           ask(kOpNth, b.key, j, b.count);
           at = sh.index;
-          prob = __fdiv_rn((float)b.w, (float)sum_double(kept_sum));
+          prob = (float)((double)b.w / sum_double(kept_sum));
         }
       }
       if (!mark && WRITE && cut && keep - last.above < last.count) {
@@ -1511,7 +1533,7 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     if (lane == 0) {
       sh.edge = edge;
       sh.least = cut ? last.key : 1u;
-      sh.inv = __fdiv_rn((float)kSumUnit, (float)sum_double(kept_sum));
+      if (WRITE) sh.inv = pair_of(kSumUnit / sum_double(kept_sum));
       if (!mark) {
         if (total == 0) raise_err(P.err, SD_ERR_ZERO_ROW);
         if (P.kept) P.kept[row] = (int32_t)keep;
@@ -1533,16 +1555,10 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
     const QuickShared* s0 = cluster.map_shared_rank(&sh, 0);
     const int op = s0->op, edge = s0->edge;
     const uint32_t least = op == kOpNothing ? 0xffffffffu : s0->least;
-    const float inv = s0->inv;
     if (op != kOpMark) {
+      const KeptValue v = {s0->inv, per_unit, top_value, 1.f};
       auto value = [&](int i, uint32_t x) {
-        if (x < least || (x == least && i > edge)) return 0.f;
-        if (PROBS) return __uint_as_float(x) * inv;
-        const float d = logit_value(x) - top_value;
-        const float y = d * per_unit.x;
-        // (the product's rounding error goes into a factor: 2^y as exact as fp32 allows)
-        const float r = fmaf(d, per_unit.x, -y) + d * per_unit.y;
-        return y > -160.f ? exp2f(y) * fmaf(r, 0.69314718f, 1.f) * inv : 0.f;
+        return x < least || (x == least && i > edge) ? 0.f : v.of<PROBS>(x);
       };
       in.write(out, P.vec_out, tid, kQThreads, value);
     }
@@ -1712,23 +1728,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
   } else {
     const uint32_t least = key(n - 1);
     const int edge = index(n - 1);  // entries of the last value are kept up to here
-    const float inv = (float)(0x1p50 / kept_sum);
-    const float scale = PROBS ? __uint_as_float((uint32_t)(127 + 126 - top_exp) << 23) : 1.f;
+    const KeptValue v = {pair_of(two_to_the(kSmallBits) / kept_sum), per_unit, top_value,
+                         PROBS ? __uint_as_float((uint32_t)(127 + 126 - top_exp) << 23) : 1.f};
     for (int i = lane; i < V; i += 32) {
       const uint32_t x = in.key_at(i);
-      float y = 0.f;
-      if (x > least || (x == least && i <= edge)) {
-        if (PROBS) {
-          y = __uint_as_float(x) * scale * inv;
-        } else if (x == top) {
-          y = inv;
-        } else {
-          const float d = logit_value(x) - top_value, e = d * per_unit.x;
-          const float r = fmaf(d, per_unit.x, -e) + d * per_unit.y;
-          y = e > -160.f ? exp2f(e) * fmaf(r, 0.69314718f, 1.f) * inv : 0.f;
-        }
-      }
-      out[i] = y;
+      // (of entries beside +inf only those that are +inf are kept)
+      out[i] = x > least || (x == least && i <= edge)
+                   ? !PROBS && x == top ? v.inv.x : v.of<PROBS>(x)
+                   : 0.f;
     }
   }
 }
