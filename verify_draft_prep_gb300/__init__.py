@@ -766,7 +766,8 @@ def sd_kv_weights(q, lse, k_cache, k_scale, block_table, ctx_lens, cu_q, weights
     q, block_table, ctx_lens, cu_q, max_q, sm_scale, causal: as for sd_kv_attend, and lse its [n, Hq]
     float32; live: [B] int32, how many of each request's query tokens count, or None for all; weights:
     [num_blocks, Hkv, block_size] float32; before: the same, what tokens had so far (it may be weights
-    itself), or None; max_q: None for n / B, rounded up.
+    itself), or None; max_q: how many query tokens the longest request has, or None for n / B, rounded
+    up: it only chooses the kernel (a batch with one prompt should say its length).
     """
     # (K alone is read: its checks serve for both)
     cache = _cache_args(k_cache, k_cache, k_scale, k_scale)

@@ -808,11 +808,18 @@ extern "C" int sd_kv_weights_launch(int B, int n, int max_q, int Hq, int Hkv, in
   P.before = before;
   P.weights = weights;
   P.err = err;
-  // Prompts of many chunks. The kernel for few against the one for many, in us: heads of 128, one token of
-  // 32000 19 to 30, 4 requests of 512, 1024, 2048 rows 38 to 44, 88 to 97, 158 to 165, 2 of 4096 and 8192
-  // rows 153 to 149, 293 to 281, a prompt of 32768 rows 751 to 362 (its units get cheaper along the
-  // context); heads of 64, 64 requests of 48 rows 85 to 204, 4 of 4096 rows 261 to 285.
-  if ((long)max_q * P.G > 4096)
+  // Prompts of many chunks, by the rows of the longest request that the caller expects. The kernel for few
+  // against the one for many, in us, without a context and behind one of 8000 tokens (one request, 8 heads
+  // of K):
+  //   heads of 128:  1024 rows 20 to 20 (4 requests), 2048 32.0 to 30.9 and 56.5 to 56.3, 4096 55.4 to 52.8
+  //     and 103 to 100, 8192 102 to 97 and 291 to 188, 32768 747 to 360; 16 requests of 2048 rows 48 to 50,
+  //     4 of 2048 behind 4000 tokens 106 to 109.
+  //   heads of 64:   2048 rows 27.9 to 29.9 and 49 to 54, 4096 49 to 52 and 91 to 97, 8192 90 to 95 and
+  //     257 to 183 (4 requests 166 to 133, 16 233 to 256), 16384 173 to 181 and 506 to 357, 32768 661 to
+  //     353; 64 requests of 48 rows 80 to 201.
+  // (Where every CTA has one unit at most the two differ by their loops alone; with more the units of a
+  // prompt are uneven, which the one for many spreads.)
+  if ((long)max_q * P.G >= (D <= 64 ? 8192 : 4096))
     return D <= 64 ? sdk::launch_weights<64, true>(P, stream)
                    : sdk::launch_weights<128, true>(P, stream);
   return D <= 64 ? sdk::launch_weights<64, false>(P, stream)
