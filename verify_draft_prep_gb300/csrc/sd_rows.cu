@@ -17,7 +17,7 @@
 // one bin in question is resolved by reading the row again (from L2).
 //
 // Two kernels. quick_kernel has 8192 bins, for logits of magnitude 2^-15 to 2^17 (and zero) and
-// probabilities from 2^-63 on: 32 or 64 KB, so that three or four rows are on an SM at a time and one
+// probabilities from 2^-63 on: 32 or 64 KB, so that four or two CTAs are on an SM at a time and one
 // row's search hides behind another's reading. A row that needs more (a cut or a draw within values
 // that have no bin of their own, rows of odd scales) is marked, and rows_kernel, whose histogram has a
 // bin for every value, does the marked rows. A row is a CTA's work, or a cluster's where rows are few:
@@ -831,12 +831,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
 // The quick kernel. Bins stand in the order of the values, larger first, as rows of 32 (a lane a bin):
 // logits have 128 rows of positive values, one for zero, 128 of negative ones; probabilities 256.
 //
-// Where its time goes (one token of each of 608 rows of 201088 logits, 4 CTAs of 256 threads an SM, 126
-// us): reading and counting 53 us (8 instructions an entry; a shared atomic of 32 different
-// addresses takes 2.5 cycles), the sums of the bins 12, the search 18, the drawn value's entries 38: 608
-// rows do not stay in L2, so they come from memory a second time. 1024 rows are two rounds of those
-// places, 331 us against 61 of memory. 2048 rows of logits cut: 964 us against 364; 384 of probabilities 476
-// against 91 (each place that is looked for reads the row again). One row of 1024: 27 us, latency.
+// Where a row's time goes (one token of each of 608 rows of 201088 logits, 4 CTAs of 256 threads an SM: 120
+// us a row, 190 for the slowest): reading and counting 57 us (8 instructions an entry; a shared atomic of
+// 32 different addresses takes 2.5 cycles), the sums of the bins 14, the search 11, the drawn value's
+// entries 34: 608 rows do not stay in L2, so they come from memory a second time. 1024 rows are two rounds
+// of those places, 340 us against 61 of memory. 2048 rows of logits cut: 974 us against 364; 384 of
+// probabilities 464 against 91 (each place that is looked for reads the row again). One row of 1024: 27
+// us, latency.
 // ---------------------------------------------------------------------------------------------
 constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQBins = 8192, kQRows = 257;
 constexpr uint16_t kLeast = 0xc7ff;  // the least logit that has a counter, -130560
@@ -1784,7 +1785,7 @@ static int launch_rows(RowsParams& P, cudaStream_t stream) {
   // CTAs of a row: more while the SMs have room for them, and a CTA some thousands of entries. Long
   // rows of probabilities are read again for every place that is looked for: with four CTAs a row
   // those on the SMs at a time stay within L2. With 1, 2, 4 CTAs 384 rows of 201088 probabilities cut
-  // take 556, 546, 488 us, 2048 of logits 956, 970, 1048, one token of each of 1024 rows 330, 342, 379.
+  // take 544, 526, 464 us, 2048 of logits 973, 986, 1072, one token of each of 1024 rows 340, 352, 388.
   int C = PROBS && P.V > 65536 ? 4 : 1;
   while (C < kMostClusters && P.n_rows * 2L * C <= 4L * n_sm && P.V > 4096 * C) C *= 2;
   P.part = parts(C);

@@ -19,16 +19,22 @@
 // stays where a request has at most two chunks and else streams by, asynchronously copied, two chunks
 // ahead. One thread issues the products.
 //
-// What bounds it (pages of 16, 8 heads of K):
+// An exponential is the hardware's (off by two places) of an argument that is one fma of S, the scale and
+// lse: off by 2^-24 of it, as lse itself is. 64 requests' numbers come out 5.0e-8 of their size from 64
+// bits, plain fp32 ones 4.3e-8, a prompt's 1.8e-7 against 2.0e-7.
+//
+// What bounds it (pages of 16, 8 heads of K; shares of the active cycles, of one launch each):
 //   - 64 requests of 6 slots, 64 heads of 64, 512 to 8192 tokens: 85 us against 22 of memory. Nothing is
-//     full (issue slots 44%, memory 18%, exponentials 10%, tensor cores 5%): the loading warps' own chain,
+//     full (issue slots 55%, memory 35%, exponentials 17%, tensor cores 9%): the loading warps' own chain,
 //     some 450 instructions a unit each, is what the others wait for. K a unit ahead in registers: 95;
 //     two units ahead in registers: 134 (spills).
-//   - A prompt of 8192 tokens of 32 heads of 128: 362 us against 146 of products. The exponentials
-//     alone take 276; tensor cores 37%, issue slots 46%. (With a quarter or an eighth of the exponentials
-//     by a polynomial it took 519 and 480 us, without 437, when the loads took more of the slots.)
-//   - One token at 32000, 32 heads of 128: 20 us against 5: 7 units a CTA, each as long as its loads; 26
-//     with all of a unit's K in registers, some of which were spilled.
+//   - A prompt of 8192 tokens of 32 heads of 128: 362 us against 146 of products and 133 of exponentials.
+//     Nothing is full either (exponentials and tensor cores 36% each, issue slots 45%): the summing warps,
+//     two on a scheduler, each wait for their S with nothing on its way behind it. (With a quarter or an
+//     eighth of the exponentials by a polynomial it took 519 and 480 us, without 437, when the loads took
+//     more of the slots.)
+//   - One token at 32000, 32 heads of 128: 19 us against 5: 7 units a CTA, each as long as its loads (issue
+//     slots 35%, memory 18%); 26 with all of a unit's K in registers, some of which were spilled.
 // S read 16 columns at a time with the next ones on their way: 64 requests 102 against 95 us, a prompt
 // 502 against 437 (registers); three warps that fetch ahead, or 8 and 12 units: no change.
 
