@@ -208,6 +208,15 @@ __device__ __forceinline__ uint32_t logit_key(uint32_t b) {
 __device__ __forceinline__ float logit_value(uint32_t k) {
   return __uint_as_float((k & 0x8000u ? k & 0x7fffu : ~k & 0xffffu) << 16);
 }
+// The least key whose logit weighs min_p (0 < min_p < 1) of the largest one, in fp64.
+__device__ __forceinline__ uint32_t least_logit_key(float top_value, float T, float min_p) {
+  const double t = (double)top_value + fmin(fmax((double)T, 0x1p-100), 0x1p100) * log((double)min_p);
+  const uint32_t o = orderable(__double2float_ru(t));
+  return o & 0x80000000u ? (o + 0xffffu) >> 16 : o >> 16;
+}
+// Weights, as counts of 2^-62, tell entries apart to 2^-43 down to this share of the largest; below it they
+// have fewer places, and then none.
+constexpr float kLeastShare = 0x1p-16f;
 __device__ __forceinline__ uint32_t prob_key(uint32_t b) {
   return b - 1u < 0x7f800000u ? min(b, 0x3f800000u) : 0u;
 }
@@ -744,9 +753,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) rows_kernel(const RowsParams P
       const Border b = find(kByKey, max(1u, __float_as_uint(t)), 0);
       m = b.above + b.count;
     } else {
-      const double t = (double)top_value + fmin(fmax((double)T, 0x1p-100), 0x1p100) * log((double)min_p);
-      const uint32_t o = orderable(__double2float_ru(t));
-      const uint32_t key = o & 0x80000000u ? (o + 0xffffu) >> 16 : o >> 16;
+      const uint32_t key = least_logit_key(top_value, T, min_p);
       const Border b = find(kByKey, min(max(key, 0x80u), top), 0);
       m = b.above + b.count;
     }
@@ -1470,18 +1477,24 @@ __global__ void __launch_bounds__(kQThreads, PROBS ? 3 : 4) quick_kernel(const R
         } else if (min_p >= 1.f) {
           m = find(0, 0, 0, 0).count;
         } else {
-          // the least logit that stays: near an estimate in fp32, 32 of them are weighed
-          const float unit = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
+          // the least logit that stays: near an estimate in fp32, 32 of them are weighed (an fp64 logarithm
+          // is slow, but right for small shares too)
           const uint32_t topk = logit_key(top_bits);
-          const uint32_t near = orderable(fmaf(unit, __logf(min_p), top_value)) >> 16;
-          const uint32_t mine = min(max((int)near - 16 + lane, 1), (int)topk);
-          const unsigned long long least_w = __float2ull_rn(min_p * (float)kSumUnit);
-          const uint32_t mine_bits = mine & 0x8000u ? mine & 0x7fffu : ~mine & 0xffffu;
-          const uint32_t stays = __ballot_sync(0xffffffffu, weight(mine_bits) >= least_w);
-          // (the weights ascend with the lane; the estimate is good to a few values, or all is marked)
-          const int at0 = stays ? __ffs(stays) - 1 : 32;
-          const uint32_t key = __shfl_sync(0xffffffffu, mine, at0 & 31);
-          if ((at0 == 0 && near > 16) || (at0 == 32 && near + 16 < topk)) mark = true;
+          uint32_t key;
+          if (min_p < kLeastShare) {
+            key = min(max(least_logit_key(top_value, T, min_p), 0x80u), topk);
+          } else {
+            const float unit = fminf(fmaxf(T, 0x1p-100f), 0x1p100f);
+            const uint32_t near = orderable(fmaf(unit, __logf(min_p), top_value)) >> 16;
+            const uint32_t mine = min(max((int)near - 16 + lane, 1), (int)topk);
+            const unsigned long long least_w = __float2ull_rn(min_p * (float)kSumUnit);
+            const uint32_t mine_bits = mine & 0x8000u ? mine & 0x7fffu : ~mine & 0xffffu;
+            const uint32_t stays = __ballot_sync(0xffffffffu, weight(mine_bits) >= least_w);
+            // (the weights ascend with the lane; the estimate is good to a few values, or all is marked)
+            const int at0 = stays ? __ffs(stays) - 1 : 32;
+            key = __shfl_sync(0xffffffffu, mine, at0 & 31);
+            if ((at0 == 0 && near > 16) || (at0 == 32 && near + 16 < topk)) mark = true;
+          }
           const uint32_t bits = key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu;
           const uint32_t mag = bits & 0x7fffu;
           if (mag >= 0x4800u) {  // beyond the bins: -2^17 or less (a larger one is not below the top)
@@ -1696,6 +1709,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 4) small_rows_kernel(const R
     } else if (PROBS) {
       const float t = __double2float_ru((double)min_p * (double)__uint_as_float(top));
       n = max(1, at_least(max(1u, __float_as_uint(t)), n));
+    } else if (min_p < kLeastShare) {
+      n = max(1, at_least(max(1u, least_logit_key(top_value, T, min_p)), n));
     } else {  // 32 places at a time, by their weights
       const double least = (double)min_p * kSumUnit;
       int lo = 0, hi = n;  // the first that goes lies in (lo, hi]; the first of all stays
