@@ -52,7 +52,7 @@ extern "C" {
 /* host-visible status codes */
 #define SD_OK 0
 #define SD_E_NULL (-1)     /* a required pointer is NULL */
-#define SD_E_SHAPE (-2)    /* a size or stride is out of range */
+#define SD_E_SHAPE (-2)    /* a size or stride is out of range, or arrays share memory that may not */
 #define SD_E_DTYPE (-3)    /* unknown dtype */
 #define SD_E_ALIGN (-4)    /* a pointer or stride breaks the stated alignment */
 #define SD_E_LAUNCH (-5)   /* the CUDA launch failed (cudaGetLastError is left set) */

@@ -112,7 +112,7 @@ const char* sd_status_string(int status) {
   switch (status) {
     case SD_OK: return "ok";
     case SD_E_NULL: return "a required pointer is NULL";
-    case SD_E_SHAPE: return "a size or stride is out of range";
+    case SD_E_SHAPE: return "a size or stride is out of range, or arrays share memory that may not";
     case SD_E_DTYPE: return "unknown dtype";
     case SD_E_ALIGN: return "a pointer or stride breaks the required alignment";
     case SD_E_LAUNCH: return "CUDA launch failed";
