@@ -628,8 +628,8 @@ SD_API int sd_kv_evict(int B, int Hkv, int D, void* k_cache, void* v_cache, long
  * The first `rot` values of every head of token i turn by its position p = positions[i] (any int32):
  * with a = 2 pi p turns[j] / 2^64, pair j (x, y) becomes
  *   scale * (x cos a - y sin a),  scale * (y cos a + x sin a),
- * or, inverse, with -a: what sends a gradient back (or a rotated key to its unrotated one). The other
- * values are copied. The angle is exact to 10^-7 at every position; values are fp32, rounded once.
+ * or, inverse, with -a and the same scale: the transposed map, which sends a gradient back (and, called
+ * with 1 / scale, a rotated key to its unrotated one). The other values are copied. The angle is exact to 10^-7 at every position; values are fp32, rounded once.
  * Arguments: n >= 0 tokens, n <= 2^31 - 1024; Hq, Hk >= 0 heads of queries and keys (0: none; their
  *   pointers may then be NULL), Hq + Hk <= 2^20; D a multiple of 8 up to 512; rot even, 0 < rot <= D;
  *   pairs SD_ROPE_HALVES or SD_ROPE_NEIGHBOURS; turns [rot / 2] (sd_rope_table's, on the device); scale

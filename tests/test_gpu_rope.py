@@ -147,3 +147,20 @@ def test_nothing_and_captured():
     sd.sd_rope(pos, turns, q=q, q_out=out, stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+def test_back_to_the_unrotated_key(pairs):
+    """Forward with a scale, then inverse with 1 / scale: the key again, rounded to bf16 twice."""
+    turns, scale = sd.sd_rope_table(64, base=5e5, kind="yarn", factor=16.0, original_len=4096, device=DEV)
+    pos = torch.tensor([0, 3, 4095, 60000], dtype=torch.int32, device=DEV)
+    k = torch.randn(4, 2, 80, device=DEV).bfloat16()
+    there, back = torch.empty_like(k), torch.empty_like(k)
+    sd.sd_rope(pos, turns, k=k, k_out=there, pairs=pairs, scale=scale)
+    sd.sd_rope(pos, turns, k=there, k_out=back, pairs=pairs, scale=1.0 / scale, inverse=True)
+    assert torch.equal(back[..., 64:], k[..., 64:])
+    x, y = k[..., :64].double(), back[..., :64].double()
+    pair = (x.view(4, 2, 2, 32).norm(dim=2, keepdim=True).expand(4, 2, 2, 32) if pairs == "halves"
+            else x.view(4, 2, 32, 2).norm(dim=3, keepdim=True).expand(4, 2, 32, 2)).reshape(4, 2, 64)
+    # each value of the turned pair is off by 2^-8 of itself, so the pair by 2^-8 of its length; then once more
+    assert torch.all((x - y).abs() <= pair * (2.0 ** -8 * (1 + 2.0 ** -8) + 2.0 ** -18) + 2.0 ** -8 * x.abs())

@@ -851,7 +851,7 @@ def sd_rope(positions, turns, q=None, k=None, q_out=None, k_out=None, pairs="hal
     positions: [n] int32; turns: [rot / 2] int64 (sd_rope_table's): the first rot values of a head
     turn; q, k: [n, heads, D] bfloat16 with contiguous heads (slices of one projection will do), either
     may be None; q_out, k_out: the same shapes, or None to turn them in place; pairs: "halves" or
-    "neighbours"; inverse: turn back (a gradient).
+    "neighbours"; inverse: turn back (a gradient; a turned key with 1 / scale).
     """
     if pairs not in _ROPE_PAIRS:
         raise SDError("pairs must be 'halves' or 'neighbours'")
